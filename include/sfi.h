@@ -461,6 +461,53 @@ SFI_API int32_t sfi_plan_splits(const sfi_attn_shape *shape, int32_t batch, int3
  */
 SFI_API int32_t sfi_attn_cluster_capacity(int32_t cluster_size);
 
+/*
+ * Head norm and position rotation, into the cache. The attention calls above take Q
+ * after, and keep K after, the norm of each head and the rotation by position; this
+ * call makes both from the projections' output, in one pass.
+ *
+ * sfi_rope describes the rotation. Pair i of the rot_dim / 2 rotated pairs of a head
+ * turns by pos * turns[i] / 2^64 whole turns, where pos is the token's position on axis
+ * axis[i]: the product wraps modulo one turn exactly, so angles are as good at position
+ * 2^31 as at 0. turns[i] = round(inv_freq[i] / (2 pi) * 2^64) modulo 2^64.
+ */
+typedef struct {
+    const uint64_t *turns; /* [rot_dim / 2] */
+    const uint8_t *axis;   /* [rot_dim / 2], each < num_axes; NULL: axis 0 */
+    int32_t rot_dim;       /* rotated dims, the first of each head: a multiple of 16 up to D */
+    int32_t num_axes;      /* position axes (1; or e.g. 3: time, height, width), 1..8 */
+    int32_t interleaved;   /* 0: pair i is dims (i, i + rot_dim / 2); 1: dims (2i, 2i + 1) */
+} sfi_rope;
+
+/*
+ * sfi_qk_norm_rope - for every new token and head: y = rotate(x * w / sqrt(mean(x^2) + eps)),
+ * in fp32, rounded once to bf16. Token t < n_r of request r (n_r = new_lens[r], or T when
+ * new_lens is NULL) has slot L_r - n_r + t; tokens t >= n_r are neither read nor written.
+ *   q, k, v   : bf16; token t of request r starts at element (r T + t) * stride of each,
+ *               its heads are contiguous ([Hq][D], [Hkv][D], [Hkv][D]), so the three may be
+ *               parts of one fused projection. Strides (in elements) are multiples of 8,
+ *               pointers 16-byte aligned. v may be NULL when kv is.
+ *   rope      : NULL: no rotation
+ *   q_weight, k_weight : bf16 [D], 16-byte aligned, or NULL: no norm for q (for k)
+ *   positions : int32, axis a of token t of request r at a * axis_stride + r T + t; or NULL:
+ *               the slot is the position on every axis. Positions may be negative.
+ *   q_out     : bf16 [B][T][Hq][D]
+ *   k_out     : bf16 [B][T][Hkv][D], or NULL
+ *   kv        : the pages that receive K and V at the tokens' slots, or NULL (then rope
+ *               without positions is refused)
+ * Outputs must not overlap inputs. At least one of k_out and kv must be given.
+ * Device errors: SFI_DEV_BAD_LEN (n_r < 0, n_r > T, or with kv L_r < n_r or L_r beyond the
+ * page table: nothing of that request is written), SFI_DEV_BAD_PAGE (that token's K and V
+ * are not written to the pages), SFI_DEV_BAD_INDEX (an axis[i] >= num_axes: pair i does
+ * not turn).
+ */
+SFI_API sfi_status sfi_qk_norm_rope(const sfi_attn_shape *shape, const sfi_rope *rope, const void *q, int64_t q_stride,
+                                    const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                    const void *q_weight, const void *k_weight, float eps, const int32_t *positions,
+                                    int64_t axis_stride, int32_t num_tokens, const int32_t *new_lens, void *q_out,
+                                    void *k_out, const sfi_paged_kv *kv, const int32_t *req_ids, int32_t batch,
+                                    int32_t *dev_status, void *stream);
+
 /* Human-readable name of a status code (static string). */
 SFI_API const char *sfi_status_string(sfi_status status);
 

@@ -7,7 +7,8 @@ that orders the kernels on a main and an aux stream. Nothing here falls back to
 another implementation: every call fails loudly if libsfi.so is missing.
 """
 from .api import (SFI_ATTN_EARLY_KV_PREFETCH, SFI_ATTN_RAGGED, SFI_ATTN_TEST_WITHHOLD, SFI_MAX_QUERY_TOKENS,
-                  AttnShape, CompactKV, PagedKV, SFIError, alloc_mixed_workspace, alloc_multi_workspace,
+                  AttnShape, CompactKV, PagedKV, Rope, SFIError, alloc_mixed_workspace,
+                  alloc_multi_workspace, rope_turns, sfi_qk_norm_rope,
                   alloc_ragged_workspace, alloc_workspace, sfi_compact_gather, sfi_dense_verify_attn,
                   sfi_fast_decode_attn, sfi_fast_decode_attn_noalloc, sfi_mixed_decode_attn,
                   sfi_mixed_workspace_size, sfi_multi_workspace_size, sfi_paged_kv_append,
@@ -19,7 +20,7 @@ from .runtime import (DecodeBatch, LayerBuffers, SFIDecoder, SlowFastSchedule, S
 
 __all__ = [
     "SFI_ATTN_EARLY_KV_PREFETCH", "SFI_ATTN_RAGGED", "SFI_ATTN_TEST_WITHHOLD", "SFI_MAX_QUERY_TOKENS", "AttnShape", "CompactKV",
-    "PagedKV", "SFIError", "alloc_mixed_workspace", "alloc_multi_workspace", "alloc_ragged_workspace",
+    "PagedKV", "Rope", "SFIError", "rope_turns", "sfi_qk_norm_rope", "alloc_mixed_workspace", "alloc_multi_workspace", "alloc_ragged_workspace",
     "alloc_workspace", "sfi_compact_gather", "sfi_dense_verify_attn", "sfi_fast_decode_attn",
     "sfi_fast_decode_attn_noalloc", "sfi_mixed_decode_attn", "sfi_mixed_workspace_size",
     "sfi_multi_workspace_size", "sfi_paged_kv_append", "sfi_paged_kv_append_tokens", "sfi_plan_splits",

@@ -30,6 +30,10 @@ class sfi_compact_kv(ctypes.Structure):
                 ("count", c_vp)]
 
 
+class sfi_rope(ctypes.Structure):
+    _fields_ = [("turns", c_vp), ("axis", c_vp), ("rot_dim", c_i32), ("num_axes", c_i32), ("interleaved", c_i32)]
+
+
 SFI_OK, SFI_ERR_INVALID_ARG, SFI_ERR_UNSUPPORTED, SFI_ERR_WORKSPACE, SFI_ERR_CUDA = range(5)
 SFI_DEV_BAD_PAGE, SFI_DEV_BAD_LEN, SFI_DEV_K_OVERFLOW = 1, 2, 4
 SFI_DEV_BAD_INDEX, SFI_DEV_TIMEOUT, SFI_DEV_BAD_COMPACT = 8, 16, 32
@@ -41,6 +45,7 @@ SFI_MAX_QUERY_TOKENS = 16
 P_SHAPE = ctypes.POINTER(sfi_attn_shape)
 P_PAGED = ctypes.POINTER(sfi_paged_kv)
 P_COMPACT = ctypes.POINTER(sfi_compact_kv)
+P_ROPE = ctypes.POINTER(sfi_rope)
 
 # name -> (restype, argtypes), in the order of include/sfi.h
 PROTOTYPES = {
@@ -70,6 +75,8 @@ PROTOTYPES = {
     "sfi_workspace_size": (c_sz, [P_SHAPE, c_i32, c_i32, c_i32]),
     "sfi_plan_splits": (c_i32, [P_SHAPE, c_i32, c_i32, c_i32]),
     "sfi_attn_cluster_capacity": (c_i32, [c_i32]),
+    "sfi_qk_norm_rope": (c_i32, [P_SHAPE, P_ROPE, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_f32, c_vp, c_i64,
+                                 c_i32, c_vp, c_vp, c_vp, P_PAGED, c_vp, c_i32, c_vp, c_vp]),
     "sfi_status_string": (ctypes.c_char_p, [c_i32]),
     "sfi_version": (c_i32, []),
 }

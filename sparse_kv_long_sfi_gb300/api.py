@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass
+from fractions import Fraction
 from typing import Optional
 
 import torch
@@ -331,6 +332,93 @@ def sfi_fast_decode_attn_noalloc(shape: AttnShape, kv: PagedKV, compact: Compact
         _ptr(req_ids, torch.int32, "req_ids"), _batch(batch, req_ids, kv.seq_lens), int(max_tokens),
         int(num_splits), int(flags), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
     _check(st, "sfi_fast_decode_attn_noalloc")
+
+
+@dataclass
+class Rope:
+    """The position rotation of sfi_qk_norm_rope: turns int64 [rot_dim / 2] (rope_turns),
+    axis uint8 [rot_dim / 2] or None, the number of position axes, and whether pairs are
+    adjacent dims (interleaved) or dims rot_dim / 2 apart."""
+    turns: torch.Tensor
+    axis: Optional[torch.Tensor] = None
+    num_axes: int = 1
+    interleaved: bool = False
+
+    def c(self) -> _abi.sfi_rope:
+        _need(self.turns, torch.int64, "rope.turns")
+        axis = _ptr(self.axis, torch.uint8, "rope.axis")
+        if self.axis is not None and self.axis.numel() != self.turns.numel():
+            raise ValueError("rope.axis needs one entry for each of rope.turns")
+        return _abi.sfi_rope(self.turns.data_ptr(), axis, 2 * self.turns.numel(), int(self.num_axes),
+                             int(bool(self.interleaved)))
+
+
+# 2 pi to 40 decimals: positions are 32-bit, so 64-bit turns need more digits than a double has
+_TWO_PI = Fraction(62831853071795864769252867665590057683943, 10 ** 40)
+
+
+def rope_turns(inv_freq, device="cuda") -> torch.Tensor:
+    """Rotation per position (inv_freq in radians, fp64) as 64-bit fixed-point turns modulo one turn."""
+    freqs = [float(f) for f in (inv_freq.tolist() if isinstance(inv_freq, torch.Tensor) else inv_freq)]
+    turns = [round(Fraction(f) * 2 ** 64 / _TWO_PI) % 2 ** 64 for f in freqs]
+    return torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
+
+
+def _on_current_device(t: torch.Tensor, name: str):
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+
+
+def _token_rows(t: torch.Tensor, heads: int, dim: int, name: str) -> int:
+    """Elements between the tokens of a [B][T][heads][dim] tensor whose heads are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 4 or t.shape[2] != heads or t.shape[3] != dim:
+        raise ValueError(f"{name} must be [B][T][{heads}][{dim}], got {list(t.shape)}")
+    b, n = t.shape[:2]
+    s = t.stride()
+    step = s[1] if n > 1 else (s[0] if b > 1 else heads * dim)
+    if s[3] != 1 or (heads > 1 and s[2] != dim) or (b > 1 and s[0] != n * step):
+        raise ValueError(f"{name} needs contiguous heads and one stride between all tokens")
+    return step
+
+
+def sfi_qk_norm_rope(shape: AttnShape, rope: Optional[Rope], q: torch.Tensor, k: torch.Tensor,
+                     v: Optional[torch.Tensor], q_out: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                     k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                     positions: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
+                     k_out: Optional[torch.Tensor] = None, kv: Optional[PagedKV] = None,
+                     req_ids: Optional[torch.Tensor] = None, batch: Optional[int] = None,
+                     dev_status: Optional[torch.Tensor] = None, stream=None):
+    """Head norm and rotation of the new tokens; q, k, v [B][T][heads][D] may be views of one
+    fused projection. positions int32 [num_axes][B][T] (or [B][T] with one axis)."""
+    hq, hkv, d = shape.num_q_heads, shape.num_kv_heads, shape.head_dim
+    _on_current_device(q, "q")
+    qs, ks = _token_rows(q, hq, d, "q"), _token_rows(k, hkv, d, "k")
+    vs = 0 if v is None else _token_rows(v, hkv, d, "v")
+    B, T = q.shape[:2]
+    if k.shape[:2] != q.shape[:2] or (v is not None and v.shape[:2] != q.shape[:2]):
+        raise ValueError("q, k and v need the same requests and tokens")
+    if q_out.shape != q.shape or (k_out is not None and k_out.shape != k.shape):
+        raise ValueError("q_out and k_out need the shapes of q and k")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and w.numel() != d:
+            raise ValueError(f"{name} must have {d} values")
+    if positions is not None and positions.numel() != (rope.num_axes if rope is not None else 1) * B * T:
+        raise ValueError("positions must be [num_axes][B][T]")
+    if new_lens is not None and new_lens.numel() != B:
+        raise ValueError("new_lens needs one entry per request")
+    st = _abi.lib().sfi_qk_norm_rope(
+        ctypes.byref(shape.c()), None if rope is None else ctypes.byref(rope.c()), q.data_ptr(), qs, k.data_ptr(), ks,
+        None if v is None else v.data_ptr(), vs, _ptr(q_weight, torch.bfloat16, "q_weight"),
+        _ptr(k_weight, torch.bfloat16, "k_weight"), float(eps), _ptr(positions, torch.int32, "positions"), B * T, T,
+        _ptr(new_lens, torch.int32, "new_lens"), _ptr(q_out, torch.bfloat16, "q_out"),
+        _ptr(k_out, torch.bfloat16, "k_out"), None if kv is None else ctypes.byref(kv.c()),
+        _ptr(req_ids, torch.int32, "req_ids"), B if batch is None and req_ids is None else _batch(batch, req_ids, None),
+        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    _check(st, "sfi_qk_norm_rope")
 
 
 def sfi_workspace_size(shape: AttnShape, batch: int, max_tokens: int, num_splits: int = 0) -> int:

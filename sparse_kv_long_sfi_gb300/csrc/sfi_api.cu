@@ -45,6 +45,10 @@ bool encode_rows(CUtensorMap *map, void *base, int64_t rows, int head_dim) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+namespace sfi {
+
 int sm_count_current_device() {
     static std::atomic<int> cache[64];
     int dev = 0;
@@ -59,8 +63,9 @@ int sm_count_current_device() {
     return n;
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+float resolve_scale(const sfi_attn_shape *s) {
+    return s->softmax_scale > 0.f ? s->softmax_scale : 1.0f / std::sqrt((float)s->head_dim);
+}
 
 sfi_status check_shape(const sfi_attn_shape *s) {
     if (!s) return SFI_ERR_INVALID_ARG;
@@ -82,6 +87,17 @@ sfi_status check_paged(const sfi_attn_shape *s, const sfi_paged_kv *kv) {
     if ((int64_t)kv->max_pages_per_req * s->page_size >= (int64_t(1) << 31)) return SFI_ERR_UNSUPPORTED;
     return SFI_OK;
 }
+
+}  // namespace sfi
+
+namespace {
+
+using sfi::aligned16;
+using sfi::aligned8;
+using sfi::check_paged;
+using sfi::check_shape;
+using sfi::resolve_scale;
+using sfi::sm_count_current_device;
 
 // Split-KV plan of one attention launch. Automatic plans fill about 85% of one wave of
 // resident CTAs (two per SM); an explicit request is honoured down to two stages per
@@ -163,10 +179,6 @@ MixedPlan plan_mixed(int64_t fast_units, int64_t slow_units, int32_t max_fast_to
     }
     m.slots = fast_units * m.fast_splits + slow_units * m.slow_splits;
     return m;
-}
-
-float resolve_scale(const sfi_attn_shape *s) {
-    return s->softmax_scale > 0.f ? s->softmax_scale : 1.0f / std::sqrt((float)s->head_dim);
 }
 
 void fill_common(AttnParams &p, const sfi_attn_shape *s, const sfi_paged_kv *kv, const void *q, float *out,

@@ -142,4 +142,33 @@ struct CopyParams {
 cudaError_t launch_paged_append(const CopyParams &p, int batch, cudaStream_t stream);
 cudaError_t launch_compact_gather(const CopyParams &p, int batch, int max_rows, cudaStream_t stream);
 
+// Helpers of the entry points (sfi_api.cu).
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+int sm_count_current_device();
+float resolve_scale(const sfi_attn_shape *s);
+sfi_status check_shape(const sfi_attn_shape *s);
+sfi_status check_paged(const sfi_attn_shape *s, const sfi_paged_kv *kv);
+
+struct NormRopeParams {
+    const __nv_bfloat16 *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements between tokens
+    const __nv_bfloat16 *q_weight, *k_weight;
+    float eps;
+    const uint64_t *turns;
+    const uint8_t *axis;
+    int32_t rot_dim, num_axes, interleaved;
+    const int32_t *positions;  // [num_axes][all requests][tokens], or null
+    int64_t axis_stride;       // entries of one axis
+    int32_t tokens;
+    const int32_t *new_lens;
+    __nv_bfloat16 *q_out, *k_out, *k_pool, *v_pool;
+    const int32_t *page_table, *seq_lens;
+    int32_t max_pages, num_pages;
+    int32_t hq, hkv;
+    const int32_t *req_ids;
+    int32_t *dev_status;
+};
+cudaError_t launch_qk_norm_rope(const NormRopeParams &p, int head_dim, int batch, cudaStream_t stream);
+
 }  // namespace sfi

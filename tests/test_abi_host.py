@@ -187,3 +187,42 @@ def test_binding_constants_match_the_header():
     assert len(defines) >= 10 and len(enums) == 5
     for name, value in {**defines, **enums}.items():
         assert getattr(_abi, name) == value, name
+
+
+def test_qk_norm_rope_validates_on_the_host(libsfi):
+    from sparse_kv_long_sfi_gb300 import _abi
+    rope = _abi.sfi_rope(4096, None, 128, 1, 0)
+
+    def call(sh=_shape(), rope=rope, q=4096, qs=2048, k=4096, ks=1024, v=4096, vs=1024, qw=None, eps=1e-6, pos=None,
+             axis_stride=0, T=1, q_out=4096, k_out=4096, kv=_paged(), batch=1):
+        return libsfi.sfi_qk_norm_rope(ctypes.byref(sh), rope and ctypes.byref(rope), q, qs, k, ks, v, vs, qw, None, eps,
+                                       pos, axis_stride, T, None, q_out, k_out, kv and ctypes.byref(kv), None, batch,
+                                       None, None)
+
+    assert call(batch=0) == 0
+    assert call(sh=_shape(16, 8, 96)) == 2 and call(sh=_shape(16, 5)) == 1
+    assert call(q=None) == 1 and call(k=None) == 1 and call(v=None) == 1 and call(q_out=None) == 1
+    assert call(k_out=None, kv=None) == 1          # nowhere to put K
+    assert call(q=4104) == 1 and call(k_out=4100) == 1 and call(qw=4098) == 1
+    assert call(qs=2040) == 1 and call(qs=2052) == 1 and call(ks=1020) == 1 and call(vs=1016) == 1
+    assert call(T=0) == 1 and call(batch=-1) == 1 and call(eps=-1.0) == 1 and call(eps=float("nan")) == 1
+    for rot, expect in ((-16, 2), (24, 2), (144, 2), (0, 0), (16, 0)):
+        assert call(rope=_abi.sfi_rope(4096, None, rot, 1, 0), batch=0) == expect
+    assert call(rope=_abi.sfi_rope(None, None, 64, 1, 0)) == 1
+    assert call(rope=_abi.sfi_rope(4096, None, 64, 0, 0)) == 1 and call(rope=_abi.sfi_rope(4096, None, 64, 9, 0)) == 1
+    assert call(rope=_abi.sfi_rope(4096, None, 64, 1, 2)) == 1
+    assert call(kv=None) == 1                      # rotation by neither slot nor position
+    assert call(rope=_abi.sfi_rope(4096, None, 64, 3, 0), pos=4096, axis_stride=4, T=5) == 1
+    assert call(rope=None, kv=None, v=None, batch=0) == 0
+
+
+def test_rope_turns_are_exact_modulo_one_turn():
+    """turns[i] is inv_freq / (2 pi) in 2^-64 turns: close to the fp64 quotient, and wrapped
+    for more than half a turn."""
+    import math
+    import sparse_kv_long_sfi_gb300 as sfi
+    f = [1.0, 1e-6, 0.37, 4.0, 2 * math.pi * 1.75]
+    got = sfi.rope_turns(f, device="cpu").tolist()
+    for x, t in zip(f, got):
+        turn = x / (2 * math.pi) % 1.0
+        assert abs((t % 2 ** 64) / 2 ** 64 - turn) <= 2.0 ** -51, x
