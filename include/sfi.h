@@ -508,6 +508,116 @@ SFI_API sfi_status sfi_qk_norm_rope(const sfi_attn_shape *shape, const sfi_rope 
                                     void *k_out, const sfi_paged_kv *kv, const int32_t *req_ids, int32_t batch,
                                     int32_t *dev_status, void *stream);
 
+/*
+ * The cache held in 4 bits. A token's K (and V) row of one head is held in groups of 16
+ * values along D: a scale s in e4m3 and 16 codes in e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives); value = code * s * g, with one power of two g for all K (k_scale) and
+ * one for all V (v_scale) of a cache. 4.5 bits a value. Quantisation: s = e4m3(min(amax /
+ * (6 g), 448)), code = e2m1(x / (s g)), both to nearest with ties to even; s = 0 gives
+ * zeros; a group with a NaN or an infinity gets the scale NaN and reads back as NaN.
+ *
+ * The block of one (page, KV head) has 18 D bytes (16-byte aligned, K and V together, so
+ * that one contiguous read brings what 16 positions need):
+ *   [0, 8D)    K codes: byte token * D/2 + d/2, the even d in the low four bits
+ *   [8D, 9D)   K scales: byte token * D/16 + d/16
+ *   [9D, 17D)  V codes, in the order the matrix instruction's lanes take them: for
+ *              d = 64 a + 16 b + 8 c + 2 e + f and token = 4 t + 2 h + l the byte
+ *              512 a + 128 e + 32 t + 16 f + 4 b + 2 h + c, l = 0 in the low four bits
+ *   [17D, 18D) V scales: byte t * D/4 + 4 * (d/16) + token % 4, t = token / 4
+ */
+typedef struct {
+    void *pool;                /* [num_pages][Hkv][18 D] bytes, 16-byte aligned */
+    int32_t num_pages;
+    int32_t max_pages_per_req; /* row stride of page_table */
+    const int32_t *page_table; /* int32 [B][max_pages_per_req] */
+    const int32_t *seq_lens;   /* int32 [B]: L of each request */
+    float k_scale, v_scale;    /* powers of two */
+} sfi_paged_kv4;
+
+/* Sink and selected rows of one layer, packed into 4-bit blocks: block i of KV head h of
+ * request r is block  page_offset[r] + h * capacity[r] + i;  its 16 rows are the compact
+ * rows [16 i, 16 i + 16) (sink rows [0, min(S, L)), selection from row S on). */
+typedef struct {
+    void *pool;                 /* [total_pages][18 D] bytes, 16-byte aligned */
+    int64_t total_pages;
+    const int64_t *page_offset; /* int64 [B] */
+    const int32_t *capacity;    /* int32 [B] blocks per KV head, >= (S + k_r + 15) / 16 */
+    const int32_t *count;       /* int32 [B] selected rows per KV head */
+} sfi_compact_kv4;
+
+/*
+ * sfi_kv4_append - quantise the n_r newest tokens of each request (n_r = new_lens[r], or
+ * num_tokens when new_lens is NULL) into the pages: token t < n_r goes to position
+ * L_r - n_r + t. Other positions of a page keep their bits. The requests of one call must
+ * not share the pages they write.
+ *   k_new, v_new : bf16 [B][num_tokens][Hkv][D], 16-byte aligned
+ * Device errors: SFI_DEV_BAD_LEN (n_r < 0, n_r > num_tokens, L_r < n_r or L_r beyond the page
+ * table: that request is skipped), SFI_DEV_BAD_PAGE (that page's tokens are skipped).
+ */
+SFI_API sfi_status sfi_kv4_append(const sfi_attn_shape *shape, const sfi_paged_kv4 *kv, const void *k_new,
+                                  const void *v_new, int32_t num_tokens, const int32_t *new_lens,
+                                  const int32_t *req_ids, int32_t batch, int32_t *dev_status, void *stream);
+
+/*
+ * sfi_kv4_read - the values the cache holds, e.g. for the attention of a prompt's next
+ * chunk: row t of request r receives position first[r] + t (first NULL: position t), in
+ * bf16 (exact unless out of bf16's range). Rows at positions >= L_r keep their contents.
+ *   k_out, v_out : bf16 [B][num_tokens][Hkv][D], 16-byte aligned
+ * Device errors: SFI_DEV_BAD_LEN (L_r < 0 or beyond the page table, or first[r] < 0: that
+ * request is skipped), SFI_DEV_BAD_PAGE (that page's rows are skipped).
+ */
+SFI_API sfi_status sfi_kv4_read(const sfi_attn_shape *shape, const sfi_paged_kv4 *kv, void *k_out, void *v_out,
+                                int32_t num_tokens, const int32_t *first, const int32_t *req_ids, int32_t batch,
+                                int32_t *dev_status, void *stream);
+
+/*
+ * sfi_kv4_compact_gather - sfi_compact_gather for the 4-bit cache: the codes and scales of
+ * sink and selected rows move as they are (nothing is quantised again). Every block up to
+ * (rows + 15) / 16 is written whole; rows that hold nothing become zeros.
+ *   idx   : int32 [B][Hkv][k_cap] ascending positions;  count : int32 [B]
+ * Device errors: SFI_DEV_BAD_LEN, SFI_DEV_K_OVERFLOW, SFI_DEV_BAD_COMPACT (that request is
+ * skipped), SFI_DEV_BAD_INDEX, SFI_DEV_BAD_PAGE (that row becomes zeros).
+ */
+SFI_API sfi_status sfi_kv4_compact_gather(const sfi_attn_shape *shape, const sfi_paged_kv4 *kv, const int32_t *idx,
+                                          const int32_t *count, int32_t k_cap, int32_t sink,
+                                          const sfi_compact_kv4 *compact, const int32_t *req_ids, int32_t batch,
+                                          int32_t *dev_status, void *stream);
+
+/*
+ * sfi_kv4_dense_attn - sfi_dense_verify_attn (num_tokens query tokens, causal; with one
+ * token sfi_slow_dense_attn_with_scores) over the 4-bit cache, whose newest tokens are in
+ * the pages already. The work is split over the GPU by the requests' real lengths, so the
+ * call takes no bound on them. num_tokens x G <= 16.
+ *   q : bf16 [B][num_tokens][Hq][D];  out : fp32 of that shape, 8-byte aligned
+ *   lse : fp32 [B][num_tokens][Hq] or NULL;  scores, score_stride : as there, or NULL
+ *   workspace : sfi_kv4_workspace_size(shape, batch, num_tokens) bytes, 256-byte aligned,
+ *               zero-filled before its first use, then used with this shape alone (its
+ *               counters are left zero); launches sharing it must not overlap, those of
+ *               captured graphs included
+ * Device errors: SFI_DEV_BAD_LEN (also L < num_tokens, or L > score_stride), SFI_DEV_BAD_PAGE.
+ */
+SFI_API sfi_status sfi_kv4_dense_attn(const sfi_attn_shape *shape, const sfi_paged_kv4 *kv, int32_t sink,
+                                      int32_t recent, const void *q, int32_t num_tokens, float *out, float *lse,
+                                      float *scores, int64_t score_stride, const int32_t *req_ids, int32_t batch,
+                                      void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * sfi_kv4_fast_attn - sfi_sparse_draft_attn (with one token sfi_fast_decode_attn) over the
+ * 4-bit compact blocks and the recent window of the 4-bit pages. A query token that sees
+ * nothing (no sink, no selection, recent = 0) gets out = 0 and lse = -inf.
+ *   other arguments : as for sfi_kv4_dense_attn
+ * Device errors: SFI_DEV_BAD_LEN, SFI_DEV_BAD_PAGE, SFI_DEV_K_OVERFLOW, SFI_DEV_BAD_COMPACT.
+ */
+SFI_API sfi_status sfi_kv4_fast_attn(const sfi_attn_shape *shape, const sfi_paged_kv4 *kv,
+                                     const sfi_compact_kv4 *compact, int32_t sink, int32_t recent, const void *q,
+                                     int32_t num_tokens, float *out, float *lse, const int32_t *req_ids,
+                                     int32_t batch, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                                     void *stream);
+
+/* Workspace bytes of the two 4-bit attention calls on the current device, valid for every
+ * batch size 1..batch and every num_tokens up to the given one (0 on invalid input). */
+SFI_API size_t sfi_kv4_workspace_size(const sfi_attn_shape *shape, int32_t batch, int32_t num_tokens);
+
 /* Human-readable name of a status code (static string). */
 SFI_API const char *sfi_status_string(sfi_status status);
 

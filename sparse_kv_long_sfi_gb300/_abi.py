@@ -34,6 +34,15 @@ class sfi_rope(ctypes.Structure):
     _fields_ = [("turns", c_vp), ("axis", c_vp), ("rot_dim", c_i32), ("num_axes", c_i32), ("interleaved", c_i32)]
 
 
+class sfi_paged_kv4(ctypes.Structure):
+    _fields_ = [("pool", c_vp), ("num_pages", c_i32), ("max_pages_per_req", c_i32), ("page_table", c_vp),
+                ("seq_lens", c_vp), ("k_scale", c_f32), ("v_scale", c_f32)]
+
+
+class sfi_compact_kv4(ctypes.Structure):
+    _fields_ = [("pool", c_vp), ("total_pages", c_i64), ("page_offset", c_vp), ("capacity", c_vp), ("count", c_vp)]
+
+
 SFI_OK, SFI_ERR_INVALID_ARG, SFI_ERR_UNSUPPORTED, SFI_ERR_WORKSPACE, SFI_ERR_CUDA = range(5)
 SFI_DEV_BAD_PAGE, SFI_DEV_BAD_LEN, SFI_DEV_K_OVERFLOW = 1, 2, 4
 SFI_DEV_BAD_INDEX, SFI_DEV_TIMEOUT, SFI_DEV_BAD_COMPACT = 8, 16, 32
@@ -46,6 +55,8 @@ P_SHAPE = ctypes.POINTER(sfi_attn_shape)
 P_PAGED = ctypes.POINTER(sfi_paged_kv)
 P_COMPACT = ctypes.POINTER(sfi_compact_kv)
 P_ROPE = ctypes.POINTER(sfi_rope)
+P_KV4 = ctypes.POINTER(sfi_paged_kv4)
+P_COMPACT4 = ctypes.POINTER(sfi_compact_kv4)
 
 # name -> (restype, argtypes), in the order of include/sfi.h
 PROTOTYPES = {
@@ -77,6 +88,14 @@ PROTOTYPES = {
     "sfi_attn_cluster_capacity": (c_i32, [c_i32]),
     "sfi_qk_norm_rope": (c_i32, [P_SHAPE, P_ROPE, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_f32, c_vp, c_i64,
                                  c_i32, c_vp, c_vp, c_vp, P_PAGED, c_vp, c_i32, c_vp, c_vp]),
+    "sfi_kv4_append": (c_i32, [P_SHAPE, P_KV4, c_vp, c_vp, c_i32, c_vp, c_vp, c_i32, c_vp, c_vp]),
+    "sfi_kv4_read": (c_i32, [P_SHAPE, P_KV4, c_vp, c_vp, c_i32, c_vp, c_vp, c_i32, c_vp, c_vp]),
+    "sfi_kv4_compact_gather": (c_i32, [P_SHAPE, P_KV4, c_vp, c_vp, c_i32, c_i32, P_COMPACT4, c_vp, c_i32, c_vp, c_vp]),
+    "sfi_kv4_dense_attn": (c_i32, [P_SHAPE, P_KV4, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp, c_vp, c_i64, c_vp, c_i32, c_vp,
+                                   c_sz, c_vp, c_vp]),
+    "sfi_kv4_fast_attn": (c_i32, [P_SHAPE, P_KV4, P_COMPACT4, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp, c_vp, c_i32, c_vp,
+                                  c_sz, c_vp, c_vp]),
+    "sfi_kv4_workspace_size": (c_sz, [P_SHAPE, c_i32, c_i32]),
     "sfi_status_string": (ctypes.c_char_p, [c_i32]),
     "sfi_version": (c_i32, []),
 }

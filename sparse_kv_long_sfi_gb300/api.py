@@ -421,6 +421,155 @@ def sfi_qk_norm_rope(shape: AttnShape, rope: Optional[Rope], q: torch.Tensor, k:
     _check(st, "sfi_qk_norm_rope")
 
 
+@dataclass
+class PagedKV4:
+    """Paged 4-bit cache: pool uint8 [num_pages][Hkv][18 D] (alloc_kv4_pool), page_table int32
+    [B][max_pages], seq_lens int32 [B]; k_scale and v_scale are powers of two."""
+    pool: torch.Tensor
+    page_table: torch.Tensor
+    seq_lens: torch.Tensor
+    k_scale: float = 1.0
+    v_scale: float = 1.0
+
+    def c(self) -> _abi.sfi_paged_kv4:
+        _need(self.pool, torch.uint8, "pool")
+        _need(self.page_table, torch.int32, "page_table")
+        _need(self.seq_lens, torch.int32, "seq_lens")
+        return _abi.sfi_paged_kv4(self.pool.data_ptr(), self.pool.shape[0], self.page_table.shape[1],
+                                  self.page_table.data_ptr(), self.seq_lens.data_ptr(), self.k_scale, self.v_scale)
+
+
+@dataclass
+class CompactKV4:
+    """4-bit compact blocks: pool uint8 [total_pages][18 D]; page_offset int64 [B]; capacity
+    (blocks per KV head) and count (selected rows) int32 [B]."""
+    pool: torch.Tensor
+    page_offset: torch.Tensor
+    capacity: torch.Tensor
+    count: torch.Tensor
+
+    def c(self) -> _abi.sfi_compact_kv4:
+        _need(self.pool, torch.uint8, "compact.pool")
+        _need(self.page_offset, torch.int64, "compact.page_offset")
+        _need(self.capacity, torch.int32, "compact.capacity")
+        _need(self.count, torch.int32, "compact.count")
+        return _abi.sfi_compact_kv4(self.pool.data_ptr(), self.pool.shape[0], self.page_offset.data_ptr(),
+                                    self.capacity.data_ptr(), self.count.data_ptr())
+
+
+def _kv4(shape: AttnShape, kv: PagedKV4):
+    _on_current_device(kv.pool, "pool")
+    if kv.pool.dim() != 3 or kv.pool.shape[1] != shape.num_kv_heads or kv.pool.shape[2] != 18 * shape.head_dim:
+        raise ValueError(f"pool must be [num_pages][{shape.num_kv_heads}][{18 * shape.head_dim}], "
+                         f"got {list(kv.pool.shape)}")
+    return ctypes.byref(kv.c())
+
+
+def alloc_kv4_pool(shape: AttnShape, num_pages: int, device="cuda") -> torch.Tensor:
+    """A zero-filled pool of the 4-bit cache."""
+    return torch.zeros((num_pages, shape.num_kv_heads, 18 * shape.head_dim), dtype=torch.uint8, device=device)
+
+
+def alloc_kv4_compact(shape: AttnShape, rows, device="cuda") -> CompactKV4:
+    """4-bit compact blocks for rows[r] = sink + k_r rows per KV head of request r."""
+    cap = torch.tensor([(int(n) + 15) // 16 for n in rows], dtype=torch.int64)
+    ends = torch.cumsum(cap * shape.num_kv_heads, 0)
+    pool = torch.zeros((max(1, int(ends[-1]) if len(cap) else 1), 18 * shape.head_dim), dtype=torch.uint8, device=device)
+    return CompactKV4(pool, (ends - cap * shape.num_kv_heads).to(device), cap.to(torch.int32).to(device),
+                      torch.zeros(len(cap), dtype=torch.int32, device=device))
+
+
+def _rows4(t: torch.Tensor, dtype, shape: AttnShape, heads: int, name: str) -> int:
+    """Tokens of a [B][T][heads][D] tensor."""
+    _need(t, dtype, name)
+    if t.dim() != 4 or t.shape[2] != heads or t.shape[3] != shape.head_dim:
+        raise ValueError(f"{name} must be [B][T][{heads}][{shape.head_dim}], got {list(t.shape)}")
+    return t.shape[1]
+
+
+def sfi_kv4_append(shape: AttnShape, kv: PagedKV4, k_new: torch.Tensor, v_new: torch.Tensor,
+                   new_lens: Optional[torch.Tensor] = None, req_ids: Optional[torch.Tensor] = None,
+                   batch: Optional[int] = None, dev_status: Optional[torch.Tensor] = None, stream=None):
+    T = _rows4(k_new, torch.bfloat16, shape, shape.num_kv_heads, "k_new")
+    if _rows4(v_new, torch.bfloat16, shape, shape.num_kv_heads, "v_new") != T or v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new need the same shape")
+    st = _abi.lib().sfi_kv4_append(
+        ctypes.byref(shape.c()), _kv4(shape, kv), k_new.data_ptr(), v_new.data_ptr(), T,
+        _ptr(new_lens, torch.int32, "new_lens"), _ptr(req_ids, torch.int32, "req_ids"),
+        _batch(batch, req_ids, kv.seq_lens), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    _check(st, "sfi_kv4_append")
+
+
+def sfi_kv4_read(shape: AttnShape, kv: PagedKV4, k_out: torch.Tensor, v_out: torch.Tensor,
+                 first: Optional[torch.Tensor] = None, req_ids: Optional[torch.Tensor] = None,
+                 batch: Optional[int] = None, dev_status: Optional[torch.Tensor] = None, stream=None):
+    T = _rows4(k_out, torch.bfloat16, shape, shape.num_kv_heads, "k_out")
+    if _rows4(v_out, torch.bfloat16, shape, shape.num_kv_heads, "v_out") != T or v_out.shape != k_out.shape:
+        raise ValueError("k_out and v_out need the same shape")
+    st = _abi.lib().sfi_kv4_read(
+        ctypes.byref(shape.c()), _kv4(shape, kv), k_out.data_ptr(), v_out.data_ptr(), T,
+        _ptr(first, torch.int32, "first"), _ptr(req_ids, torch.int32, "req_ids"),
+        _batch(batch, req_ids, kv.seq_lens), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    _check(st, "sfi_kv4_read")
+
+
+def sfi_kv4_compact_gather(shape: AttnShape, kv: PagedKV4, idx: torch.Tensor, count: torch.Tensor, sink: int,
+                           compact: CompactKV4, req_ids: Optional[torch.Tensor] = None, batch: Optional[int] = None,
+                           dev_status: Optional[torch.Tensor] = None, stream=None):
+    st = _abi.lib().sfi_kv4_compact_gather(
+        ctypes.byref(shape.c()), _kv4(shape, kv), _ptr(idx, torch.int32, "idx"), _ptr(count, torch.int32, "count"),
+        int(idx.shape[-1]), int(sink), ctypes.byref(compact.c()), _ptr(req_ids, torch.int32, "req_ids"),
+        _batch(batch, req_ids, kv.seq_lens), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    _check(st, "sfi_kv4_compact_gather")
+
+
+def _kv4_query(shape: AttnShape, q: torch.Tensor, out: torch.Tensor, lse: Optional[torch.Tensor]) -> int:
+    T = _rows4(q, torch.bfloat16, shape, shape.num_q_heads, "q")
+    _need(out, torch.float32, "out")
+    if out.shape != q.shape or (lse is not None and lse.shape != q.shape[:3]):
+        raise ValueError("out needs the shape of q, lse that without its last dimension")
+    return T
+
+
+def sfi_kv4_dense_attn(shape: AttnShape, kv: PagedKV4, sink: int, recent: int, q: torch.Tensor, out: torch.Tensor,
+                       lse: Optional[torch.Tensor] = None, scores: Optional[torch.Tensor] = None,
+                       req_ids: Optional[torch.Tensor] = None, batch: Optional[int] = None,
+                       workspace: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
+                       stream=None):
+    """q [B][T][Hq][D] (T query tokens per request), out fp32 of that shape, lse [B][T][Hq]."""
+    T = _kv4_query(shape, q, out, lse)
+    st = _abi.lib().sfi_kv4_dense_attn(
+        ctypes.byref(shape.c()), _kv4(shape, kv), int(sink), int(recent), q.data_ptr(), T, out.data_ptr(),
+        _ptr(lse, torch.float32, "lse"), _ptr(scores, torch.float32, "scores"),
+        0 if scores is None else int(scores.shape[-1]), _ptr(req_ids, torch.int32, "req_ids"),
+        _batch(batch, req_ids, kv.seq_lens), _ptr(workspace, torch.uint8, "workspace"),
+        0 if workspace is None else workspace.numel(), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    _check(st, "sfi_kv4_dense_attn")
+
+
+def sfi_kv4_fast_attn(shape: AttnShape, kv: PagedKV4, compact: CompactKV4, sink: int, recent: int, q: torch.Tensor,
+                      out: torch.Tensor, lse: Optional[torch.Tensor] = None, req_ids: Optional[torch.Tensor] = None,
+                      batch: Optional[int] = None, workspace: Optional[torch.Tensor] = None,
+                      dev_status: Optional[torch.Tensor] = None, stream=None):
+    """q [B][T][Hq][D] (T query tokens per request), out fp32 of that shape, lse [B][T][Hq]."""
+    T = _kv4_query(shape, q, out, lse)
+    st = _abi.lib().sfi_kv4_fast_attn(
+        ctypes.byref(shape.c()), _kv4(shape, kv), ctypes.byref(compact.c()), int(sink), int(recent), q.data_ptr(), T,
+        out.data_ptr(), _ptr(lse, torch.float32, "lse"), _ptr(req_ids, torch.int32, "req_ids"),
+        _batch(batch, req_ids, kv.seq_lens), _ptr(workspace, torch.uint8, "workspace"),
+        0 if workspace is None else workspace.numel(), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    _check(st, "sfi_kv4_fast_attn")
+
+
+def sfi_kv4_workspace_size(shape: AttnShape, batch: int, num_tokens: int = 1) -> int:
+    return int(_abi.lib().sfi_kv4_workspace_size(ctypes.byref(shape.c()), int(batch), int(num_tokens)))
+
+
+def alloc_kv4_workspace(shape: AttnShape, batch: int, num_tokens: int = 1, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace of the 4-bit attention calls, valid for every batch size 1..batch."""
+    return torch.zeros(max(256, sfi_kv4_workspace_size(shape, batch, num_tokens)), dtype=torch.uint8, device=device)
+
+
 def sfi_workspace_size(shape: AttnShape, batch: int, max_tokens: int, num_splits: int = 0) -> int:
     return int(_abi.lib().sfi_workspace_size(ctypes.byref(shape.c()), int(batch), int(max_tokens), int(num_splits)))
 

@@ -1,0 +1,369 @@
+// The calls that fill, read back and compact the 4-bit cache.
+//
+// One warp owns one (page, KV head) block at a time, so the half-byte updates of a partly
+// written page race with nobody. K rows are contiguous in a block; V codes lie in the
+// order of the matrix instruction's lanes, so rows of V pass through shared memory.
+// All three are copies with a conversion: bound by HBM when there are many tokens, by
+// launch latency in a decode step.
+#include <algorithm>
+
+#include "kv4_format.cuh"
+
+namespace sfi {
+
+constexpr int kKv4Warps = 8;
+
+// Shared memory of a warp: a page's V codes and scales by token.
+template <int D>
+struct Kv4Tile {
+    uint32_t code[16][D / 8];  // eight codes of a token
+    uint8_t scale[16][D / 16];
+};
+
+// Codes and scale of eight values (a lane's part of a row; the lane beside it holds the
+// other half of the group of 16).
+__device__ __forceinline__ uint32_t quantise8(int4 raw, float six_g, float g, uint32_t *scale) {
+    const uint32_t w[4] = {(uint32_t)raw.x, (uint32_t)raw.y, (uint32_t)raw.z, (uint32_t)raw.w};
+    // the largest magnitude, compared as bits: infinities and NaN are the largest of all
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    const bool fine = top < 0x7f80u;
+    const uint32_t s = fine ? group_scale(__uint_as_float(top << 16), six_g) : kE4m3Nan;
+    *scale = s;
+    float x[8];
+    bf16x8_to_f32(raw, x);
+    const float step = e4m3_to_f32(s) * g;
+    if (!fine || !(step > 0.f)) return 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __fdiv_rn(x[i], step);
+    return f32x8_to_e2m1(x);
+}
+
+// Rows [a, b) of the block from K and V rows (token tok at src + (tok - a) * stride).
+template <int D>
+__device__ void write_block(uint8_t *block, Kv4Tile<D> &tile, const __nv_bfloat16 *ks, const __nv_bfloat16 *vs,
+                            int64_t stride, int a, int b, float k_scale, float v_scale, int lane) {
+    using F = Kv4<D>;
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+    const int sub = lane / kLanes, l = lane % kLanes;
+#pragma unroll 2
+    for (int row0 = a; row0 < b; row0 += kRows) {
+        const int row = row0 + sub;
+        const bool in = row < b;
+        int4 kr = make_int4(0, 0, 0, 0), vr = kr;
+        if (in) {
+            kr = ld_nc_v4(ks + (int64_t)(row - a) * stride + l * 8);
+            vr = ld_nc_v4(vs + (int64_t)(row - a) * stride + l * 8);
+        }
+        uint32_t sk, sv;
+        const uint32_t ck = quantise8(kr, 6.f * k_scale, k_scale, &sk);
+        const uint32_t cv = quantise8(vr, 6.f * v_scale, v_scale, &sv);
+        if (in) {
+            *reinterpret_cast<uint32_t *>(block + row * F::kKRow + l * 4) = ck;
+            tile.code[row][l] = cv;
+            if ((l & 1) == 0) {
+                block[F::kKScale + row * F::kGroups + l / 2] = (uint8_t)sk;
+                tile.scale[row][l / 2] = (uint8_t)sv;
+            }
+        }
+    }
+    __syncwarp();
+    const bool whole = a == 0 && b == 16;
+#pragma unroll
+    for (int u = lane; u < D / 2; u += 32) {
+        const VUnit x(u);
+        int4 *dst = reinterpret_cast<int4 *>(block + F::kVCode) + u;
+        uint32_t keep = 0;  // bits of a word that belong to tokens outside [a, b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (4 * x.t + i < a || 4 * x.t + i >= b) keep |= 0x0f0fu << (16 * (i >> 1) + 4 * (i & 1));
+        if (keep == 0xffffffffu) continue;
+        const int4 old = whole ? make_int4(0, 0, 0, 0) : *dst;
+        const uint32_t o[4] = {(uint32_t)old.x, (uint32_t)old.y, (uint32_t)old.z, (uint32_t)old.w};
+        uint32_t res[4];
+#pragma unroll
+        for (int jr = 0; jr < 4; ++jr) {
+            const int j = x.quad * 4 + jr;
+            uint32_t v = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t lo = (tile.code[4 * x.t + i][2 * j] >> (4 * x.g)) & 15u;
+                const uint32_t hi = (tile.code[4 * x.t + i][2 * j + 1] >> (4 * x.g)) & 15u;
+                v |= (lo | hi << 8) << (16 * (i >> 1) + 4 * (i & 1));
+            }
+            res[jr] = (o[jr] & keep) | (v & ~keep);
+        }
+        *dst = make_int4((int)res[0], (int)res[1], (int)res[2], (int)res[3]);
+    }
+    for (int i = lane; i < 16 * F::kGroups; i += 32) {
+        const int tok = i & 3 | (i / (4 * F::kGroups)) << 2, grp = (i / 4) % F::kGroups;
+        if (tok >= a && tok < b) block[F::kVScale + i] = tile.scale[tok][grp];
+    }
+    __syncwarp();
+}
+
+template <int D>
+__global__ void __launch_bounds__(kKv4Warps * 32) kv4_append_kernel(const Kv4CopyParams p, int batch, int page_slots) {
+    __shared__ Kv4Tile<D> s_tile[kKv4Warps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t items = (int64_t)batch * page_slots * p.hkv;
+    for (int64_t item = (int64_t)blockIdx.x * kKv4Warps + warp; item < items;
+         item += (int64_t)gridDim.x * kKv4Warps) {
+        const int h = (int)(item % p.hkv);
+        const int64_t at = item / p.hkv;
+        const int ps = (int)(at % page_slots), bi = (int)(at / page_slots);
+        const int r = p.req_ids ? p.req_ids[bi] : bi;
+        const int L = p.seq_lens[r];
+        const int n = p.new_lens ? p.new_lens[r] : p.tokens;
+        if (n < 0 || n > p.tokens || L < n || L > p.max_pages * kSubTokens) {
+            if (lane == 0 && h == 0 && ps == 0) report(p.dev_status, SFI_DEV_BAD_LEN);
+            continue;
+        }
+        const int first = L - n;
+        const int pg = first / kSubTokens + ps;
+        const int pos0 = pg * kSubTokens;
+        const int a = max(first - pos0, 0), b = min(L - pos0, kSubTokens);
+        if (a >= b) continue;
+        const int page = p.page_table[(int64_t)r * p.max_pages + pg];
+        if (page < 0 || page >= p.num_pages) {
+            if (lane == 0) report(p.dev_status, SFI_DEV_BAD_PAGE);
+            continue;
+        }
+        const int64_t row = ((int64_t)r * p.tokens + (pos0 + a - first)) * p.hkv + h;
+        write_block<D>(p.pool + ((int64_t)page * p.hkv + h) * Kv4<D>::kBlock, s_tile[warp], p.k_new + row * D,
+                       p.v_new + row * D, (int64_t)p.hkv * D, a, b, p.k_scale, p.v_scale, lane);
+    }
+}
+
+// Rows [a, b) of a block as bf16 rows (row tok to dst + (tok - a) * stride).
+template <int D>
+__device__ void read_block(const uint8_t *block, Kv4Tile<D> &tile, __nv_bfloat16 *ks, __nv_bfloat16 *vs,
+                           int64_t stride, int a, int b, float k_scale, float v_scale, int lane) {
+    using F = Kv4<D>;
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+    const int sub = lane / kLanes, l = lane % kLanes;
+    // V codes as they lie (D / 2 units of 16 bytes), V scales by token
+    int4 *raw = reinterpret_cast<int4 *>(&tile.code[0][0]);
+#pragma unroll
+    for (int u = lane; u < D / 2; u += 32) raw[u] = ld_nc_v4(block + F::kVCode + u * 16);
+    for (int i = lane; i < 16 * F::kGroups; i += 32)
+        tile.scale[i & 3 | (i / (4 * F::kGroups)) << 2][(i / 4) % F::kGroups] = block[F::kVScale + i];
+    __syncwarp();
+    const uint8_t *vb = reinterpret_cast<const uint8_t *>(raw);
+#pragma unroll 2
+    for (int row0 = a; row0 < b; row0 += kRows) {
+        const int row = row0 + sub;
+        if (row < b) {
+            uint32_t h[4];
+            float x[8];
+            e2m1x8_to_f16(*reinterpret_cast<const uint32_t *>(block + row * F::kKRow + l * 4), h);
+            const float sk = e4m3_to_f32(block[F::kKScale + row * F::kGroups + l / 2]) * k_scale;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+                x[2 * i] = v.x * sk;
+                x[2 * i + 1] = v.y * sk;
+            }
+            *reinterpret_cast<int4 *>(ks + (int64_t)(row - a) * stride + l * 8) = f32x8_to_bf16(x);
+            // dims 8l .. 8l+7: j = l / 2, the lower (l even) or upper eight of its sixteen
+            uint32_t code = 0;
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+                const int u = (l >> 3) * 32 + (g >> 1) * 8 + (row >> 2) * 2 + (g & 1);
+                const uint32_t byte = vb[u * 16 + ((l >> 1) & 3) * 4 + (row & 2) + (l & 1)];
+                code |= ((byte >> (4 * (row & 1))) & 15u) << (4 * g);
+            }
+            e2m1x8_to_f16(code, h);
+            const float sv = e4m3_to_f32(tile.scale[row][l / 2]) * v_scale;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+                x[2 * i] = v.x * sv;
+                x[2 * i + 1] = v.y * sv;
+            }
+            *reinterpret_cast<int4 *>(vs + (int64_t)(row - a) * stride + l * 8) = f32x8_to_bf16(x);
+        }
+    }
+    __syncwarp();
+}
+
+template <int D>
+__global__ void __launch_bounds__(kKv4Warps * 32) kv4_read_kernel(const Kv4CopyParams p, int batch, int page_slots) {
+    __shared__ __align__(16) Kv4Tile<D> s_tile[kKv4Warps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t items = (int64_t)batch * page_slots * p.hkv;
+    for (int64_t item = (int64_t)blockIdx.x * kKv4Warps + warp; item < items;
+         item += (int64_t)gridDim.x * kKv4Warps) {
+        const int h = (int)(item % p.hkv);
+        const int64_t at = item / p.hkv;
+        const int ps = (int)(at % page_slots), bi = (int)(at / page_slots);
+        const int r = p.req_ids ? p.req_ids[bi] : bi;
+        const int L = p.seq_lens[r];
+        const int first = p.first ? p.first[r] : 0;
+        if (L < 0 || L > p.max_pages * kSubTokens || first < 0) {
+            if (lane == 0 && h == 0 && ps == 0) report(p.dev_status, SFI_DEV_BAD_LEN);
+            continue;
+        }
+        const int end = (int)min((int64_t)L, (int64_t)first + p.tokens);
+        const int64_t pos0 = ((int64_t)first / kSubTokens + ps) * kSubTokens;
+        const int a = (int)max(first - pos0, (int64_t)0), b = (int)min(end - pos0, (int64_t)kSubTokens);
+        if (a >= b) continue;
+        const int page = p.page_table[(int64_t)r * p.max_pages + pos0 / kSubTokens];
+        if (page < 0 || page >= p.num_pages) {
+            if (lane == 0) report(p.dev_status, SFI_DEV_BAD_PAGE);
+            continue;
+        }
+        const int64_t row = ((int64_t)r * p.tokens + (pos0 + a - first)) * p.hkv + h;
+        read_block<D>(p.pool + ((int64_t)page * p.hkv + h) * Kv4<D>::kBlock, s_tile[warp], p.k_out + row * D,
+                      p.v_out + row * D, (int64_t)p.hkv * D, a, b, p.k_scale, p.v_scale, lane);
+    }
+}
+
+// Compact blocks: each warp writes one block whole. Row i of it comes from one position's
+// page; the codes and scales move unchanged. A token's V codes are a quarter of the 32-byte
+// sectors they lie in, so a row's gather reads 64 + 32 + 2 D + 32 bytes (D = 128).
+template <int D>
+__global__ void __launch_bounds__(kKv4Warps * 32) kv4_compact_kernel(const Kv4CopyParams p, int batch, int slots) {
+    using F = Kv4<D>;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t items = (int64_t)batch * slots * p.hkv;
+    for (int64_t item = (int64_t)blockIdx.x * kKv4Warps + warp; item < items;
+         item += (int64_t)gridDim.x * kKv4Warps) {
+        const int h = (int)(item % p.hkv);
+        const int64_t at = item / p.hkv;
+        const int ps = (int)(at % slots), bi = (int)(at / slots);
+        const int r = p.req_ids ? p.req_ids[bi] : bi;
+        const int L = p.seq_lens[r], cnt = p.count[r], cap = p.c_capacity[r];
+        const int64_t off = p.c_page_offset[r];
+        uint32_t err = 0;
+        if (L < 1 || L > p.max_pages * kSubTokens) err = SFI_DEV_BAD_LEN;
+        else if (cnt < 0 || cnt > p.k_cap || cap < 0 || ((int64_t)p.sink + cnt + 15) / 16 > cap || (cnt > 0 && L < p.sink))
+            err = SFI_DEV_K_OVERFLOW;
+        else if (off < 0 || off + (int64_t)p.hkv * cap > p.c_total_pages) err = SFI_DEV_BAD_COMPACT;
+        if (err) {
+            if (lane == 0 && h == 0 && ps == 0) report(p.dev_status, err);
+            continue;
+        }
+        const int ns = min(p.sink, L);
+        const int rows = ns + cnt;  // cnt > 0 only with ns == sink
+        if (ps * 16 >= rows) continue;
+        // lane i (and i + 16) looks up row i: its page's block and its slot there
+        const int i = ps * 16 + (lane & 15);
+        int64_t src = -1;
+        int slot = 0;
+        if (i < rows) {
+            const int pos = i < ns ? i : p.idx[((int64_t)r * p.hkv + h) * p.k_cap + (i - p.sink)];
+            if (pos < 0 || pos >= L) {
+                err = SFI_DEV_BAD_INDEX;
+            } else {
+                const int page = p.page_table[(int64_t)r * p.max_pages + pos / kSubTokens];
+                if (page < 0 || page >= p.num_pages) err = SFI_DEV_BAD_PAGE;
+                else src = ((int64_t)page * p.hkv + h) * F::kBlock;
+                slot = pos % kSubTokens;
+            }
+        }
+        if (err && lane < 16) report(p.dev_status, err);
+        uint8_t *dst = p.c_pool + (off + (int64_t)h * cap + ps) * F::kBlock;
+        // K: rows of kKRow bytes and kGroups scales
+        constexpr int kLanes = F::kKRow / 16;  // 16-byte pieces of a row
+#pragma unroll
+        for (int u = lane; u < 16 * kLanes; u += 32) {
+            const int row = u / kLanes, piece = u % kLanes;
+            const int64_t s = __shfl_sync(0xffffffffu, src, row);
+            const int sl = __shfl_sync(0xffffffffu, slot, row);
+            int4 v = make_int4(0, 0, 0, 0);
+            if (s >= 0) v = ld_nc_v4(p.pool + s + sl * F::kKRow + piece * 16);
+            st_v4(dst + row * F::kKRow + piece * 16, v);
+        }
+        {  // two lanes per row: half of its scales each
+            const int row = lane >> 1, part = lane & 1;
+            const int64_t s = __shfl_sync(0xffffffffu, src, row);
+            const int sl = __shfl_sync(0xffffffffu, slot, row);
+            constexpr int kHalf = F::kGroups / 2;  // 4 or 2 bytes
+            const int koff = F::kKScale + sl * F::kGroups + part * kHalf;
+            const int kdst = F::kKScale + row * F::kGroups + part * kHalf;
+            if constexpr (kHalf == 4)
+                *reinterpret_cast<uint32_t *>(dst + kdst) = s >= 0 ? *reinterpret_cast<const uint32_t *>(p.pool + s + koff) : 0u;
+            else
+                *reinterpret_cast<uint16_t *>(dst + kdst) =
+                    s >= 0 ? *reinterpret_cast<const uint16_t *>(p.pool + s + koff) : (uint16_t)0;
+        }
+        // V: each 16-byte unit joins the half bytes of four tokens
+#pragma unroll
+        for (int u = lane; u < D / 2; u += 32) {
+            const VUnit x(u);
+            uint32_t res[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t s = __shfl_sync(0xffffffffu, src, 4 * x.t + q);
+                const int sl = __shfl_sync(0xffffffffu, slot, 4 * x.t + q);
+                if (s >= 0) {
+                    // the same dims of the source token's group of four
+                    const int4 w = ld_nc_v4(p.pool + s + F::kVCode + (u - 2 * x.t + 2 * (sl >> 2)) * 16);
+                    const int from = 16 * ((sl >> 1) & 1) + 4 * (sl & 1), to = 16 * (q >> 1) + 4 * (q & 1);
+                    const uint32_t ww[4] = {(uint32_t)w.x, (uint32_t)w.y, (uint32_t)w.z, (uint32_t)w.w};
+#pragma unroll
+                    for (int jr = 0; jr < 4; ++jr) res[jr] |= ((ww[jr] >> from) & 0x0f0fu) << to;
+                }
+            }
+            st_v4(dst + F::kVCode + u * 16, make_int4((int)res[0], (int)res[1], (int)res[2], (int)res[3]));
+        }
+        {  // lane w: the word of four tokens' scales (16 words at D = 64)
+            const int w = lane % (4 * F::kGroups);
+            const int t = w / F::kGroups, grp = w % F::kGroups;
+            uint32_t v = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t s = __shfl_sync(0xffffffffu, src, 4 * t + q);
+                const int sl = __shfl_sync(0xffffffffu, slot, 4 * t + q);
+                if (s >= 0)
+                    v |= (uint32_t)p.pool[s + F::kVScale + (sl >> 2) * F::kVScaleT + grp * 4 + (sl & 3)] << (8 * q);
+            }
+            if (lane < 4 * F::kGroups) *reinterpret_cast<uint32_t *>(dst + F::kVScale + w * 4) = v;
+        }
+    }
+}
+
+namespace {
+
+// One warp per item, as many CTAs as there are items up to several waves.
+int copy_grid(int64_t items) {
+    const int sms = sm_count_current_device();
+    return (int)std::max<int64_t>(1, std::min<int64_t>((items + kKv4Warps - 1) / kKv4Warps, (int64_t)sms * 32));
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_append(const Kv4CopyParams &p, int head_dim, int batch, cudaStream_t stream) {
+    const int slots = (int)(((int64_t)p.tokens + 30) / 16);  // pages that `tokens` positions can touch
+    const int grid = copy_grid((int64_t)batch * slots * p.hkv);
+    if (head_dim == 128)
+        kv4_append_kernel<128><<<grid, kKv4Warps * 32, 0, stream>>>(p, batch, slots);
+    else
+        kv4_append_kernel<64><<<grid, kKv4Warps * 32, 0, stream>>>(p, batch, slots);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv4_read(const Kv4CopyParams &p, int head_dim, int batch, cudaStream_t stream) {
+    const int slots = (int)(((int64_t)p.tokens + 30) / 16);
+    const int grid = copy_grid((int64_t)batch * slots * p.hkv);
+    if (head_dim == 128)
+        kv4_read_kernel<128><<<grid, kKv4Warps * 32, 0, stream>>>(p, batch, slots);
+    else
+        kv4_read_kernel<64><<<grid, kKv4Warps * 32, 0, stream>>>(p, batch, slots);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv4_compact(const Kv4CopyParams &p, int head_dim, int batch, cudaStream_t stream) {
+    const int slots = (p.sink + p.k_cap + 15) / 16;
+    const int grid = copy_grid((int64_t)batch * slots * p.hkv);
+    if (head_dim == 128)
+        kv4_compact_kernel<128><<<grid, kKv4Warps * 32, 0, stream>>>(p, batch, slots);
+    else
+        kv4_compact_kernel<64><<<grid, kKv4Warps * 32, 0, stream>>>(p, batch, slots);
+    return cudaGetLastError();
+}
+
+}  // namespace sfi

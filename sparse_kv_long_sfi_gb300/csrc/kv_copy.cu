@@ -20,19 +20,6 @@ constexpr int kCompactRowsPerCta = 64;
 // Requests handled by one compaction launch (the chunk prefix lives in shared memory).
 constexpr int kCompactMaxBatch = 512;
 
-__device__ __forceinline__ int4 ld_nc_v4(const void *p) {
-    int4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.s32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
-__device__ __forceinline__ void st_v4(void *p, int4 v) {
-    asm volatile("st.global.v4.s32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                 : "memory");
-}
-
 // Append of the p.tokens newest tokens of each request: token t goes to position
 // L - tokens + t (L counts them); k_new/v_new are [request][tokens][Hkv][D].
 template <int D>

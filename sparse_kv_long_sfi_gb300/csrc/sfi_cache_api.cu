@@ -11,6 +11,117 @@ using sfi::aligned8;
 
 sfi_status launched(cudaError_t e) { return e == cudaSuccess ? SFI_OK : SFI_ERR_CUDA; }
 
+// A power of two well inside fp32's range (so that 6 g, s g and the softmax scale times g stay normal).
+bool power_of_two(float g) {
+    int e = 0;
+    return std::isfinite(g) && std::frexp(g, &e) == 0.5f && e >= -63 && e <= 64;
+}
+
+sfi_status check_kv4(const sfi_attn_shape *s, const sfi_paged_kv4 *kv) {
+    const sfi_status st = sfi::check_shape(s);
+    if (st != SFI_OK) return st;
+    if (!kv || !kv->pool || !kv->page_table || !kv->seq_lens) return SFI_ERR_INVALID_ARG;
+    if (kv->num_pages <= 0 || kv->max_pages_per_req <= 0 || !aligned16(kv->pool)) return SFI_ERR_INVALID_ARG;
+    if (!power_of_two(kv->k_scale) || !power_of_two(kv->v_scale)) return SFI_ERR_INVALID_ARG;
+    if ((int64_t)kv->max_pages_per_req * s->page_size >= (int64_t(1) << 31)) return SFI_ERR_UNSUPPORTED;
+    return SFI_OK;
+}
+
+sfi_status check_compact4(const sfi_compact_kv4 *c) {
+    if (!c || !c->pool || !c->page_offset || !c->capacity || !c->count) return SFI_ERR_INVALID_ARG;
+    return c->total_pages > 0 && aligned16(c->pool) ? SFI_OK : SFI_ERR_INVALID_ARG;
+}
+
+sfi::Kv4CopyParams copy_params(const sfi_attn_shape *shape, const sfi_paged_kv4 *kv, const int32_t *req_ids,
+                               int32_t *dev_status) {
+    sfi::Kv4CopyParams p{};
+    p.pool = static_cast<uint8_t *>(kv->pool);
+    p.k_scale = kv->k_scale;
+    p.v_scale = kv->v_scale;
+    p.page_table = kv->page_table;
+    p.seq_lens = kv->seq_lens;
+    p.max_pages = kv->max_pages_per_req;
+    p.num_pages = kv->num_pages;
+    p.hkv = shape->num_kv_heads;
+    p.req_ids = req_ids;
+    p.dev_status = dev_status;
+    return p;
+}
+
+// Workspace of the 4-bit attention: the counters of one launch's units, then the partial
+// states (m, l) and O of up to two units per CTA, sixteen rows each.
+struct Kv4Workspace {
+    size_t ml, part, total;
+};
+
+Kv4Workspace kv4_workspace(const sfi_attn_shape *shape) {
+    const size_t slots = (size_t)sfi::sm_count_current_device() * sfi::kKv4CtasPerSm * 2 * sfi::kMaxRows;
+    Kv4Workspace w{};
+    w.ml = ((size_t)sfi::kKv4MaxBatch * shape->num_kv_heads * 4 + 255) / 256 * 256;
+    w.part = w.ml + slots * 2 * 4;
+    w.total = w.part + slots * shape->head_dim * 4;
+    return w;
+}
+
+sfi_status kv4_attention(const sfi_attn_shape *shape, const sfi_paged_kv4 *kv, const sfi_compact_kv4 *compact,
+                         int32_t sink, int32_t recent, const void *q, int32_t num_tokens, float *out, float *lse,
+                         float *scores, int64_t score_stride, const int32_t *req_ids, int32_t batch, void *workspace,
+                         size_t workspace_bytes, int32_t *dev_status, void *stream) {
+    const sfi_status st = check_kv4(shape, kv);
+    if (st != SFI_OK) return st;
+    if (batch < 0 || sink < 0 || recent < 0 || !q || !out || !aligned16(q) || !aligned8(out))
+        return SFI_ERR_INVALID_ARG;
+    if (num_tokens < 1 || num_tokens > SFI_MAX_QUERY_TOKENS || (scores && score_stride <= 0))
+        return SFI_ERR_INVALID_ARG;
+    const int group = shape->num_q_heads / shape->num_kv_heads;
+    if (num_tokens * group > sfi::kMaxRows) return SFI_ERR_UNSUPPORTED;
+    if (batch == 0) return SFI_OK;
+    const Kv4Workspace w = kv4_workspace(shape);
+    if (!workspace || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return SFI_ERR_WORKSPACE;
+    char *ws = static_cast<char *>(workspace);
+    sfi::Kv4AttnParams p{};
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.out = out;
+    p.lse = lse;
+    p.scores = scores;
+    p.score_stride = score_stride;
+    p.pool = static_cast<const uint8_t *>(kv->pool);
+    p.page_table = kv->page_table;
+    p.seq_lens = kv->seq_lens;
+    p.max_pages = kv->max_pages_per_req;
+    p.num_pages = kv->num_pages;
+    if (compact) {
+        p.c_pool = static_cast<const uint8_t *>(compact->pool);
+        p.c_total_pages = compact->total_pages;
+        p.c_page_offset = compact->page_offset;
+        p.c_capacity = compact->capacity;
+        p.c_count = compact->count;
+    }
+    p.hq = shape->num_q_heads;
+    p.hkv = shape->num_kv_heads;
+    p.group = group;
+    p.tokens = num_tokens;
+    p.rows = num_tokens * group;
+    p.sink = sink;
+    p.recent = recent;
+    p.k_mul = sfi::resolve_scale(shape) * kv->k_scale;
+    p.v_scale = kv->v_scale;
+    p.ws_count = reinterpret_cast<int32_t *>(ws);
+    p.ws_ml = reinterpret_cast<float *>(ws + w.ml);
+    p.ws_part = reinterpret_cast<float *>(ws + w.part);
+    p.dev_status = dev_status;
+    // more requests than one launch takes: launches in turn on the stream
+    for (int32_t b = 0; b < batch; b += sfi::kKv4MaxBatch) {
+        p.first = b;
+        p.req_ids = req_ids;
+        p.batch = batch - b < sfi::kKv4MaxBatch ? batch - b : sfi::kKv4MaxBatch;
+        if (sfi::launch_kv4_attn(p, shape->head_dim, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+            return SFI_ERR_CUDA;
+    }
+    return SFI_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -78,6 +189,83 @@ sfi_status sfi_qk_norm_rope(const sfi_attn_shape *shape, const sfi_rope *rope, c
     p.req_ids = req_ids;
     p.dev_status = dev_status;
     return launched(sfi::launch_qk_norm_rope(p, shape->head_dim, batch, static_cast<cudaStream_t>(stream)));
+}
+
+sfi_status sfi_kv4_append(const sfi_attn_shape *shape, const sfi_paged_kv4 *kv, const void *k_new, const void *v_new,
+                          int32_t num_tokens, const int32_t *new_lens, const int32_t *req_ids, int32_t batch,
+                          int32_t *dev_status, void *stream) {
+    const sfi_status st = check_kv4(shape, kv);
+    if (st != SFI_OK) return st;
+    if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new) || num_tokens < 1 || batch < 0)
+        return SFI_ERR_INVALID_ARG;
+    if (batch == 0) return SFI_OK;
+    sfi::Kv4CopyParams p = copy_params(shape, kv, req_ids, dev_status);
+    p.tokens = num_tokens;
+    p.new_lens = new_lens;
+    p.k_new = static_cast<const __nv_bfloat16 *>(k_new);
+    p.v_new = static_cast<const __nv_bfloat16 *>(v_new);
+    return launched(sfi::launch_kv4_append(p, shape->head_dim, batch, static_cast<cudaStream_t>(stream)));
+}
+
+sfi_status sfi_kv4_read(const sfi_attn_shape *shape, const sfi_paged_kv4 *kv, void *k_out, void *v_out,
+                        int32_t num_tokens, const int32_t *first, const int32_t *req_ids, int32_t batch,
+                        int32_t *dev_status, void *stream) {
+    const sfi_status st = check_kv4(shape, kv);
+    if (st != SFI_OK) return st;
+    if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out) || num_tokens < 1 || batch < 0)
+        return SFI_ERR_INVALID_ARG;
+    if (batch == 0) return SFI_OK;
+    sfi::Kv4CopyParams p = copy_params(shape, kv, req_ids, dev_status);
+    p.tokens = num_tokens;
+    p.first = first;
+    p.k_out = static_cast<__nv_bfloat16 *>(k_out);
+    p.v_out = static_cast<__nv_bfloat16 *>(v_out);
+    return launched(sfi::launch_kv4_read(p, shape->head_dim, batch, static_cast<cudaStream_t>(stream)));
+}
+
+sfi_status sfi_kv4_compact_gather(const sfi_attn_shape *shape, const sfi_paged_kv4 *kv, const int32_t *idx,
+                                  const int32_t *count, int32_t k_cap, int32_t sink, const sfi_compact_kv4 *compact,
+                                  const int32_t *req_ids, int32_t batch, int32_t *dev_status, void *stream) {
+    sfi_status st = check_kv4(shape, kv);
+    if (st != SFI_OK) return st;
+    if ((st = check_compact4(compact)) != SFI_OK) return st;
+    if (!idx || !count || k_cap < 0 || sink < 0 || batch < 0) return SFI_ERR_INVALID_ARG;
+    if (batch == 0 || (int64_t)sink + k_cap == 0) return SFI_OK;
+    if ((int64_t)sink + k_cap + 15 >= (int64_t(1) << 31)) return SFI_ERR_INVALID_ARG;
+    sfi::Kv4CopyParams p = copy_params(shape, kv, req_ids, dev_status);
+    p.idx = idx;
+    p.count = count;
+    p.k_cap = k_cap;
+    p.sink = sink;
+    p.c_pool = static_cast<uint8_t *>(compact->pool);
+    p.c_total_pages = compact->total_pages;
+    p.c_page_offset = compact->page_offset;
+    p.c_capacity = compact->capacity;
+    return launched(sfi::launch_kv4_compact(p, shape->head_dim, batch, static_cast<cudaStream_t>(stream)));
+}
+
+sfi_status sfi_kv4_dense_attn(const sfi_attn_shape *shape, const sfi_paged_kv4 *kv, int32_t sink, int32_t recent,
+                              const void *q, int32_t num_tokens, float *out, float *lse, float *scores,
+                              int64_t score_stride, const int32_t *req_ids, int32_t batch, void *workspace,
+                              size_t workspace_bytes, int32_t *dev_status, void *stream) {
+    return kv4_attention(shape, kv, nullptr, sink, recent, q, num_tokens, out, lse, scores, score_stride, req_ids,
+                         batch, workspace, workspace_bytes, dev_status, stream);
+}
+
+sfi_status sfi_kv4_fast_attn(const sfi_attn_shape *shape, const sfi_paged_kv4 *kv, const sfi_compact_kv4 *compact,
+                             int32_t sink, int32_t recent, const void *q, int32_t num_tokens, float *out, float *lse,
+                             const int32_t *req_ids, int32_t batch, void *workspace, size_t workspace_bytes,
+                             int32_t *dev_status, void *stream) {
+    const sfi_status st = check_compact4(compact);
+    if (st != SFI_OK) return st;
+    return kv4_attention(shape, kv, compact, sink, recent, q, num_tokens, out, lse, nullptr, 0, req_ids, batch,
+                         workspace, workspace_bytes, dev_status, stream);
+}
+
+size_t sfi_kv4_workspace_size(const sfi_attn_shape *shape, int32_t batch, int32_t num_tokens) {
+    if (sfi::check_shape(shape) != SFI_OK || batch < 0 || num_tokens < 1) return 0;
+    if (num_tokens * (shape->num_q_heads / shape->num_kv_heads) > sfi::kMaxRows) return 0;
+    return kv4_workspace(shape).total;
 }
 
 }  // extern "C"

@@ -171,4 +171,58 @@ struct NormRopeParams {
 };
 cudaError_t launch_qk_norm_rope(const NormRopeParams &p, int head_dim, int batch, cudaStream_t stream);
 
+// The calls that copy to and from the 4-bit cache.
+struct Kv4CopyParams {
+    uint8_t *pool;
+    float k_scale, v_scale;
+    const int32_t *page_table, *seq_lens;
+    int32_t max_pages, num_pages, hkv;
+    const int32_t *req_ids;
+    int32_t *dev_status;
+    // append and read of `tokens` positions
+    int32_t tokens;
+    const int32_t *new_lens, *first;
+    const __nv_bfloat16 *k_new, *v_new;
+    __nv_bfloat16 *k_out, *v_out;
+    // compaction
+    const int32_t *idx, *count;
+    int32_t k_cap, sink;
+    uint8_t *c_pool;
+    int64_t c_total_pages;
+    const int64_t *c_page_offset;
+    const int32_t *c_capacity;
+};
+cudaError_t launch_kv4_append(const Kv4CopyParams &p, int head_dim, int batch, cudaStream_t stream);
+cudaError_t launch_kv4_read(const Kv4CopyParams &p, int head_dim, int batch, cudaStream_t stream);
+cudaError_t launch_kv4_compact(const Kv4CopyParams &p, int head_dim, int batch, cudaStream_t stream);
+
+struct Kv4AttnParams {
+    const __nv_bfloat16 *q;
+    float *out, *lse, *scores;
+    int64_t score_stride;
+    const uint8_t *pool;
+    const int32_t *page_table, *seq_lens;
+    int32_t max_pages, num_pages;
+    const uint8_t *c_pool;  // compact blocks (fast step), or null
+    int64_t c_total_pages;
+    const int64_t *c_page_offset;
+    const int32_t *c_capacity, *c_count;
+    const int32_t *req_ids;
+    int32_t first, batch;  // this launch takes the requests first .. first + batch - 1 of the call
+    int32_t hq, hkv, group;
+    int32_t tokens, rows;
+    int32_t sink, recent;
+    float k_mul;    // softmax scale * k_scale
+    float v_scale;
+    int32_t *ws_count;  // [batch * hkv], zero between launches
+    float *ws_ml;       // [CTAs][2][16 rows][2]
+    float *ws_part;     // [CTAs][2][16 rows][D]
+    int32_t *dev_status;
+};
+// Requests of one launch (their page counts' prefix lies in shared memory) and the CTAs of
+// the largest launch on a device of `sms` SMs.
+constexpr int kKv4MaxBatch = 512;
+constexpr int kKv4CtasPerSm = 2;
+cudaError_t launch_kv4_attn(const Kv4AttnParams &p, int head_dim, cudaStream_t stream);
+
 }  // namespace sfi

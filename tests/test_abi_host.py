@@ -226,3 +226,57 @@ def test_rope_turns_are_exact_modulo_one_turn():
     for x, t in zip(f, got):
         turn = x / (2 * math.pi) % 1.0
         assert abs((t % 2 ** 64) / 2 ** 64 - turn) <= 2.0 ** -51, x
+
+
+def _kv4(k_scale=1.0, v_scale=1.0, pool=4096, npages=4, maxp=4):
+    from sparse_kv_long_sfi_gb300 import _abi
+    return _abi.sfi_paged_kv4(pool, npages, maxp, 12288, 16384, k_scale, v_scale)
+
+
+def test_kv4_calls_validate_on_the_host(libsfi):
+    from sparse_kv_long_sfi_gb300 import _abi
+    comp = _abi.sfi_compact_kv4(4096, 8, 4096, 4096, 4096)
+    ref = lambda x: x and ctypes.byref(x)  # noqa: E731
+
+    def append(sh=_shape(), kv=_kv4(), k=4096, v=4096, T=1, batch=1):
+        return libsfi.sfi_kv4_append(ref(sh), ref(kv), k, v, T, None, None, batch, None, None)
+
+    def read(sh=_shape(), kv=_kv4(), k=4096, v=4096, T=1, batch=1):
+        return libsfi.sfi_kv4_read(ref(sh), ref(kv), k, v, T, None, None, batch, None, None)
+
+    def gather(kv=_kv4(), idx=4096, count=4096, k_cap=8, sink=4, c=comp, batch=1):
+        return libsfi.sfi_kv4_compact_gather(ref(_shape()), ref(kv), idx, count, k_cap, sink, ref(c), None, batch, None,
+                                             None)
+
+    def dense(sh=_shape(), kv=_kv4(), sink=4, recent=32, q=4096, T=1, out=4096, scores=None, stride=0, batch=1, ws=None,
+              ws_bytes=0):
+        return libsfi.sfi_kv4_dense_attn(ref(sh), ref(kv), sink, recent, q, T, out, None, scores, stride, None, batch, ws,
+                                         ws_bytes, None, None)
+
+    def fast(kv=_kv4(), c=comp, q=4096, T=1, out=4096, batch=1):
+        return libsfi.sfi_kv4_fast_attn(ref(_shape()), ref(kv), ref(c), 4, 32, q, T, out, None, None, batch, None, 0, None,
+                                        None)
+
+    for call in (append, read):
+        assert call(batch=0) == 0
+        assert call(sh=_shape(16, 8, 96)) == 2 and call(k=None) == 1 and call(v=4097) == 1
+        assert call(T=0) == 1 and call(batch=-1) == 1
+    for call in (append, read, gather, dense, fast):
+        assert call(kv=None) == 1
+        assert call(kv=_kv4(pool=4097)) == 1 and call(kv=_kv4(npages=0)) == 1 and call(kv=_kv4(maxp=0)) == 1
+        assert call(kv=_kv4(maxp=1 << 28)) == 2
+        for bad in (0.0, -1.0, 3.0, float("inf"), float("nan"), 2.0 ** -100, 2.0 ** 90):
+            assert call(kv=_kv4(k_scale=bad)) == 1 and call(kv=_kv4(v_scale=bad)) == 1
+        assert call(kv=_kv4(2.0 ** -20, 2.0 ** 20), batch=0) == 0
+    assert gather(idx=None) == 1 and gather(k_cap=-1) == 1 and gather(sink=-1) == 1 and gather(c=None) == 1
+    assert gather(k_cap=0, sink=0) == 0
+    assert gather(c=_abi.sfi_compact_kv4(4096, 0, 4096, 4096, 4096)) == 1
+    assert fast(c=None) == 1 and fast(c=_abi.sfi_compact_kv4(4104, 8, 4096, 4096, 4096)) == 1
+    assert dense(q=None) == 1 and dense(out=4100) == 1 and dense(sink=-1) == 1 and dense(recent=-1) == 1
+    assert dense(T=0) == 1 and dense(T=17) == 1 and dense(T=9) == 2 and dense(T=8, batch=0) == 0
+    assert dense(scores=4096, stride=0) == 1
+    assert dense() == 3 and fast() == 3                   # no workspace
+    assert dense(ws=4096, ws_bytes=16) == 3 and dense(ws=4100, ws_bytes=1 << 40) == 3
+    sh = _shape()
+    assert libsfi.sfi_kv4_workspace_size(ref(sh), 4, 8) > 0 and libsfi.sfi_kv4_workspace_size(ref(sh), 4, 9) == 0
+    assert libsfi.sfi_kv4_workspace_size(ref(_shape(16, 8, 96)), 4, 1) == 0
