@@ -18,6 +18,7 @@
 // probabilities off the subnormals), so the output is as good as fp32's. The running
 // maximum moves only when a score passes it by 2^8.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv4_format.cuh"
 
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
         enter_ahead();
     }
 #pragma unroll
-    for (int i = 0; i < T::kDepth - 1; ++i) issue(i);
+    for (int i = 0; i < T::kDepth; ++i) issue(i);
 
     // ---- page ids of every request this CTA touches: one bad id drops the request ----
     {
@@ -277,21 +278,51 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
 
     // ---- this warp's units ----
     uint32_t bq[NT][kKs][2];     // Q as B fragments
-    float mul[NT][2];            // fp16 product -> score in powers of two (scores: natural)
+    float mul[NT][2];            // fp16 product -> score in powers of two
+    float nat[NT][2];            // ... -> score (scores mode; 0 in rows that are not there)
     int rtok[NT][2];             // query token of this lane's rows
     float o[NT][kKs][4];
-    float m[NT][2], l[NT][2];
+    float base[NT][2], l[NT][2];  // kLift - running maximum (+inf: nothing seen), sum of 2^(score + base)
     ReqPlan plan{};
     int64_t f = f0, unit0 = 0;
     int slot = 0;
     bool bad = false;
     const bool multi = p.tokens > 1;
+    // blocks that every row sees whole: [0, in_comp) and [in_from, in_to)
+    int in_comp = 0, in_from = 0, in_to = 0;
+    float *score_row = nullptr;
+
+    // positions (or compact rows) [lo, hi) that query token i sees
+    auto span = [&](bool comp, int i, int &lo, int &hi) {
+        const int Lt = plan.L - p.tokens + 1 + i;
+        if (MODE == kKv4Fast) {
+            lo = comp ? 0 : max(p.sink, Lt - p.recent);
+            hi = comp ? min(p.sink, Lt) + plan.nvis : Lt;
+        } else {
+            lo = 0;
+            hi = Lt;
+        }
+    };
 
     auto enter_unit = [&]() {
         plan = plan_request<MODE>(p, at.b, &none);
         unit0 = f - at.pg;
         bad = (s_bad[at.b >> 5] >> (at.b & 31)) & 1u;
         const int r = request_id(p, at.b);
+        {
+            int lo_a, hi_a, lo_z, hi_z;
+            span(false, 0, lo_a, hi_a);
+            span(false, p.tokens - 1, lo_z, hi_z);
+            // pages from ceil(lo_z / 16) to floor(hi_a / 16), counted in blocks of the unit
+            in_from = (lo_z + 15) / 16 - plan.page0 + plan.ncomp;
+            in_to = hi_a / 16 - plan.page0 + plan.ncomp;
+            in_from = max(in_from, plan.ncomp);
+            if (MODE == kKv4Fast) {
+                span(true, 0, lo_a, hi_a);
+                in_comp = hi_a / 16;
+            }
+        }
+        if (MODE == kKv4Scores) score_row = p.scores + ((int64_t)r * p.hkv + at.h) * p.score_stride;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int row = nt * 8 + g;
@@ -331,10 +362,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
             }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {  // S^T's columns of this lane are rows 2t, 2t + 1
-                mul[nt][c] = __shfl_sync(0xffffffffu, down, (2 * t + c) * 4) * p.k_mul;
-                if (MODE != kKv4Scores) mul[nt][c] *= kLog2e;
-                rtok[nt][c] = min((nt * 8 + 2 * t + c) / p.group, p.tokens - 1);
-                m[nt][c] = -INFINITY;
+                const int col = nt * 8 + 2 * t + c;
+                const float x = __shfl_sync(0xffffffffu, down, (2 * t + c) * 4) * p.k_mul;
+                mul[nt][c] = x * kLog2e;
+                nat[nt][c] = col < p.rows ? x : 0.f;
+                rtok[nt][c] = min(col / p.group, p.tokens - 1);
+                base[nt][c] = INFINITY;
                 l[nt][c] = 0.f;
             }
 #pragma unroll
@@ -344,190 +377,211 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
         }
     };
 
-    // positions (or compact rows) [lo, hi) that query token i sees
-    auto span = [&](bool comp, int i, int &lo, int &hi) {
-        const int Lt = plan.L - p.tokens + 1 + i;
-        if (MODE == kKv4Fast) {
-            lo = comp ? 0 : max(p.sink, Lt - p.recent);
-            hi = comp ? min(p.sink, Lt) + plan.nvis : Lt;
-        } else {
-            lo = 0;
-            hi = Lt;
-        }
-    };
-
-    auto consume = [&](const uint8_t *blk) {
-        const bool comp = MODE == kKv4Fast && at.pg < plan.ncomp;
-        const int pos0 = 16 * (comp ? at.pg : plan.page0 + at.pg - plan.ncomp);
-        int lo_a, hi_a, lo_z, hi_z;
-        span(comp, 0, lo_a, hi_a);
-        span(comp, p.tokens - 1, lo_z, hi_z);
-        const bool edge = pos0 < lo_z || pos0 + 16 > hi_a;
-        // ---- S^T: rows g -> tokens tu and (g + 8) tu + 2, columns 2t, 2t + 1 ----
-        const int tu = 4 * (g >> 1) + (g & 1);
-        float s[NT][4];
+    // S^T of one block: rows g -> tokens tu and (g + 8) tu + 2, columns 2t, 2t + 1
+    const int tu = 4 * (g >> 1) + (g & 1);
+    auto products = [&](const uint8_t *blk, float (&s)[NT][4]) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 4; ++c) s[nt][c] = 0.f;
-        {
-            uint32_t ka[D / 32], kb[D / 32];  // codes of the two tokens, dims t D/4 ...
-            uint32_t sa[D / 64], sb[D / 64];  // their scales, twice in a register
-            if constexpr (D == 128) {
-                const uint4 a = *reinterpret_cast<const uint4 *>(blk + tu * F::kKRow + t * 16);
-                const uint4 b = *reinterpret_cast<const uint4 *>(blk + (tu + 2) * F::kKRow + t * 16);
-                ka[0] = a.x; ka[1] = a.y; ka[2] = a.z; ka[3] = a.w;
-                kb[0] = b.x; kb[1] = b.y; kb[2] = b.z; kb[3] = b.w;
-                const uint32_t ha = e4m3x2_to_f16(*reinterpret_cast<const uint16_t *>(blk + F::kKScale + tu * 8 + t * 2));
-                const uint32_t hb = e4m3x2_to_f16(*reinterpret_cast<const uint16_t *>(blk + F::kKScale + (tu + 2) * 8 + t * 2));
-                sa[0] = __byte_perm(ha, 0, 0x1010); sa[1] = __byte_perm(ha, 0, 0x3232);
-                sb[0] = __byte_perm(hb, 0, 0x1010); sb[1] = __byte_perm(hb, 0, 0x3232);
-            } else {
-                const uint2 a = *reinterpret_cast<const uint2 *>(blk + tu * F::kKRow + t * 8);
-                const uint2 b = *reinterpret_cast<const uint2 *>(blk + (tu + 2) * F::kKRow + t * 8);
-                ka[0] = a.x; ka[1] = a.y;
-                kb[0] = b.x; kb[1] = b.y;
-                sa[0] = __byte_perm(e4m3x2_to_f16(blk[F::kKScale + tu * 4 + t]), 0, 0x1010);
-                sb[0] = __byte_perm(e4m3x2_to_f16(blk[F::kKScale + (tu + 2) * 4 + t]), 0, 0x1010);
-            }
+        uint32_t ka[D / 32], kb[D / 32];  // codes of the two tokens, dims t D/4 ...
+        uint32_t sa[D / 64], sb[D / 64];  // their scales, twice in a register
+        if constexpr (D == 128) {
+            const uint4 a = *reinterpret_cast<const uint4 *>(blk + tu * F::kKRow + t * 16);
+            const uint4 b = *reinterpret_cast<const uint4 *>(blk + (tu + 2) * F::kKRow + t * 16);
+            ka[0] = a.x; ka[1] = a.y; ka[2] = a.z; ka[3] = a.w;
+            kb[0] = b.x; kb[1] = b.y; kb[2] = b.z; kb[3] = b.w;
+            const uint32_t ha = e4m3x2_to_f16(*reinterpret_cast<const uint16_t *>(blk + F::kKScale + tu * 8 + t * 2));
+            const uint32_t hb = e4m3x2_to_f16(*reinterpret_cast<const uint16_t *>(blk + F::kKScale + (tu + 2) * 8 + t * 2));
+            sa[0] = __byte_perm(ha, 0, 0x1010); sa[1] = __byte_perm(ha, 0, 0x3232);
+            sb[0] = __byte_perm(hb, 0, 0x1010); sb[1] = __byte_perm(hb, 0, 0x3232);
+        } else {
+            const uint2 a = *reinterpret_cast<const uint2 *>(blk + tu * F::kKRow + t * 8);
+            const uint2 b = *reinterpret_cast<const uint2 *>(blk + (tu + 2) * F::kKRow + t * 8);
+            ka[0] = a.x; ka[1] = a.y;
+            kb[0] = b.x; kb[1] = b.y;
+            sa[0] = __byte_perm(e4m3x2_to_f16(blk[F::kKScale + tu * 4 + t]), 0, 0x1010);
+            sb[0] = __byte_perm(e4m3x2_to_f16(blk[F::kKScale + (tu + 2) * 4 + t]), 0, 0x1010);
+        }
 #pragma unroll
-            for (int w = 0; w < D / 32; ++w) {
-                uint32_t xa[4], xb[4];
-                e2m1x8_to_f16(ka[w], xa);
-                e2m1x8_to_f16(kb[w], xb);
+        for (int w = 0; w < D / 32; ++w) {
+            uint32_t xa[4], xb[4];
+            e2m1x8_to_f16(ka[w], xa);
+            e2m1x8_to_f16(kb[w], xb);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t a[4] = {hmul2(xa[2 * k], sa[w / 2]), hmul2(xb[2 * k], sb[w / 2]),
-                                           hmul2(xa[2 * k + 1], sa[w / 2]), hmul2(xb[2 * k + 1], sb[w / 2])};
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t a[4] = {hmul2(xa[2 * k], sa[w / 2]), hmul2(xb[2 * k], sb[w / 2]),
+                                       hmul2(xa[2 * k + 1], sa[w / 2]), hmul2(xb[2 * k + 1], sb[w / 2])};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma_f16_16816(s[nt], a, bq[nt][2 * w + k][0], bq[nt][2 * w + k][1]);
-                }
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_f16_16816(s[nt], a, bq[nt][2 * w + k][0], bq[nt][2 * w + k][1]);
             }
         }
-        // ---- scale, mask, scores ----
-        uint32_t seen[NT];  // bits c: this lane's four scores that are seen
-        float sum_a = 0.f, sum_b = 0.f;
+    };
+
+    // PB blocks from blk on (EDGE: one block, some of whose tokens some rows do not see).
+    auto consume = [&](auto pb_tag, auto edge_tag, const uint8_t *blk0, const uint8_t *blk1) {
+        constexpr int PB = decltype(pb_tag)::value;
+        constexpr bool EDGE = decltype(edge_tag)::value;
+        const bool comp = EDGE && MODE == kKv4Fast && at.pg < plan.ncomp;
+        const int pos0 = 16 * (comp ? at.pg : plan.page0 + at.pg - plan.ncomp);
+        float s[PB][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            seen[nt] = 15u;
+        for (int b = 0; b < PB; ++b) products(b ? blk1 : blk0, s[b]);
+        // ---- scores (natural units), masks, exponents ----
+        uint32_t hide = 0;  // bits 4 nt + c: not seen
+        if (EDGE) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) s[nt][c] *= mul[nt][c & 1];
-            if (edge) {
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     int lo, hi;
                     span(comp, rtok[nt][c & 1], lo, hi);
                     const int pos = pos0 + tu + (c & 2);
-                    if (pos < lo || pos >= hi) {
-                        seen[nt] &= ~(1u << c);
-                        s[nt][c] = -INFINITY;
-                    }
+                    if (pos < lo || pos >= hi) hide |= 1u << (4 * nt + c);
                 }
-            }
-            if (MODE == kKv4Scores) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (((seen[nt] >> c) & 1u) && nt * 8 + 2 * t + (c & 1) < p.rows) {
-                        if (c & 2) sum_b += s[nt][c]; else sum_a += s[nt][c];
-                    }
-                    s[nt][c] *= kLog2e;
-                }
-            }
         }
         if (MODE == kKv4Scores) {
+            // the rows' sum of each token; lane t of four ends up with token tu + 2 (t & 1) of block t / 2
+            float sum[PB][2];
 #pragma unroll
-            for (int off = 1; off <= 2; off <<= 1) {
-                sum_a += __shfl_xor_sync(0xffffffffu, sum_a, off);
-                sum_b += __shfl_xor_sync(0xffffffffu, sum_b, off);
+            for (int b = 0; b < PB; ++b)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float x = 0.f;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const float y = s[b][nt][2 * k + c] * nat[nt][c];
+                            x += EDGE && ((hide >> (4 * nt + 2 * k + c)) & 1u) ? 0.f : y;
+                        }
+                    sum[b][k] = x;
+                }
+            float one[PB];
+#pragma unroll
+            for (int b = 0; b < PB; ++b) {
+                const float give = (t & 1) ? sum[b][0] : sum[b][1];
+                one[b] = ((t & 1) ? sum[b][1] : sum[b][0]) + __shfl_xor_sync(0xffffffffu, give, 1);
             }
-            const int pos = pos0 + tu + (t == 1 ? 2 : 0);
-            if (t < 2 && pos < plan.L) {
-                const int r = request_id(p, at.b);
-                const bool cand = pos >= p.sink && pos < plan.L - p.recent;
-                p.scores[((int64_t)r * p.hkv + at.h) * p.score_stride + pos] =
-                    cand ? (t == 0 ? sum_a : sum_b) : -INFINITY;
+            float all;
+            if constexpr (PB == 2) {
+                const float give = (t & 2) ? one[0] : one[1];
+                all = ((t & 2) ? one[1] : one[0]) + __shfl_xor_sync(0xffffffffu, give, 2);
+            } else {
+                all = one[0] + __shfl_xor_sync(0xffffffffu, one[0], 2);
             }
+            const int pos = pos0 + tu + 2 * (t & 1) + (PB == 2 ? 8 * (t & 2) : 0);
+            if ((PB == 2 || t < 2) && (!EDGE || pos < plan.L))
+                score_row[pos] = pos >= p.sink && pos < plan.L - p.recent ? all : -INFINITY;
         }
-        // ---- the running maximum, moved only when it falls far behind ----
-        bool behind = false;
+        // y = score in powers of two above the running maximum, plus kLift
+        float y[PB][NT][4];
+        float top = -INFINITY;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int b = 0; b < PB; ++b)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) behind |= fmaxf(s[nt][c], s[nt][c + 2]) > m[nt][c] + kLazy;
-        if (__any_sync(0xffffffffu, behind)) {
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+                for (int c = 0; c < 4; ++c) {
+                    y[b][nt][c] = fmaf(s[b][nt][c], mul[nt][c & 1], base[nt][c & 1]);
+                    if (EDGE && ((hide >> (4 * nt + c)) & 1u)) y[b][nt][c] = -INFINITY;
+                    top = fmaxf(top, y[b][nt][c]);
+                }
+        if (__any_sync(0xffffffffu, top > kLift + kLazy)) {  // the maximum has fallen far behind: move it
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    float x = fmaxf(s[nt][c], s[nt][c + 2]);
+                    float x = -INFINITY;
+#pragma unroll
+                    for (int b = 0; b < PB; ++b)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            if (!EDGE || !((hide >> (4 * nt + c + 2 * k)) & 1u))
+                                x = fmaxf(x, s[b][nt][c + 2 * k] * mul[nt][c]);
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                    const float mn = fmaxf(m[nt][c], x);
-                    const float a = m[nt][c] == mn ? 1.f : fast_exp2(m[nt][c] - mn);
-                    m[nt][c] = mn;
+                    const float was = kLift - base[nt][c], now = fmaxf(was, x);
+                    const float a = was == now ? 1.f : fast_exp2(was - now);
+                    base[nt][c] = kLift - now;
                     l[nt][c] *= a;
 #pragma unroll
                     for (int j = 0; j < kKs; ++j) {
                         o[nt][j][c] *= a;
                         o[nt][j][c + 2] *= a;
                     }
+#pragma unroll
+                    for (int b = 0; b < PB; ++b)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float &z = y[b][nt][c + 2 * k];
+                            z = fmaf(s[b][nt][c + 2 * k], mul[nt][c], base[nt][c]);
+                            if (EDGE && ((hide >> (4 * nt + c + 2 * k)) & 1u)) z = -INFINITY;
+                        }
                 }
-            }
         }
         // ---- P^T as two fp16 terms ----
-        uint32_t ph[NT][2], pl[NT][2];
+        uint32_t ph[PB][NT][2], pl[PB][NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float x[4];
+        for (int b = 0; b < PB; ++b)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                x[c] = fast_exp2(s[nt][c] - m[nt][c & 1] + kLift);
-                if (edge) x[c] = (seen[nt] >> c) & 1u ? x[c] : 0.f;
+            for (int nt = 0; nt < NT; ++nt) {
+                float x[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) x[c] = fast_exp2(y[b][nt][c]);
+                l[nt][0] += x[0] + x[2];
+                l[nt][1] += x[1] + x[3];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t h = pack_f16x2(x[2 * k], x[2 * k + 1]);
+                    const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+                    ph[b][nt][k] = transpose_8x8(h);
+                    pl[b][nt][k] = transpose_8x8(pack_f16x2(x[2 * k] - hf.x, x[2 * k + 1] - hf.y));
+                }
             }
-            l[nt][0] += x[0] + x[2];
-            l[nt][1] += x[1] + x[3];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t h = pack_f16x2(x[2 * k], x[2 * k + 1]);
-                const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-                ph[nt][k] = transpose_8x8(h);
-                pl[nt][k] = transpose_8x8(pack_f16x2(x[2 * k] - hf.x, x[2 * k + 1] - hf.y));
-            }
-        }
         // ---- O^T += V^T P^T: rows g, g + 8 -> dims 16 j + g, 16 j + g + 8; k -> tokens 4t .. 4t + 3 ----
-        uint32_t keep = 0xffffffffu, part = 0;  // scale bytes of tokens seen by some row; by some but not all
-        if (edge) {
-            keep = 0;
+        uint32_t keep = 0, part = 0;  // scale bytes of tokens seen by some row; by some but not all
+        if (EDGE) {
+            int lo_a, hi_a, lo_z, hi_z;
+            span(comp, 0, lo_a, hi_a);
+            span(comp, p.tokens - 1, lo_z, hi_z);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int pos = pos0 + 4 * t + i;
-                if (pos >= lo_a && pos < hi_z) keep |= 0xffu << (8 * i);
-                if (multi && pos >= lo_a && pos < hi_z && !(pos >= lo_z && pos < hi_a)) part |= 0xffu << (8 * i);
+                if (pos >= lo_a && pos < hi_z) {
+                    keep |= 0xffu << (8 * i);
+                    if (multi && !(pos >= lo_z && pos < hi_a)) part |= 0xffu << (8 * i);
+                }
             }
         }
 #pragma unroll
         for (int q = 0; q < F::kQuads; ++q) {
-            const uint4 cw = *reinterpret_cast<const uint4 *>(blk + F::kVCode + q * 512 + (g >> 1) * 128 + t * 32 +
-                                                              (g & 1) * 16);
-            const uint4 sw = *reinterpret_cast<const uint4 *>(blk + F::kVScale + t * F::kVScaleT + q * 16);
-            const uint32_t cv[4] = {cw.x, cw.y, cw.z, cw.w};
-            uint32_t sv[4] = {sw.x, sw.y, sw.z, sw.w};
+            uint32_t cv[PB][4], sv[PB][4];
+#pragma unroll
+            for (int b = 0; b < PB; ++b) {
+                const uint8_t *blk = b ? blk1 : blk0;
+                const uint4 cw = *reinterpret_cast<const uint4 *>(blk + F::kVCode + q * 512 + (g >> 1) * 128 + t * 32 +
+                                                                  (g & 1) * 16);
+                const uint4 sw = *reinterpret_cast<const uint4 *>(blk + F::kVScale + t * F::kVScaleT + q * 16);
+                cv[b][0] = cw.x; cv[b][1] = cw.y; cv[b][2] = cw.z; cv[b][3] = cw.w;
+                sv[b][0] = sw.x; sv[b][1] = sw.y; sv[b][2] = sw.z; sv[b][3] = sw.w;
+            }
 #pragma unroll
             for (int jr = 0; jr < 4; ++jr) {
                 const int j = q * 4 + jr;
-                if (edge) {
-                    sv[jr] &= keep;
+                if (EDGE) {
+                    sv[0][jr] &= keep;
                     if (multi) {
                         // A NaN of a token that only some rows see must not reach the others through
                         // 0 * NaN: it is taken out here and given to the rows that see it.
                         uint32_t nan = 0;
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if ((part >> (8 * i) & 1u) && ((sv[jr] >> (8 * i)) & 0x7fu) == 0x7fu) {
+                            if ((part >> (8 * i) & 1u) && ((sv[0][jr] >> (8 * i)) & 0x7fu) == 0x7fu) {
                                 nan |= 1u << (4 * t + i);
-                                sv[jr] &= ~(0xffu << (8 * i));
+                                sv[0][jr] &= ~(0xffu << (8 * i));
                             }
                         if (__any_sync(0xffffffffu, nan != 0)) {
                             nan |= __shfl_xor_sync(0xffffffffu, nan, 1);
@@ -546,15 +600,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
                         }
                     }
                 }
-                uint32_t x[4];
-                e2m1x8_to_f16(cv[jr], x);
-                const uint32_t s01 = e4m3x2_to_f16((uint16_t)sv[jr]), s23 = e4m3x2_to_f16((uint16_t)(sv[jr] >> 16));
-                const uint32_t a[4] = {hmul2(x[0], s01), hmul2(x[1], s01), hmul2(x[2], s23), hmul2(x[3], s23)};
+                // the blocks' own sum first, then one rounded addition: the matrix instruction
+                // truncates, which over a long run would bias O
+                float sum[NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma_f16_16816(o[nt][j], a, ph[nt][0], ph[nt][1]);
-                    mma_f16_16816(o[nt][j], a, pl[nt][0], pl[nt][1]);
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) sum[nt][c] = 0.f;
+#pragma unroll
+                for (int b = 0; b < PB; ++b) {
+                    uint32_t x[4];
+                    e2m1x8_to_f16(cv[b][jr], x);
+                    const uint32_t s01 = e4m3x2_to_f16((uint16_t)sv[b][jr]),
+                                   s23 = e4m3x2_to_f16((uint16_t)(sv[b][jr] >> 16));
+                    const uint32_t a[4] = {hmul2(x[0], s01), hmul2(x[1], s01), hmul2(x[2], s23), hmul2(x[3], s23)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16_16816(sum[nt], a, pl[b][nt][0], pl[b][nt][1]);
+                        mma_f16_16816(sum[nt], a, ph[b][nt][0], ph[b][nt][1]);
+                    }
                 }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) o[nt][j][c] += sum[nt][c];
             }
         }
     };
@@ -599,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
                             p.out[to * D + 16 * j + g + 8] = o[nt][j][c + 2] * w;
                         }
                         if (p.lse && g == 0)
-                            p.lse[to] = l[nt][c] == 0.f ? -INFINITY : (m[nt][c] - kLift + log2f(l[nt][c])) * kLn2;
+                            p.lse[to] = l[nt][c] == 0.f ? -INFINITY : (log2f(l[nt][c]) - base[nt][c]) * kLn2;
                     }
                 } else {
 #pragma unroll
@@ -608,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
                         dst[row * D + 16 * j + g + 8] = o[nt][j][c + 2];
                     }
                     if (g == 0) {
-                        s_ml[part][row][0] = m[nt][c];
+                        s_ml[part][row][0] = kLift - base[nt][c];
                         s_ml[part][row][1] = l[nt][c];
                     }
                 }
@@ -622,14 +691,28 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
     int64_t run0 = f0;
     if (f < f1) enter_unit();
     while (f < f1) {
-        __syncwarp();  // every lane is done with the block that the next copy replaces
-        issue(slot + T::kDepth - 1 < T::kDepth ? slot + T::kDepth - 1 : slot - 1);
-        cp_async_wait<T::kDepth - 1>();
-        __syncwarp();
-        if (!bad) consume(ring + slot * F::kBlock);
-        slot = slot + 1 == T::kDepth ? 0 : slot + 1;
-        ++f;
-        if (++at.pg == plan.n || f == f1) {
+        const uint8_t *blk0 = ring + slot * F::kBlock;
+        const int slot1 = slot + 1 == T::kDepth ? 0 : slot + 1;
+        // two blocks at once where every row sees both whole
+        const bool pair = !bad && f + 2 <= f1 && ((at.pg >= in_from && at.pg + 2 <= in_to) ||
+                                                  (MODE == kKv4Fast && at.pg + 2 <= in_comp));
+        if (pair) {
+            cp_async_wait<T::kDepth - 2>();
+            __syncwarp();
+            consume(std::integral_constant<int, 2>{}, std::false_type{}, blk0, ring + slot1 * F::kBlock);
+        } else {
+            cp_async_wait<T::kDepth - 1>();
+            __syncwarp();
+            if (!bad) consume(std::integral_constant<int, 1>{}, std::true_type{}, blk0, blk0);
+        }
+        __syncwarp();  // every lane is done with the blocks that the next copies replace
+        issue(slot);
+        if (pair) issue(slot1);
+        const int step = pair ? 2 : 1;
+        slot = pair ? (slot1 + 1 == T::kDepth ? 0 : slot1 + 1) : slot1;
+        f += step;
+        at.pg += step;
+        if (at.pg == plan.n || f == f1) {
             leave_unit(run0, f);
             run0 = f;
             if (f < f1) {
