@@ -107,6 +107,8 @@ _lib = None
 def lib(path: str = LIB):
     """The loaded libsfi (raises if it has not been built)."""
     global _lib
+    if _lib is not None:  # set once, with every prototype in place
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):

@@ -43,8 +43,12 @@ class AttnShape:
         return self.num_q_heads // self.num_kv_heads
 
     def c(self) -> _abi.sfi_attn_shape:
-        return _abi.sfi_attn_shape(self.num_q_heads, self.num_kv_heads, self.head_dim, self.page_size,
-                                   float(self.softmax_scale))
+        c = self.__dict__.get("_c")
+        if c is None:  # the fields are frozen, so the C view is made once
+            c = _abi.sfi_attn_shape(self.num_q_heads, self.num_kv_heads, self.head_dim, self.page_size,
+                                    float(self.softmax_scale))
+            object.__setattr__(self, "_c", c)
+        return c
 
 
 @dataclass
@@ -83,6 +87,8 @@ class CompactKV:
 
 
 def _need(t: Optional[torch.Tensor], dtype, name: str):
+    if t is not None and t.is_cuda and t.dtype is dtype and t.is_contiguous():
+        return
     if t is None:
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
@@ -103,7 +109,8 @@ def _ptr(t: Optional[torch.Tensor], dtype=None, name: str = "") -> Optional[int]
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream().cuda_stream without the Stream object (3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -365,7 +372,7 @@ def rope_turns(inv_freq, device="cuda") -> torch.Tensor:
 
 
 def _on_current_device(t: torch.Tensor, name: str):
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
+    if t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on {t.device}, not on the current device")
 
 
@@ -373,11 +380,12 @@ def _token_rows(t: torch.Tensor, heads: int, dim: int, name: str) -> int:
     """Elements between the tokens of a [B][T][heads][dim] tensor whose heads are contiguous."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 4 or t.shape[2] != heads or t.shape[3] != dim:
-        raise ValueError(f"{name} must be [B][T][{heads}][{dim}], got {list(t.shape)}")
-    b, n = t.shape[:2]
+    dims = t.shape
+    if len(dims) != 4 or dims[2] != heads or dims[3] != dim:
+        raise ValueError(f"{name} must be [B][T][{heads}][{dim}], got {list(dims)}")
+    b, n = dims[0], dims[1]
     s = t.stride()
     step = s[1] if n > 1 else (s[0] if b > 1 else heads * dim)
     if s[3] != 1 or (heads > 1 and s[2] != dim) or (b > 1 and s[0] != n * step):
@@ -398,8 +406,8 @@ def sfi_qk_norm_rope(shape: AttnShape, rope: Optional[Rope], q: torch.Tensor, k:
     _on_current_device(q, "q")
     qs, ks = _token_rows(q, hq, d, "q"), _token_rows(k, hkv, d, "k")
     vs = 0 if v is None else _token_rows(v, hkv, d, "v")
-    B, T = q.shape[:2]
-    if k.shape[:2] != q.shape[:2] or (v is not None and v.shape[:2] != q.shape[:2]):
+    B, T = q.shape[0], q.shape[1]
+    if k.shape[0] != B or k.shape[1] != T or (v is not None and (v.shape[0] != B or v.shape[1] != T)):
         raise ValueError("q, k and v need the same requests and tokens")
     if q_out.shape != q.shape or (k_out is not None and k_out.shape != k.shape):
         raise ValueError("q_out and k_out need the shapes of q and k")
@@ -459,9 +467,9 @@ class CompactKV4:
 
 def _kv4(shape: AttnShape, kv: PagedKV4):
     _on_current_device(kv.pool, "pool")
-    if kv.pool.dim() != 3 or kv.pool.shape[1] != shape.num_kv_heads or kv.pool.shape[2] != 18 * shape.head_dim:
-        raise ValueError(f"pool must be [num_pages][{shape.num_kv_heads}][{18 * shape.head_dim}], "
-                         f"got {list(kv.pool.shape)}")
+    dims = kv.pool.shape
+    if len(dims) != 3 or dims[1] != shape.num_kv_heads or dims[2] != 18 * shape.head_dim:
+        raise ValueError(f"pool must be [num_pages][{shape.num_kv_heads}][{18 * shape.head_dim}], got {list(dims)}")
     return ctypes.byref(kv.c())
 
 
@@ -482,9 +490,10 @@ def alloc_kv4_compact(shape: AttnShape, rows, device="cuda") -> CompactKV4:
 def _rows4(t: torch.Tensor, dtype, shape: AttnShape, heads: int, name: str) -> int:
     """Tokens of a [B][T][heads][D] tensor."""
     _need(t, dtype, name)
-    if t.dim() != 4 or t.shape[2] != heads or t.shape[3] != shape.head_dim:
-        raise ValueError(f"{name} must be [B][T][{heads}][{shape.head_dim}], got {list(t.shape)}")
-    return t.shape[1]
+    dims = t.shape
+    if len(dims) != 4 or dims[2] != heads or dims[3] != shape.head_dim:
+        raise ValueError(f"{name} must be [B][T][{heads}][{shape.head_dim}], got {list(dims)}")
+    return dims[1]
 
 
 def sfi_kv4_append(shape: AttnShape, kv: PagedKV4, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -526,7 +535,7 @@ def sfi_kv4_compact_gather(shape: AttnShape, kv: PagedKV4, idx: torch.Tensor, co
 def _kv4_query(shape: AttnShape, q: torch.Tensor, out: torch.Tensor, lse: Optional[torch.Tensor]) -> int:
     T = _rows4(q, torch.bfloat16, shape, shape.num_q_heads, "q")
     _need(out, torch.float32, "out")
-    if out.shape != q.shape or (lse is not None and lse.shape != q.shape[:3]):
+    if out.shape != q.shape or (lse is not None and tuple(lse.shape) != tuple(q.shape)[:3]):
         raise ValueError("out needs the shape of q, lse that without its last dimension")
     return T
 
