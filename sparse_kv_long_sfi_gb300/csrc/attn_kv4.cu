@@ -18,6 +18,7 @@
 // probabilities off the subnormals), so the output is as good as fp32's. The running
 // maximum moves only when a score passes it by 2^8.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "kv4_format.cuh"
@@ -28,6 +29,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
+constexpr int kParts = 2 * kWarps;  // partials of a CTA: the first and the last run of each warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.f;   // the maximum may lag by this (in powers of two)
@@ -36,15 +38,20 @@ constexpr int kMinPages = 2;   // blocks per warp at least, before fewer CTAs wo
 
 enum Kv4Mode : int { kKv4Dense = 0, kKv4Scores = 1, kKv4Fast = 2 };
 
-template <int D, int NT>
+// ROWS: the query rows of a KV head that a variant takes. Up to four, P's two terms share
+// the N tile (columns 0..3 the first, 4..7 the second, over the same rows); up to eight,
+// they take an instruction each; up to sixteen, there are two N tiles.
+template <int D, int ROWS>
 struct Tile {
-    static constexpr int kDepth = NT == 1 ? 4 : 6;  // blocks in flight per warp
+    static constexpr int kNt = ROWS > 8 ? 2 : 1;
+    static constexpr bool kShared = ROWS <= 4;
+    static constexpr int kDepth = kNt == 1 ? 4 : 6;  // blocks in flight per warp
     static constexpr int kRing = kDepth * Kv4<D>::kBlock;
-    static constexpr int kRowsPad = 8 * NT;
-    static constexpr int kPart = kRowsPad * D * 4;  // a partial O
+    static constexpr int kPart = ROWS * D * 4;  // a partial O
     static constexpr int kFirst = kWarps * kRing;
     static constexpr int kSmem = kFirst + kWarps * kPart;
     static_assert(kRing >= kPart, "a warp's ring holds its last partial");
+    static_assert(kSmem >= kThreads * 24, "the merge's arrays lie where the rings were");
 };
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -125,6 +132,11 @@ __device__ __forceinline__ ReqPlan plan_request(const Kv4AttnParams &p, int b, u
     return q;
 }
 
+// a / b for a >= 0, b > 0, in 32 bits where both fit.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return ((uint64_t)(a | b) >> 32) ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // A place in the row of work: block `pg` of KV head h of request b.
 struct Place {
     int b, h, pg;
@@ -139,154 +151,184 @@ __device__ __forceinline__ Place locate(const int64_t *prefix, int batch, int hk
     const int64_t n = prefix[lo + 1] - prefix[lo], in = f - prefix[lo] * hkv;
     Place at;
     at.b = lo;
-    at.h = (int)(in / n);
+    at.h = (int)quotient(in, n);
     at.pg = (int)(in - at.h * n);
     return at;
 }
 
-// Page ids of a unit, 32 at a time (lane i: number base + i).
-struct PageIds {
-    int ids, base;
+// Four values of an output row (at `at`) from the merged sum and normaliser; lse_at >= 0: its log-sum-exp too.
+__device__ __forceinline__ void write_row(const Kv4AttnParams &p, int64_t at, float4 acc, float mx, float sum,
+                                          int64_t lse_at) {
+    const float w = sum == 0.f ? 0.f : p.v_scale / sum;
+    float2 *out = reinterpret_cast<float2 *>(p.out + at);
+    out[0] = make_float2(acc.x * w, acc.y * w);
+    out[1] = make_float2(acc.z * w, acc.w * w);
+    if (p.lse && lse_at >= 0) p.lse[lse_at] = sum == 0.f ? -INFINITY : (mx - kLift + log2f(sum)) * kLn2;
+}
+
+// Run w of `parts` nearly equal runs of [0, total): the first total % parts are one longer.
+struct Runs {
+    int64_t parts, q, r;
+    __device__ __forceinline__ Runs(int64_t total, int64_t n) : parts(n), q(quotient(total, n)), r(total - q * n) {}
+    __device__ __forceinline__ int64_t start(int64_t w) const { return w * q + min(w, r); }
+    __device__ __forceinline__ int64_t owner(int64_t f) const {
+        return f < r * (q + 1) ? quotient(f, q + 1) : r + quotient(f - r * (q + 1), q);
+    }
 };
+
+// The warps' runs: as many CTAs as give each warp kMinPages blocks, at most the grid's.
+__device__ __forceinline__ Runs runs_of(const Kv4AttnParams &p, const int64_t *prefix) {
+    const int64_t total = prefix[p.batch] * p.hkv;
+    const int64_t ctas = min((int64_t)gridDim.x, (total + kWarps * kMinPages - 1) / (kWarps * kMinPages));
+    return Runs(total, max(ctas * kWarps, (int64_t)1));
+}
 
 }  // namespace
 
-template <int D, int NT, int MODE>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(const Kv4AttnParams p) {
+template <int D, int ROWS, int MODE>
+__global__ void __launch_bounds__(kThreads, ROWS <= 8 ? 2 : 1) kv4_attn_kernel(const Kv4AttnParams p) {
     using F = Kv4<D>;
-    using T = Tile<D, NT>;
+    using T = Tile<D, ROWS>;
+    constexpr int NT = T::kNt;
     constexpr int kKs = D / 16;  // k steps of S, and m tiles of O
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_prefix[kKv4MaxBatch + 1];
-    __shared__ uint32_t s_bad[kKv4MaxBatch / 32];
-    __shared__ int64_t s_carry[kWarps];
-    __shared__ int64_t s_unit0[2 * kWarps];            // first block of a partial's unit
-    __shared__ int s_unit[2 * kWarps];                 // its unit, or -1
-    __shared__ float s_ml[2 * kWarps][T::kRowsPad][2];
-    __shared__ int s_last;
+    __shared__ uint32_t s_drop[kKv4MaxBatch / 32];  // scores mode: requests with a bad page id
+    __shared__ int64_t s_unit0[kParts];             // first block of a partial's unit
+    __shared__ int s_unit[kParts];                  // its unit, or -1
+    __shared__ int s_bad[kParts];                   // its run met a bad page id
+    __shared__ float s_ml[kParts][ROWS][2];
+    __shared__ int s_last[2], s_open[2];
+    __shared__ int64_t s_open0[2];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
 
-    // ---- the row of work: blocks of each request, summed up ----
-    uint32_t err = 0;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    // ---- the row of work: blocks of each request, summed up (every warp for itself) ----
     {
+        uint32_t err = 0;
         int64_t carry = 0;
-        for (int base = 0; base < p.batch; base += kThreads) {
-            const int b = base + tid;
-            int64_t v = b < p.batch ? plan_request<MODE>(p, b, &err).n : 0;
+        for (int base = 0; base < p.batch; base += 32) {
+            const int b = base + lane;
+            const int64_t v = b < p.batch ? plan_request<MODE>(p, b, &err).n : 0;
             int64_t incl = v;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
                 if (lane >= off) incl += o;
             }
-            if (lane == 31) s_carry[warp] = incl;
-            __syncthreads();
-            int64_t before = carry, all = carry;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < warp) before += s_carry[w];
-                all += s_carry[w];
-            }
-            if (b < p.batch) s_prefix[b] = before + incl - v;
-            carry = all;
-            __syncthreads();
+            if (b < p.batch) s_prefix[b] = carry + incl - v;
+            carry += __shfl_sync(0xffffffffu, incl, 31);
         }
-        if (tid == 0) s_prefix[p.batch] = carry;
-        if (tid < kKv4MaxBatch / 32) s_bad[tid] = 0;
-        if (tid < 2 * kWarps) s_unit[tid] = -1;
-        if (err && blockIdx.x == 0) report(p.dev_status, err);
+        if (lane == 0) s_prefix[p.batch] = carry;
+        if (err && blockIdx.x == 0 && warp == 0) report(p.dev_status, err);
     }
-    __syncthreads();
-    const int64_t total = s_prefix[p.batch] * p.hkv;
-    const int64_t ctas = min((int64_t)gridDim.x, (total + kWarps * kMinPages - 1) / (kWarps * kMinPages));
-    if ((int64_t)blockIdx.x >= ctas) return;
-    const int64_t warps = ctas * kWarps;
-    const int64_t f0 = ((int64_t)blockIdx.x * kWarps + warp) * total / warps;
-    const int64_t f1 = ((int64_t)blockIdx.x * kWarps + warp + 1) * total / warps;
-    const int64_t cta0 = (int64_t)blockIdx.x * kWarps * total / warps;
-    const int64_t cta1 = ((int64_t)blockIdx.x + 1) * kWarps * total / warps;
+    if (lane < 2) s_unit[2 * warp + lane] = -1;
+    if (tid < 2) s_open[tid] = -1;
+    __syncwarp();
+    int64_t f0, f1;
+    {
+        const Runs runs = runs_of(p, s_prefix);
+        if (s_prefix[p.batch] == 0 || (int64_t)blockIdx.x * kWarps >= runs.parts) return;
+        f0 = runs.start((int64_t)blockIdx.x * kWarps + warp);
+        f1 = runs.start((int64_t)blockIdx.x * kWarps + warp + 1);
+    }
 
     // ---- copies: this warp's blocks, kDepth of them in flight ----
     uint8_t *ring = smem + warp * T::kRing;
     Place ahead{};
     ReqPlan aplan{};
-    PageIds ids{0, 0};
-    int64_t fa = f0;  // next block to copy
-    auto load_ids = [&](int first) {  // page ids [first, first + 32) of the unit's pages
-        ids.base = first;
-        const int r = request_id(p, ahead.b);
-        const int i = first + lane;
-        ids.ids = i < aplan.n - aplan.ncomp ? p.page_table[(int64_t)r * p.max_pages + aplan.page0 + i] : 0;
-    };
+    int ids = 0, ids_base = 0;     // page ids of the unit, 32 at a time (lane i: number ids_base + i)
+    const int32_t *id_row = nullptr;
+    const int run = (int)(f1 - f0);  // blocks of this warp
+    int left = run;                  // those still to be copied
+    uint32_t bad_units = 0;        // bit (number of the unit in this run) % 32: it has a bad page id
+    int unit_ahead = 0, unit_here = 0;
     uint32_t none = 0;
+    auto load_ids = [&](int first) {
+        ids_base = first;
+        ids = first + lane < aplan.n - aplan.ncomp ? id_row[first + lane] : 0;
+        const bool out = (uint32_t)ids >= (uint32_t)p.num_pages;
+        if (out) ids = 0;  // any page: the unit writes nothing
+        if (__any_sync(0xffffffffu, out)) {
+            bad_units |= 1u << (unit_ahead & 31);
+            if (lane == 0) report(p.dev_status, SFI_DEV_BAD_PAGE);
+        }
+    };
     auto enter_ahead = [&]() {
         aplan = plan_request<MODE>(p, ahead.b, &none);
+        id_row = p.page_table + (int64_t)request_id(p, ahead.b) * p.max_pages + aplan.page0;
+        bad_units &= ~(1u << (unit_ahead & 31));
         load_ids(max(0, ahead.pg - aplan.ncomp));
     };
     auto issue = [&](int slot) {
-        if (fa < f1) {
+        if (left > 0) {
             const uint8_t *src;
             if (MODE == kKv4Fast && ahead.pg < aplan.ncomp) {
                 src = p.c_pool + (aplan.cblock + (int64_t)ahead.h * aplan.cap + ahead.pg) * F::kBlock;
             } else {
                 const int i = ahead.pg - aplan.ncomp;
-                if (i >= ids.base + 32) load_ids(i);
-                int page = __shfl_sync(0xffffffffu, ids.ids, i - ids.base);
-                if (page < 0 || page >= p.num_pages) page = 0;  // the unit is dropped below
+                if (i >= ids_base + 32) load_ids(i);
+                const int page = __shfl_sync(0xffffffffu, ids, i - ids_base);
                 src = p.pool + ((int64_t)page * p.hkv + ahead.h) * F::kBlock;
             }
-            uint8_t *dst = ring + slot * F::kBlock;
+            src += lane * 16;
+            uint8_t *dst = ring + slot * F::kBlock + lane * 16;
 #pragma unroll
-            for (int c = lane; c < F::kBlock / 16; c += 32) cp_async16(dst + c * 16, src + c * 16);
-            ++fa;
-            if (++ahead.pg == aplan.n && fa < f1) {
+            for (int c = 0; c < F::kBlock / 16; c += 32)
+                if (c + 32 <= F::kBlock / 16 || lane < F::kBlock / 16 - c) cp_async16(dst + c * 16, src + c * 16);
+            --left;
+            if (++ahead.pg == aplan.n && left > 0) {
                 ahead.pg = 0;
                 if (++ahead.h == p.hkv) {
                     ahead.h = 0;
                     do ++ahead.b; while (s_prefix[ahead.b + 1] == s_prefix[ahead.b]);
                 }
+                ++unit_ahead;
                 enter_ahead();
             }
         }
         cp_async_commit();
     };
+    const int gshift = __ffs(p.group) - 1;  // the group size is a power of two
+    // a unit's query rows as they lie (lane (g, t): dims t D/4 .. of row g)
+    auto load_query = [&](const Place &x, int4 (&raw_q)[NT][D / 32]) {
+        const int64_t tok0 = (int64_t)request_id(p, x.b) * p.tokens;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = T::kShared ? g & 3 : nt * 8 + g;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) raw_q[nt][i] = make_int4(0, 0, 0, 0);
+            if (row < p.rows) {
+                const int head = x.h * p.group + (row & (p.group - 1));
+                const __nv_bfloat16 *src = p.q + ((tok0 + (row >> gshift)) * p.hq + head) * D + t * (D / 4);
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) raw_q[nt][i] = *reinterpret_cast<const int4 *>(src + i * 8);
+            }
+        }
+    };
     Place at{};
-    if (f0 < f1) {
+    int4 raw_query[NT][D / 32];
+    if (run > 0) {
         at = locate(s_prefix, p.batch, p.hkv, f0);
+        load_query(at, raw_query);  // on their way while page ids and blocks are fetched
         ahead = at;
         enter_ahead();
     }
 #pragma unroll
     for (int i = 0; i < T::kDepth; ++i) issue(i);
 
-    // ---- page ids of every request this CTA touches: one bad id drops the request ----
-    {
-        const int b0 = locate(s_prefix, p.batch, p.hkv, cta0).b, b1 = locate(s_prefix, p.batch, p.hkv, cta1 - 1).b;
-        for (int b = b0; b <= b1; ++b) {
-            const ReqPlan q = plan_request<MODE>(p, b, &none);
-            const int r = request_id(p, b);
-            const int32_t *row = p.page_table + (int64_t)r * p.max_pages + q.page0;
-            bool bad = false;
-#pragma unroll 8
-            for (int i = tid; i < q.n - q.ncomp; i += kThreads) bad |= (uint32_t)__ldg(row + i) >= (uint32_t)p.num_pages;
-            if (bad) atomicOr(&s_bad[b >> 5], 1u << (b & 31));
-        }
-    }
-    __syncthreads();
-
     // ---- this warp's units ----
     uint32_t bq[NT][kKs][2];     // Q as B fragments
     float mul[NT][2];            // fp16 product -> score in powers of two
-    float nat[NT][2];            // ... -> score (scores mode; 0 in rows that are not there)
-    int rtok[NT][2];             // query token of this lane's rows
     float o[NT][kKs][4];
     float base[NT][2], l[NT][2];  // kLift - running maximum (+inf: nothing seen), sum of 2^(score + base)
     ReqPlan plan{};
-    int64_t f = f0, unit0 = 0;
+    int f = 0, unit0 = 0;        // this block, and the first of its unit, counted from the warp's first
     int slot = 0;
-    bool bad = false;
+    bool drop = false;
     const bool multi = p.tokens > 1;
     // blocks that every row sees whole: [0, in_comp) and [in_from, in_to)
     int in_comp = 0, in_from = 0, in_to = 0;
@@ -304,10 +346,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
         }
     };
 
-    auto enter_unit = [&]() {
+    auto token_of = [&](int row) { return min(row >> gshift, p.tokens - 1); };
+    auto row_of = [&](int nt, int c) { return T::kShared ? (2 * t + c) & 3 : nt * 8 + 2 * t + c; };
+    const float second = T::kShared && t >= 2 ? -1.f : 0.f;  // this lane's columns take P's second term
+
+    auto dropped = [&]() { return MODE == kKv4Scores && ((s_drop[at.b >> 5] >> (at.b & 31)) & 1u); };
+    auto enter_unit = [&](const int4 (&raw_q)[NT][D / 32]) {
         plan = plan_request<MODE>(p, at.b, &none);
         unit0 = f - at.pg;
-        bad = (s_bad[at.b >> 5] >> (at.b & 31)) & 1u;
+        drop = dropped();
         const int r = request_id(p, at.b);
         {
             int lo_a, hi_a, lo_z, hi_z;
@@ -325,16 +372,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
         if (MODE == kKv4Scores) score_row = p.scores + ((int64_t)r * p.hkv + at.h) * p.score_stride;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int row = nt * 8 + g;
-            int4 raw[D / 32];
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) raw[i] = make_int4(0, 0, 0, 0);
-            if (row < p.rows) {
-                const int tok = row / p.group, head = at.h * p.group + row % p.group;
-                const __nv_bfloat16 *src = p.q + (((int64_t)r * p.tokens + tok) * p.hq + head) * D + t * (D / 4);
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) raw[i] = *reinterpret_cast<const int4 *>(src + i * 8);
-            }
+            const int4(&raw)[D / 32] = raw_q[nt];
             // the row's largest magnitude, as bits; 2^shift takes it to [2^14, 2^15)
             uint32_t top = 0;
 #pragma unroll
@@ -361,12 +399,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
                 }
             }
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {  // S^T's columns of this lane are rows 2t, 2t + 1
-                const int col = nt * 8 + 2 * t + c;
-                const float x = __shfl_sync(0xffffffffu, down, (2 * t + c) * 4) * p.k_mul;
-                mul[nt][c] = x * kLog2e;
-                nat[nt][c] = col < p.rows ? x : 0.f;
-                rtok[nt][c] = min(col / p.group, p.tokens - 1);
+            for (int c = 0; c < 2; ++c) {  // S^T's columns 2t, 2t + 1 are this lane's
+                mul[nt][c] = __shfl_sync(0xffffffffu, down, (2 * t + c) * 4) * p.k_mul * kLog2e;
                 base[nt][c] = INFINITY;
                 l[nt][c] = 0.f;
             }
@@ -420,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
     };
 
     // PB blocks from blk on (EDGE: one block, some of whose tokens some rows do not see).
-    auto consume = [&](auto pb_tag, auto edge_tag, const uint8_t *blk0, const uint8_t *blk1) {
+    auto consume = [&](auto pb_tag, auto edge_tag, uint8_t *blk0, uint8_t *blk1) {
         constexpr int PB = decltype(pb_tag)::value;
         constexpr bool EDGE = decltype(edge_tag)::value;
         const bool comp = EDGE && MODE == kKv4Fast && at.pg < plan.ncomp;
@@ -428,6 +462,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
         float s[PB][NT][4];
 #pragma unroll
         for (int b = 0; b < PB; ++b) products(b ? blk1 : blk0, s[b]);
+        if constexpr (!EDGE) {
+            // V scales in fp16 for the whole warp, where the K codes were: lane w converts word w
+            // (four tokens of one group)
+            __syncwarp();
+#pragma unroll
+            for (int b = 0; b < PB; ++b) {
+                uint8_t *blk = b ? blk1 : blk0;
+                if (D == 128 || lane < D / 4) {
+                    const uint32_t w = *reinterpret_cast<const uint32_t *>(blk + F::kVScale + lane * 4);
+                    *reinterpret_cast<uint2 *>(blk + lane * 8) =
+                        make_uint2(e4m3x2_to_f16((uint16_t)w), e4m3x2_to_f16((uint16_t)(w >> 16)));
+                }
+            }
+            __syncwarp();
+        }
         // ---- scores (natural units), masks, exponents ----
         uint32_t hide = 0;  // bits 4 nt + c: not seen
         if (EDGE) {
@@ -436,44 +485,42 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     int lo, hi;
-                    span(comp, rtok[nt][c & 1], lo, hi);
+                    span(comp, token_of(row_of(nt, c & 1)), lo, hi);
                     const int pos = pos0 + tu + (c & 2);
                     if (pos < lo || pos >= hi) hide |= 1u << (4 * nt + c);
                 }
         }
         if (MODE == kKv4Scores) {
-            // the rows' sum of each token; lane t of four ends up with token tu + 2 (t & 1) of block t / 2
-            float sum[PB][2];
-#pragma unroll
-            for (int b = 0; b < PB; ++b)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    float x = 0.f;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const float y = s[b][nt][2 * k + c] * nat[nt][c];
-                            x += EDGE && ((hide >> (4 * nt + 2 * k + c)) & 1u) ? 0.f : y;
-                        }
-                    sum[b][k] = x;
-                }
+            // The rows' sum of each token (rows that are not there hold zeros). Over the four lanes
+            // of a token group the sums end up one in each: lane t has token tu + 2 (t & 1) of block
+            // t / 2. With shared columns lanes t and t + 2 hold the same rows.
             float one[PB];
 #pragma unroll
             for (int b = 0; b < PB; ++b) {
-                const float give = (t & 1) ? sum[b][0] : sum[b][1];
-                one[b] = ((t & 1) ? sum[b][1] : sum[b][0]) + __shfl_xor_sync(0xffffffffu, give, 1);
+                float sum[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    sum[k] = 0.f;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            if (!EDGE || !((hide >> (4 * nt + 2 * k + c)) & 1u))
+                                sum[k] = fmaf(s[b][nt][2 * k + c], mul[nt][c], sum[k]);
+                }
+                const float give = (t & 1) ? sum[0] : sum[1];
+                one[b] = ((t & 1) ? sum[1] : sum[0]) + __shfl_xor_sync(0xffffffffu, give, 1);
             }
-            float all;
+            float all = one[0];
             if constexpr (PB == 2) {
-                const float give = (t & 2) ? one[0] : one[1];
-                all = ((t & 2) ? one[1] : one[0]) + __shfl_xor_sync(0xffffffffu, give, 2);
-            } else {
-                all = one[0] + __shfl_xor_sync(0xffffffffu, one[0], 2);
+                all = (t & 2) ? one[1] : one[0];
+                if (!T::kShared) all += __shfl_xor_sync(0xffffffffu, (t & 2) ? one[0] : one[1], 2);
+            } else if (!T::kShared) {
+                all += __shfl_xor_sync(0xffffffffu, one[0], 2);
             }
             const int pos = pos0 + tu + 2 * (t & 1) + (PB == 2 ? 8 * (t & 2) : 0);
             if ((PB == 2 || t < 2) && (!EDGE || pos < plan.L))
-                score_row[pos] = pos >= p.sink && pos < plan.L - p.recent ? all : -INFINITY;
+                score_row[pos] = pos >= p.sink && pos < plan.L - p.recent ? all * kLn2 : -INFINITY;
         }
         // y = score in powers of two above the running maximum, plus kLift
         float y[PB][NT][4];
@@ -523,7 +570,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
                 }
         }
         // ---- P^T as two fp16 terms ----
-        uint32_t ph[PB][NT][2], pl[PB][NT][2];
+        uint32_t ph[PB][NT][2];
+        [[maybe_unused]] uint32_t pl[PB][NT][2];
 #pragma unroll
         for (int b = 0; b < PB; ++b)
 #pragma unroll
@@ -537,8 +585,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
                 for (int k = 0; k < 2; ++k) {
                     const uint32_t h = pack_f16x2(x[2 * k], x[2 * k + 1]);
                     const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-                    ph[b][nt][k] = transpose_8x8(h);
-                    pl[b][nt][k] = transpose_8x8(pack_f16x2(x[2 * k] - hf.x, x[2 * k + 1] - hf.y));
+                    if constexpr (T::kShared) {
+                        ph[b][nt][k] = transpose_8x8(pack_f16x2(fmaf(hf.x, second, x[2 * k]), fmaf(hf.y, second, x[2 * k + 1])));
+                    } else {
+                        ph[b][nt][k] = transpose_8x8(h);
+                        pl[b][nt][k] = transpose_8x8(pack_f16x2(x[2 * k] - hf.x, x[2 * k + 1] - hf.y));
+                    }
                 }
             }
         // ---- O^T += V^T P^T: rows g, g + 8 -> dims 16 j + g, 16 j + g + 8; k -> tokens 4t .. 4t + 3 ----
@@ -558,30 +610,37 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
         }
 #pragma unroll
         for (int q = 0; q < F::kQuads; ++q) {
-            uint32_t cv[PB][4], sv[PB][4];
+            uint32_t cv[PB][4], sv[4], sh[PB][4][2];
 #pragma unroll
             for (int b = 0; b < PB; ++b) {
                 const uint8_t *blk = b ? blk1 : blk0;
                 const uint4 cw = *reinterpret_cast<const uint4 *>(blk + F::kVCode + q * 512 + (g >> 1) * 128 + t * 32 +
                                                                   (g & 1) * 16);
-                const uint4 sw = *reinterpret_cast<const uint4 *>(blk + F::kVScale + t * F::kVScaleT + q * 16);
                 cv[b][0] = cw.x; cv[b][1] = cw.y; cv[b][2] = cw.z; cv[b][3] = cw.w;
-                sv[b][0] = sw.x; sv[b][1] = sw.y; sv[b][2] = sw.z; sv[b][3] = sw.w;
+                if constexpr (EDGE) {
+                    const uint4 sw = *reinterpret_cast<const uint4 *>(blk + F::kVScale + t * F::kVScaleT + q * 16);
+                    sv[0] = sw.x; sv[1] = sw.y; sv[2] = sw.z; sv[3] = sw.w;
+                } else {
+                    const uint4 *sw = reinterpret_cast<const uint4 *>(blk + t * (D / 2) + q * 32);
+                    const uint4 x = sw[0], y4 = sw[1];
+                    sh[b][0][0] = x.x; sh[b][0][1] = x.y; sh[b][1][0] = x.z; sh[b][1][1] = x.w;
+                    sh[b][2][0] = y4.x; sh[b][2][1] = y4.y; sh[b][3][0] = y4.z; sh[b][3][1] = y4.w;
+                }
             }
 #pragma unroll
             for (int jr = 0; jr < 4; ++jr) {
                 const int j = q * 4 + jr;
                 if (EDGE) {
-                    sv[0][jr] &= keep;
+                    sv[jr] &= keep;
                     if (multi) {
                         // A NaN of a token that only some rows see must not reach the others through
                         // 0 * NaN: it is taken out here and given to the rows that see it.
                         uint32_t nan = 0;
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if ((part >> (8 * i) & 1u) && ((sv[0][jr] >> (8 * i)) & 0x7fu) == 0x7fu) {
+                            if ((part >> (8 * i) & 1u) && ((sv[jr] >> (8 * i)) & 0x7fu) == 0x7fu) {
                                 nan |= 1u << (4 * t + i);
-                                sv[0][jr] &= ~(0xffu << (8 * i));
+                                sv[jr] &= ~(0xffu << (8 * i));
                             }
                         if (__any_sync(0xffffffffu, nan != 0)) {
                             nan |= __shfl_xor_sync(0xffffffffu, nan, 1);
@@ -591,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
 #pragma unroll
                                 for (int c = 0; c < 2; ++c) {
                                     int lo, hi;
-                                    span(comp, rtok[nt][c], lo, hi);
+                                    span(comp, token_of(row_of(nt, c)), lo, hi);
                                     uint32_t mine = 0;
                                     for (int i = 0; i < 16; ++i)
                                         if (pos0 + i >= lo && pos0 + i < hi) mine |= 1u << i;
@@ -611,12 +670,18 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
                 for (int b = 0; b < PB; ++b) {
                     uint32_t x[4];
                     e2m1x8_to_f16(cv[b][jr], x);
-                    const uint32_t s01 = e4m3x2_to_f16((uint16_t)sv[b][jr]),
-                                   s23 = e4m3x2_to_f16((uint16_t)(sv[b][jr] >> 16));
+                    uint32_t s01, s23;
+                    if constexpr (EDGE) {
+                        s01 = e4m3x2_to_f16((uint16_t)sv[jr]);
+                        s23 = e4m3x2_to_f16((uint16_t)(sv[jr] >> 16));
+                    } else {
+                        s01 = sh[b][jr][0];
+                        s23 = sh[b][jr][1];
+                    }
                     const uint32_t a[4] = {hmul2(x[0], s01), hmul2(x[1], s01), hmul2(x[2], s23), hmul2(x[3], s23)};
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16_16816(sum[nt], a, pl[b][nt][0], pl[b][nt][1]);
+                        if constexpr (!T::kShared) mma_f16_16816(sum[nt], a, pl[b][nt][0], pl[b][nt][1]);
                         mma_f16_16816(sum[nt], a, ph[b][nt][0], ph[b][nt][1]);
                     }
                 }
@@ -628,14 +693,18 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
         }
     };
 
-    const int r_rows = p.rows;
     // the end of this warp's run of a unit: its output when the run is the whole unit, else a partial
-    auto leave_unit = [&](int64_t run0, int64_t run1) {
+    auto leave_unit = [&](int run0, int run1) {
         const bool whole = run0 == unit0 && run1 == unit0 + plan.n;
-        if (bad) {
-            if (lane == 0 && run0 == unit0) report(p.dev_status, SFI_DEV_BAD_PAGE);
-            return;
+        const bool bad = drop || ((bad_units >> (unit_here & 31)) & 1u);
+        const bool last = run1 == run;
+        const int part = warp * 2 + (last ? 1 : 0);
+        if (lane == 0 && !whole) {
+            s_unit[part] = at.b * p.hkv + at.h;
+            s_unit0[part] = runs_of(p, s_prefix).start((int64_t)blockIdx.x * kWarps + warp) + unit0;
+            s_bad[part] = bad;
         }
+        if (bad) return;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -643,10 +712,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
                 l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], 4);
                 l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], 8);
                 l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], 16);
+                if (T::kShared) {  // O of P's second term, two lanes on
+#pragma unroll
+                    for (int j = 0; j < kKs; ++j) {
+                        o[nt][j][c] += __shfl_xor_sync(0xffffffffu, o[nt][j][c], 2);
+                        o[nt][j][c + 2] += __shfl_xor_sync(0xffffffffu, o[nt][j][c + 2], 2);
+                    }
+                }
             }
         const int r = request_id(p, at.b);
-        const bool last = run1 == f1;
-        const int part = warp * 2 + (last ? 1 : 0);
         float *dst = last ? reinterpret_cast<float *>(ring)
                           : reinterpret_cast<float *>(smem + T::kFirst + warp * T::kPart);
         if (!whole && last) {  // the ring is done with once every copy has landed
@@ -657,19 +731,18 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const int row = nt * 8 + 2 * t + c;
+                const int row = row_of(nt, c);
+                if (row >= p.rows || (T::kShared && t >= 2)) continue;
                 if (whole) {
-                    if (row < r_rows) {
-                        const int64_t to = ((int64_t)r * p.tokens + row / p.group) * p.hq + at.h * p.group + row % p.group;
-                        const float w = l[nt][c] == 0.f ? 0.f : p.v_scale / l[nt][c];
+                    const int64_t to = ((int64_t)r * p.tokens + row / p.group) * p.hq + at.h * p.group + row % p.group;
+                    const float w = l[nt][c] == 0.f ? 0.f : p.v_scale / l[nt][c];
 #pragma unroll
-                        for (int j = 0; j < kKs; ++j) {
-                            p.out[to * D + 16 * j + g] = o[nt][j][c] * w;
-                            p.out[to * D + 16 * j + g + 8] = o[nt][j][c + 2] * w;
-                        }
-                        if (p.lse && g == 0)
-                            p.lse[to] = l[nt][c] == 0.f ? -INFINITY : (log2f(l[nt][c]) - base[nt][c]) * kLn2;
+                    for (int j = 0; j < kKs; ++j) {
+                        p.out[to * D + 16 * j + g] = o[nt][j][c] * w;
+                        p.out[to * D + 16 * j + g + 8] = o[nt][j][c + 2] * w;
                     }
+                    if (p.lse && g == 0)
+                        p.lse[to] = l[nt][c] == 0.f ? -INFINITY : (log2f(l[nt][c]) - base[nt][c]) * kLn2;
                 } else {
 #pragma unroll
                     for (int j = 0; j < kKs; ++j) {
@@ -682,148 +755,267 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_attn_kernel(con
                     }
                 }
             }
-        if (!whole && lane == 0) {
-            s_unit[part] = at.b * p.hkv + at.h;
-            s_unit0[part] = unit0;
-        }
     };
 
-    int64_t run0 = f0;
-    if (f < f1) enter_unit();
-    while (f < f1) {
-        const uint8_t *blk0 = ring + slot * F::kBlock;
-        const int slot1 = slot + 1 == T::kDepth ? 0 : slot + 1;
+    int run0 = 0;
+    if (run > 0) enter_unit(raw_query);
+    // ---- scores are written on the way: the page ids of the CTA's requests are looked at first ----
+    if (MODE == kKv4Scores) {
+        if (tid < kKv4MaxBatch / 32) s_drop[tid] = 0;
+        if (tid == 0) s_last[0] = run > 0 ? at.b : 0;
+        __syncthreads();
+        const int64_t end = runs_of(p, s_prefix).start((int64_t)(blockIdx.x + 1) * kWarps);
+        for (int b = s_last[0]; b < p.batch && s_prefix[b] * p.hkv < end; ++b) {
+            const int n = (int)(s_prefix[b + 1] - s_prefix[b]);
+            const int32_t *row = p.page_table + (int64_t)request_id(p, b) * p.max_pages;
+            bool out = false;
+#pragma unroll 8
+            for (int i = tid; i < n; i += kThreads) out |= (uint32_t)row[i] >= (uint32_t)p.num_pages;
+            if (out) atomicOr(&s_drop[b >> 5], 1u << (b & 31));
+        }
+        __syncthreads();
+        if (run > 0) drop = dropped();
+    }
+    while (f < run) {
         // two blocks at once where every row sees both whole
-        const bool pair = !bad && f + 2 <= f1 && ((at.pg >= in_from && at.pg + 2 <= in_to) ||
-                                                  (MODE == kKv4Fast && at.pg + 2 <= in_comp));
-        if (pair) {
-            cp_async_wait<T::kDepth - 2>();
-            __syncwarp();
-            consume(std::integral_constant<int, 2>{}, std::false_type{}, blk0, ring + slot1 * F::kBlock);
+        int pairs = 0;
+        if (!drop) {
+            int inside = at.pg >= in_from ? in_to - at.pg : 0;
+            if (MODE == kKv4Fast) inside = max(inside, in_comp - at.pg);
+            pairs = min(inside, run - f) / 2;
+        }
+        if (pairs > 0) {
+            for (int i = 0; i < pairs; ++i) {
+                const int slot1 = slot + 1 == T::kDepth ? 0 : slot + 1;
+                cp_async_wait<T::kDepth - 2>();
+                __syncwarp();
+                consume(std::integral_constant<int, 2>{}, std::false_type{}, ring + slot * F::kBlock,
+                        ring + slot1 * F::kBlock);
+                __syncwarp();  // every lane is done with the blocks that the next copies replace
+                issue(slot);
+                issue(slot1);
+                slot = slot1 + 1 == T::kDepth ? 0 : slot1 + 1;
+                at.pg += 2;
+            }
+            f += 2 * pairs;
         } else {
             cp_async_wait<T::kDepth - 1>();
             __syncwarp();
-            if (!bad) consume(std::integral_constant<int, 1>{}, std::true_type{}, blk0, blk0);
+            if (!drop) consume(std::integral_constant<int, 1>{}, std::true_type{}, ring + slot * F::kBlock, ring);
+            __syncwarp();
+            issue(slot);
+            slot = slot + 1 == T::kDepth ? 0 : slot + 1;
+            ++f;
+            ++at.pg;
         }
-        __syncwarp();  // every lane is done with the blocks that the next copies replace
-        issue(slot);
-        if (pair) issue(slot1);
-        const int step = pair ? 2 : 1;
-        slot = pair ? (slot1 + 1 == T::kDepth ? 0 : slot1 + 1) : slot1;
-        f += step;
-        at.pg += step;
-        if (at.pg == plan.n || f == f1) {
+        if (at.pg == plan.n || f == run) {
             leave_unit(run0, f);
             run0 = f;
-            if (f < f1) {
+            if (f < run) {
                 at.pg = 0;
                 if (++at.h == p.hkv) {
                     at.h = 0;
                     do ++at.b; while (s_prefix[at.b + 1] == s_prefix[at.b]);
                 }
-                enter_unit();
+                ++unit_here;
+                load_query(at, raw_query);
+                enter_unit(raw_query);
             }
         }
     }
     cp_async_wait<0>();
     __syncthreads();
 
-    // ---- partials of the CTA, unit by unit (in order) ----
-    auto part_ptr = [&](int i) {
-        return (i & 1) ? reinterpret_cast<const float *>(smem + (i >> 1) * T::kRing)
-                       : reinterpret_cast<const float *>(smem + T::kFirst + (i >> 1) * T::kPart);
-    };
-    for (int i = 0; i < 2 * kWarps;) {
-        const int u = s_unit[i];
-        if (u < 0) {
-            ++i;
-            continue;
-        }
-        int end = i + 1;
-        for (int k = i + 1; k < 2 * kWarps; ++k)
-            if (s_unit[k] == u) end = k + 1;
+    // ---- the CTA's partials, unit by unit: the unit's output where the CTA holds all of it, else
+    // the CTA's part of it (s_open: units begun before this CTA, or going on after it) ----
+    const Runs runs = runs_of(p, s_prefix);
+    const int64_t cta0 = runs.start((int64_t)blockIdx.x * kWarps), cta1 = runs.start((int64_t)(blockIdx.x + 1) * kWarps);
+    const int my_unit = lane < kParts ? s_unit[lane] : -1;
+    const uint32_t mine = __match_any_sync(0xffffffffu, my_unit);
+    const uint32_t bads = __ballot_sync(0xffffffffu, lane < kParts && my_unit >= 0 && s_bad[lane & (kParts - 1)]);
+    for (uint32_t todo = __ballot_sync(0xffffffffu, my_unit >= 0); todo;) {
+        const int first = __ffs(todo) - 1;
+        const int u = __shfl_sync(0xffffffffu, my_unit, first);
+        const uint32_t parts = __shfl_sync(0xffffffffu, mine, first);
+        todo &= ~parts;
+        const bool bad = bads & parts;
         const int b = u / p.hkv, h = u - b * p.hkv;
         const int r = request_id(p, b);
-        const int64_t u0 = s_unit0[i], u1 = u0 + (s_prefix[b + 1] - s_prefix[b]);
+        const int64_t u0 = s_unit0[first], u1 = u0 + (s_prefix[b + 1] - s_prefix[b]);
         const bool complete = u0 >= cta0 && u1 <= cta1;
-        // this CTA's slot: 0 when the unit began before it, else 1
-        const int64_t ws_slot = (int64_t)blockIdx.x * 2 + (u0 < cta0 ? 0 : 1);
-        for (int e = tid; e < r_rows * D; e += kThreads) {
-            const int row = e / D, d = e % D;
-            float mx = -INFINITY, sum = 0.f, acc = 0.f;
-            for (int k = i; k < end; ++k)
-                if (s_unit[k] == u) mx = fmaxf(mx, s_ml[k][row][0]);
-            for (int k = i; k < end; ++k)
-                if (s_unit[k] == u) {
-                    const float mk = s_ml[k][row][0];
-                    const float w = mk == mx ? 1.f : fast_exp2(mk - mx);
-                    sum = fmaf(w, s_ml[k][row][1], sum);
-                    acc = fmaf(w, part_ptr(k)[row * D + d], acc);
-                }
+        const int side = u0 < cta0 ? 0 : 1;  // this CTA's slot for it in the workspace
+        const int64_t ws_row = ((int64_t)blockIdx.x * 2 + side) * kMaxRows;
+        if (!complete && tid == 0) {
+            s_open[side] = u;
+            s_open0[side] = u0;
+        }
+        for (int e = tid; e < p.rows * (D / 4) && !(complete && bad); e += kThreads) {
+            const int row = e / (D / 4), d = e % (D / 4) * 4;
+            float m[kParts];
+            float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) {
+                m[k] = (parts >> k) & 1u ? s_ml[k][row][0] : -INFINITY;
+                mx = fmaxf(mx, m[k]);
+            }
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) {
+                if (!((parts >> k) & 1u)) continue;
+                const float w = m[k] == mx ? 1.f : fast_exp2(m[k] - mx);
+                const float4 x = *reinterpret_cast<const float4 *>(
+                    smem + ((k & 1) ? (k >> 1) * T::kRing : T::kFirst + (k >> 1) * T::kPart) + (row * D + d) * 4);
+                sum = fmaf(w, s_ml[k][row][1], sum);
+                acc.x = fmaf(w, x.x, acc.x);
+                acc.y = fmaf(w, x.y, acc.y);
+                acc.z = fmaf(w, x.z, acc.z);
+                acc.w = fmaf(w, x.w, acc.w);
+            }
             if (complete) {
                 const int64_t to = ((int64_t)r * p.tokens + row / p.group) * p.hq + h * p.group + row % p.group;
-                p.out[to * D + d] = sum == 0.f ? 0.f : acc * (p.v_scale / sum);
-                if (p.lse && d == 0) p.lse[to] = sum == 0.f ? -INFINITY : (mx - kLift + log2f(sum)) * kLn2;
+                write_row(p, to * D + d, acc, mx, sum, d == 0 ? to : -1);
             } else {
-                p.ws_part[(ws_slot * 16 + row) * D + d] = acc;
-                if (d == 0) {
-                    p.ws_ml[(ws_slot * 16 + row) * 2] = mx;
-                    p.ws_ml[(ws_slot * 16 + row) * 2 + 1] = sum;
-                }
+                __stcg(reinterpret_cast<float4 *>(p.ws_part + (ws_row + row) * D + d), acc);
+                // a maximum of NaN: the part met a bad page id (its sums are not read)
+                if (d == 0) __stcg(reinterpret_cast<float2 *>(p.ws_ml) + ws_row + row, make_float2(bad ? NAN : mx, sum));
             }
         }
-        if (!complete) {
-            const int c0 = (int)(((u0 + 1) * ctas - 1) / total), c1 = (int)((u1 * ctas - 1) / total);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const int old = atomicAdd(p.ws_count + u, 1);
-                s_last = old == c1 - c0;
-                if (s_last) p.ws_count[u] = 0;
-            }
-            __syncthreads();
-            if (s_last) {
-                __threadfence();
-                for (int e = tid; e < r_rows * D; e += kThreads) {
-                    const int row = e / D, d = e % D;
-                    float mx = -INFINITY, sum = 0.f, acc = 0.f;
-#pragma unroll 8
-                    for (int c = c0; c <= c1; ++c)
-                        mx = fmaxf(mx, __ldcg(p.ws_ml + (((int64_t)c * 2 + (c == c0)) * 16 + row) * 2));
-#pragma unroll 8
-                    for (int c = c0; c <= c1; ++c) {
-                        const int64_t at_row = ((int64_t)c * 2 + (c == c0)) * 16 + row;
-                        const float mk = __ldcg(p.ws_ml + at_row * 2);
-                        const float w = mk == mx ? 1.f : fast_exp2(mk - mx);
-                        sum = fmaf(w, __ldcg(p.ws_ml + at_row * 2 + 1), sum);
-                        acc = fmaf(w, __ldcg(p.ws_part + at_row * D + d), acc);
+    }
+
+    // ---- units shared with other CTAs: the last of them to come here adds the parts up ----
+    __syncthreads();
+    if (tid < 2) {
+        const int u = s_open[tid];
+        int last = 0;
+        if (u >= 0) {
+            const int64_t u0 = s_open0[tid], u1 = u0 + (s_prefix[u / p.hkv + 1] - s_prefix[u / p.hkv]);
+            const int others = (int)(runs.owner(u1 - 1) / kWarps - runs.owner(u0) / kWarps);
+            // releases the CTA's part (ordered before it by the barrier) and acquires the others'
+            int old;
+            asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(p.ws_count + u) : "memory");
+            last = old == others;
+            if (last) p.ws_count[u] = 0;
+        }
+        s_last[tid] = last;
+    }
+    __syncthreads();
+    for (int side = 0; side < 2; ++side) {
+        if (!s_last[side]) continue;
+        const int u = s_open[side];
+        const int b = u / p.hkv, h = u - b * p.hkv;
+        const int r = request_id(p, b);
+        const int64_t u0 = s_open0[side], u1 = u0 + (s_prefix[b + 1] - s_prefix[b]);
+        const int c0 = (int)(runs.owner(u0) / kWarps), c1 = (int)(runs.owner(u1 - 1) / kWarps);
+        const int parts = c1 - c0 + 1;
+        // slot of part c: a unit lies in the second slot of the CTA it begins in, else in the first
+        auto row_at = [&](int c, int row) { return ((int64_t)(c0 + c) * 2 + (c == 0)) * kMaxRows + row; };
+        // a thread takes four dims of a row; where there are fewer such items than threads, `ways`
+        // threads share one, each with every ways-th part
+        const int items = p.rows * (D / 4);
+        const int ways = max(1, kThreads / items), wide = min(items, kThreads);
+        float2 *red_ml = reinterpret_cast<float2 *>(smem);
+        float4 *red = reinterpret_cast<float4 *>(smem + kThreads * 8);
+        for (int e0 = 0; e0 < items; e0 += kThreads) {
+            const int e = e0 + tid % wide, way = tid / wide;
+            const int row = e / (D / 4), d = e % (D / 4) * 4;
+            const bool busy = e < items && way < ways;
+            float mx = -INFINITY, sum = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            bool bad = false;
+            auto add = [&](float m, float v, const float4 &x) {  // weight 2^(m - mx)
+                const float w = m == mx ? 1.f : fast_exp2(m - mx);
+                sum = fmaf(w, v, sum);
+                acc.x = fmaf(w, x.x, acc.x);
+                acc.y = fmaf(w, x.y, acc.y);
+                acc.z = fmaf(w, x.z, acc.z);
+                acc.w = fmaf(w, x.w, acc.w);
+            };
+            auto raise = [&](float m) {
+                const float now = fmaxf(mx, m), w = mx == now ? 1.f : fast_exp2(mx - now);
+                mx = now;
+                sum *= w;
+                acc.x *= w;
+                acc.y *= w;
+                acc.z *= w;
+                acc.w *= w;
+            };
+            constexpr int kBatch = 8;  // parts in flight
+            for (int c = way; c < parts && busy; c += ways * kBatch) {
+                float2 y[kBatch];
+                float4 x[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int k = c + i * ways;
+                    y[i] = make_float2(-INFINITY, 0.f);
+                    x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (k < parts) {
+                        y[i] = __ldcg(reinterpret_cast<const float2 *>(p.ws_ml) + row_at(k, row));
+                        x[i] = __ldcg(reinterpret_cast<const float4 *>(p.ws_part + row_at(k, row) * D + d));
                     }
-                    const int64_t to = ((int64_t)r * p.tokens + row / p.group) * p.hq + h * p.group + row % p.group;
-                    p.out[to * D + d] = sum == 0.f ? 0.f : acc * (p.v_scale / sum);
-                    if (p.lse && d == 0) p.lse[to] = sum == 0.f ? -INFINITY : (mx - kLift + log2f(sum)) * kLn2;
                 }
+                float top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    bad |= isnan(y[i].x);
+                    top = fmaxf(top, y[i].x);
+                }
+                raise(top);
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) add(y[i].x, y[i].y, x[i]);
             }
-            __syncthreads();
+            if (ways > 1) {
+                __syncthreads();
+                red_ml[tid] = make_float2(bad ? NAN : mx, sum);
+                red[tid] = acc;
+                __syncthreads();
+                if (way == 0)
+                    for (int k = 1; k < ways; ++k) {
+                        const float2 y = red_ml[k * wide + e];
+                        bad |= isnan(y.x);
+                        raise(y.x);
+                        add(y.x, y.y, red[k * wide + e]);
+                    }
+            }
+            if (busy && way == 0 && !bad) {
+                const int64_t to = ((int64_t)r * p.tokens + row / p.group) * p.hq + h * p.group + row % p.group;
+                write_row(p, to * D + d, acc, mx, sum, d == 0 ? to : -1);
+            }
         }
-        i = end;
     }
 }
 
 namespace {
 
-template <int D, int NT, int MODE>
+template <int D, int ROWS, int MODE>
 cudaError_t launch_one(const Kv4AttnParams &p, int ctas, cudaStream_t stream) {
-    auto kernel = kv4_attn_kernel<D, NT, MODE>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Tile<D, NT>::kSmem);
+    auto kernel = kv4_attn_kernel<D, ROWS, MODE>;
+    // The shared-memory opt-in is a per-device function attribute: set it once per device.
+    static std::atomic<uint64_t> configured{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    kernel<<<ctas, kThreads, Tile<D, NT>::kSmem, stream>>>(p);
-    return cudaGetLastError();
+    const uint64_t bit = (dev >= 0 && dev < 64) ? (uint64_t(1) << dev) : 0;
+    if (!bit || !(configured.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Tile<D, ROWS>::kSmem);
+        if (e != cudaSuccess) return e;
+        configured.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    return launch_dependent(kernel, ctas, kThreads, Tile<D, ROWS>::kSmem, stream, p);
 }
 
-template <int D, int NT>
+template <int D, int ROWS>
 cudaError_t launch_mode(const Kv4AttnParams &p, int ctas, cudaStream_t stream) {
-    if (p.c_pool) return launch_one<D, NT, kKv4Fast>(p, ctas, stream);
-    return p.scores ? launch_one<D, NT, kKv4Scores>(p, ctas, stream) : launch_one<D, NT, kKv4Dense>(p, ctas, stream);
+    if (p.c_pool) return launch_one<D, ROWS, kKv4Fast>(p, ctas, stream);
+    return p.scores ? launch_one<D, ROWS, kKv4Scores>(p, ctas, stream)
+                    : launch_one<D, ROWS, kKv4Dense>(p, ctas, stream);
+}
+
+template <int D>
+cudaError_t launch_rows(const Kv4AttnParams &p, int sms, cudaStream_t stream) {
+    // one wave: two CTAs per SM for up to eight rows, one for up to sixteen (registers)
+    const int two = std::min(sms * kKv4CtasPerSm, kKv4MaxCtas), one = std::min(sms, kKv4MaxCtas);
+    if (p.rows <= 4) return launch_mode<D, 4>(p, two, stream);
+    return p.rows <= 8 ? launch_mode<D, 8>(p, two, stream) : launch_mode<D, 16>(p, one, stream);
 }
 
 }  // namespace
@@ -831,11 +1023,7 @@ cudaError_t launch_mode(const Kv4AttnParams &p, int ctas, cudaStream_t stream) {
 cudaError_t launch_kv4_attn(const Kv4AttnParams &p, int head_dim, cudaStream_t stream) {
     const int sms = sm_count_current_device();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    // one wave: two CTAs per SM for up to eight rows, one for up to sixteen (registers)
-    if (p.rows <= 8)
-        return head_dim == 128 ? launch_mode<128, 1>(p, sms * kKv4CtasPerSm, stream)
-                               : launch_mode<64, 1>(p, sms * kKv4CtasPerSm, stream);
-    return head_dim == 128 ? launch_mode<128, 2>(p, sms, stream) : launch_mode<64, 2>(p, sms, stream);
+    return head_dim == 128 ? launch_rows<128>(p, sms, stream) : launch_rows<64>(p, sms, stream);
 }
 
 }  // namespace sfi

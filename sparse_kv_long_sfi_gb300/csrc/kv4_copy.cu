@@ -54,8 +54,8 @@ __device__ void write_block(uint8_t *block, Kv4Tile<D> &tile, const __nv_bfloat1
         const bool in = row < b;
         int4 kr = make_int4(0, 0, 0, 0), vr = kr;
         if (in) {
-            kr = ld_nc_v4(ks + (int64_t)(row - a) * stride + l * 8);
-            vr = ld_nc_v4(vs + (int64_t)(row - a) * stride + l * 8);
+            kr = ld_stream_v4(ks + (int64_t)(row - a) * stride + l * 8);
+            vr = ld_stream_v4(vs + (int64_t)(row - a) * stride + l * 8);
         }
         uint32_t sk, sv;
         const uint32_t ck = quantise8(kr, 6.f * k_scale, k_scale, &sk);
@@ -109,6 +109,8 @@ __global__ void __launch_bounds__(kKv4Warps * 32) kv4_append_kernel(const Kv4Cop
     __shared__ Kv4Tile<D> s_tile[kKv4Warps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t items = (int64_t)batch * page_slots * p.hkv;
+    grid_launch_dependents();
+    grid_dependency_wait();
     for (int64_t item = (int64_t)blockIdx.x * kKv4Warps + warp; item < items;
          item += (int64_t)gridDim.x * kKv4Warps) {
         const int h = (int)(item % p.hkv);
@@ -147,7 +149,7 @@ __device__ void read_block(const uint8_t *block, Kv4Tile<D> &tile, __nv_bfloat16
     // V codes as they lie (D / 2 units of 16 bytes), V scales by token
     int4 *raw = reinterpret_cast<int4 *>(&tile.code[0][0]);
 #pragma unroll
-    for (int u = lane; u < D / 2; u += 32) raw[u] = ld_nc_v4(block + F::kVCode + u * 16);
+    for (int u = lane; u < D / 2; u += 32) raw[u] = ld_stream_v4(block + F::kVCode + u * 16);
     for (int i = lane; i < 16 * F::kGroups; i += 32)
         tile.scale[i & 3 | (i / (4 * F::kGroups)) << 2][(i / 4) % F::kGroups] = block[F::kVScale + i];
     __syncwarp();
@@ -194,6 +196,8 @@ __global__ void __launch_bounds__(kKv4Warps * 32) kv4_read_kernel(const Kv4CopyP
     __shared__ __align__(16) Kv4Tile<D> s_tile[kKv4Warps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t items = (int64_t)batch * page_slots * p.hkv;
+    grid_launch_dependents();
+    grid_dependency_wait();
     for (int64_t item = (int64_t)blockIdx.x * kKv4Warps + warp; item < items;
          item += (int64_t)gridDim.x * kKv4Warps) {
         const int h = (int)(item % p.hkv);
@@ -229,6 +233,8 @@ __global__ void __launch_bounds__(kKv4Warps * 32) kv4_compact_kernel(const Kv4Co
     using F = Kv4<D>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t items = (int64_t)batch * slots * p.hkv;
+    grid_launch_dependents();
+    grid_dependency_wait();
     for (int64_t item = (int64_t)blockIdx.x * kKv4Warps + warp; item < items;
          item += (int64_t)gridDim.x * kKv4Warps) {
         const int h = (int)(item % p.hkv);
@@ -274,7 +280,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32) kv4_compact_kernel(const Kv4Co
             const int64_t s = __shfl_sync(0xffffffffu, src, row);
             const int sl = __shfl_sync(0xffffffffu, slot, row);
             int4 v = make_int4(0, 0, 0, 0);
-            if (s >= 0) v = ld_nc_v4(p.pool + s + sl * F::kKRow + piece * 16);
+            if (s >= 0) v = ld_stream_v4(p.pool + s + sl * F::kKRow + piece * 16);
             st_v4(dst + row * F::kKRow + piece * 16, v);
         }
         {  // two lanes per row: half of its scales each
@@ -301,7 +307,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32) kv4_compact_kernel(const Kv4Co
                 const int sl = __shfl_sync(0xffffffffu, slot, 4 * x.t + q);
                 if (s >= 0) {
                     // the same dims of the source token's group of four
-                    const int4 w = ld_nc_v4(p.pool + s + F::kVCode + (u - 2 * x.t + 2 * (sl >> 2)) * 16);
+                    const int4 w = ld_stream_v4(p.pool + s + F::kVCode + (u - 2 * x.t + 2 * (sl >> 2)) * 16);
                     const int from = 16 * ((sl >> 1) & 1) + 4 * (sl & 1), to = 16 * (q >> 1) + 4 * (q & 1);
                     const uint32_t ww[4] = {(uint32_t)w.x, (uint32_t)w.y, (uint32_t)w.z, (uint32_t)w.w};
 #pragma unroll
@@ -339,31 +345,22 @@ int copy_grid(int64_t items) {
 cudaError_t launch_kv4_append(const Kv4CopyParams &p, int head_dim, int batch, cudaStream_t stream) {
     const int slots = (int)(((int64_t)p.tokens + 30) / 16);  // pages that `tokens` positions can touch
     const int grid = copy_grid((int64_t)batch * slots * p.hkv);
-    if (head_dim == 128)
-        kv4_append_kernel<128><<<grid, kKv4Warps * 32, 0, stream>>>(p, batch, slots);
-    else
-        kv4_append_kernel<64><<<grid, kKv4Warps * 32, 0, stream>>>(p, batch, slots);
-    return cudaGetLastError();
+    return launch_dependent(head_dim == 128 ? kv4_append_kernel<128> : kv4_append_kernel<64>, grid, kKv4Warps * 32, 0, stream,
+                            p, batch, slots);
 }
 
 cudaError_t launch_kv4_read(const Kv4CopyParams &p, int head_dim, int batch, cudaStream_t stream) {
     const int slots = (int)(((int64_t)p.tokens + 30) / 16);
     const int grid = copy_grid((int64_t)batch * slots * p.hkv);
-    if (head_dim == 128)
-        kv4_read_kernel<128><<<grid, kKv4Warps * 32, 0, stream>>>(p, batch, slots);
-    else
-        kv4_read_kernel<64><<<grid, kKv4Warps * 32, 0, stream>>>(p, batch, slots);
-    return cudaGetLastError();
+    return launch_dependent(head_dim == 128 ? kv4_read_kernel<128> : kv4_read_kernel<64>, grid, kKv4Warps * 32, 0, stream,
+                            p, batch, slots);
 }
 
 cudaError_t launch_kv4_compact(const Kv4CopyParams &p, int head_dim, int batch, cudaStream_t stream) {
     const int slots = (p.sink + p.k_cap + 15) / 16;
     const int grid = copy_grid((int64_t)batch * slots * p.hkv);
-    if (head_dim == 128)
-        kv4_compact_kernel<128><<<grid, kKv4Warps * 32, 0, stream>>>(p, batch, slots);
-    else
-        kv4_compact_kernel<64><<<grid, kKv4Warps * 32, 0, stream>>>(p, batch, slots);
-    return cudaGetLastError();
+    return launch_dependent(head_dim == 128 ? kv4_compact_kernel<128> : kv4_compact_kernel<64>, grid, kKv4Warps * 32, 0, stream,
+                            p, batch, slots);
 }
 
 }  // namespace sfi

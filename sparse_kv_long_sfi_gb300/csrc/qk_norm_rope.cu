@@ -50,6 +50,8 @@ __global__ void __launch_bounds__(kNormWarps * 32) qk_norm_rope_kernel(const Nor
     // the lane that holds the other member of this lane's pairs (split halves)
     const int mate = p.interleaved || !rotated ? lane : (l * 8 < half ? lane + half / 8 : lane - half / 8);
     const bool second = l * 8 >= half;
+    grid_launch_dependents();
+    grid_dependency_wait();
 
     for (int64_t item = (int64_t)blockIdx.x * kNormWarps + warp; item < items; item += (int64_t)gridDim.x * kNormWarps) {
         const int64_t tok = item / chunks;
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(kNormWarps * 32) qk_norm_rope_kernel(const Nor
                 if (w) {
                     const float rs = rsqrtf(ss * (1.f / D) + p.eps);
                     float wf[8];
-                    unpack8(__ldg(reinterpret_cast<const int4 *>(w + l * 8)), wf);
+                    unpack8(*reinterpret_cast<const int4 *>(w + l * 8), wf);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) x[i] = x[i] * rs * wf[i];
                 }
@@ -191,11 +193,8 @@ cudaError_t launch_qk_norm_rope(const NormRopeParams &p, int head_dim, int batch
     const int chunks = (rows + rows_per_item - 1) / rows_per_item;
     const int64_t ctas = (tokens * chunks + kNormWarps - 1) / kNormWarps;
     const int grid = (int)std::min<int64_t>(ctas, (int64_t)sms * 64);
-    if (head_dim == 128)
-        qk_norm_rope_kernel<128><<<grid, kNormWarps * 32, 0, stream>>>(p, batch, rows_per_item, chunks);
-    else
-        qk_norm_rope_kernel<64><<<grid, kNormWarps * 32, 0, stream>>>(p, batch, rows_per_item, chunks);
-    return cudaGetLastError();
+    return launch_dependent(head_dim == 128 ? qk_norm_rope_kernel<128> : qk_norm_rope_kernel<64>, grid, kNormWarps * 32,
+                            0, stream, p, batch, rows_per_item, chunks);
 }
 
 }  // namespace sfi

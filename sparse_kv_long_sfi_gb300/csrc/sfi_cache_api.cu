@@ -1,5 +1,6 @@
 // C ABI of the cache-side operators (declared in include/sfi.h): argument validation and
 // kernel dispatch. Allocates nothing.
+#include <algorithm>
 #include <cmath>
 
 #include "sfi_internal.h"
@@ -55,7 +56,8 @@ struct Kv4Workspace {
 };
 
 Kv4Workspace kv4_workspace(const sfi_attn_shape *shape) {
-    const size_t slots = (size_t)sfi::sm_count_current_device() * sfi::kKv4CtasPerSm * 2 * sfi::kMaxRows;
+    const int ctas = std::min(sfi::sm_count_current_device() * sfi::kKv4CtasPerSm, sfi::kKv4MaxCtas);
+    const size_t slots = (size_t)ctas * 2 * sfi::kMaxRows;
     Kv4Workspace w{};
     w.ml = ((size_t)sfi::kKv4MaxBatch * shape->num_kv_heads * 4 + 255) / 256 * 256;
     w.part = w.ml + slots * 2 * 4;
@@ -75,6 +77,8 @@ sfi_status kv4_attention(const sfi_attn_shape *shape, const sfi_paged_kv4 *kv, c
         return SFI_ERR_INVALID_ARG;
     const int group = shape->num_q_heads / shape->num_kv_heads;
     if (num_tokens * group > sfi::kMaxRows) return SFI_ERR_UNSUPPORTED;
+    // a warp counts its blocks in 32 bits
+    if ((int64_t)shape->num_kv_heads * kv->max_pages_per_req >= (int64_t(1) << 31)) return SFI_ERR_UNSUPPORTED;
     if (batch == 0) return SFI_OK;
     const Kv4Workspace w = kv4_workspace(shape);
     if (!workspace || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))

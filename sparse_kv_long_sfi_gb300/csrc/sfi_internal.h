@@ -219,10 +219,10 @@ struct Kv4AttnParams {
     float *ws_part;     // [CTAs][2][16 rows][D]
     int32_t *dev_status;
 };
-// Requests of one launch (their page counts' prefix lies in shared memory) and the CTAs of
-// the largest launch on a device of `sms` SMs.
+// Requests of one launch (their page counts' prefix lies in shared memory), and CTAs of one.
 constexpr int kKv4MaxBatch = 512;
 constexpr int kKv4CtasPerSm = 2;
+constexpr int kKv4MaxCtas = 512;
 cudaError_t launch_kv4_attn(const Kv4AttnParams &p, int head_dim, cudaStream_t stream);
 
 }  // namespace sfi
