@@ -86,6 +86,7 @@ typedef enum {
 #define SFI_DEV_BAD_INDEX 8u    /* a selected position outside [0, L) */
 #define SFI_DEV_TIMEOUT 16u     /* an in-kernel pipeline wait ran past its bound */
 #define SFI_DEV_BAD_COMPACT 32u /* compact rows of a request fall outside the buffer */
+#define SFI_DEV_NO_PAGE 64u     /* fewer free pages than a reservation needs */
 
 /* Launch flags of the attention entry points (bitwise OR). */
 /* SFI_ATTN_EARLY_KV_PREFETCH: the kernel that precedes this call on the stream does
@@ -114,6 +115,8 @@ typedef enum {
 /* Most query tokens per request in the multi-token calls (tokens x G must also be
  * <= 16: G = 2 allows 8 tokens, G = 4 four, G = 8 two). */
 #define SFI_MAX_QUERY_TOKENS 16
+/* Most requests in one sfi_page_reserve call. */
+#define SFI_MAX_PAGE_REQS 1024
 
 /* Attention geometry shared by all calls. */
 typedef struct {
@@ -617,6 +620,100 @@ SFI_API sfi_status sfi_kv4_fast_attn(const sfi_attn_shape *shape, const sfi_page
 /* Workspace bytes of the two 4-bit attention calls on the current device, valid for every
  * batch size 1..batch and every num_tokens up to the given one (0 on invalid input). */
 SFI_API size_t sfi_kv4_workspace_size(const sfi_attn_shape *shape, int32_t batch, int32_t num_tokens);
+
+/*
+ * Pages shared between requests. A page id names the same page in every pool of a cache
+ * (each layer's K and V, or the 4-bit pools). ref_count[p] says how many requests hold
+ * page p (0: free); request r holds the pages page_table[r][0 .. (seq_lens[r] + 15) / 16).
+ * The calls keep all state on the device, and their results do not depend on the order in
+ * which the GPU runs them: free pages are handed out lowest id first.
+ */
+typedef struct {
+    int32_t *page_table;       /* int32 [num_reqs][max_pages_per_req] */
+    int32_t *seq_lens;         /* int32 [num_reqs] */
+    int32_t *ref_count;        /* int32 [num_pages] */
+    int32_t num_reqs;
+    int32_t max_pages_per_req;
+    int32_t num_pages;
+    int32_t page_size;         /* 16 */
+} sfi_page_map;
+
+typedef struct {
+    void *const *pools;  /* device array of num_pools device pointers, each 16-byte aligned */
+    int32_t num_pools;
+    int64_t page_bytes;  /* bytes of a page in each pool, a multiple of 16 */
+    int32_t num_pages;   /* pages of each pool */
+} sfi_page_pools;
+
+/*
+ * sfi_page_copy - page src[i] -> page dst[i] in every pool, i < n. No page may be a
+ * destination twice, or both a source and a destination.
+ * Device errors: SFI_DEV_BAD_PAGE (that pair is skipped).
+ */
+SFI_API sfi_status sfi_page_copy(const sfi_page_pools *pools, const int32_t *src, const int32_t *dst, int32_t n,
+                                 int32_t *dev_status, void *stream);
+
+/*
+ * sfi_page_fork - request dst[i] becomes a branch of request src[i]: it holds the pages of
+ * the first fork_lens[i] tokens (NULL: all of them), and its length is that. No page is
+ * copied; sfi_page_reserve copies what a branch is about to write. What dst[i] held before
+ * is not released: free it first. A request may be the source of many branches, but the
+ * destination of one, and not both.
+ * Device errors: SFI_DEV_BAD_INDEX (a request id out of range, or src[i] == dst[i]),
+ * SFI_DEV_BAD_LEN (a length out of range), SFI_DEV_BAD_PAGE (the source holds an id out of
+ * range): that branch is skipped.
+ */
+SFI_API sfi_status sfi_page_fork(const sfi_page_map *map, const int32_t *src, const int32_t *dst,
+                                 const int32_t *fork_lens, int32_t n, int32_t *dev_status, void *stream);
+
+/*
+ * sfi_page_reserve - room for the next append: request reqs[i] (reqs NULL: request i) grows
+ * to new_lens[i] >= its length, its part-filled last page becomes its own (when others hold
+ * it too, it is copied in every pool to a free page; of the holders in one call the last
+ * in the list keeps the original if nobody else holds it), and free pages are taken for the
+ * rest. Pages are handed out in the order of the list, then of positions, lowest id first.
+ *   pools     : may be NULL when no request's last page is shared
+ *   workspace : sfi_page_workspace_size(map) bytes, 16-byte aligned; no initial contents;
+ *               launches sharing it must not overlap
+ * n <= SFI_MAX_PAGE_REQS; a request may appear once. All or nothing: when a request is
+ * refused or the free pages do not suffice, nothing changes.
+ * Device errors: SFI_DEV_BAD_INDEX, SFI_DEV_BAD_LEN, SFI_DEV_BAD_PAGE, SFI_DEV_NO_PAGE.
+ */
+SFI_API sfi_status sfi_page_reserve(const sfi_page_map *map, const sfi_page_pools *pools, const int32_t *new_lens,
+                                    const int32_t *reqs, int32_t n, void *workspace, size_t workspace_bytes,
+                                    int32_t *dev_status, void *stream);
+
+/*
+ * sfi_page_free - request reqs[i] lets go of its pages (pages nobody holds are free again)
+ * and has length 0. A request named twice lets go of them once.
+ * Device errors: SFI_DEV_BAD_INDEX, SFI_DEV_BAD_LEN (that request is skipped),
+ * SFI_DEV_BAD_PAGE (an id out of range, or a page with no holder left: that page is
+ * skipped).
+ */
+SFI_API sfi_status sfi_page_free(const sfi_page_map *map, const int32_t *reqs, int32_t n, int32_t *dev_status,
+                                 void *stream);
+
+/*
+ * sfi_page_compact - the live pages move to the front of the pools: with N pages held, the
+ * j-th held page with an id >= N moves to the j-th free id below N, in every pool. The new
+ * table and counts are written beside the old ones, which stay valid for reads already on
+ * their way (only free pages are overwritten) until the caller changes over; whoever takes
+ * pages in between must use the new ones. Table entries behind a request's length are
+ * copied as they are.
+ *   table_out : int32 [num_reqs][max_pages_per_req];  ref_out : int32 [num_pages]
+ *   live_out  : int32 [1], N
+ *   workspace : sfi_page_workspace_size(map) bytes, 16-byte aligned; no initial contents;
+ *               launches sharing it must not overlap
+ * table_out and ref_out must not be the map's own arrays.
+ * Device errors: SFI_DEV_BAD_LEN, SFI_DEV_BAD_PAGE (entries that are out of range are copied
+ * as they are).
+ */
+SFI_API sfi_status sfi_page_compact(const sfi_page_map *map, const sfi_page_pools *pools, int32_t *table_out,
+                                    int32_t *ref_out, int32_t *live_out, void *workspace, size_t workspace_bytes,
+                                    int32_t *dev_status, void *stream);
+
+/* Workspace bytes of sfi_page_reserve and sfi_page_compact (0 on invalid input). */
+SFI_API size_t sfi_page_workspace_size(const sfi_page_map *map);
 
 /* Human-readable name of a status code (static string). */
 SFI_API const char *sfi_status_string(sfi_status status);

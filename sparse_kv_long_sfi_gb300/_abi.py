@@ -43,18 +43,30 @@ class sfi_compact_kv4(ctypes.Structure):
     _fields_ = [("pool", c_vp), ("total_pages", c_i64), ("page_offset", c_vp), ("capacity", c_vp), ("count", c_vp)]
 
 
+class sfi_page_map(ctypes.Structure):
+    _fields_ = [("page_table", c_vp), ("seq_lens", c_vp), ("ref_count", c_vp), ("num_reqs", c_i32),
+                ("max_pages_per_req", c_i32), ("num_pages", c_i32), ("page_size", c_i32)]
+
+
+class sfi_page_pools(ctypes.Structure):
+    _fields_ = [("pools", c_vp), ("num_pools", c_i32), ("page_bytes", c_i64), ("num_pages", c_i32)]
+
+
 SFI_OK, SFI_ERR_INVALID_ARG, SFI_ERR_UNSUPPORTED, SFI_ERR_WORKSPACE, SFI_ERR_CUDA = range(5)
 SFI_DEV_BAD_PAGE, SFI_DEV_BAD_LEN, SFI_DEV_K_OVERFLOW = 1, 2, 4
-SFI_DEV_BAD_INDEX, SFI_DEV_TIMEOUT, SFI_DEV_BAD_COMPACT = 8, 16, 32
+SFI_DEV_BAD_INDEX, SFI_DEV_TIMEOUT, SFI_DEV_BAD_COMPACT, SFI_DEV_NO_PAGE = 8, 16, 32, 64
 SFI_ATTN_EARLY_KV_PREFETCH = 1
 SFI_ATTN_RAGGED = 2
 SFI_ATTN_TEST_WITHHOLD = 4
 SFI_MAX_QUERY_TOKENS = 16
+SFI_MAX_PAGE_REQS = 1024
 
 P_SHAPE = ctypes.POINTER(sfi_attn_shape)
 P_PAGED = ctypes.POINTER(sfi_paged_kv)
 P_COMPACT = ctypes.POINTER(sfi_compact_kv)
 P_ROPE = ctypes.POINTER(sfi_rope)
+P_MAP = ctypes.POINTER(sfi_page_map)
+P_POOLS = ctypes.POINTER(sfi_page_pools)
 P_KV4 = ctypes.POINTER(sfi_paged_kv4)
 P_COMPACT4 = ctypes.POINTER(sfi_compact_kv4)
 
@@ -96,6 +108,12 @@ PROTOTYPES = {
     "sfi_kv4_fast_attn": (c_i32, [P_SHAPE, P_KV4, P_COMPACT4, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp, c_vp, c_i32, c_vp,
                                   c_sz, c_vp, c_vp]),
     "sfi_kv4_workspace_size": (c_sz, [P_SHAPE, c_i32, c_i32]),
+    "sfi_page_copy": (c_i32, [P_POOLS, c_vp, c_vp, c_i32, c_vp, c_vp]),
+    "sfi_page_fork": (c_i32, [P_MAP, c_vp, c_vp, c_vp, c_i32, c_vp, c_vp]),
+    "sfi_page_reserve": (c_i32, [P_MAP, P_POOLS, c_vp, c_vp, c_i32, c_vp, c_sz, c_vp, c_vp]),
+    "sfi_page_free": (c_i32, [P_MAP, c_vp, c_i32, c_vp, c_vp]),
+    "sfi_page_compact": (c_i32, [P_MAP, P_POOLS, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp, c_vp]),
+    "sfi_page_workspace_size": (c_sz, [P_MAP]),
     "sfi_status_string": (ctypes.c_char_p, [c_i32]),
     "sfi_version": (c_i32, []),
 }

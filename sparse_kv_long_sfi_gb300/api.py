@@ -19,6 +19,7 @@ from . import _abi
 
 SFI_ATTN_EARLY_KV_PREFETCH = _abi.SFI_ATTN_EARLY_KV_PREFETCH
 SFI_MAX_QUERY_TOKENS = _abi.SFI_MAX_QUERY_TOKENS
+SFI_MAX_PAGE_REQS = _abi.SFI_MAX_PAGE_REQS
 SFI_ATTN_RAGGED = _abi.SFI_ATTN_RAGGED
 SFI_ATTN_TEST_WITHHOLD = _abi.SFI_ATTN_TEST_WITHHOLD
 
@@ -577,6 +578,111 @@ def sfi_kv4_workspace_size(shape: AttnShape, batch: int, num_tokens: int = 1) ->
 def alloc_kv4_workspace(shape: AttnShape, batch: int, num_tokens: int = 1, device="cuda") -> torch.Tensor:
     """A zero-filled workspace of the 4-bit attention calls, valid for every batch size 1..batch."""
     return torch.zeros(max(256, sfi_kv4_workspace_size(shape, batch, num_tokens)), dtype=torch.uint8, device=device)
+
+
+@dataclass
+class PageMap:
+    """Who holds which page: page_table int32 [num_reqs][max_pages], seq_lens int32 [num_reqs],
+    ref_count int32 [num_pages] (holders of each page)."""
+    page_table: torch.Tensor
+    seq_lens: torch.Tensor
+    ref_count: torch.Tensor
+
+    def c(self) -> _abi.sfi_page_map:
+        _need(self.page_table, torch.int32, "page_table")
+        _need(self.seq_lens, torch.int32, "seq_lens")
+        _need(self.ref_count, torch.int32, "ref_count")
+        _on_current_device(self.page_table, "page_table")
+        dims = self.page_table.shape
+        if len(dims) != 2 or self.seq_lens.numel() != dims[0]:
+            raise ValueError("page_table must be [num_reqs][max_pages], seq_lens [num_reqs]")
+        return _abi.sfi_page_map(self.page_table.data_ptr(), self.seq_lens.data_ptr(), self.ref_count.data_ptr(),
+                                 dims[0], dims[1], self.ref_count.numel(), 16)
+
+
+class PagePools:
+    """The pools of a cache whose pages share their ids: contiguous tensors [num_pages][...] of
+    one page size (each layer's k_pool and v_pool, or the 4-bit pools). Keeps the tensors and
+    a device array of their addresses."""
+
+    def __init__(self, pools):
+        if not pools:
+            raise ValueError("at least one pool is needed")
+        first = pools[0]
+        for t in pools:
+            _need(t, t.dtype, "pool")
+            if t.get_device() != first.get_device() or t.shape[0] != first.shape[0] or t.nbytes != first.nbytes:
+                raise ValueError("the pools need the same device, number of pages and page size")
+            if t.data_ptr() % 16:
+                raise ValueError("a pool must be 16-byte aligned")
+        self.pools = list(pools)
+        self.addresses = torch.tensor([t.data_ptr() for t in pools], dtype=torch.int64).to(first.device)
+        self._c = _abi.sfi_page_pools(self.addresses.data_ptr(), len(pools), first.nbytes // max(1, first.shape[0]),
+                                      first.shape[0])
+
+    def c(self) -> _abi.sfi_page_pools:
+        _on_current_device(self.addresses, "pools")
+        return self._c
+
+
+def sfi_page_copy(pools: PagePools, src: torch.Tensor, dst: torch.Tensor, dev_status: Optional[torch.Tensor] = None,
+                  stream=None):
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst need the same number of pages")
+    st = _abi.lib().sfi_page_copy(ctypes.byref(pools.c()), _ptr(src, torch.int32, "src"), _ptr(dst, torch.int32, "dst"),
+                                  src.numel(), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    _check(st, "sfi_page_copy")
+
+
+def sfi_page_fork(page_map: PageMap, src: torch.Tensor, dst: torch.Tensor, fork_lens: Optional[torch.Tensor] = None,
+                  dev_status: Optional[torch.Tensor] = None, stream=None):
+    if src.numel() != dst.numel() or (fork_lens is not None and fork_lens.numel() != src.numel()):
+        raise ValueError("src, dst and fork_lens need one entry per branch")
+    st = _abi.lib().sfi_page_fork(ctypes.byref(page_map.c()), _ptr(src, torch.int32, "src"),
+                                  _ptr(dst, torch.int32, "dst"), _ptr(fork_lens, torch.int32, "fork_lens"), src.numel(),
+                                  _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    _check(st, "sfi_page_fork")
+
+
+def sfi_page_reserve(page_map: PageMap, pools: Optional[PagePools], new_lens: torch.Tensor,
+                     reqs: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     dev_status: Optional[torch.Tensor] = None, stream=None):
+    if reqs is not None and reqs.numel() != new_lens.numel():
+        raise ValueError("reqs and new_lens need one entry per request")
+    st = _abi.lib().sfi_page_reserve(
+        ctypes.byref(page_map.c()), None if pools is None else ctypes.byref(pools.c()),
+        _ptr(new_lens, torch.int32, "new_lens"), _ptr(reqs, torch.int32, "reqs"), new_lens.numel(),
+        _ptr(workspace, torch.uint8, "workspace"), 0 if workspace is None else workspace.numel(),
+        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    _check(st, "sfi_page_reserve")
+
+
+def sfi_page_free(page_map: PageMap, reqs: torch.Tensor, dev_status: Optional[torch.Tensor] = None, stream=None):
+    st = _abi.lib().sfi_page_free(ctypes.byref(page_map.c()), _ptr(reqs, torch.int32, "reqs"), reqs.numel(),
+                                  _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    _check(st, "sfi_page_free")
+
+
+def sfi_page_compact(page_map: PageMap, pools: PagePools, table_out: torch.Tensor, ref_out: torch.Tensor,
+                     live_out: torch.Tensor, workspace: Optional[torch.Tensor] = None,
+                     dev_status: Optional[torch.Tensor] = None, stream=None):
+    if table_out.shape != page_map.page_table.shape or ref_out.numel() != page_map.ref_count.numel():
+        raise ValueError("table_out and ref_out need the shapes of page_table and ref_count")
+    st = _abi.lib().sfi_page_compact(
+        ctypes.byref(page_map.c()), ctypes.byref(pools.c()), _ptr(table_out, torch.int32, "table_out"),
+        _ptr(ref_out, torch.int32, "ref_out"), _ptr(live_out, torch.int32, "live_out"),
+        _ptr(workspace, torch.uint8, "workspace"), 0 if workspace is None else workspace.numel(),
+        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    _check(st, "sfi_page_compact")
+
+
+def sfi_page_workspace_size(page_map: PageMap) -> int:
+    return int(_abi.lib().sfi_page_workspace_size(ctypes.byref(page_map.c())))
+
+
+def alloc_page_workspace(page_map: PageMap) -> torch.Tensor:
+    """A workspace of sfi_page_reserve and sfi_page_compact for this map."""
+    return torch.empty(sfi_page_workspace_size(page_map), dtype=torch.uint8, device=page_map.ref_count.device)
 
 
 def sfi_workspace_size(shape: AttnShape, batch: int, max_tokens: int, num_splits: int = 0) -> int:

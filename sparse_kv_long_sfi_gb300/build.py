@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libsfi.so")
 SOURCES = ["attn_decode.cu", "attn_multi.cu", "select_topk.cu", "kv_copy.cu", "sfi_api.cu", "attn_noalloc.cu",
-           "sfi_cache_api.cu", "qk_norm_rope.cu", "kv4_copy.cu", "attn_kv4.cu"]
+           "sfi_cache_api.cu", "qk_norm_rope.cu", "kv4_copy.cu", "attn_kv4.cu", "page_ops.cu"]
 HEADERS = ["attn_kernel.cuh", "kv4_format.cuh", "sfi_device.cuh", "sfi_internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

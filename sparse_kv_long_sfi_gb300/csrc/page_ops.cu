@@ -1,0 +1,382 @@
+// Pages shared between requests: copying, forking, reserving (copy on write), freeing and
+// compacting. All state (page table, lengths, a holder count per page) is on the device.
+//
+// Planning is integer work on small arrays and is done where its result cannot depend on
+// the order of threads: counts change by atomic additions alone, free pages are found by
+// one CTA that scans the counts in page order (ranks by prefix sums), and lists are
+// written at those ranks. The bytes move in a second launch that reads the list's length
+// on the device; it is bound by HBM (a page is read and written once per pool).
+#include <algorithm>
+
+#include "sfi_device.cuh"
+#include "sfi_internal.h"
+
+namespace sfi {
+
+namespace {
+
+constexpr int kPageThreads = 256;
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kCopyChunk = 8192;  // bytes of a pool's page that a CTA moves at once
+
+// Workspace (int32): [0] moves, [1] unused .. [3], then the moves' sources, their
+// destinations (num_pages each), and the free or new page ids (num_pages).
+struct PageLists {
+    int32_t *moves, *src, *dst, *ids;
+    __host__ __device__ PageLists(void *ws, int32_t num_pages)
+        : moves(static_cast<int32_t *>(ws)), src(moves + 4), dst(src + num_pages), ids(dst + num_pages) {}
+};
+
+// Exclusive sum over the CTA's threads; *total receives the whole.
+__device__ __forceinline__ int block_scan(int v, int *s_warp, int *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
+    }
+    __syncthreads();  // the last round's sums have been read
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int w = lane < kPlanWarps ? s_warp[lane] : 0;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, w, off);
+        if (lane >= off) w += o;
+    }
+    *total = __shfl_sync(0xffffffffu, w, 31);
+    const int before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+    return (warp ? before : 0) + incl - v;
+}
+
+__device__ __forceinline__ int pages_of(int len) { return (len + kSubTokens - 1) / kSubTokens; }
+
+}  // namespace
+
+// ---- copy: page src[i] -> dst[i] of every pool, in chunks ------------------------------
+__global__ void __launch_bounds__(kPageThreads) page_copy_kernel(void *const *pools, int num_pools, int64_t page_bytes,
+                                                                 int num_pages, const int32_t *src, const int32_t *dst,
+                                                                 int n_host, const int32_t *n_dev,
+                                                                 int32_t *dev_status) {
+    constexpr int kLoads = kCopyChunk / 16 / kPageThreads;
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int n = n_dev ? *n_dev : n_host;
+    const int chunks = (int)((page_bytes + kCopyChunk - 1) / kCopyChunk);
+    const int64_t items = (int64_t)n * num_pools * chunks;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int chunk = (int)(item % chunks);
+        const int64_t at = item / chunks;
+        const int pool = (int)(at % num_pools), i = (int)(at / num_pools);
+        const int a = src[i], z = dst[i];
+        if (a < 0 || a >= num_pages || z < 0 || z >= num_pages) {
+            if (threadIdx.x == 0) report(dev_status, SFI_DEV_BAD_PAGE);
+            continue;
+        }
+        uint8_t *base = static_cast<uint8_t *>(pools[pool]);
+        const int64_t off = (int64_t)chunk * kCopyChunk + threadIdx.x * 16;
+        const uint8_t *from = base + a * page_bytes;
+        uint8_t *to = base + z * page_bytes;
+        int4 v[kLoads];
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k)
+            if (off + k * kPageThreads * 16 < page_bytes) v[k] = ld_stream_v4(from + off + k * kPageThreads * 16);
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k)
+            if (off + k * kPageThreads * 16 < page_bytes) st_v4(to + off + k * kPageThreads * 16, v[k]);
+    }
+}
+
+// ---- fork and free: one CTA per request -------------------------------------------------
+__global__ void __launch_bounds__(kPageThreads) page_fork_kernel(const PageMapParams m, const int32_t *src,
+                                                                 const int32_t *dst, const int32_t *fork_lens,
+                                                                 int32_t *dev_status) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int a = src[blockIdx.x], z = dst[blockIdx.x];
+    uint32_t err = 0;
+    int len = 0;
+    if (a < 0 || a >= m.num_reqs || z < 0 || z >= m.num_reqs || a == z) {
+        err = SFI_DEV_BAD_INDEX;
+    } else {
+        const int L = m.seq_lens[a];
+        len = fork_lens ? fork_lens[blockIdx.x] : L;
+        if (L < 0 || pages_of(L) > m.max_pages || len < 0 || len > L) err = SFI_DEV_BAD_LEN;
+    }
+    const int held = err ? 0 : pages_of(len);
+    const int32_t *from = m.page_table + (int64_t)a * m.max_pages;
+    bool out = false;
+    for (int i = threadIdx.x; i < held; i += kPageThreads) out |= (uint32_t)from[i] >= (uint32_t)m.num_pages;
+    if (__syncthreads_or(out)) err = SFI_DEV_BAD_PAGE;
+    if (err) {
+        if (threadIdx.x == 0) report(dev_status, err);
+        return;
+    }
+    int32_t *to = m.page_table + (int64_t)z * m.max_pages;
+    for (int i = threadIdx.x; i < held; i += kPageThreads) {
+        const int page = from[i];
+        to[i] = page;
+        atomicAdd(m.ref_count + page, 1);
+    }
+    if (threadIdx.x == 0) m.seq_lens[z] = len;
+}
+
+__global__ void __launch_bounds__(kPageThreads) page_free_kernel(const PageMapParams m, const int32_t *reqs,
+                                                                 int32_t *dev_status) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int r = reqs ? reqs[blockIdx.x] : blockIdx.x;
+    if (r < 0 || r >= m.num_reqs) {
+        if (threadIdx.x == 0) report(dev_status, SFI_DEV_BAD_INDEX);
+        return;
+    }
+    // the length is taken, so that a request named twice lets go of its pages once
+    __shared__ int s_len;
+    if (threadIdx.x == 0) {
+        s_len = atomicExch(m.seq_lens + r, 0);
+        if (s_len < 0 || pages_of(s_len) > m.max_pages) {
+            m.seq_lens[r] = s_len;
+            report(dev_status, SFI_DEV_BAD_LEN);
+            s_len = 0;
+        }
+    }
+    __syncthreads();
+    const int L = s_len;
+    const int32_t *row = m.page_table + (int64_t)r * m.max_pages;
+    const int held = pages_of(L);
+    for (int i = threadIdx.x; i < held; i += kPageThreads) {
+        const int page = row[i];
+        if (page < 0 || page >= m.num_pages) {
+            report(dev_status, SFI_DEV_BAD_PAGE);
+        } else if (atomicSub(m.ref_count + page, 1) <= 0) {
+            atomicAdd(m.ref_count + page, 1);  // nobody held it: as it was
+            report(dev_status, SFI_DEV_BAD_PAGE);
+        }
+    }
+}
+
+// ---- reserve: one CTA plans for all requests --------------------------------------------
+// Three passes: what each request needs (and whether its last page is its own), the lowest
+// free pages, and their distribution; then the copies of shared last pages are launched.
+__global__ void __launch_bounds__(kPlanThreads) page_reserve_kernel(const PageMapParams m, const int32_t *new_lens,
+                                                                    const int32_t *reqs, int n, int can_copy, void *ws,
+                                                                    int32_t *dev_status) {
+    __shared__ int s_warp[kPlanWarps];
+    __shared__ int s_last[kPlanThreads];   // part-filled last page of list entry i, or -1
+    __shared__ int s_first[kPlanThreads];  // rank of its first page among those handed out
+    __shared__ int s_req[kPlanThreads];
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const PageLists lists(ws, m.num_pages);
+    const int tid = threadIdx.x;
+    uint32_t err = 0;
+    int r = -1, len = 0, want = 0, last = -1, fresh = 0;
+    if (tid < n) {
+        r = reqs ? reqs[tid] : tid;
+        if (r < 0 || r >= m.num_reqs) {
+            err = SFI_DEV_BAD_INDEX;
+        } else {
+            len = m.seq_lens[r];
+            want = new_lens[tid];
+            if (len < 0 || want < len || (int64_t)want > (int64_t)m.max_pages * kSubTokens) {
+                err = SFI_DEV_BAD_LEN;
+            } else {
+                fresh = pages_of(want) - pages_of(len);
+                if (want > len && len % kSubTokens) {
+                    last = m.page_table[(int64_t)r * m.max_pages + len / kSubTokens];
+                    if (last < 0 || last >= m.num_pages) {
+                        err = SFI_DEV_BAD_PAGE;
+                        last = -1;
+                    }
+                }
+            }
+        }
+    }
+    s_last[tid] = last;
+    s_req[tid] = r;
+    if (tid == 0) lists.moves[0] = 0;
+    __syncthreads();
+    int before = 0;  // holders of the same last page that come earlier in the list
+    for (int i = 0; i < min(tid, n); ++i) {
+        before += last >= 0 && s_last[i] == last;
+        if (tid < n && !err && s_req[i] == r) err = SFI_DEV_BAD_INDEX;  // named twice
+    }
+    if (__syncthreads_or(err != 0)) {
+        if (err) report(dev_status, err);
+        return;
+    }
+    // a shared last page is copied, except by the last of its holders in the list when they
+    // are all there are
+    const bool copy = last >= 0 && m.ref_count[last] - before > 1;
+    int total = 0, copies = 0;
+    const int first = block_scan(fresh + copy, s_warp, &total);
+    const int move = block_scan(copy, s_warp, &copies);
+    s_first[tid] = first;
+    if (copies && !can_copy) {
+        if (tid == 0) report(dev_status, SFI_DEV_BAD_PAGE);
+        return;
+    }
+    // the `total` lowest free pages
+    int found = 0;
+    for (int base = 0; base < m.num_pages && found < total; base += kPlanThreads * 4) {
+        const int p0 = base + tid * 4;
+        int c[4], k = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            c[i] = p0 + i < m.num_pages ? m.ref_count[p0 + i] : 1;
+            k += c[i] == 0;
+        }
+        int here = 0;
+        int at = found + block_scan(k, s_warp, &here);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c[i] == 0) {
+                if (at < total) lists.ids[at] = p0 + i;
+                ++at;
+            }
+        found += here;
+    }
+    if (found < total) {
+        if (tid == 0) report(dev_status, SFI_DEV_NO_PAGE);
+        return;
+    }
+    __syncthreads();  // ids are written, counts are read
+    for (int i = tid; i < total; i += kPlanThreads) m.ref_count[lists.ids[i]] = 1;
+    if (tid < n) {
+        if (copy) {
+            lists.src[move] = last;
+            lists.dst[move] = lists.ids[first];
+            atomicSub(m.ref_count + last, 1);
+        }
+        m.seq_lens[r] = want;
+    }
+    if (tid == 0) lists.moves[0] = copies;
+    // table entries: a warp per request (entries [full pages, pages wanted) take the next ids)
+    for (int e = tid >> 5; e < n; e += kPlanWarps) {
+        const int rr = reqs ? reqs[e] : e;
+        const int before = e + 1 < n ? s_first[e + 1] : total;
+        const int have = before - s_first[e];
+        const int end = pages_of(new_lens[e]);
+        for (int i = tid & 31; i < have; i += 32)
+            m.page_table[(int64_t)rr * m.max_pages + end - have + i] = lists.ids[s_first[e] + i];
+    }
+}
+
+// ---- compact: one CTA pairs the live pages behind the first N with the holes before it ---
+__global__ void __launch_bounds__(kPlanThreads) page_compact_plan_kernel(const PageMapParams m, int32_t *ref_out,
+                                                                         int32_t *live_out, void *ws) {
+    __shared__ int s_warp[kPlanWarps];
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const PageLists lists(ws, m.num_pages);
+    const int tid = threadIdx.x;
+    int mine = 0;
+    for (int i = tid; i < m.num_pages; i += kPlanThreads) mine += m.ref_count[i] > 0;
+    int live = 0;
+    block_scan(mine, s_warp, &live);
+    // below N: holes in order; from N on: movers in order; there are as many of each
+    int holes = 0, movers = 0;
+    for (int base = 0; base < m.num_pages; base += kPlanThreads) {
+        const int i = base + tid;
+        const int c = i < m.num_pages ? m.ref_count[i] : 0;
+        const bool hole = i < live && c <= 0, mover = i >= live && i < m.num_pages && c > 0;
+        // both ranks in one scan: holes in the lower, movers in the upper half (at most 1024 of each)
+        int both = 0;
+        const int rank = block_scan((hole ? 1 : 0) | (mover ? 1 << 16 : 0), s_warp, &both);
+        if (hole) lists.dst[holes + (rank & 0xffff)] = i;
+        if (mover) lists.src[movers + (rank >> 16)] = i;
+        holes += both & 0xffff;
+        movers += both >> 16;
+        if (i < m.num_pages) {
+            lists.ids[i] = i;
+            ref_out[i] = mover ? 0 : c;
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < movers; i += kPlanThreads) {
+        lists.ids[lists.src[i]] = lists.dst[i];
+        ref_out[lists.dst[i]] = m.ref_count[lists.src[i]];
+    }
+    if (tid == 0) {
+        lists.moves[0] = movers;
+        *live_out = live;
+    }
+}
+
+__global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageMapParams m, int32_t *table_out, void *ws,
+                                                                  int32_t *dev_status) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const PageLists lists(ws, m.num_pages);
+    const int r = blockIdx.x;
+    const int L = m.seq_lens[r];
+    const bool fine = L >= 0 && pages_of(L) <= m.max_pages;
+    if (!fine && threadIdx.x == 0) report(dev_status, SFI_DEV_BAD_LEN);
+    const int held = fine ? pages_of(L) : 0;
+    for (int i = threadIdx.x; i < m.max_pages; i += kPageThreads) {
+        int page = m.page_table[(int64_t)r * m.max_pages + i];
+        if (i < held) {
+            if (page < 0 || page >= m.num_pages)
+                report(dev_status, SFI_DEV_BAD_PAGE);
+            else
+                page = lists.ids[page];
+        }
+        table_out[(int64_t)r * m.max_pages + i] = page;
+    }
+}
+
+namespace {
+
+cudaError_t launch_copy(const PagePoolParams &q, const int32_t *src, const int32_t *dst, int n, int most,
+                        const int32_t *n_dev, int32_t *dev_status, cudaStream_t stream) {
+    const int sms = sm_count_current_device();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    const int64_t chunks = (q.page_bytes + kCopyChunk - 1) / kCopyChunk;
+    const int64_t items = (int64_t)most * q.num_pools * chunks;
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(items, (int64_t)sms * 8));
+    return launch_dependent(page_copy_kernel, grid, kPageThreads, 0, stream, q.pools, q.num_pools, q.page_bytes,
+                            q.num_pages, src, dst, n, n_dev, dev_status);
+}
+
+}  // namespace
+
+size_t page_workspace_bytes(int32_t num_pages) { return ((size_t)num_pages * 3 + 4) * 4; }
+
+cudaError_t launch_page_copy(const PagePoolParams &q, const int32_t *src, const int32_t *dst, int n,
+                             int32_t *dev_status, cudaStream_t stream) {
+    return launch_copy(q, src, dst, n, n, nullptr, dev_status, stream);
+}
+
+cudaError_t launch_page_fork(const PageMapParams &m, const int32_t *src, const int32_t *dst, const int32_t *fork_lens,
+                             int n, int32_t *dev_status, cudaStream_t stream) {
+    return launch_dependent(page_fork_kernel, n, kPageThreads, 0, stream, m, src, dst, fork_lens, dev_status);
+}
+
+cudaError_t launch_page_free(const PageMapParams &m, const int32_t *reqs, int n, int32_t *dev_status,
+                             cudaStream_t stream) {
+    return launch_dependent(page_free_kernel, n, kPageThreads, 0, stream, m, reqs, dev_status);
+}
+
+cudaError_t launch_page_reserve(const PageMapParams &m, const PagePoolParams *q, const int32_t *new_lens,
+                                const int32_t *reqs, int n, void *ws, int32_t *dev_status, cudaStream_t stream) {
+    const cudaError_t e = launch_dependent(page_reserve_kernel, 1, kPlanThreads, 0, stream, m, new_lens, reqs, n,
+                                           q != nullptr ? 1 : 0, ws, dev_status);
+    if (e != cudaSuccess || !q) return e;
+    const PageLists lists(ws, m.num_pages);
+    return launch_copy(*q, lists.src, lists.dst, 0, n, lists.moves, dev_status, stream);
+}
+
+cudaError_t launch_page_compact(const PageMapParams &m, const PagePoolParams &q, int32_t *table_out, int32_t *ref_out,
+                                int32_t *live_out, void *ws, int32_t *dev_status, cudaStream_t stream) {
+    cudaError_t e = launch_dependent(page_compact_plan_kernel, 1, kPlanThreads, 0, stream, m, ref_out, live_out, ws);
+    const PageLists lists(ws, m.num_pages);
+    if (e == cudaSuccess)
+        e = launch_copy(q, lists.src, lists.dst, 0, m.num_pages / 2, lists.moves, dev_status, stream);
+    if (e == cudaSuccess && m.num_reqs > 0)
+        e = launch_dependent(page_table_kernel, m.num_reqs, kPageThreads, 0, stream, m, table_out, ws, dev_status);
+    return e;
+}
+
+}  // namespace sfi

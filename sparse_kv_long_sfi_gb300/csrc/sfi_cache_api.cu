@@ -126,6 +126,27 @@ sfi_status kv4_attention(const sfi_attn_shape *shape, const sfi_paged_kv4 *kv, c
     return SFI_OK;
 }
 
+sfi_status check_map(const sfi_page_map *m) {
+    if (!m || !m->page_table || !m->seq_lens || !m->ref_count) return SFI_ERR_INVALID_ARG;
+    if (m->num_reqs <= 0 || m->max_pages_per_req <= 0 || m->num_pages <= 0) return SFI_ERR_INVALID_ARG;
+    if (m->page_size != sfi::kSubTokens) return SFI_ERR_UNSUPPORTED;
+    if ((int64_t)m->max_pages_per_req * m->page_size >= (int64_t(1) << 31)) return SFI_ERR_UNSUPPORTED;
+    return SFI_OK;
+}
+
+sfi_status check_pools(const sfi_page_pools *q) {
+    if (!q || !q->pools || q->num_pools <= 0 || q->num_pages <= 0) return SFI_ERR_INVALID_ARG;
+    return q->page_bytes > 0 && q->page_bytes % 16 == 0 ? SFI_OK : SFI_ERR_INVALID_ARG;
+}
+
+sfi::PageMapParams map_params(const sfi_page_map *m) {
+    return {m->page_table, m->seq_lens, m->ref_count, m->num_reqs, m->max_pages_per_req, m->num_pages};
+}
+
+sfi::PagePoolParams pool_params(const sfi_page_pools *q) {
+    return {q->pools, q->num_pools, q->page_bytes, q->num_pages};
+}
+
 }  // namespace
 
 extern "C" {
@@ -270,6 +291,70 @@ size_t sfi_kv4_workspace_size(const sfi_attn_shape *shape, int32_t batch, int32_
     if (sfi::check_shape(shape) != SFI_OK || batch < 0 || num_tokens < 1) return 0;
     if (num_tokens * (shape->num_q_heads / shape->num_kv_heads) > sfi::kMaxRows) return 0;
     return kv4_workspace(shape).total;
+}
+
+sfi_status sfi_page_copy(const sfi_page_pools *pools, const int32_t *src, const int32_t *dst, int32_t n,
+                         int32_t *dev_status, void *stream) {
+    const sfi_status st = check_pools(pools);
+    if (st != SFI_OK) return st;
+    if (!src || !dst || n < 0) return SFI_ERR_INVALID_ARG;
+    if (n == 0) return SFI_OK;
+    return launched(
+        sfi::launch_page_copy(pool_params(pools), src, dst, n, dev_status, static_cast<cudaStream_t>(stream)));
+}
+
+sfi_status sfi_page_fork(const sfi_page_map *map, const int32_t *src, const int32_t *dst, const int32_t *fork_lens,
+                         int32_t n, int32_t *dev_status, void *stream) {
+    const sfi_status st = check_map(map);
+    if (st != SFI_OK) return st;
+    if (!src || !dst || n < 0) return SFI_ERR_INVALID_ARG;
+    if (n == 0) return SFI_OK;
+    return launched(
+        sfi::launch_page_fork(map_params(map), src, dst, fork_lens, n, dev_status, static_cast<cudaStream_t>(stream)));
+}
+
+sfi_status sfi_page_reserve(const sfi_page_map *map, const sfi_page_pools *pools, const int32_t *new_lens,
+                            const int32_t *reqs, int32_t n, void *workspace, size_t workspace_bytes,
+                            int32_t *dev_status, void *stream) {
+    sfi_status st = check_map(map);
+    if (st != SFI_OK) return st;
+    if (pools && (st = check_pools(pools)) != SFI_OK) return st;
+    if (!new_lens || n < 0 || (pools && pools->num_pages < map->num_pages)) return SFI_ERR_INVALID_ARG;
+    if (!reqs && n > map->num_reqs) return SFI_ERR_INVALID_ARG;
+    if (n > SFI_MAX_PAGE_REQS) return SFI_ERR_UNSUPPORTED;
+    if (n == 0) return SFI_OK;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < sfi::page_workspace_bytes(map->num_pages))
+        return SFI_ERR_WORKSPACE;
+    sfi::PagePoolParams q{};
+    if (pools) q = pool_params(pools);
+    return launched(sfi::launch_page_reserve(map_params(map), pools ? &q : nullptr, new_lens, reqs, n, workspace,
+                                             dev_status, static_cast<cudaStream_t>(stream)));
+}
+
+sfi_status sfi_page_free(const sfi_page_map *map, const int32_t *reqs, int32_t n, int32_t *dev_status, void *stream) {
+    const sfi_status st = check_map(map);
+    if (st != SFI_OK) return st;
+    if (!reqs || n < 0) return SFI_ERR_INVALID_ARG;
+    if (n == 0) return SFI_OK;
+    return launched(sfi::launch_page_free(map_params(map), reqs, n, dev_status, static_cast<cudaStream_t>(stream)));
+}
+
+sfi_status sfi_page_compact(const sfi_page_map *map, const sfi_page_pools *pools, int32_t *table_out, int32_t *ref_out,
+                            int32_t *live_out, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                            void *stream) {
+    sfi_status st = check_map(map);
+    if (st != SFI_OK) return st;
+    if ((st = check_pools(pools)) != SFI_OK) return st;
+    if (!table_out || !ref_out || !live_out || pools->num_pages < map->num_pages) return SFI_ERR_INVALID_ARG;
+    if (table_out == map->page_table || ref_out == map->ref_count) return SFI_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < sfi::page_workspace_bytes(map->num_pages))
+        return SFI_ERR_WORKSPACE;
+    return launched(sfi::launch_page_compact(map_params(map), pool_params(pools), table_out, ref_out, live_out,
+                                             workspace, dev_status, static_cast<cudaStream_t>(stream)));
+}
+
+size_t sfi_page_workspace_size(const sfi_page_map *map) {
+    return check_map(map) == SFI_OK ? sfi::page_workspace_bytes(map->num_pages) : 0;
 }
 
 }  // extern "C"

@@ -225,4 +225,27 @@ constexpr int kKv4CtasPerSm = 2;
 constexpr int kKv4MaxCtas = 512;
 cudaError_t launch_kv4_attn(const Kv4AttnParams &p, int head_dim, cudaStream_t stream);
 
+// Page operators.
+struct PageMapParams {
+    int32_t *page_table, *seq_lens, *ref_count;
+    int32_t num_reqs, max_pages, num_pages;
+};
+struct PagePoolParams {
+    void *const *pools;
+    int32_t num_pools;
+    int64_t page_bytes;
+    int32_t num_pages;
+};
+size_t page_workspace_bytes(int32_t num_pages);
+cudaError_t launch_page_copy(const PagePoolParams &q, const int32_t *src, const int32_t *dst, int n,
+                             int32_t *dev_status, cudaStream_t stream);
+cudaError_t launch_page_fork(const PageMapParams &m, const int32_t *src, const int32_t *dst, const int32_t *fork_lens,
+                             int n, int32_t *dev_status, cudaStream_t stream);
+cudaError_t launch_page_free(const PageMapParams &m, const int32_t *reqs, int n, int32_t *dev_status,
+                             cudaStream_t stream);
+cudaError_t launch_page_reserve(const PageMapParams &m, const PagePoolParams *q, const int32_t *new_lens,
+                                const int32_t *reqs, int n, void *ws, int32_t *dev_status, cudaStream_t stream);
+cudaError_t launch_page_compact(const PageMapParams &m, const PagePoolParams &q, int32_t *table_out, int32_t *ref_out,
+                                int32_t *live_out, void *ws, int32_t *dev_status, cudaStream_t stream);
+
 }  // namespace sfi

@@ -280,3 +280,46 @@ def test_kv4_calls_validate_on_the_host(libsfi):
     sh = _shape()
     assert libsfi.sfi_kv4_workspace_size(ref(sh), 4, 8) > 0 and libsfi.sfi_kv4_workspace_size(ref(sh), 4, 9) == 0
     assert libsfi.sfi_kv4_workspace_size(ref(_shape(16, 8, 96)), 4, 1) == 0
+
+
+def test_page_calls_validate_on_the_host(libsfi):
+    from sparse_kv_long_sfi_gb300 import _abi
+    ref = lambda x: x and ctypes.byref(x)  # noqa: E731
+    mp = lambda **k: _abi.sfi_page_map(**{**dict(page_table=4096, seq_lens=4096, ref_count=4096, num_reqs=4,  # noqa: E731
+                                                max_pages_per_req=8, num_pages=32, page_size=16), **k})
+    pl = lambda **k: _abi.sfi_page_pools(**{**dict(pools=4096, num_pools=2, page_bytes=4608, num_pages=32), **k})  # noqa: E731
+
+    def copy(q=pl(), src=4096, dst=4096, n=1):
+        return libsfi.sfi_page_copy(ref(q), src, dst, n, None, None)
+
+    def fork(m=mp(), src=4096, dst=4096, n=1):
+        return libsfi.sfi_page_fork(ref(m), src, dst, None, n, None, None)
+
+    def reserve(m=mp(), q=pl(), new=4096, reqs=4096, n=1, ws=4096, size=1 << 20):
+        return libsfi.sfi_page_reserve(ref(m), ref(q), new, reqs, n, ws, size, None, None)
+
+    def free(m=mp(), reqs=4096, n=1):
+        return libsfi.sfi_page_free(ref(m), reqs, n, None, None)
+
+    def compact(m=mp(), q=pl(), table=8192, ref_out=8192, live=8192, ws=4096, size=1 << 20):
+        return libsfi.sfi_page_compact(ref(m), ref(q), table, ref_out, live, ws, size, None, None)
+
+    for call in (fork, reserve, free, compact):
+        assert call(m=None) == 1 and call(m=mp(page_table=None)) == 1 and call(m=mp(seq_lens=None)) == 1
+        assert call(m=mp(ref_count=None)) == 1 and call(m=mp(num_reqs=0)) == 1 and call(m=mp(num_pages=0)) == 1
+        assert call(m=mp(max_pages_per_req=0)) == 1 and call(m=mp(page_size=32)) == 2
+        assert call(m=mp(max_pages_per_req=1 << 28)) == 2
+    for call in (copy, reserve, compact):
+        assert call(q=pl(pools=None)) == 1 and call(q=pl(num_pools=0)) == 1 and call(q=pl(page_bytes=24)) == 1
+        assert call(q=pl(page_bytes=0)) == 1 and call(q=pl(num_pages=0)) == 1
+    assert copy(q=None) == 1 and copy(src=None) == 1 and copy(dst=None) == 1 and copy(n=-1) == 1 and copy(n=0) == 0
+    assert fork(src=None) == 1 and fork(dst=None) == 1 and fork(n=-1) == 1 and fork(n=0) == 0
+    assert free(reqs=None) == 1 and free(n=-1) == 1 and free(n=0) == 0
+    assert reserve(new=None) == 1 and reserve(n=-1) == 1 and reserve(n=1025) == 2 and reserve(n=0) == 0
+    assert reserve(reqs=None, n=5) == 1 and reserve(q=pl(num_pages=31)) == 1
+    assert reserve(ws=None) == 3 and reserve(ws=4100) == 3 and reserve(size=16) == 3
+    assert compact(q=None) == 1 and compact(table=None) == 1 and compact(ref_out=None) == 1 and compact(live=None) == 1
+    assert compact(table=4096) == 1 and compact(ref_out=4096) == 1 and compact(q=pl(num_pages=31)) == 1
+    assert compact(ws=None) == 3 and compact(size=16) == 3
+    m = mp()
+    assert libsfi.sfi_page_workspace_size(ref(m)) >= 3 * 32 * 4 and libsfi.sfi_page_workspace_size(None) == 0
