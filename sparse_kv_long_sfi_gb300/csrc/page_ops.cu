@@ -18,7 +18,7 @@ namespace {
 constexpr int kPageThreads = 256;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kCopyChunk = 8192;  // bytes of a pool's page that a CTA moves at once
+constexpr int kCopyChunk = 16384;  // bytes of a pool's page that a CTA moves at once
 
 // Workspace (int32): [0] moves, [1] unused .. [3], then the moves' sources, their
 // destinations (num_pages each), and the free or new page ids (num_pages).
@@ -164,9 +164,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_reserve_kernel(const PageMa
                                                                     const int32_t *reqs, int n, int can_copy, void *ws,
                                                                     int32_t *dev_status) {
     __shared__ int s_warp[kPlanWarps];
-    __shared__ int s_last[kPlanThreads];   // part-filled last page of list entry i, or -1
-    __shared__ int s_first[kPlanThreads];  // rank of its first page among those handed out
-    __shared__ int s_req[kPlanThreads];
+    __shared__ int2 s_entry[kPlanThreads];  // request and part-filled last page (or -1) of list entry i
+    __shared__ int s_first[kPlanThreads];   // rank of its first page among those handed out
     grid_launch_dependents();
     grid_dependency_wait();
     const PageLists lists(ws, m.num_pages);
@@ -194,15 +193,21 @@ __global__ void __launch_bounds__(kPlanThreads) page_reserve_kernel(const PageMa
             }
         }
     }
-    s_last[tid] = last;
-    s_req[tid] = r;
+    s_entry[tid] = make_int2(r, last);
     if (tid == 0) lists.moves[0] = 0;
     __syncthreads();
     int before = 0;  // holders of the same last page that come earlier in the list
-    for (int i = 0; i < min(tid, n); ++i) {
-        before += last >= 0 && s_last[i] == last;
-        if (tid < n && !err && s_req[i] == r) err = SFI_DEV_BAD_INDEX;  // named twice
+    bool twice = false;
+#pragma unroll 8
+    for (int i = 0; i < min(tid & ~31, n); ++i) {  // the warps before this one, then its own lanes
+        const int2 e = s_entry[i];
+        before += e.y == last;
+        twice |= e.x == r;
     }
+    const uint32_t lower = (1u << (tid & 31)) - 1u;
+    before += __popc(__match_any_sync(0xffffffffu, last) & lower);
+    twice |= (__match_any_sync(0xffffffffu, r) & lower) != 0;
+    if (tid < n && r >= 0 && twice) err = SFI_DEV_BAD_INDEX;  // named twice
     if (__syncthreads_or(err != 0)) {
         if (err) report(dev_status, err);
         return;
@@ -273,26 +278,49 @@ __global__ void __launch_bounds__(kPlanThreads) page_compact_plan_kernel(const P
     const PageLists lists(ws, m.num_pages);
     const int tid = threadIdx.x;
     int mine = 0;
+#pragma unroll 8
     for (int i = tid; i < m.num_pages; i += kPlanThreads) mine += m.ref_count[i] > 0;
     int live = 0;
     block_scan(mine, s_warp, &live);
-    // below N: holes in order; from N on: movers in order; there are as many of each
+    // below N: holes in order; from N on: movers in order; there are as many of each. A warp
+    // takes 32 kEach pages in a row; its ranks come from ballots, and one scan over the warps
+    // serves both lists (holes in the lower half).
+    constexpr int kEach = 8;
+    const int lane = tid & 31;
+    const uint32_t lower = (1u << lane) - 1u;
     int holes = 0, movers = 0;
-    for (int base = 0; base < m.num_pages; base += kPlanThreads) {
-        const int i = base + tid;
-        const int c = i < m.num_pages ? m.ref_count[i] : 0;
-        const bool hole = i < live && c <= 0, mover = i >= live && i < m.num_pages && c > 0;
-        // both ranks in one scan: holes in the lower, movers in the upper half (at most 1024 of each)
+    for (int base = 0; base < m.num_pages; base += kPlanThreads * kEach) {
+        const int p0 = base + (tid >> 5) * (32 * kEach) + lane;
+        int c[kEach], count = 0;
+        uint32_t hole[kEach], mover[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) c[k] = p0 + 32 * k < m.num_pages ? m.ref_count[p0 + 32 * k] : 0;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int i = p0 + 32 * k;
+            hole[k] = __ballot_sync(0xffffffffu, i < live && c[k] <= 0);
+            mover[k] = __ballot_sync(0xffffffffu, i >= live && i < m.num_pages && c[k] > 0);
+            count += __popc(hole[k]) | __popc(mover[k]) << 16;
+        }
         int both = 0;
-        const int rank = block_scan((hole ? 1 : 0) | (mover ? 1 << 16 : 0), s_warp, &both);
-        if (hole) lists.dst[holes + (rank & 0xffff)] = i;
-        if (mover) lists.src[movers + (rank >> 16)] = i;
+        // the warp's count enters the scan through its first lane; every lane gets what came before
+        const int before = __shfl_sync(0xffffffffu, block_scan(lane == 0 ? count : 0, s_warp, &both), 0);
+        int h = holes + (before & 0xffff), v = movers + (before >> 16);
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int i = p0 + 32 * k;
+            if (i < m.num_pages) {
+                const bool moves = (mover[k] >> lane) & 1u;
+                if ((hole[k] >> lane) & 1u) lists.dst[h + __popc(hole[k] & lower)] = i;
+                if (moves) lists.src[v + __popc(mover[k] & lower)] = i;
+                lists.ids[i] = i;
+                ref_out[i] = moves ? 0 : c[k];
+            }
+            h += __popc(hole[k]);
+            v += __popc(mover[k]);
+        }
         holes += both & 0xffff;
         movers += both >> 16;
-        if (i < m.num_pages) {
-            lists.ids[i] = i;
-            ref_out[i] = mover ? 0 : c;
-        }
     }
     __syncthreads();
     for (int i = tid; i < movers; i += kPlanThreads) {
