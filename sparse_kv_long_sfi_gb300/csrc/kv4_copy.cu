@@ -16,13 +16,13 @@ constexpr int kKv4Warps = 8;
 // Shared memory of a warp: a page's V codes and scales by token.
 template <int D>
 struct Kv4Tile {
-    uint32_t code[16][D / 8];  // eight codes of a token
+    uint2 code[16][D / 16];  // sixteen codes of a token
     uint8_t scale[16][D / 16];
 };
 
 // Codes and scale of eight values (a lane's part of a row; the lane beside it holds the
 // other half of the group of 16).
-__device__ __forceinline__ uint32_t quantise8(int4 raw, float six_g, float g, uint32_t *scale) {
+__device__ __forceinline__ uint32_t quantise8(int4 raw, float inv6g, float g, uint32_t *scale) {
     const uint32_t w[4] = {(uint32_t)raw.x, (uint32_t)raw.y, (uint32_t)raw.z, (uint32_t)raw.w};
     // the largest magnitude, compared as bits: infinities and NaN are the largest of all
     uint32_t top = 0;
@@ -30,14 +30,15 @@ __device__ __forceinline__ uint32_t quantise8(int4 raw, float six_g, float g, ui
     for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     const bool fine = top < 0x7f80u;
-    const uint32_t s = fine ? group_scale(__uint_as_float(top << 16), six_g) : kE4m3Nan;
+    const uint32_t s = fine ? group_scale(__uint_as_float(top << 16), inv6g) : kE4m3Nan;
     *scale = s;
     float x[8];
     bf16x8_to_f32(raw, x);
     const float step = e4m3_to_f32(s) * g;
-    if (!fine || !(step > 0.f)) return 0;
+    const bool some = fine && step > 0.f;
+    const float inv = some ? __frcp_rn(step) : 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __fdiv_rn(x[i], step);
+    for (int i = 0; i < 8; ++i) x[i] = some ? round16(x[i] * inv) : 0.f;
     return f32x8_to_e2m1(x);
 }
 
@@ -48,7 +49,8 @@ __device__ void write_block(uint8_t *block, Kv4Tile<D> &tile, const __nv_bfloat1
     using F = Kv4<D>;
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;
     const int sub = lane / kLanes, l = lane % kLanes;
-#pragma unroll 2
+    const float k_inv6g = 1.f / (6.f * k_scale), v_inv6g = 1.f / (6.f * v_scale);
+#pragma unroll 4
     for (int row0 = a; row0 < b; row0 += kRows) {
         const int row = row0 + sub;
         const bool in = row < b;
@@ -58,11 +60,11 @@ __device__ void write_block(uint8_t *block, Kv4Tile<D> &tile, const __nv_bfloat1
             vr = ld_stream_v4(vs + (int64_t)(row - a) * stride + l * 8);
         }
         uint32_t sk, sv;
-        const uint32_t ck = quantise8(kr, 6.f * k_scale, k_scale, &sk);
-        const uint32_t cv = quantise8(vr, 6.f * v_scale, v_scale, &sv);
+        const uint32_t ck = quantise8(kr, k_inv6g, k_scale, &sk);
+        const uint32_t cv = quantise8(vr, v_inv6g, v_scale, &sv);
         if (in) {
             *reinterpret_cast<uint32_t *>(block + row * F::kKRow + l * 4) = ck;
-            tile.code[row][l] = cv;
+            reinterpret_cast<uint32_t *>(tile.code[row])[l] = cv;
             if ((l & 1) == 0) {
                 block[F::kKScale + row * F::kGroups + l / 2] = (uint8_t)sk;
                 tile.scale[row][l / 2] = (uint8_t)sv;
@@ -70,32 +72,28 @@ __device__ void write_block(uint8_t *block, Kv4Tile<D> &tile, const __nv_bfloat1
         }
     }
     __syncwarp();
-    const bool whole = a == 0 && b == 16;
-#pragma unroll
-    for (int u = lane; u < D / 2; u += 32) {
-        const VUnit x(u);
-        int4 *dst = reinterpret_cast<int4 *>(block + F::kVCode) + u;
+    // a lane per (four tokens, sixteen dims): their codes as the eight words they make in the block
+    if (lane < 4 * F::kGroups) {
+        const int t = lane / F::kGroups, j = lane % F::kGroups;
         uint32_t keep = 0;  // bits of a word that belong to tokens outside [a, b)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (4 * x.t + i < a || 4 * x.t + i >= b) keep |= 0x0f0fu << (16 * (i >> 1) + 4 * (i & 1));
-        if (keep == 0xffffffffu) continue;
-        const int4 old = whole ? make_int4(0, 0, 0, 0) : *dst;
-        const uint32_t o[4] = {(uint32_t)old.x, (uint32_t)old.y, (uint32_t)old.z, (uint32_t)old.w};
-        uint32_t res[4];
-#pragma unroll
-        for (int jr = 0; jr < 4; ++jr) {
-            const int j = x.quad * 4 + jr;
-            uint32_t v = 0;
+            if (4 * t + i < a || 4 * t + i >= b) keep |= 0x0f0fu << (16 * (i >> 1) + 4 * (i & 1));
+        if (keep != 0xffffffffu) {
+            uint32_t in[4][2], out[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t lo = (tile.code[4 * x.t + i][2 * j] >> (4 * x.g)) & 15u;
-                const uint32_t hi = (tile.code[4 * x.t + i][2 * j + 1] >> (4 * x.g)) & 15u;
-                v |= (lo | hi << 8) << (16 * (i >> 1) + 4 * (i & 1));
+                const uint2 c = tile.code[4 * t + i][j];
+                in[i][0] = c.x;
+                in[i][1] = c.y;
             }
-            res[jr] = (o[jr] & keep) | (v & ~keep);
+            v_pack(in, out);
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+                uint32_t *dst = reinterpret_cast<uint32_t *>(block + F::kVCode + v_word(j, g, t));
+                *dst = keep ? (*dst & keep) | (out[g] & ~keep) : out[g];
+            }
         }
-        *dst = make_int4((int)res[0], (int)res[1], (int)res[2], (int)res[3]);
     }
     for (int i = lane; i < 16 * F::kGroups; i += 32) {
         const int tok = i & 3 | (i / (4 * F::kGroups)) << 2, grp = (i / 4) % F::kGroups;
@@ -146,15 +144,22 @@ __device__ void read_block(const uint8_t *block, Kv4Tile<D> &tile, __nv_bfloat16
     using F = Kv4<D>;
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;
     const int sub = lane / kLanes, l = lane % kLanes;
-    // V codes as they lie (D / 2 units of 16 bytes), V scales by token
-    int4 *raw = reinterpret_cast<int4 *>(&tile.code[0][0]);
+    // a lane per (four tokens, sixteen dims) brings V's codes into rows
+    if (lane < 4 * F::kGroups) {
+        const int t = lane / F::kGroups, j = lane % F::kGroups;
+        uint32_t in[4][2], out[8];
 #pragma unroll
-    for (int u = lane; u < D / 2; u += 32) raw[u] = ld_stream_v4(block + F::kVCode + u * 16);
-    for (int i = lane; i < 16 * F::kGroups; i += 32)
-        tile.scale[i & 3 | (i / (4 * F::kGroups)) << 2][(i / 4) % F::kGroups] = block[F::kVScale + i];
+        for (int g = 0; g < 8; ++g) out[g] = *reinterpret_cast<const uint32_t *>(block + F::kVCode + v_word(j, g, t));
+        const uint32_t sc = *reinterpret_cast<const uint32_t *>(block + F::kVScale + lane * 4);
+        v_unpack(out, in);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            tile.code[4 * t + i][j] = make_uint2(in[i][0], in[i][1]);
+            tile.scale[4 * t + i][j] = (uint8_t)(sc >> (8 * i));
+        }
+    }
     __syncwarp();
-    const uint8_t *vb = reinterpret_cast<const uint8_t *>(raw);
-#pragma unroll 2
+#pragma unroll 4
     for (int row0 = a; row0 < b; row0 += kRows) {
         const int row = row0 + sub;
         if (row < b) {
@@ -169,15 +174,7 @@ __device__ void read_block(const uint8_t *block, Kv4Tile<D> &tile, __nv_bfloat16
                 x[2 * i + 1] = v.y * sk;
             }
             *reinterpret_cast<int4 *>(ks + (int64_t)(row - a) * stride + l * 8) = f32x8_to_bf16(x);
-            // dims 8l .. 8l+7: j = l / 2, the lower (l even) or upper eight of its sixteen
-            uint32_t code = 0;
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {
-                const int u = (l >> 3) * 32 + (g >> 1) * 8 + (row >> 2) * 2 + (g & 1);
-                const uint32_t byte = vb[u * 16 + ((l >> 1) & 3) * 4 + (row & 2) + (l & 1)];
-                code |= ((byte >> (4 * (row & 1))) & 15u) << (4 * g);
-            }
-            e2m1x8_to_f16(code, h);
+            e2m1x8_to_f16(reinterpret_cast<const uint32_t *>(tile.code[row])[l], h);
             const float sv = e4m3_to_f32(tile.scale[row][l / 2]) * v_scale;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

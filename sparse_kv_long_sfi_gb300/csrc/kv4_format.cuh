@@ -45,11 +45,21 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// The e4m3 scale of a group whose largest magnitude is amax (6g = 6 times the cache's power
-// of two); nearest even, at most 448.
-__device__ __forceinline__ uint32_t group_scale(float amax, float six_g) {
+// v rounded to 16 significant bits. A bf16 value over a step of a few bits is either exactly
+// halfway between two codes (or two e4m3 scales) or at least 2^-8.4 of itself away from there:
+// with x = X 2^a (X < 256), the step S 2^b (S < 16, or 3 for the scale itself) and the halfway
+// point T 2^c (T < 32), |X 2^k - T S| is a whole number in the unit where both sides are, hence
+// at least 1 of at most 480. So the value times the step's fp32 reciprocal (off by 2^-22)
+// decides every rounding like the exact quotient once its last bits are rounded away.
+__device__ __forceinline__ float round16(float v) {
+    return __uint_as_float((__float_as_uint(v) + 0x80u) & 0xffffff00u);
+}
+
+// The e4m3 scale of a group whose largest magnitude is amax (inv6g: 1 / (6 g)); nearest even,
+// at most 448.
+__device__ __forceinline__ uint32_t group_scale(float amax, float inv6g) {
     uint16_t s;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s) : "f"(0.f), "f"(__fdiv_rn(amax, six_g)));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s) : "f"(0.f), "f"(round16(amax * inv6g)));
     return s & 0xffu;
 }
 
@@ -96,5 +106,43 @@ struct VUnit {
     __device__ __forceinline__ explicit VUnit(int u)
         : quad(u >> 5), g(((u >> 3) & 3) * 2 + (u & 1)), t((u >> 1) & 3) {}
 };
+
+// Codes of four tokens' dims 16 j .. 16 j + 15 (in[i][c]: token 4t + i, dims 16 j + 8 c ..,
+// one code in four bits) <-> the words of j in the units g = 0 .. 7 of t.
+__device__ __forceinline__ void v_pack(const uint32_t (&in)[4][2], uint32_t (&out)[8]) {
+    uint32_t even[2][2], odd[2][2];  // [pair of tokens][c]: byte k holds dim 2k (2k + 1) of both
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const uint32_t a = in[2 * h][c], b = in[2 * h + 1][c];
+            even[h][c] = (a & 0x0f0f0f0fu) | ((b & 0x0f0f0f0fu) << 4);
+            odd[h][c] = ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+        }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t sel = k | (4 + k) << 4;
+        out[2 * k] = __byte_perm(__byte_perm(even[0][0], even[0][1], sel), __byte_perm(even[1][0], even[1][1], sel), 0x5410);
+        out[2 * k + 1] = __byte_perm(__byte_perm(odd[0][0], odd[0][1], sel), __byte_perm(odd[1][0], odd[1][1], sel), 0x5410);
+    }
+}
+__device__ __forceinline__ void v_unpack(const uint32_t (&out)[8], uint32_t (&in)[4][2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int byte = 2 * h + c;
+            const uint32_t sel = byte | (4 + byte) << 4;
+            const uint32_t even = __byte_perm(__byte_perm(out[0], out[2], sel), __byte_perm(out[4], out[6], sel), 0x5410);
+            const uint32_t odd = __byte_perm(__byte_perm(out[1], out[3], sel), __byte_perm(out[5], out[7], sel), 0x5410);
+            in[2 * h][c] = (even & 0x0f0f0f0fu) | ((odd & 0x0f0f0f0fu) << 4);
+            in[2 * h + 1][c] = ((even >> 4) & 0x0f0f0f0fu) | (odd & 0xf0f0f0f0u);
+        }
+}
+
+// Byte offset, within a block's V codes, of word j of unit g of t.
+__device__ __forceinline__ int v_word(int j, int g, int t) {
+    return (j >> 2) * 512 + (g >> 1) * 128 + t * 32 + (g & 1) * 16 + (j & 3) * 4;
+}
 
 }  // namespace sfi

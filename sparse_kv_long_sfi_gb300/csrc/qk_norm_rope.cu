@@ -6,10 +6,14 @@
 // wraps modulo one turn by itself, so nothing of the angle is lost at far positions and
 // no table of cosines is read; the upper 32 bits give the fraction of the turn to 2^-32.
 //
-// Bound by HBM: each row is read and written once. A row is held by D / 8 lanes (16 bytes
-// each), a warp takes one token's rows two (four at D = 64) at a time, with four such
-// loads in flight; its lanes compute the token's rot_dim / 2 cosines and sines once and
-// keep the eight pairs of their own dims in registers for all rows.
+// Bound by HBM: each row is read and written once. A row is held by D / 8 lanes, a warp takes
+// one token's rows two (four at D = 64) at a time with four such loads in flight. Norm weight
+// and rotation of a token become two factors per dim, once for its Q and once for its K rows:
+// y = (x A + x' B) / rms, x' the other member of the pair. Where whole heads turn in split
+// halves a lane holds both members (dims 4 l .. and D/2 + 4 l ..); otherwise it holds eight
+// dims in a row and fetches x' from its mate lane. Three CTAs per SM (80 registers) keep enough
+// loads in flight: 2 x 8192 tokens of 32/8/128 heads take 73.9 us (5.4 TB/s) against 85.4 us
+// with two and 77.4 us with four, which spill.
 #include <algorithm>
 
 #include "sfi_device.cuh"
@@ -34,9 +38,26 @@ __device__ __forceinline__ int4 pack8(const float (&x)[8]) {
                      (int)pack_bf16x2(x[6], x[7]));
 }
 
+// A lane's eight values of a row: in a row, or four of each half.
+template <int D, bool HALVES>
+__device__ __forceinline__ int4 load_row(const __nv_bfloat16 *row, int l) {
+    if constexpr (!HALVES) return *reinterpret_cast<const int4 *>(row + l * 8);
+    const int2 a = *reinterpret_cast<const int2 *>(row + l * 4), b = *reinterpret_cast<const int2 *>(row + D / 2 + l * 4);
+    return make_int4(a.x, a.y, b.x, b.y);
+}
+template <int D, bool HALVES>
+__device__ __forceinline__ void store_row(__nv_bfloat16 *row, int l, int4 v) {
+    if constexpr (!HALVES) {
+        *reinterpret_cast<int4 *>(row + l * 8) = v;
+    } else {
+        *reinterpret_cast<int2 *>(row + l * 4) = make_int2(v.x, v.y);
+        *reinterpret_cast<int2 *>(row + D / 2 + l * 4) = make_int2(v.z, v.w);
+    }
+}
+
 // One warp takes rows [chunk * rows_per_item, ...) of one token's q, k and v rows.
-template <int D>
-__global__ void __launch_bounds__(kNormWarps * 32) qk_norm_rope_kernel(const NormRopeParams p, int batch,
+template <int D, bool HALVES>
+__global__ void __launch_bounds__(kNormWarps * 32, HALVES ? 3 : 2) qk_norm_rope_kernel(const NormRopeParams p, int batch,
                                                                        int rows_per_item, int chunks) {
     constexpr int kLanes = D / 8;          // lanes per row
     constexpr int kRows = 32 / kLanes;     // rows per load
@@ -44,12 +65,11 @@ __global__ void __launch_bounds__(kNormWarps * 32) qk_norm_rope_kernel(const Nor
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int sub = lane / kLanes, l = lane % kLanes;
     const int64_t items = (int64_t)batch * p.tokens * chunks;
-    const int rows_all = p.hq + p.hkv + (p.v ? p.hkv : 0);
     const int half = p.rot_dim / 2;
-    const bool rotated = l * 8 < p.rot_dim;
-    // the lane that holds the other member of this lane's pairs (split halves)
-    const int mate = p.interleaved || !rotated ? lane : (l * 8 < half ? lane + half / 8 : lane - half / 8);
-    const bool second = l * 8 >= half;
+    const bool rotated = HALVES || l * 8 < p.rot_dim;
+    const bool second = l * 8 >= half;  // this lane's dims are the second members (split halves)
+    // the lane that holds the other members of this lane's pairs (split halves)
+    const int mate = p.interleaved || !rotated ? lane : (second ? lane - half / 8 : lane + half / 8);
     grid_launch_dependents();
     grid_dependency_wait();
 
@@ -81,7 +101,9 @@ __global__ void __launch_bounds__(kNormWarps * 32) qk_norm_rope_kernel(const Nor
         }
         // the token's rotations
         float cs[8], sn[8];
-        if (p.rot_dim > 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
+        if (HALVES || p.rot_dim > 0) {
             __syncwarp();
             for (int i = lane; i < half; i += 32) {
                 const int a = p.axis ? p.axis[i] : 0;
@@ -101,78 +123,100 @@ __global__ void __launch_bounds__(kNormWarps * 32) qk_norm_rope_kernel(const Nor
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int e = l * 8 + i;
-                const int pair = p.interleaved ? e / 2 : (second ? e - half : e);
-                const float2 v = rotated ? s_cs[warp][pair] : make_float2(1.f, 0.f);
-                cs[i] = v.x;
-                // the sign of the mate's share: minus for the first member of a pair
-                sn[i] = (p.interleaved ? (i & 1) == 0 : !second) ? -v.y : v.y;
+                const int pair = HALVES ? l * 4 + (i & 3) : (p.interleaved ? e / 2 : (second ? e - half : e));
+                if (rotated) {
+                    const float2 v = s_cs[warp][pair];
+                    cs[i] = v.x;
+                    // the sign of the mate's share: minus for the first member of a pair
+                    sn[i] = (HALVES ? i < 4 : (p.interleaved ? (i & 1) == 0 : !second)) ? -v.y : v.y;
+                }
             }
         }
-        const int row_end = min(rows_all, (chunk + 1) * rows_per_item);
-        for (int row0 = chunk * rows_per_item; row0 < row_end; row0 += kRows * kNormBatch) {
-            int4 raw[kNormBatch];
+        // rows [first, last) of the item within a group of `heads` rows that starts at row `from`
+        const int lo = chunk * rows_per_item, hi = lo + rows_per_item;
+        auto rows_of = [&](int from, int heads, int &first, int &last) {
+            first = min(max(lo - from, 0), heads);
+            last = min(max(hi - from, 0), heads);
+        };
+        // norm and rotation of rows [first, last); put(head, value) stores one
+        auto turn_rows = [&](const __nv_bfloat16 *src, const __nv_bfloat16 *weight, int first, int last, auto put) {
+            if (first >= last) return;
+            float A[8], B[8];
 #pragma unroll
-            for (int u = 0; u < kNormBatch; ++u) {
-                const int row = row0 + u * kRows + sub;
-                if (row < row_end) {
-                    const __nv_bfloat16 *src;
-                    if (row < p.hq)
-                        src = p.q + row_tok * p.q_stride + (int64_t)row * D;
-                    else if (row < p.hq + p.hkv)
-                        src = p.k + row_tok * p.k_stride + (int64_t)(row - p.hq) * D;
-                    else
-                        src = p.v + row_tok * p.v_stride + (int64_t)(row - p.hq - p.hkv) * D;
-                    raw[u] = *reinterpret_cast<const int4 *>(src + l * 8);
-                } else {
-                    raw[u] = make_int4(0, 0, 0, 0);
-                }
+            for (int i = 0; i < 8; ++i) A[i] = 1.f;
+            if (weight) unpack8(load_row<D, HALVES>(weight, l), A);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float w = HALVES ? A[i ^ 4] : (p.interleaved ? A[i ^ 1] : __shfl_sync(0xffffffffu, A[i], mate));
+                B[i] = w * sn[i];
             }
 #pragma unroll
-            for (int u = 0; u < kNormBatch; ++u) {
-                if (row0 + u * kRows >= row_end) break;
-                const int row = row0 + u * kRows + sub;
-                const bool is_q = row < p.hq, is_v = row >= p.hq + p.hkv;
-                const __nv_bfloat16 *w = is_q ? p.q_weight : p.k_weight;
-                int4 res = raw[u];
-                float x[8];
-                unpack8(raw[u], x);
-                float ss = 0.f;
+            for (int i = 0; i < 8; ++i) A[i] *= cs[i];
+            for (int row0 = first; row0 < last; row0 += kRows * kNormBatch) {
+                int4 raw[kNormBatch];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-                for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-                if (w) {
-                    const float rs = rsqrtf(ss * (1.f / D) + p.eps);
-                    float wf[8];
-                    unpack8(*reinterpret_cast<const int4 *>(w + l * 8), wf);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = x[i] * rs * wf[i];
+                for (int u = 0; u < kNormBatch; ++u) {
+                    const int row = row0 + u * kRows + sub;
+                    raw[u] = make_int4(0, 0, 0, 0);
+                    if (row < last) raw[u] = load_row<D, HALVES>(src + (int64_t)row * D, l);
                 }
-                if (p.rot_dim > 0) {
-                    float y[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], mate);
-                    if (rotated) {
-                        if (p.interleaved) {
+                for (int u = 0; u < kNormBatch; ++u) {
+                    if (row0 + u * kRows >= last) break;
+                    const int row = row0 + u * kRows + sub;
+                    float x[8], y[8];
+                    unpack8(raw[u], x);
+                    float rs = 1.f;
+                    if (weight) {
+                        float ss = 0.f;
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
-                        }
+                        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = fmaf(y[i], sn[i], x[i] * cs[i]);
+                        for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+                        rs = rsqrtf(ss * (1.f / D) + p.eps);
                     }
+                    if (HALVES || p.interleaved) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[i] = x[HALVES ? i ^ 4 : i ^ 1];
+                    } else if (p.rot_dim > 0) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], mate);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (rotated && (HALVES || p.rot_dim > 0))
+                            x[i] = fmaf(y[i], B[i], x[i] * A[i]) * rs;
+                        else
+                            x[i] = x[i] * A[i] * rs;
+                    }
+                    if (row < last) put(row, pack8(x));
                 }
-                if (row >= row_end) continue;
-                if (!is_v) res = pack8(x);
-                if (is_q) {
-                    *reinterpret_cast<int4 *>(p.q_out + (row_tok * p.hq + row) * D + l * 8) = res;
-                } else {
-                    const int h = row - p.hq - (is_v ? p.hkv : 0);
-                    if (p.k_out && !is_v) *reinterpret_cast<int4 *>(p.k_out + (row_tok * p.hkv + h) * D + l * 8) = res;
-                    if (page >= 0)
-                        *reinterpret_cast<int4 *>((is_v ? p.v_pool : p.k_pool) +
-                                                  (((int64_t)page * p.hkv + h) * kSubTokens + slot % kSubTokens) * D +
-                                                  l * 8) = res;
-                }
+            }
+        };
+        int first, last;
+        rows_of(0, p.hq, first, last);
+        turn_rows(p.q + row_tok * p.q_stride, p.q_weight, first, last, [&](int h, int4 v) {
+            store_row<D, HALVES>(p.q_out + (row_tok * p.hq + h) * D, l, v);
+        });
+        const int64_t page_row = ((int64_t)page * p.hkv * kSubTokens + slot % kSubTokens) * D;
+        rows_of(p.hq, p.hkv, first, last);
+        turn_rows(p.k + row_tok * p.k_stride, p.k_weight, first, last, [&](int h, int4 v) {
+            if (p.k_out) store_row<D, HALVES>(p.k_out + (row_tok * p.hkv + h) * D, l, v);
+            if (page >= 0) store_row<D, HALVES>(p.k_pool + page_row + (int64_t)h * kSubTokens * D, l, v);
+        });
+        if (p.v && page >= 0) {
+            rows_of(p.hq + p.hkv, p.hkv, first, last);
+            const __nv_bfloat16 *src = p.v + row_tok * p.v_stride + l * 8;
+            __nv_bfloat16 *dst = p.v_pool + page_row + l * 8;
+            for (int row0 = first + sub; row0 < last; row0 += kRows * kNormBatch) {
+                int4 raw[kNormBatch];
+#pragma unroll
+                for (int u = 0; u < kNormBatch; ++u)
+                    if (row0 + u * kRows < last) raw[u] = *reinterpret_cast<const int4 *>(src + (int64_t)(row0 + u * kRows) * D);
+#pragma unroll
+                for (int u = 0; u < kNormBatch; ++u)
+                    if (row0 + u * kRows < last)
+                        *reinterpret_cast<int4 *>(dst + (int64_t)(row0 + u * kRows) * kSubTokens * D) = raw[u];
             }
         }
     }
@@ -193,8 +237,10 @@ cudaError_t launch_qk_norm_rope(const NormRopeParams &p, int head_dim, int batch
     const int chunks = (rows + rows_per_item - 1) / rows_per_item;
     const int64_t ctas = (tokens * chunks + kNormWarps - 1) / kNormWarps;
     const int grid = (int)std::min<int64_t>(ctas, (int64_t)sms * 64);
-    return launch_dependent(head_dim == 128 ? qk_norm_rope_kernel<128> : qk_norm_rope_kernel<64>, grid, kNormWarps * 32,
-                            0, stream, p, batch, rows_per_item, chunks);
+    const bool halves = p.rot_dim == head_dim && !p.interleaved;
+    auto kernel = head_dim == 128 ? (halves ? qk_norm_rope_kernel<128, true> : qk_norm_rope_kernel<128, false>)
+                                  : (halves ? qk_norm_rope_kernel<64, true> : qk_norm_rope_kernel<64, false>);
+    return launch_dependent(kernel, grid, kNormWarps * 32, 0, stream, p, batch, rows_per_item, chunks);
 }
 
 }  // namespace sfi
