@@ -132,11 +132,6 @@ __device__ __forceinline__ ReqPlan plan_request(const Kv4AttnParams &p, int b, u
     return q;
 }
 
-// a / b for a >= 0, b > 0, in 32 bits where both fit.
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-    return ((uint64_t)(a | b) >> 32) ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
-
 // A place in the row of work: block `pg` of KV head h of request b.
 struct Place {
     int b, h, pg;

@@ -1,7 +1,7 @@
 // The calls that fill, read back and compact the 4-bit cache.
 //
-// One warp owns one (page, KV head) block at a time, so the half-byte updates of a partly
-// written page race with nobody. K rows are contiguous in a block; V codes lie in the
+// One warp owns K or V of one (page, KV head) block at a time, so the half-byte updates of a
+// partly written page race with nobody. K rows are contiguous in a block; V codes lie in the
 // order of the matrix instruction's lanes, so rows of V pass through shared memory.
 // All three are copies with a conversion: bound by HBM when there are many tokens, by
 // launch latency in a decode step.
@@ -20,84 +20,106 @@ struct Kv4Tile {
     uint8_t scale[16][D / 16];
 };
 
+// The larger magnitudes of two pairs of bf16.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7fff7fffu), "r"(b & 0x7fff7fffu));
+    return r;
+}
+
 // Codes and scale of eight values (a lane's part of a row; the lane beside it holds the
 // other half of the group of 16).
 __device__ __forceinline__ uint32_t quantise8(int4 raw, float inv6g, float g, uint32_t *scale) {
     const uint32_t w[4] = {(uint32_t)raw.x, (uint32_t)raw.y, (uint32_t)raw.z, (uint32_t)raw.w};
-    // the largest magnitude, compared as bits: infinities and NaN are the largest of all
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    // the largest magnitude; a NaN wins
+    uint32_t top2 = max_abs_bf16x2(max_abs_bf16x2(w[0], w[1]), max_abs_bf16x2(w[2], w[3]));
+    top2 = max_abs_bf16x2(top2, __shfl_xor_sync(0xffffffffu, top2, 1));
+    const uint32_t top = max(top2 & 0xffffu, top2 >> 16);
     const bool fine = top < 0x7f80u;
     const uint32_t s = fine ? group_scale(__uint_as_float(top << 16), inv6g) : kE4m3Nan;
     *scale = s;
     float x[8];
     bf16x8_to_f32(raw, x);
     const float step = e4m3_to_f32(s) * g;
-    const bool some = fine && step > 0.f;
-    const float inv = some ? __frcp_rn(step) : 0.f;
+    const float inv = reciprocal(step);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = some ? round16(x[i] * inv) : 0.f;
-    return f32x8_to_e2m1(x);
+    for (int i = 0; i < 8; ++i) x[i] = round16(x[i] * inv);
+    return fine && step > 0.f ? f32x8_to_e2m1(x) : 0u;
 }
 
-// Rows [a, b) of the block from K and V rows (token tok at src + (tok - a) * stride).
+// An item of the append and the read: K or V of one page of one KV head of one request.
+struct Kv4Item {
+    int is_v, h, slot, entry;
+    __device__ __forceinline__ Kv4Item(int64_t item, int hkv, int slots) {
+        is_v = (int)(item & 1);
+        const int64_t at = item >> 1, page = quotient(at, hkv);
+        h = (int)(at - page * hkv);
+        entry = (int)quotient(page, slots);
+        slot = (int)(page - (int64_t)entry * slots);
+    }
+};
+
+// Rows [a, b) of the block's K or V (row tok from src + (tok - a) * stride).
 template <int D>
-__device__ void write_block(uint8_t *block, Kv4Tile<D> &tile, const __nv_bfloat16 *ks, const __nv_bfloat16 *vs,
-                            int64_t stride, int a, int b, float k_scale, float v_scale, int lane) {
+__device__ void write_block(uint8_t *block, Kv4Tile<D> &tile, const __nv_bfloat16 *src, int64_t stride, int a, int b,
+                            bool is_v, float g, int lane) {
     using F = Kv4<D>;
-    constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kIters = 16 / kRows;
     const int sub = lane / kLanes, l = lane % kLanes;
-    const float k_inv6g = 1.f / (6.f * k_scale), v_inv6g = 1.f / (6.f * v_scale);
-#pragma unroll 4
-    for (int row0 = a; row0 < b; row0 += kRows) {
-        const int row = row0 + sub;
-        const bool in = row < b;
-        int4 kr = make_int4(0, 0, 0, 0), vr = kr;
-        if (in) {
-            kr = ld_stream_v4(ks + (int64_t)(row - a) * stride + l * 8);
-            vr = ld_stream_v4(vs + (int64_t)(row - a) * stride + l * 8);
-        }
-        uint32_t sk, sv;
-        const uint32_t ck = quantise8(kr, k_inv6g, k_scale, &sk);
-        const uint32_t cv = quantise8(vr, v_inv6g, v_scale, &sv);
-        if (in) {
-            *reinterpret_cast<uint32_t *>(block + row * F::kKRow + l * 4) = ck;
-            reinterpret_cast<uint32_t *>(tile.code[row])[l] = cv;
-            if ((l & 1) == 0) {
-                block[F::kKScale + row * F::kGroups + l / 2] = (uint8_t)sk;
-                tile.scale[row][l / 2] = (uint8_t)sv;
-            }
+    const float inv6g = reciprocal(6.f * g);
+    int4 raw[kIters];
+#pragma unroll
+    for (int i = 0; i < kIters; ++i) {
+        const int row = i * kRows + sub;
+        raw[i] = make_int4(0, 0, 0, 0);
+        if (row >= a && row < b) raw[i] = ld_stream_v4(src + (int64_t)(row - a) * stride + l * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < kIters; ++i) {
+        const int row = i * kRows + sub;
+        if ((i + 1) * kRows <= a || i * kRows >= b) continue;  // no row of this load (the same in all lanes)
+        uint32_t s;
+        const uint32_t code = quantise8(raw[i], inv6g, g, &s);
+        if (row < a || row >= b) continue;
+        if (is_v) {
+            reinterpret_cast<uint32_t *>(tile.code[row])[l] = code;
+            if ((l & 1) == 0) tile.scale[row][l / 2] = (uint8_t)s;
+        } else {
+            *reinterpret_cast<uint32_t *>(block + row * F::kKRow + l * 4) = code;
+            if ((l & 1) == 0) block[F::kKScale + row * F::kGroups + l / 2] = (uint8_t)s;
         }
     }
+    if (!is_v) return;
     __syncwarp();
-    // a lane per (four tokens, sixteen dims): their codes as the eight words they make in the block
+    // a lane per (four tokens, sixteen dims): their codes as the eight words they make in the
+    // block, their scales as the word of the four
     if (lane < 4 * F::kGroups) {
         const int t = lane / F::kGroups, j = lane % F::kGroups;
-        uint32_t keep = 0;  // bits of a word that belong to tokens outside [a, b)
+        uint32_t keep = 0, keep_scale = 0;  // bits of a word that belong to tokens outside [a, b)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (4 * t + i < a || 4 * t + i >= b) keep |= 0x0f0fu << (16 * (i >> 1) + 4 * (i & 1));
+            if (4 * t + i < a || 4 * t + i >= b) {
+                keep |= 0x0f0fu << (16 * (i >> 1) + 4 * (i & 1));
+                keep_scale |= 0xffu << (8 * i);
+            }
         if (keep != 0xffffffffu) {
-            uint32_t in[4][2], out[8];
+            uint32_t in[4][2], out[8], sc = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint2 c = tile.code[4 * t + i][j];
                 in[i][0] = c.x;
                 in[i][1] = c.y;
+                sc |= (uint32_t)tile.scale[4 * t + i][j] << (8 * i);
             }
             v_pack(in, out);
 #pragma unroll
-            for (int g = 0; g < 8; ++g) {
-                uint32_t *dst = reinterpret_cast<uint32_t *>(block + F::kVCode + v_word(j, g, t));
-                *dst = keep ? (*dst & keep) | (out[g] & ~keep) : out[g];
+            for (int k = 0; k < 8; ++k) {
+                uint32_t *dst = reinterpret_cast<uint32_t *>(block + F::kVCode + v_word(j, k, t));
+                *dst = keep ? (*dst & keep) | (out[k] & ~keep) : out[k];
             }
+            uint32_t *dst = reinterpret_cast<uint32_t *>(block + F::kVScale + lane * 4);
+            *dst = keep_scale ? (*dst & keep_scale) | (sc & ~keep_scale) : sc;
         }
-    }
-    for (int i = lane; i < 16 * F::kGroups; i += 32) {
-        const int tok = i & 3 | (i / (4 * F::kGroups)) << 2, grp = (i / 4) % F::kGroups;
-        if (tok >= a && tok < b) block[F::kVScale + i] = tile.scale[tok][grp];
     }
     __syncwarp();
 }
@@ -106,23 +128,21 @@ template <int D>
 __global__ void __launch_bounds__(kKv4Warps * 32) kv4_append_kernel(const Kv4CopyParams p, int batch, int page_slots) {
     __shared__ Kv4Tile<D> s_tile[kKv4Warps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t items = (int64_t)batch * page_slots * p.hkv;
+    const int64_t items = (int64_t)batch * page_slots * p.hkv * 2;
     grid_launch_dependents();
     grid_dependency_wait();
     for (int64_t item = (int64_t)blockIdx.x * kKv4Warps + warp; item < items;
          item += (int64_t)gridDim.x * kKv4Warps) {
-        const int h = (int)(item % p.hkv);
-        const int64_t at = item / p.hkv;
-        const int ps = (int)(at % page_slots), bi = (int)(at / page_slots);
-        const int r = p.req_ids ? p.req_ids[bi] : bi;
+        const Kv4Item x(item, p.hkv, page_slots);
+        const int r = p.req_ids ? p.req_ids[x.entry] : x.entry;
         const int L = p.seq_lens[r];
         const int n = p.new_lens ? p.new_lens[r] : p.tokens;
         if (n < 0 || n > p.tokens || L < n || L > p.max_pages * kSubTokens) {
-            if (lane == 0 && h == 0 && ps == 0) report(p.dev_status, SFI_DEV_BAD_LEN);
+            if (lane == 0 && x.h == 0 && x.slot == 0) report(p.dev_status, SFI_DEV_BAD_LEN);
             continue;
         }
         const int first = L - n;
-        const int pg = first / kSubTokens + ps;
+        const int pg = first / kSubTokens + x.slot;
         const int pos0 = pg * kSubTokens;
         const int a = max(first - pos0, 0), b = min(L - pos0, kSubTokens);
         if (a >= b) continue;
@@ -131,84 +151,87 @@ __global__ void __launch_bounds__(kKv4Warps * 32) kv4_append_kernel(const Kv4Cop
             if (lane == 0) report(p.dev_status, SFI_DEV_BAD_PAGE);
             continue;
         }
-        const int64_t row = ((int64_t)r * p.tokens + (pos0 + a - first)) * p.hkv + h;
-        write_block<D>(p.pool + ((int64_t)page * p.hkv + h) * Kv4<D>::kBlock, s_tile[warp], p.k_new + row * D,
-                       p.v_new + row * D, (int64_t)p.hkv * D, a, b, p.k_scale, p.v_scale, lane);
+        const int64_t row = ((int64_t)r * p.tokens + (pos0 + a - first)) * p.hkv + x.h;
+        write_block<D>(p.pool + ((int64_t)page * p.hkv + x.h) * Kv4<D>::kBlock, s_tile[warp],
+                       (x.is_v ? p.v_new : p.k_new) + row * D, (int64_t)p.hkv * D, a, b, x.is_v,
+                       x.is_v ? p.v_scale : p.k_scale, lane);
     }
 }
 
-// Rows [a, b) of a block as bf16 rows (row tok to dst + (tok - a) * stride).
+// Rows [a, b) of a block's K or V as bf16 rows (row tok to dst + (tok - a) * stride).
 template <int D>
-__device__ void read_block(const uint8_t *block, Kv4Tile<D> &tile, __nv_bfloat16 *ks, __nv_bfloat16 *vs,
-                           int64_t stride, int a, int b, float k_scale, float v_scale, int lane) {
+__device__ void read_block(const uint8_t *block, Kv4Tile<D> &tile, __nv_bfloat16 *dst, int64_t stride, int a, int b,
+                           bool is_v, float g, int lane) {
     using F = Kv4<D>;
-    constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kIters = 16 / kRows;
     const int sub = lane / kLanes, l = lane % kLanes;
-    // a lane per (four tokens, sixteen dims) brings V's codes into rows
-    if (lane < 4 * F::kGroups) {
-        const int t = lane / F::kGroups, j = lane % F::kGroups;
-        uint32_t in[4][2], out[8];
+    uint32_t code[kIters], scale[kIters];
+    if (is_v) {
+        // a lane per (four tokens, sixteen dims) brings V's codes into rows
+        if (lane < 4 * F::kGroups) {
+            const int t = lane / F::kGroups, j = lane % F::kGroups;
+            uint32_t in[4][2], out[8];
 #pragma unroll
-        for (int g = 0; g < 8; ++g) out[g] = *reinterpret_cast<const uint32_t *>(block + F::kVCode + v_word(j, g, t));
-        const uint32_t sc = *reinterpret_cast<const uint32_t *>(block + F::kVScale + lane * 4);
-        v_unpack(out, in);
+            for (int k = 0; k < 8; ++k) out[k] = *reinterpret_cast<const uint32_t *>(block + F::kVCode + v_word(j, k, t));
+            const uint32_t sc = *reinterpret_cast<const uint32_t *>(block + F::kVScale + lane * 4);
+            v_unpack(out, in);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            tile.code[4 * t + i][j] = make_uint2(in[i][0], in[i][1]);
-            tile.scale[4 * t + i][j] = (uint8_t)(sc >> (8 * i));
+            for (int i = 0; i < 4; ++i) {
+                tile.code[4 * t + i][j] = make_uint2(in[i][0], in[i][1]);
+                tile.scale[4 * t + i][j] = (uint8_t)(sc >> (8 * i));
+            }
+        }
+        __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < kIters; ++i) {
+        const int row = i * kRows + sub;
+        if (is_v) {
+            code[i] = reinterpret_cast<const uint32_t *>(tile.code[row])[l];
+            scale[i] = tile.scale[row][l / 2];
+        } else {
+            code[i] = *reinterpret_cast<const uint32_t *>(block + row * F::kKRow + l * 4);
+            scale[i] = block[F::kKScale + row * F::kGroups + l / 2];
         }
     }
-    __syncwarp();
-#pragma unroll 4
-    for (int row0 = a; row0 < b; row0 += kRows) {
-        const int row = row0 + sub;
-        if (row < b) {
-            uint32_t h[4];
-            float x[8];
-            e2m1x8_to_f16(*reinterpret_cast<const uint32_t *>(block + row * F::kKRow + l * 4), h);
-            const float sk = e4m3_to_f32(block[F::kKScale + row * F::kGroups + l / 2]) * k_scale;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
-                x[2 * i] = v.x * sk;
-                x[2 * i + 1] = v.y * sk;
-            }
-            *reinterpret_cast<int4 *>(ks + (int64_t)(row - a) * stride + l * 8) = f32x8_to_bf16(x);
-            e2m1x8_to_f16(reinterpret_cast<const uint32_t *>(tile.code[row])[l], h);
-            const float sv = e4m3_to_f32(tile.scale[row][l / 2]) * v_scale;
+    for (int i = 0; i < kIters; ++i) {
+        const int row = i * kRows + sub;
+        if (row < a || row >= b) continue;
+        uint32_t h[4];
+        float x[8];
+        e2m1x8_to_f16(code[i], h);
+        const float s = e4m3_to_f32(scale[i]) * g;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
-                x[2 * i] = v.x * sv;
-                x[2 * i + 1] = v.y * sv;
-            }
-            *reinterpret_cast<int4 *>(vs + (int64_t)(row - a) * stride + l * 8) = f32x8_to_bf16(x);
+        for (int k = 0; k < 4; ++k) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[k]));
+            x[2 * k] = v.x * s;
+            x[2 * k + 1] = v.y * s;
         }
+        st_v4(dst + (int64_t)(row - a) * stride + l * 8, f32x8_to_bf16(x));
     }
     __syncwarp();
 }
 
 template <int D>
 __global__ void __launch_bounds__(kKv4Warps * 32) kv4_read_kernel(const Kv4CopyParams p, int batch, int page_slots) {
-    __shared__ __align__(16) Kv4Tile<D> s_tile[kKv4Warps];
+    __shared__ Kv4Tile<D> s_tile[kKv4Warps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t items = (int64_t)batch * page_slots * p.hkv;
+    const int64_t items = (int64_t)batch * page_slots * p.hkv * 2;
     grid_launch_dependents();
     grid_dependency_wait();
     for (int64_t item = (int64_t)blockIdx.x * kKv4Warps + warp; item < items;
          item += (int64_t)gridDim.x * kKv4Warps) {
-        const int h = (int)(item % p.hkv);
-        const int64_t at = item / p.hkv;
-        const int ps = (int)(at % page_slots), bi = (int)(at / page_slots);
-        const int r = p.req_ids ? p.req_ids[bi] : bi;
+        const Kv4Item x(item, p.hkv, page_slots);
+        const int r = p.req_ids ? p.req_ids[x.entry] : x.entry;
         const int L = p.seq_lens[r];
         const int first = p.first ? p.first[r] : 0;
         if (L < 0 || L > p.max_pages * kSubTokens || first < 0) {
-            if (lane == 0 && h == 0 && ps == 0) report(p.dev_status, SFI_DEV_BAD_LEN);
+            if (lane == 0 && x.h == 0 && x.slot == 0) report(p.dev_status, SFI_DEV_BAD_LEN);
             continue;
         }
         const int end = (int)min((int64_t)L, (int64_t)first + p.tokens);
-        const int64_t pos0 = ((int64_t)first / kSubTokens + ps) * kSubTokens;
+        const int64_t pos0 = ((int64_t)first / kSubTokens + x.slot) * kSubTokens;
         const int a = (int)max(first - pos0, (int64_t)0), b = (int)min(end - pos0, (int64_t)kSubTokens);
         if (a >= b) continue;
         const int page = p.page_table[(int64_t)r * p.max_pages + pos0 / kSubTokens];
@@ -216,9 +239,10 @@ __global__ void __launch_bounds__(kKv4Warps * 32) kv4_read_kernel(const Kv4CopyP
             if (lane == 0) report(p.dev_status, SFI_DEV_BAD_PAGE);
             continue;
         }
-        const int64_t row = ((int64_t)r * p.tokens + (pos0 + a - first)) * p.hkv + h;
-        read_block<D>(p.pool + ((int64_t)page * p.hkv + h) * Kv4<D>::kBlock, s_tile[warp], p.k_out + row * D,
-                      p.v_out + row * D, (int64_t)p.hkv * D, a, b, p.k_scale, p.v_scale, lane);
+        const int64_t row = ((int64_t)r * p.tokens + (pos0 + a - first)) * p.hkv + x.h;
+        read_block<D>(p.pool + ((int64_t)page * p.hkv + x.h) * Kv4<D>::kBlock, s_tile[warp],
+                      (x.is_v ? p.v_out : p.k_out) + row * D, (int64_t)p.hkv * D, a, b, x.is_v,
+                      x.is_v ? p.v_scale : p.k_scale, lane);
     }
 }
 
@@ -341,14 +365,14 @@ int copy_grid(int64_t items) {
 
 cudaError_t launch_kv4_append(const Kv4CopyParams &p, int head_dim, int batch, cudaStream_t stream) {
     const int slots = (int)(((int64_t)p.tokens + 30) / 16);  // pages that `tokens` positions can touch
-    const int grid = copy_grid((int64_t)batch * slots * p.hkv);
+    const int grid = copy_grid((int64_t)batch * slots * p.hkv * 2);
     return launch_dependent(head_dim == 128 ? kv4_append_kernel<128> : kv4_append_kernel<64>, grid, kKv4Warps * 32, 0, stream,
                             p, batch, slots);
 }
 
 cudaError_t launch_kv4_read(const Kv4CopyParams &p, int head_dim, int batch, cudaStream_t stream) {
     const int slots = (int)(((int64_t)p.tokens + 30) / 16);
-    const int grid = copy_grid((int64_t)batch * slots * p.hkv);
+    const int grid = copy_grid((int64_t)batch * slots * p.hkv * 2);
     return launch_dependent(head_dim == 128 ? kv4_read_kernel<128> : kv4_read_kernel<64>, grid, kKv4Warps * 32, 0, stream,
                             p, batch, slots);
 }

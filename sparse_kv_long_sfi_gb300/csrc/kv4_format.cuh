@@ -49,10 +49,17 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 // halfway between two codes (or two e4m3 scales) or at least 2^-8.4 of itself away from there:
 // with x = X 2^a (X < 256), the step S 2^b (S < 16, or 3 for the scale itself) and the halfway
 // point T 2^c (T < 32), |X 2^k - T S| is a whole number in the unit where both sides are, hence
-// at least 1 of at most 480. So the value times the step's fp32 reciprocal (off by 2^-22)
+// at least 1 of at most 480. So the value times the step's fp32 reciprocal (off by 2^-21)
 // decides every rounding like the exact quotient once its last bits are rounded away.
 __device__ __forceinline__ float round16(float v) {
     return __uint_as_float((__float_as_uint(v) + 0x80u) & 0xffffff00u);
+}
+
+// 1 / v to 2^-23 of itself.
+__device__ __forceinline__ float reciprocal(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 // The e4m3 scale of a group whose largest magnitude is amax (inv6g: 1 / (6 g)); nearest even,
