@@ -72,8 +72,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+// The stream is read once: it must not push what stays (code, queries, partials) out of L2.
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::256B [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+                 "l"(policy)
+                 : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -233,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, ROWS <= 8 ? 2 : 1) kv4_attn_kernel(c
 
     // ---- copies: this warp's blocks, kDepth of them in flight ----
     uint8_t *ring = smem + warp * T::kRing;
+    const uint64_t policy = l2_policy_evict_first();
     Place ahead{};
     ReqPlan aplan{};
     int ids = 0, ids_base = 0;     // page ids of the unit, 32 at a time (lane i: number ids_base + i)
@@ -273,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, ROWS <= 8 ? 2 : 1) kv4_attn_kernel(c
             uint8_t *dst = ring + slot * F::kBlock + lane * 16;
 #pragma unroll
             for (int c = 0; c < F::kBlock / 16; c += 32)
-                if (c + 32 <= F::kBlock / 16 || lane < F::kBlock / 16 - c) cp_async16(dst + c * 16, src + c * 16);
+                if (c + 32 <= F::kBlock / 16 || lane < F::kBlock / 16 - c) cp_async16(dst + c * 16, src + c * 16, policy);
             --left;
             if (++ahead.pg == aplan.n && left > 0) {
                 ahead.pg = 0;
