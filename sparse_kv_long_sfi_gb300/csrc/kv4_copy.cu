@@ -255,7 +255,6 @@ __global__ void __launch_bounds__(kKv4Warps * 32) kv4_compact_kernel(const Kv4Co
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t items = (int64_t)batch * slots * p.hkv;
     grid_launch_dependents();
-    grid_dependency_wait();
     for (int64_t item = (int64_t)blockIdx.x * kKv4Warps + warp; item < items;
          item += (int64_t)gridDim.x * kKv4Warps) {
         const int h = (int)(item % p.hkv);
@@ -380,8 +379,12 @@ cudaError_t launch_kv4_read(const Kv4CopyParams &p, int head_dim, int batch, cud
 cudaError_t launch_kv4_compact(const Kv4CopyParams &p, int head_dim, int batch, cudaStream_t stream) {
     const int slots = (p.sink + p.k_cap + 15) / 16;
     const int grid = copy_grid((int64_t)batch * slots * p.hkv);
-    return launch_dependent(head_dim == 128 ? kv4_compact_kernel<128> : kv4_compact_kernel<64>, grid, kKv4Warps * 32, 0, stream,
-                            p, batch, slots);
+    // Not a dependent launch: behind an attention launch it would run with the shared-memory
+    // split of that kernel, whose L1 is too small for it (32 requests of 1792 rows and the
+    // attention after them: 134 us a pair against 106 us).
+    auto kernel = head_dim == 128 ? kv4_compact_kernel<128> : kv4_compact_kernel<64>;
+    kernel<<<grid, kKv4Warps * 32, 0, stream>>>(p, batch, slots);
+    return cudaGetLastError();
 }
 
 }  // namespace sfi
