@@ -27,9 +27,6 @@ namespace sfi {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kParts = 2 * kWarps;  // partials of a CTA: the first and the last run of each warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.f;   // the maximum may lag by this (in powers of two)
@@ -40,15 +37,19 @@ enum Kv4Mode : int { kKv4Dense = 0, kKv4Scores = 1, kKv4Fast = 2 };
 
 // ROWS: the query rows of a KV head that a variant takes. Up to four, P's two terms share
 // the N tile (columns 0..3 the first, 4..7 the second, over the same rows); up to eight,
-// they take an instruction each; up to sixteen, there are two N tiles.
+// they take an instruction each; up to sixteen, there are two N tiles, whose accumulators leave
+// room for one CTA per SM.
 template <int D, int ROWS>
 struct Tile {
     static constexpr int kNt = ROWS > 8 ? 2 : 1;
     static constexpr bool kShared = ROWS <= 4;
-    static constexpr int kDepth = kNt == 1 ? 4 : 6;  // blocks in flight per warp
+    static constexpr int kWarps = 8;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kParts = 2 * kWarps;  // partials of a CTA: the first and the last run of each warp
+    static constexpr int kDepth = 4;           // blocks in flight per warp
     static constexpr int kRing = kDepth * Kv4<D>::kBlock;
     static constexpr int kPart = ROWS * D * 4;  // a partial O
-    static constexpr int kFirst = kWarps * kRing;
+    static constexpr int kFirst = kWarps * kRing;  // partials of first runs
     static constexpr int kSmem = kFirst + kWarps * kPart;
     static_assert(kRing >= kPart, "a warp's ring holds its last partial");
     static_assert(kSmem >= kThreads * 24, "the merge's arrays lie where the rings were");
@@ -175,6 +176,7 @@ struct Runs {
 };
 
 // The warps' runs: as many CTAs as give each warp kMinPages blocks, at most the grid's.
+template <int kWarps>
 __device__ __forceinline__ Runs runs_of(const Kv4AttnParams &p, const int64_t *prefix) {
     const int64_t total = prefix[p.batch] * p.hkv;
     const int64_t ctas = min((int64_t)gridDim.x, (total + kWarps * kMinPages - 1) / (kWarps * kMinPages));
@@ -184,10 +186,10 @@ __device__ __forceinline__ Runs runs_of(const Kv4AttnParams &p, const int64_t *p
 }  // namespace
 
 template <int D, int ROWS, int MODE>
-__global__ void __launch_bounds__(kThreads, ROWS <= 8 ? 2 : 1) kv4_attn_kernel(const Kv4AttnParams p) {
+__global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv4_attn_kernel(const Kv4AttnParams p) {
     using F = Kv4<D>;
     using T = Tile<D, ROWS>;
-    constexpr int NT = T::kNt;
+    constexpr int NT = T::kNt, kWarps = T::kWarps, kThreads = T::kThreads, kParts = T::kParts;
     constexpr int kKs = D / 16;  // k steps of S, and m tiles of O
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_prefix[kKv4MaxBatch + 1];
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, ROWS <= 8 ? 2 : 1) kv4_attn_kernel(c
     __syncwarp();
     int64_t f0, f1;
     {
-        const Runs runs = runs_of(p, s_prefix);
+        const Runs runs = runs_of<kWarps>(p, s_prefix);
         if (s_prefix[p.batch] == 0 || (int64_t)blockIdx.x * kWarps >= runs.parts) return;
         f0 = runs.start((int64_t)blockIdx.x * kWarps + warp);
         f1 = runs.start((int64_t)blockIdx.x * kWarps + warp + 1);
@@ -388,11 +390,11 @@ __global__ void __launch_bounds__(kThreads, ROWS <= 8 ? 2 : 1) kv4_attn_kernel(c
             const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
             const float down = __uint_as_float((uint32_t)(127 - shift) << 23);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
+            for (int i = 0; i < D / 32; ++i) {  // k steps 2 i and 2 i + 1: four dims each of these eight
                 float x[8];
                 bf16x8_to_f32(raw[i], x);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {  // k step 2 i + k: dims 4 k .. 4 k + 3 of these eight
+                for (int k = 0; k < 2; ++k) {
                     bq[nt][2 * i + k][0] = pack_f16x2(x[4 * k] * up, x[4 * k + 1] * up);
                     bq[nt][2 * i + k][1] = pack_f16x2(x[4 * k + 2] * up, x[4 * k + 3] * up);
                 }
@@ -410,44 +412,52 @@ __global__ void __launch_bounds__(kThreads, ROWS <= 8 ? 2 : 1) kv4_attn_kernel(c
         }
     };
 
-    // S^T of one block: rows g -> tokens tu and (g + 8) tu + 2, columns 2t, 2t + 1
+    // S^T of PB blocks: rows g -> tokens tu and (g + 8) tu + 2, columns 2t, 2t + 1
     const int tu = 4 * (g >> 1) + (g & 1);
-    auto products = [&](const uint8_t *blk, float (&s)[NT][4]) {
+    auto products = [&](auto pb_tag, const uint8_t *blk0, const uint8_t *blk1, auto &s) {
+        constexpr int PB = decltype(pb_tag)::value;
+        uint32_t ka[PB][D / 32], kb[PB][D / 32];  // codes of the two tokens, dims t D/4 ...
+        uint32_t sa[PB][D / 64], sb[PB][D / 64];  // their scales, twice in a register
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int b = 0; b < PB; ++b) {
+            const uint8_t *blk = b ? blk1 : blk0;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) s[nt][c] = 0.f;
-        uint32_t ka[D / 32], kb[D / 32];  // codes of the two tokens, dims t D/4 ...
-        uint32_t sa[D / 64], sb[D / 64];  // their scales, twice in a register
-        if constexpr (D == 128) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(blk + tu * F::kKRow + t * 16);
-            const uint4 b = *reinterpret_cast<const uint4 *>(blk + (tu + 2) * F::kKRow + t * 16);
-            ka[0] = a.x; ka[1] = a.y; ka[2] = a.z; ka[3] = a.w;
-            kb[0] = b.x; kb[1] = b.y; kb[2] = b.z; kb[3] = b.w;
-            const uint32_t ha = e4m3x2_to_f16(*reinterpret_cast<const uint16_t *>(blk + F::kKScale + tu * 8 + t * 2));
-            const uint32_t hb = e4m3x2_to_f16(*reinterpret_cast<const uint16_t *>(blk + F::kKScale + (tu + 2) * 8 + t * 2));
-            sa[0] = __byte_perm(ha, 0, 0x1010); sa[1] = __byte_perm(ha, 0, 0x3232);
-            sb[0] = __byte_perm(hb, 0, 0x1010); sb[1] = __byte_perm(hb, 0, 0x3232);
-        } else {
-            const uint2 a = *reinterpret_cast<const uint2 *>(blk + tu * F::kKRow + t * 8);
-            const uint2 b = *reinterpret_cast<const uint2 *>(blk + (tu + 2) * F::kKRow + t * 8);
-            ka[0] = a.x; ka[1] = a.y;
-            kb[0] = b.x; kb[1] = b.y;
-            sa[0] = __byte_perm(e4m3x2_to_f16(blk[F::kKScale + tu * 4 + t]), 0, 0x1010);
-            sb[0] = __byte_perm(e4m3x2_to_f16(blk[F::kKScale + (tu + 2) * 4 + t]), 0, 0x1010);
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) s[b][nt][c] = 0.f;
+            if constexpr (D == 128) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(blk + tu * F::kKRow + t * 16);
+                const uint4 y = *reinterpret_cast<const uint4 *>(blk + (tu + 2) * F::kKRow + t * 16);
+                ka[b][0] = x.x; ka[b][1] = x.y; ka[b][2] = x.z; ka[b][3] = x.w;
+                kb[b][0] = y.x; kb[b][1] = y.y; kb[b][2] = y.z; kb[b][3] = y.w;
+                const uint32_t ha = e4m3x2_to_f16(*reinterpret_cast<const uint16_t *>(blk + F::kKScale + tu * 8 + t * 2));
+                const uint32_t hb =
+                    e4m3x2_to_f16(*reinterpret_cast<const uint16_t *>(blk + F::kKScale + (tu + 2) * 8 + t * 2));
+                sa[b][0] = __byte_perm(ha, 0, 0x1010); sa[b][1] = __byte_perm(ha, 0, 0x3232);
+                sb[b][0] = __byte_perm(hb, 0, 0x1010); sb[b][1] = __byte_perm(hb, 0, 0x3232);
+            } else {
+                const uint2 x = *reinterpret_cast<const uint2 *>(blk + tu * F::kKRow + t * 8);
+                const uint2 y = *reinterpret_cast<const uint2 *>(blk + (tu + 2) * F::kKRow + t * 8);
+                ka[b][0] = x.x; ka[b][1] = x.y;
+                kb[b][0] = y.x; kb[b][1] = y.y;
+                sa[b][0] = __byte_perm(e4m3x2_to_f16(blk[F::kKScale + tu * 4 + t]), 0, 0x1010);
+                sb[b][0] = __byte_perm(e4m3x2_to_f16(blk[F::kKScale + (tu + 2) * 4 + t]), 0, 0x1010);
+            }
         }
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
-            uint32_t xa[4], xb[4];
-            e2m1x8_to_f16(ka[w], xa);
-            e2m1x8_to_f16(kb[w], xb);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t a[4] = {hmul2(xa[2 * k], sa[w / 2]), hmul2(xb[2 * k], sb[w / 2]),
-                                       hmul2(xa[2 * k + 1], sa[w / 2]), hmul2(xb[2 * k + 1], sb[w / 2])};
+            for (int b = 0; b < PB; ++b) {
+                uint32_t xa[4], xb[4];
+                e2m1x8_to_f16(ka[b][w], xa);
+                e2m1x8_to_f16(kb[b][w], xb);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma_f16_16816(s[nt], a, bq[nt][2 * w + k][0], bq[nt][2 * w + k][1]);
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t a[4] = {hmul2(xa[2 * k], sa[b][w / 2]), hmul2(xb[2 * k], sb[b][w / 2]),
+                                           hmul2(xa[2 * k + 1], sa[b][w / 2]), hmul2(xb[2 * k + 1], sb[b][w / 2])};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[b][nt], a, bq[nt][2 * w + k][0], bq[nt][2 * w + k][1]);
+                }
             }
         }
     };
@@ -459,8 +469,7 @@ __global__ void __launch_bounds__(kThreads, ROWS <= 8 ? 2 : 1) kv4_attn_kernel(c
         const bool comp = EDGE && MODE == kKv4Fast && at.pg < plan.ncomp;
         const int pos0 = 16 * (comp ? at.pg : plan.page0 + at.pg - plan.ncomp);
         float s[PB][NT][4];
-#pragma unroll
-        for (int b = 0; b < PB; ++b) products(b ? blk1 : blk0, s[b]);
+        products(pb_tag, blk0, blk1, s);
         if constexpr (!EDGE) {
             // V scales in fp16 for the whole warp, where the K codes were: lane w converts word w
             // (four tokens of one group)
@@ -700,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, ROWS <= 8 ? 2 : 1) kv4_attn_kernel(c
         const int part = warp * 2 + (last ? 1 : 0);
         if (lane == 0 && !whole) {
             s_unit[part] = at.b * p.hkv + at.h;
-            s_unit0[part] = runs_of(p, s_prefix).start((int64_t)blockIdx.x * kWarps + warp) + unit0;
+            s_unit0[part] = runs_of<kWarps>(p, s_prefix).start((int64_t)blockIdx.x * kWarps + warp) + unit0;
             s_bad[part] = bad;
         }
         if (bad) return;
@@ -720,8 +729,7 @@ __global__ void __launch_bounds__(kThreads, ROWS <= 8 ? 2 : 1) kv4_attn_kernel(c
                 }
             }
         const int r = request_id(p, at.b);
-        float *dst = last ? reinterpret_cast<float *>(ring)
-                          : reinterpret_cast<float *>(smem + T::kFirst + warp * T::kPart);
+        float *dst = reinterpret_cast<float *>(last ? ring : smem + T::kFirst + warp * T::kPart);
         if (!whole && last) {  // the ring is done with once every copy has landed
             cp_async_wait<0>();
             __syncwarp();
@@ -763,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, ROWS <= 8 ? 2 : 1) kv4_attn_kernel(c
         if (tid < kKv4MaxBatch / 32) s_drop[tid] = 0;
         if (tid == 0) s_last[0] = run > 0 ? at.b : 0;
         __syncthreads();
-        const int64_t end = runs_of(p, s_prefix).start((int64_t)(blockIdx.x + 1) * kWarps);
+        const int64_t end = runs_of<kWarps>(p, s_prefix).start((int64_t)(blockIdx.x + 1) * kWarps);
         for (int b = s_last[0]; b < p.batch && s_prefix[b] * p.hkv < end; ++b) {
             const int n = (int)(s_prefix[b + 1] - s_prefix[b]);
             const int32_t *row = p.page_table + (int64_t)request_id(p, b) * p.max_pages;
@@ -827,11 +835,11 @@ __global__ void __launch_bounds__(kThreads, ROWS <= 8 ? 2 : 1) kv4_attn_kernel(c
 
     // ---- the CTA's partials, unit by unit: the unit's output where the CTA holds all of it, else
     // the CTA's part of it (s_open: units begun before this CTA, or going on after it) ----
-    const Runs runs = runs_of(p, s_prefix);
+    const Runs runs = runs_of<kWarps>(p, s_prefix);
     const int64_t cta0 = runs.start((int64_t)blockIdx.x * kWarps), cta1 = runs.start((int64_t)(blockIdx.x + 1) * kWarps);
     const int my_unit = lane < kParts ? s_unit[lane] : -1;
     const uint32_t mine = __match_any_sync(0xffffffffu, my_unit);
-    const uint32_t bads = __ballot_sync(0xffffffffu, lane < kParts && my_unit >= 0 && s_bad[lane & (kParts - 1)]);
+    const uint32_t bads = __ballot_sync(0xffffffffu, lane < kParts && my_unit >= 0 && s_bad[min(lane, kParts - 1)]);
     for (uint32_t todo = __ballot_sync(0xffffffffu, my_unit >= 0); todo;) {
         const int first = __ffs(todo) - 1;
         const int u = __shfl_sync(0xffffffffu, my_unit, first);
@@ -850,20 +858,18 @@ __global__ void __launch_bounds__(kThreads, ROWS <= 8 ? 2 : 1) kv4_attn_kernel(c
         }
         for (int e = tid; e < p.rows * (D / 4) && !(complete && bad); e += kThreads) {
             const int row = e / (D / 4), d = e % (D / 4) * 4;
-            float m[kParts];
             float mx = -INFINITY, sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < kParts; ++k) {
-                m[k] = (parts >> k) & 1u ? s_ml[k][row][0] : -INFINITY;
-                mx = fmaxf(mx, m[k]);
-            }
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < kParts; ++k) {
-                if (!((parts >> k) & 1u)) continue;
-                const float w = m[k] == mx ? 1.f : fast_exp2(m[k] - mx);
-                const float4 x = *reinterpret_cast<const float4 *>(
-                    smem + ((k & 1) ? (k >> 1) * T::kRing : T::kFirst + (k >> 1) * T::kPart) + (row * D + d) * 4);
+            // loops over the parts that are there, kept rolled: most of their time is fetching code
+#pragma unroll 1
+            for (uint32_t left = parts; left; left &= left - 1) mx = fmaxf(mx, s_ml[__ffs(left) - 1][row][0]);
+#pragma unroll 1
+            for (uint32_t left = parts; left; left &= left - 1) {
+                const int k = __ffs(left) - 1;
+                const float m = s_ml[k][row][0];
+                const float w = m == mx ? 1.f : fast_exp2(m - mx);
+                const uint8_t *part = smem + ((k & 1) ? (k >> 1) * T::kRing : T::kFirst + (k >> 1) * T::kPart);
+                const float4 x = *reinterpret_cast<const float4 *>(part + (row * D + d) * 4);
                 sum = fmaf(w, s_ml[k][row][1], sum);
                 acc.x = fmaf(w, x.x, acc.x);
                 acc.y = fmaf(w, x.y, acc.y);
@@ -999,7 +1005,7 @@ cudaError_t launch_one(const Kv4AttnParams &p, int ctas, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit, std::memory_order_acq_rel);
     }
-    return launch_dependent(kernel, ctas, kThreads, Tile<D, ROWS>::kSmem, stream, p);
+    return launch_dependent(kernel, ctas, Tile<D, ROWS>::kThreads, Tile<D, ROWS>::kSmem, stream, p);
 }
 
 template <int D, int ROWS>
