@@ -498,7 +498,9 @@ typedef struct {
  *   k_out     : bf16 [B][T][Hkv][D], or NULL
  *   kv        : the pages that receive K and V at the tokens' slots, or NULL (then rope
  *               without positions is refused)
- * Outputs must not overlap inputs. At least one of k_out and kv must be given.
+ * Outputs must not overlap inputs. At least one of k_out and kv must be given. An attention
+ * call that follows on the stream and reads the pages written here must not be given
+ * SFI_ATTN_EARLY_KV_PREFETCH.
  * Device errors: SFI_DEV_BAD_LEN (n_r < 0, n_r > T, or with kv L_r < n_r or L_r beyond the
  * page table: nothing of that request is written), SFI_DEV_BAD_PAGE (that token's K and V
  * are not written to the pages), SFI_DEV_BAD_INDEX (an axis[i] >= num_axes: pair i does

@@ -372,6 +372,25 @@ def rope_turns(inv_freq, device="cuda") -> torch.Tensor:
     return torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
 
 
+def _requests(kv, batch, req_ids, **arrays) -> int:
+    """The number of requests a call takes; arrays indexed by request id must cover the table's
+    requests."""
+    B = kv.page_table.shape[0]
+    if kv.seq_lens.numel() != B:
+        raise ValueError("seq_lens needs one entry per row of page_table")
+    for name, t in arrays.items():
+        if t is not None and t.shape[0] != B:
+            raise ValueError(f"{name} needs one entry for each of {B} requests, has {t.shape[0]}")
+    if req_ids is not None:
+        n = req_ids.numel()
+        if batch is not None and batch > n:
+            raise ValueError(f"batch {batch} is beyond the {n} req_ids")
+        return n if batch is None else int(batch)
+    if batch is not None and batch > B:
+        raise ValueError(f"batch {batch} is beyond the {B} requests")
+    return B if batch is None else int(batch)
+
+
 def _on_current_device(t: torch.Tensor, name: str):
     if t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on {t.device}, not on the current device")
@@ -419,14 +438,22 @@ def sfi_qk_norm_rope(shape: AttnShape, rope: Optional[Rope], q: torch.Tensor, k:
         raise ValueError("positions must be [num_axes][B][T]")
     if new_lens is not None and new_lens.numel() != B:
         raise ValueError("new_lens needs one entry per request")
+    if kv is not None:
+        n = _requests(kv, batch, req_ids, q=q)
+        if kv.k_pool.shape != kv.v_pool.shape or tuple(kv.k_pool.shape[1:]) != (hkv, shape.page_size, d):
+            raise ValueError(f"the pools must be [num_pages][{hkv}][{shape.page_size}][{d}]")
+    else:
+        n = B if req_ids is None else req_ids.numel()
+        if batch is not None and batch > n:
+            raise ValueError(f"batch {batch} is beyond the {n} requests")
+        n = n if batch is None else int(batch)
     st = _abi.lib().sfi_qk_norm_rope(
         ctypes.byref(shape.c()), None if rope is None else ctypes.byref(rope.c()), q.data_ptr(), qs, k.data_ptr(), ks,
         None if v is None else v.data_ptr(), vs, _ptr(q_weight, torch.bfloat16, "q_weight"),
         _ptr(k_weight, torch.bfloat16, "k_weight"), float(eps), _ptr(positions, torch.int32, "positions"), B * T, T,
         _ptr(new_lens, torch.int32, "new_lens"), _ptr(q_out, torch.bfloat16, "q_out"),
         _ptr(k_out, torch.bfloat16, "k_out"), None if kv is None else ctypes.byref(kv.c()),
-        _ptr(req_ids, torch.int32, "req_ids"), B if batch is None and req_ids is None else _batch(batch, req_ids, None),
-        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+        _ptr(req_ids, torch.int32, "req_ids"), n, _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
     _check(st, "sfi_qk_norm_rope")
 
 
@@ -474,6 +501,11 @@ def _kv4(shape: AttnShape, kv: PagedKV4):
     return ctypes.byref(kv.c())
 
 
+def _compact4(shape: AttnShape, compact: CompactKV4):
+    if compact.pool.dim() != 2 or compact.pool.shape[1] != 18 * shape.head_dim:
+        raise ValueError(f"compact.pool must be [total_pages][{18 * shape.head_dim}]")
+
+
 def alloc_kv4_pool(shape: AttnShape, num_pages: int, device="cuda") -> torch.Tensor:
     """A zero-filled pool of the 4-bit cache."""
     return torch.zeros((num_pages, shape.num_kv_heads, 18 * shape.head_dim), dtype=torch.uint8, device=device)
@@ -503,10 +535,11 @@ def sfi_kv4_append(shape: AttnShape, kv: PagedKV4, k_new: torch.Tensor, v_new: t
     T = _rows4(k_new, torch.bfloat16, shape, shape.num_kv_heads, "k_new")
     if _rows4(v_new, torch.bfloat16, shape, shape.num_kv_heads, "v_new") != T or v_new.shape != k_new.shape:
         raise ValueError("k_new and v_new need the same shape")
+    n = _requests(kv, batch, req_ids, k_new=k_new, new_lens=new_lens)
     st = _abi.lib().sfi_kv4_append(
         ctypes.byref(shape.c()), _kv4(shape, kv), k_new.data_ptr(), v_new.data_ptr(), T,
         _ptr(new_lens, torch.int32, "new_lens"), _ptr(req_ids, torch.int32, "req_ids"),
-        _batch(batch, req_ids, kv.seq_lens), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+        n, _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
     _check(st, "sfi_kv4_append")
 
 
@@ -516,20 +549,25 @@ def sfi_kv4_read(shape: AttnShape, kv: PagedKV4, k_out: torch.Tensor, v_out: tor
     T = _rows4(k_out, torch.bfloat16, shape, shape.num_kv_heads, "k_out")
     if _rows4(v_out, torch.bfloat16, shape, shape.num_kv_heads, "v_out") != T or v_out.shape != k_out.shape:
         raise ValueError("k_out and v_out need the same shape")
+    n = _requests(kv, batch, req_ids, k_out=k_out, first=first)
     st = _abi.lib().sfi_kv4_read(
         ctypes.byref(shape.c()), _kv4(shape, kv), k_out.data_ptr(), v_out.data_ptr(), T,
         _ptr(first, torch.int32, "first"), _ptr(req_ids, torch.int32, "req_ids"),
-        _batch(batch, req_ids, kv.seq_lens), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+        n, _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
     _check(st, "sfi_kv4_read")
 
 
 def sfi_kv4_compact_gather(shape: AttnShape, kv: PagedKV4, idx: torch.Tensor, count: torch.Tensor, sink: int,
                            compact: CompactKV4, req_ids: Optional[torch.Tensor] = None, batch: Optional[int] = None,
                            dev_status: Optional[torch.Tensor] = None, stream=None):
+    if idx.dim() != 3 or idx.shape[1] != shape.num_kv_heads:
+        raise ValueError(f"idx must be [B][{shape.num_kv_heads}][k_cap]")
+    _compact4(shape, compact)
+    n = _requests(kv, batch, req_ids, idx=idx, count=count, page_offset=compact.page_offset, capacity=compact.capacity)
     st = _abi.lib().sfi_kv4_compact_gather(
         ctypes.byref(shape.c()), _kv4(shape, kv), _ptr(idx, torch.int32, "idx"), _ptr(count, torch.int32, "count"),
         int(idx.shape[-1]), int(sink), ctypes.byref(compact.c()), _ptr(req_ids, torch.int32, "req_ids"),
-        _batch(batch, req_ids, kv.seq_lens), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+        n, _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
     _check(st, "sfi_kv4_compact_gather")
 
 
@@ -546,13 +584,17 @@ def sfi_kv4_dense_attn(shape: AttnShape, kv: PagedKV4, sink: int, recent: int, q
                        req_ids: Optional[torch.Tensor] = None, batch: Optional[int] = None,
                        workspace: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
                        stream=None):
-    """q [B][T][Hq][D] (T query tokens per request), out fp32 of that shape, lse [B][T][Hq]."""
+    """q [B][T][Hq][D] (T query tokens per request), out fp32 of that shape, lse [B][T][Hq],
+    scores [B][Hkv][score_stride]."""
     T = _kv4_query(shape, q, out, lse)
+    if scores is not None and (scores.dim() != 3 or scores.shape[1] != shape.num_kv_heads):
+        raise ValueError(f"scores must be [B][{shape.num_kv_heads}][score_stride]")
+    n = _requests(kv, batch, req_ids, q=q, scores=scores)
     st = _abi.lib().sfi_kv4_dense_attn(
         ctypes.byref(shape.c()), _kv4(shape, kv), int(sink), int(recent), q.data_ptr(), T, out.data_ptr(),
         _ptr(lse, torch.float32, "lse"), _ptr(scores, torch.float32, "scores"),
         0 if scores is None else int(scores.shape[-1]), _ptr(req_ids, torch.int32, "req_ids"),
-        _batch(batch, req_ids, kv.seq_lens), _ptr(workspace, torch.uint8, "workspace"),
+        n, _ptr(workspace, torch.uint8, "workspace"),
         0 if workspace is None else workspace.numel(), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
     _check(st, "sfi_kv4_dense_attn")
 
@@ -563,10 +605,12 @@ def sfi_kv4_fast_attn(shape: AttnShape, kv: PagedKV4, compact: CompactKV4, sink:
                       dev_status: Optional[torch.Tensor] = None, stream=None):
     """q [B][T][Hq][D] (T query tokens per request), out fp32 of that shape, lse [B][T][Hq]."""
     T = _kv4_query(shape, q, out, lse)
+    _compact4(shape, compact)
+    n = _requests(kv, batch, req_ids, q=q, page_offset=compact.page_offset, capacity=compact.capacity, count=compact.count)
     st = _abi.lib().sfi_kv4_fast_attn(
         ctypes.byref(shape.c()), _kv4(shape, kv), ctypes.byref(compact.c()), int(sink), int(recent), q.data_ptr(), T,
         out.data_ptr(), _ptr(lse, torch.float32, "lse"), _ptr(req_ids, torch.int32, "req_ids"),
-        _batch(batch, req_ids, kv.seq_lens), _ptr(workspace, torch.uint8, "workspace"),
+        n, _ptr(workspace, torch.uint8, "workspace"),
         0 if workspace is None else workspace.numel(), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
     _check(st, "sfi_kv4_fast_attn")
 
@@ -666,8 +710,9 @@ def sfi_page_free(page_map: PageMap, reqs: torch.Tensor, dev_status: Optional[to
 def sfi_page_compact(page_map: PageMap, pools: PagePools, table_out: torch.Tensor, ref_out: torch.Tensor,
                      live_out: torch.Tensor, workspace: Optional[torch.Tensor] = None,
                      dev_status: Optional[torch.Tensor] = None, stream=None):
-    if table_out.shape != page_map.page_table.shape or ref_out.numel() != page_map.ref_count.numel():
-        raise ValueError("table_out and ref_out need the shapes of page_table and ref_count")
+    if (table_out.shape != page_map.page_table.shape or ref_out.numel() != page_map.ref_count.numel()
+            or live_out.numel() < 1):
+        raise ValueError("table_out and ref_out need the shapes of page_table and ref_count, live_out one entry")
     st = _abi.lib().sfi_page_compact(
         ctypes.byref(page_map.c()), ctypes.byref(pools.c()), _ptr(table_out, torch.int32, "table_out"),
         _ptr(ref_out, torch.int32, "ref_out"), _ptr(live_out, torch.int32, "live_out"),

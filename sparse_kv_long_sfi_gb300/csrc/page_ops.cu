@@ -6,6 +6,10 @@
 // one CTA that scans the counts in page order (ranks by prefix sums), and lists are
 // written at those ranks. The bytes move in a second launch that reads the list's length
 // on the device; it is bound by HBM (a page is read and written once per pool).
+//
+// The kernels wait for the stream's previous kernel as dependent launches, but none releases
+// its own dependents early: they write page tables, lengths and pages, which an attention
+// launch may be allowed to read ahead of its wait (SFI_ATTN_EARLY_KV_PREFETCH).
 #include <algorithm>
 
 #include "sfi_device.cuh"
@@ -61,7 +65,6 @@ __global__ void __launch_bounds__(kPageThreads) page_copy_kernel(void *const *po
                                                                  int n_host, const int32_t *n_dev,
                                                                  int32_t *dev_status) {
     constexpr int kLoads = kCopyChunk / 16 / kPageThreads;
-    grid_launch_dependents();
     grid_dependency_wait();
     const int n = n_dev ? *n_dev : n_host;
     const int chunks = (int)((page_bytes + kCopyChunk - 1) / kCopyChunk);
@@ -93,7 +96,6 @@ __global__ void __launch_bounds__(kPageThreads) page_copy_kernel(void *const *po
 __global__ void __launch_bounds__(kPageThreads) page_fork_kernel(const PageMapParams m, const int32_t *src,
                                                                  const int32_t *dst, const int32_t *fork_lens,
                                                                  int32_t *dev_status) {
-    grid_launch_dependents();
     grid_dependency_wait();
     const int a = src[blockIdx.x], z = dst[blockIdx.x];
     uint32_t err = 0;
@@ -125,7 +127,6 @@ __global__ void __launch_bounds__(kPageThreads) page_fork_kernel(const PageMapPa
 
 __global__ void __launch_bounds__(kPageThreads) page_free_kernel(const PageMapParams m, const int32_t *reqs,
                                                                  int32_t *dev_status) {
-    grid_launch_dependents();
     grid_dependency_wait();
     const int r = reqs ? reqs[blockIdx.x] : blockIdx.x;
     if (r < 0 || r >= m.num_reqs) {
@@ -166,7 +167,6 @@ __global__ void __launch_bounds__(kPlanThreads) page_reserve_kernel(const PageMa
     __shared__ int s_warp[kPlanWarps];
     __shared__ int2 s_entry[kPlanThreads];  // request and part-filled last page (or -1) of list entry i
     __shared__ int s_first[kPlanThreads];   // rank of its first page among those handed out
-    grid_launch_dependents();
     grid_dependency_wait();
     const PageLists lists(ws, m.num_pages);
     const int tid = threadIdx.x;
@@ -273,7 +273,6 @@ __global__ void __launch_bounds__(kPlanThreads) page_reserve_kernel(const PageMa
 __global__ void __launch_bounds__(kPlanThreads) page_compact_plan_kernel(const PageMapParams m, int32_t *ref_out,
                                                                          int32_t *live_out, void *ws) {
     __shared__ int s_warp[kPlanWarps];
-    grid_launch_dependents();
     grid_dependency_wait();
     const PageLists lists(ws, m.num_pages);
     const int tid = threadIdx.x;
@@ -335,7 +334,6 @@ __global__ void __launch_bounds__(kPlanThreads) page_compact_plan_kernel(const P
 
 __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageMapParams m, int32_t *table_out, void *ws,
                                                                   int32_t *dev_status) {
-    grid_launch_dependents();
     grid_dependency_wait();
     const PageLists lists(ws, m.num_pages);
     const int r = blockIdx.x;

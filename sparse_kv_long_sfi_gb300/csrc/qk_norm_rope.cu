@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, HALVES ? 3 : 2) qk_norm_rope_
     const bool second = l * 8 >= half;  // this lane's dims are the second members (split halves)
     // the lane that holds the other members of this lane's pairs (split halves)
     const int mate = p.interleaved || !rotated ? lane : (second ? lane - half / 8 : lane + half / 8);
-    grid_launch_dependents();
+    // (no early release of dependents: an attention launch may be allowed to read the pages ahead)
     grid_dependency_wait();
 
     for (int64_t item = (int64_t)blockIdx.x * kNormWarps + warp; item < items; item += (int64_t)gridDim.x * kNormWarps) {
