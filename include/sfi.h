@@ -494,23 +494,24 @@ typedef struct {
  *   q_weight, k_weight : bf16 [D], 16-byte aligned, or NULL: no norm for q (for k)
  *   positions : int32, axis a of token t of request r at a * axis_stride + r T + t; or NULL:
  *               the slot is the position on every axis. Positions may be negative.
+ *   seq_lens  : int32 [B], the lengths L_r when kv is NULL (with kv its own are used), or NULL
  *   q_out     : bf16 [B][T][Hq][D]
  *   k_out     : bf16 [B][T][Hkv][D], or NULL
  *   kv        : the pages that receive K and V at the tokens' slots, or NULL (then rope
- *               without positions is refused)
+ *               needs positions or seq_lens)
  * Outputs must not overlap inputs. At least one of k_out and kv must be given. An attention
  * call that follows on the stream and reads the pages written here must not be given
  * SFI_ATTN_EARLY_KV_PREFETCH.
- * Device errors: SFI_DEV_BAD_LEN (n_r < 0, n_r > T, or with kv L_r < n_r or L_r beyond the
- * page table: nothing of that request is written), SFI_DEV_BAD_PAGE (that token's K and V
+ * Device errors: SFI_DEV_BAD_LEN (n_r < 0, n_r > T, L_r < n_r, or L_r beyond the page
+ * table: nothing of that request is written), SFI_DEV_BAD_PAGE (that token's K and V
  * are not written to the pages), SFI_DEV_BAD_INDEX (an axis[i] >= num_axes: pair i does
  * not turn).
  */
 SFI_API sfi_status sfi_qk_norm_rope(const sfi_attn_shape *shape, const sfi_rope *rope, const void *q, int64_t q_stride,
                                     const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                                     const void *q_weight, const void *k_weight, float eps, const int32_t *positions,
-                                    int64_t axis_stride, int32_t num_tokens, const int32_t *new_lens, void *q_out,
-                                    void *k_out, const sfi_paged_kv *kv, const int32_t *req_ids, int32_t batch,
+                                    int64_t axis_stride, int32_t num_tokens, const int32_t *new_lens,
+                                    const int32_t *seq_lens, void *q_out, void *k_out, const sfi_paged_kv *kv, const int32_t *req_ids, int32_t batch,
                                     int32_t *dev_status, void *stream);
 
 /*
@@ -555,12 +556,14 @@ typedef struct {
  * num_tokens when new_lens is NULL) into the pages: token t < n_r goes to position
  * L_r - n_r + t. Other positions of a page keep their bits. The requests of one call must
  * not share the pages they write.
- *   k_new, v_new : bf16 [B][num_tokens][Hkv][D], 16-byte aligned
+ *   k_new, v_new : bf16, 16-byte aligned; token t of request r starts at element
+ *                  (r num_tokens + t) * k_stride (v_stride), its heads are contiguous [Hkv][D];
+ *                  strides are multiples of 8
  * Device errors: SFI_DEV_BAD_LEN (n_r < 0, n_r > num_tokens, L_r < n_r or L_r beyond the page
  * table: that request is skipped), SFI_DEV_BAD_PAGE (that page's tokens are skipped).
  */
 SFI_API sfi_status sfi_kv4_append(const sfi_attn_shape *shape, const sfi_paged_kv4 *kv, const void *k_new,
-                                  const void *v_new, int32_t num_tokens, const int32_t *new_lens,
+                                  int64_t k_stride, const void *v_new, int64_t v_stride, int32_t num_tokens, const int32_t *new_lens,
                                   const int32_t *req_ids, int32_t batch, int32_t *dev_status, void *stream);
 
 /*

@@ -99,8 +99,8 @@ PROTOTYPES = {
     "sfi_plan_splits": (c_i32, [P_SHAPE, c_i32, c_i32, c_i32]),
     "sfi_attn_cluster_capacity": (c_i32, [c_i32]),
     "sfi_qk_norm_rope": (c_i32, [P_SHAPE, P_ROPE, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_f32, c_vp, c_i64,
-                                 c_i32, c_vp, c_vp, c_vp, P_PAGED, c_vp, c_i32, c_vp, c_vp]),
-    "sfi_kv4_append": (c_i32, [P_SHAPE, P_KV4, c_vp, c_vp, c_i32, c_vp, c_vp, c_i32, c_vp, c_vp]),
+                                 c_i32, c_vp, c_vp, c_vp, c_vp, P_PAGED, c_vp, c_i32, c_vp, c_vp]),
+    "sfi_kv4_append": (c_i32, [P_SHAPE, P_KV4, c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_vp, c_i32, c_vp, c_vp]),
     "sfi_kv4_read": (c_i32, [P_SHAPE, P_KV4, c_vp, c_vp, c_i32, c_vp, c_vp, c_i32, c_vp, c_vp]),
     "sfi_kv4_compact_gather": (c_i32, [P_SHAPE, P_KV4, c_vp, c_vp, c_i32, c_i32, P_COMPACT4, c_vp, c_i32, c_vp, c_vp]),
     "sfi_kv4_dense_attn": (c_i32, [P_SHAPE, P_KV4, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp, c_vp, c_i64, c_vp, c_i32, c_vp,

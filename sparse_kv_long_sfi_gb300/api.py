@@ -417,7 +417,8 @@ def sfi_qk_norm_rope(shape: AttnShape, rope: Optional[Rope], q: torch.Tensor, k:
                      v: Optional[torch.Tensor], q_out: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
                      k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
                      positions: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
-                     k_out: Optional[torch.Tensor] = None, kv: Optional[PagedKV] = None,
+                     seq_lens: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                     kv: Optional[PagedKV] = None,
                      req_ids: Optional[torch.Tensor] = None, batch: Optional[int] = None,
                      dev_status: Optional[torch.Tensor] = None, stream=None):
     """Head norm and rotation of the new tokens; q, k, v [B][T][heads][D] may be views of one
@@ -436,8 +437,8 @@ def sfi_qk_norm_rope(shape: AttnShape, rope: Optional[Rope], q: torch.Tensor, k:
             raise ValueError(f"{name} must have {d} values")
     if positions is not None and positions.numel() != (rope.num_axes if rope is not None else 1) * B * T:
         raise ValueError("positions must be [num_axes][B][T]")
-    if new_lens is not None and new_lens.numel() != B:
-        raise ValueError("new_lens needs one entry per request")
+    if (new_lens is not None and new_lens.numel() != B) or (seq_lens is not None and seq_lens.numel() != B):
+        raise ValueError("new_lens and seq_lens need one entry per request")
     if kv is not None:
         n = _requests(kv, batch, req_ids, q=q)
         if kv.k_pool.shape != kv.v_pool.shape or tuple(kv.k_pool.shape[1:]) != (hkv, shape.page_size, d):
@@ -451,7 +452,8 @@ def sfi_qk_norm_rope(shape: AttnShape, rope: Optional[Rope], q: torch.Tensor, k:
         ctypes.byref(shape.c()), None if rope is None else ctypes.byref(rope.c()), q.data_ptr(), qs, k.data_ptr(), ks,
         None if v is None else v.data_ptr(), vs, _ptr(q_weight, torch.bfloat16, "q_weight"),
         _ptr(k_weight, torch.bfloat16, "k_weight"), float(eps), _ptr(positions, torch.int32, "positions"), B * T, T,
-        _ptr(new_lens, torch.int32, "new_lens"), _ptr(q_out, torch.bfloat16, "q_out"),
+        _ptr(new_lens, torch.int32, "new_lens"), _ptr(seq_lens, torch.int32, "seq_lens"),
+        _ptr(q_out, torch.bfloat16, "q_out"),
         _ptr(k_out, torch.bfloat16, "k_out"), None if kv is None else ctypes.byref(kv.c()),
         _ptr(req_ids, torch.int32, "req_ids"), n, _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
     _check(st, "sfi_qk_norm_rope")
@@ -532,12 +534,14 @@ def _rows4(t: torch.Tensor, dtype, shape: AttnShape, heads: int, name: str) -> i
 def sfi_kv4_append(shape: AttnShape, kv: PagedKV4, k_new: torch.Tensor, v_new: torch.Tensor,
                    new_lens: Optional[torch.Tensor] = None, req_ids: Optional[torch.Tensor] = None,
                    batch: Optional[int] = None, dev_status: Optional[torch.Tensor] = None, stream=None):
-    T = _rows4(k_new, torch.bfloat16, shape, shape.num_kv_heads, "k_new")
-    if _rows4(v_new, torch.bfloat16, shape, shape.num_kv_heads, "v_new") != T or v_new.shape != k_new.shape:
+    """k_new, v_new [B][T][Hkv][D]; either may be a view of a fused projection (contiguous heads)."""
+    ks = _token_rows(k_new, shape.num_kv_heads, shape.head_dim, "k_new")
+    vs = _token_rows(v_new, shape.num_kv_heads, shape.head_dim, "v_new")
+    if v_new.shape != k_new.shape:
         raise ValueError("k_new and v_new need the same shape")
     n = _requests(kv, batch, req_ids, k_new=k_new, new_lens=new_lens)
     st = _abi.lib().sfi_kv4_append(
-        ctypes.byref(shape.c()), _kv4(shape, kv), k_new.data_ptr(), v_new.data_ptr(), T,
+        ctypes.byref(shape.c()), _kv4(shape, kv), k_new.data_ptr(), ks, v_new.data_ptr(), vs, k_new.shape[1],
         _ptr(new_lens, torch.int32, "new_lens"), _ptr(req_ids, torch.int32, "req_ids"),
         n, _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
     _check(st, "sfi_kv4_append")

@@ -151,9 +151,10 @@ __global__ void __launch_bounds__(kKv4Warps * 32) kv4_append_kernel(const Kv4Cop
             if (lane == 0) report(p.dev_status, SFI_DEV_BAD_PAGE);
             continue;
         }
-        const int64_t row = ((int64_t)r * p.tokens + (pos0 + a - first)) * p.hkv + x.h;
-        write_block<D>(p.pool + ((int64_t)page * p.hkv + x.h) * Kv4<D>::kBlock, s_tile[warp],
-                       (x.is_v ? p.v_new : p.k_new) + row * D, (int64_t)p.hkv * D, a, b, x.is_v,
+        const int64_t stride = x.is_v ? p.v_stride : p.k_stride;
+        const __nv_bfloat16 *src = (x.is_v ? p.v_new : p.k_new) +
+                                   ((int64_t)r * p.tokens + (pos0 + a - first)) * stride + (int64_t)x.h * D;
+        write_block<D>(p.pool + ((int64_t)page * p.hkv + x.h) * Kv4<D>::kBlock, s_tile[warp], src, stride, a, b, x.is_v,
                        x.is_v ? p.v_scale : p.k_scale, lane);
     }
 }

@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, HALVES ? 3 : 2) qk_norm_rope_
         bool bad = n < 0 || n > p.tokens;
         if (p.seq_lens) {
             const int L = p.seq_lens[r];
-            bad = bad || L < n || L > p.max_pages * kSubTokens;
+            bad = bad || L < n || (p.page_table && L > p.max_pages * kSubTokens);
             slot = L - n + t;
         }
         if (bad) {
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, HALVES ? 3 : 2) qk_norm_rope_
         }
         if (t >= n) continue;
         const int64_t row_tok = (int64_t)r * p.tokens + t;
-        if (p.seq_lens) {
+        if (p.page_table) {
             page = p.page_table[(int64_t)r * p.max_pages + slot / kSubTokens];
             if (page < 0 || page >= p.num_pages) {
                 page = -1;

@@ -154,8 +154,8 @@ extern "C" {
 sfi_status sfi_qk_norm_rope(const sfi_attn_shape *shape, const sfi_rope *rope, const void *q, int64_t q_stride,
                             const void *k, int64_t k_stride, const void *v, int64_t v_stride, const void *q_weight,
                             const void *k_weight, float eps, const int32_t *positions, int64_t axis_stride,
-                            int32_t num_tokens, const int32_t *new_lens, void *q_out, void *k_out,
-                            const sfi_paged_kv *kv, const int32_t *req_ids, int32_t batch, int32_t *dev_status,
+                            int32_t num_tokens, const int32_t *new_lens, const int32_t *seq_lens, void *q_out,
+                            void *k_out, const sfi_paged_kv *kv, const int32_t *req_ids, int32_t batch, int32_t *dev_status,
                             void *stream) {
     sfi_status st = sfi::check_shape(shape);
     if (st != SFI_OK) return st;
@@ -173,7 +173,7 @@ sfi_status sfi_qk_norm_rope(const sfi_attn_shape *shape, const sfi_rope *rope, c
         if (rope->rot_dim < 0 || rope->rot_dim > d || rope->rot_dim % 16) return SFI_ERR_UNSUPPORTED;
         if (!rope->turns || rope->num_axes < 1 || rope->num_axes > 8 || (rope->interleaved & ~1))
             return SFI_ERR_INVALID_ARG;
-        if (!positions && !kv) return SFI_ERR_INVALID_ARG;
+        if (!positions && !kv && !seq_lens) return SFI_ERR_INVALID_ARG;
         if (positions && rope->num_axes > 1 && axis_stride < num_tokens) return SFI_ERR_INVALID_ARG;
     }
     if (batch == 0) return SFI_OK;
@@ -199,6 +199,7 @@ sfi_status sfi_qk_norm_rope(const sfi_attn_shape *shape, const sfi_rope *rope, c
     p.axis_stride = axis_stride;
     p.tokens = num_tokens;
     p.new_lens = new_lens;
+    p.seq_lens = seq_lens;
     p.q_out = static_cast<__nv_bfloat16 *>(q_out);
     p.k_out = static_cast<__nv_bfloat16 *>(k_out);
     if (kv) {
@@ -216,15 +217,19 @@ sfi_status sfi_qk_norm_rope(const sfi_attn_shape *shape, const sfi_rope *rope, c
     return launched(sfi::launch_qk_norm_rope(p, shape->head_dim, batch, static_cast<cudaStream_t>(stream)));
 }
 
-sfi_status sfi_kv4_append(const sfi_attn_shape *shape, const sfi_paged_kv4 *kv, const void *k_new, const void *v_new,
-                          int32_t num_tokens, const int32_t *new_lens, const int32_t *req_ids, int32_t batch,
+sfi_status sfi_kv4_append(const sfi_attn_shape *shape, const sfi_paged_kv4 *kv, const void *k_new, int64_t k_stride,
+                          const void *v_new, int64_t v_stride, int32_t num_tokens, const int32_t *new_lens, const int32_t *req_ids, int32_t batch,
                           int32_t *dev_status, void *stream) {
     const sfi_status st = check_kv4(shape, kv);
     if (st != SFI_OK) return st;
     if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new) || num_tokens < 1 || batch < 0)
         return SFI_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)shape->num_kv_heads * shape->head_dim;
+    if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8) return SFI_ERR_INVALID_ARG;
     if (batch == 0) return SFI_OK;
     sfi::Kv4CopyParams p = copy_params(shape, kv, req_ids, dev_status);
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
     p.tokens = num_tokens;
     p.new_lens = new_lens;
     p.k_new = static_cast<const __nv_bfloat16 *>(k_new);

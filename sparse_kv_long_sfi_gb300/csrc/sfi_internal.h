@@ -183,6 +183,7 @@ struct Kv4CopyParams {
     int32_t tokens;
     const int32_t *new_lens, *first;
     const __nv_bfloat16 *k_new, *v_new;
+    int64_t k_stride, v_stride;  // elements between tokens of k_new, v_new
     __nv_bfloat16 *k_out, *v_out;
     // compaction
     const int32_t *idx, *count;

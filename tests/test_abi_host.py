@@ -194,10 +194,10 @@ def test_qk_norm_rope_validates_on_the_host(libsfi):
     rope = _abi.sfi_rope(4096, None, 128, 1, 0)
 
     def call(sh=_shape(), rope=rope, q=4096, qs=2048, k=4096, ks=1024, v=4096, vs=1024, qw=None, eps=1e-6, pos=None,
-             axis_stride=0, T=1, q_out=4096, k_out=4096, kv=_paged(), batch=1):
+             axis_stride=0, T=1, lens=None, q_out=4096, k_out=4096, kv=_paged(), batch=1):
         return libsfi.sfi_qk_norm_rope(ctypes.byref(sh), rope and ctypes.byref(rope), q, qs, k, ks, v, vs, qw, None, eps,
-                                       pos, axis_stride, T, None, q_out, k_out, kv and ctypes.byref(kv), None, batch,
-                                       None, None)
+                                       pos, axis_stride, T, None, lens, q_out, k_out, kv and ctypes.byref(kv), None,
+                                       batch, None, None)
 
     assert call(batch=0) == 0
     assert call(sh=_shape(16, 8, 96)) == 2 and call(sh=_shape(16, 5)) == 1
@@ -212,6 +212,7 @@ def test_qk_norm_rope_validates_on_the_host(libsfi):
     assert call(rope=_abi.sfi_rope(4096, None, 64, 0, 0)) == 1 and call(rope=_abi.sfi_rope(4096, None, 64, 9, 0)) == 1
     assert call(rope=_abi.sfi_rope(4096, None, 64, 1, 2)) == 1
     assert call(kv=None) == 1                      # rotation by neither slot nor position
+    assert call(kv=None, lens=4096, batch=0) == 0
     assert call(rope=_abi.sfi_rope(4096, None, 64, 3, 0), pos=4096, axis_stride=4, T=5) == 1
     assert call(rope=None, kv=None, v=None, batch=0) == 0
 
@@ -238,8 +239,8 @@ def test_kv4_calls_validate_on_the_host(libsfi):
     comp = _abi.sfi_compact_kv4(4096, 8, 4096, 4096, 4096)
     ref = lambda x: x and ctypes.byref(x)  # noqa: E731
 
-    def append(sh=_shape(), kv=_kv4(), k=4096, v=4096, T=1, batch=1):
-        return libsfi.sfi_kv4_append(ref(sh), ref(kv), k, v, T, None, None, batch, None, None)
+    def append(sh=_shape(), kv=_kv4(), k=4096, v=4096, T=1, batch=1, ks=1024, vs=1024):
+        return libsfi.sfi_kv4_append(ref(sh), ref(kv), k, ks, v, vs, T, None, None, batch, None, None)
 
     def read(sh=_shape(), kv=_kv4(), k=4096, v=4096, T=1, batch=1):
         return libsfi.sfi_kv4_read(ref(sh), ref(kv), k, v, T, None, None, batch, None, None)
@@ -261,6 +262,7 @@ def test_kv4_calls_validate_on_the_host(libsfi):
         assert call(batch=0) == 0
         assert call(sh=_shape(16, 8, 96)) == 2 and call(k=None) == 1 and call(v=4097) == 1
         assert call(T=0) == 1 and call(batch=-1) == 1
+    assert append(ks=1016) == 1 and append(vs=1023) == 1 and append(vs=1028) == 1 and append(ks=2048, batch=0) == 0
     for call in (append, read, gather, dense, fast):
         assert call(kv=None) == 1
         assert call(kv=_kv4(pool=4097)) == 1 and call(kv=_kv4(npages=0)) == 1 and call(kv=_kv4(maxp=0)) == 1

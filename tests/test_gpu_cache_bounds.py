@@ -189,6 +189,7 @@ def test_wrappers_check_sizes():
         lambda: sfi.sfi_kv4_append(shape, kv, bf(2, 1, 2, 64), bf(2, 1, 2, 64), req_ids=dev_i32([0]), batch=2),
         lambda: sfi.sfi_kv4_append(shape, kv, bf(2, 1, 2, 64).float(), bf(2, 1, 2, 64)),
         lambda: sfi.sfi_kv4_append(shape, kv, bf(2, 2, 3, 64).transpose(1, 2), bf(2, 3, 2, 64)),
+        lambda: sfi.sfi_kv4_append(shape, kv, bf(3, 2, 2, 64).transpose(0, 1)[:, :2], bf(2, 2, 2, 64)),
         lambda: sfi.sfi_kv4_read(shape, kv, bf(2, 1, 2, 64), bf(2, 1, 2, 64), first=dev_i32([0])),
         lambda: sfi.sfi_kv4_dense_attn(shape, kv, 0, 0, bf(1, 1, 4, 64), f(1, 1, 4, 64), workspace=ws),
         lambda: sfi.sfi_kv4_dense_attn(shape, kv, 0, 0, bf(2, 1, 4, 64), f(2, 1, 4, 32), workspace=ws),

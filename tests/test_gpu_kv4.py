@@ -459,6 +459,63 @@ def test_selector_and_both_steps_together():
                      _fast_sets(c, 1, sink, recent, idx.cpu().numpy(), [k, k]))
 
 
+def test_a_decode_step_from_the_projection_to_the_output_as_one_graph():
+    """Head norm and rotation of a fused projection, the 4-bit append of its K and V, and the slow
+    step over them: captured once and replayed on new inputs and lengths, against the same calls
+    and against the formulas."""
+    sfi = _sfi()
+    hkv, G, d, sink, recent = 2, 4, 128, 4, 32
+    hq = hkv * G
+    c = Cache(61, [500, 37], hkv, d)
+    shape, ws, st = sfi.AttnShape(hq, hkv, d), None, _status()
+    ws = sfi.alloc_kv4_workspace(shape, 2)
+    inv = [float(1e6 ** (-i / 64)) for i in range(64)]
+    rope = sfi.Rope(sfi.rope_turns(inv))
+    g = torch.Generator().manual_seed(4)
+    rand = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    x, qw, kw = rand(2, 1, (hq + 2 * hkv) * d), rand(d), rand(d)
+    q, k, v = (t.unflatten(-1, (-1, d)) for t in x.split([hq * d, hkv * d, hkv * d], -1))
+    qn, kn = torch.empty(2, 1, hq, d, dtype=torch.bfloat16, device="cuda"), torch.empty(2, 1, hkv, d, dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.empty(2, 1, hq, d, device="cuda"), torch.empty(2, 1, hq, device="cuda")
+    scores = torch.full((2, hkv, 505), SENTINEL, device="cuda")
+
+    def step():
+        sfi.sfi_qk_norm_rope(shape, rope, q, k, v, qn, q_weight=qw, k_weight=kw, seq_lens=c.kv.seq_lens, k_out=kn,
+                             dev_status=st)
+        sfi.sfi_kv4_append(shape, c.kv, kn, v, dev_status=st)
+        sfi.sfi_kv4_dense_attn(shape, c.kv, sink, recent, qn, out, lse=lse, scores=scores, workspace=ws, dev_status=st)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for n in (1, 2):
+        c.lens = [500 + n, 37 + n]
+        if c.lens[0] > 16 * c.table.shape[1]:
+            break
+        c.kv.seq_lens.copy_(dev_i32(c.lens))
+        x.copy_(rand(2, 1, (hq + 2 * hkv) * d))
+        graph.replay()
+        torch.cuda.synchronize()
+        c.pool = c.d_pool.cpu().numpy()
+        _check_attention(c, qn, out, lse, 1, G, 1 / math.sqrt(d), _dense_sets(c, 1), scores, sink, recent)
+        for r, L in enumerate(c.lens):
+            # what the cache holds for the newest token is the quantised rotated key
+            key = kn[r, 0].double().cpu().numpy()
+            want = ref.values(*ref.quantise(key, 1.0), 1.0)
+            assert np.array_equal(c.rows(r)[0][:, L - 1], want)
+            t = k[r, 0].double().cpu().numpy()
+            t = t / np.sqrt((t * t).mean(-1, keepdims=True) + 1e-6) * kw.double().cpu().numpy()
+            a = (L - 1) * np.array(inv)
+            y = np.concatenate([t[:, :64] * np.cos(a) - t[:, 64:] * np.sin(a), t[:, 64:] * np.cos(a) + t[:, :64] * np.sin(a)], 1)
+            r2 = np.tile(np.hypot(t[:, :64], t[:, 64:]), (1, 2))
+            assert (np.abs(key - y) <= 2.0 ** -8 * np.abs(y) + 2.0 ** -17 * r2).all()
+        eager = out.clone()
+        step()
+        assert torch.equal(out, eager)
+    assert st.item() == 0
+
+
 # ---- refusals ---------------------------------------------------------------------------------------------------
 
 def test_bad_requests_are_left_out_whole():
