@@ -193,7 +193,6 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
     constexpr int kKs = D / 16;  // k steps of S, and m tiles of O
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_prefix[kKv4MaxBatch + 1];
-    __shared__ uint32_t s_drop[kKv4MaxBatch / 32];  // scores mode: requests with a bad page id
     __shared__ int64_t s_unit0[kParts];             // first block of a partial's unit
     __shared__ int s_unit[kParts];                  // its unit, or -1
     __shared__ int s_bad[kParts];                   // its run met a bad page id
@@ -329,7 +328,8 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
     ReqPlan plan{};
     int f = 0, unit0 = 0;        // this block, and the first of its unit, counted from the warp's first
     int slot = 0;
-    bool drop = false;
+    bool drop = false;   // scores mode: the request has a bad page id
+    int looked_at = -1;  // the request that this says
     const bool multi = p.tokens > 1;
     // blocks that every row sees whole: [0, in_comp) and [in_from, in_to)
     int in_comp = 0, in_from = 0, in_to = 0;
@@ -351,12 +351,19 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
     auto row_of = [&](int nt, int c) { return T::kShared ? (2 * t + c) & 3 : nt * 8 + 2 * t + c; };
     const float second = T::kShared && t >= 2 ? -1.f : 0.f;  // this lane's columns take P's second term
 
-    auto dropped = [&]() { return MODE == kKv4Scores && ((s_drop[at.b >> 5] >> (at.b & 31)) & 1u); };
     auto enter_unit = [&](const int4 (&raw_q)[NT][D / 32]) {
         plan = plan_request<MODE>(p, at.b, &none);
         unit0 = f - at.pg;
-        drop = dropped();
         const int r = request_id(p, at.b);
+        if (MODE == kKv4Scores && looked_at != at.b) {
+            // scores are written on the way, so all page ids of the request are looked at before
+            looked_at = at.b;
+            const int32_t *row = p.page_table + (int64_t)r * p.max_pages;
+            bool out = false;
+#pragma unroll 8
+            for (int i = lane; i < plan.n; i += 32) out |= (uint32_t)row[i] >= (uint32_t)p.num_pages;
+            drop = __any_sync(0xffffffffu, out);
+        }
         {
             int lo_a, hi_a, lo_z, hi_z;
             span(false, 0, lo_a, hi_a);
@@ -766,23 +773,6 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
 
     int run0 = 0;
     if (run > 0) enter_unit(raw_query);
-    // ---- scores are written on the way: the page ids of the CTA's requests are looked at first ----
-    if (MODE == kKv4Scores) {
-        if (tid < kKv4MaxBatch / 32) s_drop[tid] = 0;
-        if (tid == 0) s_last[0] = run > 0 ? at.b : 0;
-        __syncthreads();
-        const int64_t end = runs_of<kWarps>(p, s_prefix).start((int64_t)(blockIdx.x + 1) * kWarps);
-        for (int b = s_last[0]; b < p.batch && s_prefix[b] * p.hkv < end; ++b) {
-            const int n = (int)(s_prefix[b + 1] - s_prefix[b]);
-            const int32_t *row = p.page_table + (int64_t)request_id(p, b) * p.max_pages;
-            bool out = false;
-#pragma unroll 8
-            for (int i = tid; i < n; i += kThreads) out |= (uint32_t)row[i] >= (uint32_t)p.num_pages;
-            if (out) atomicOr(&s_drop[b >> 5], 1u << (b & 31));
-        }
-        __syncthreads();
-        if (run > 0) drop = dropped();
-    }
     while (f < run) {
         // two blocks at once where every row sees both whole
         int pairs = 0;

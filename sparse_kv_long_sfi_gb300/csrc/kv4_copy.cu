@@ -293,63 +293,79 @@ __global__ void __launch_bounds__(kKv4Warps * 32) kv4_compact_kernel(const Kv4Co
         }
         if (err && lane < 16) report(p.dev_status, err);
         uint8_t *dst = p.c_pool + (off + (int64_t)h * cap + ps) * F::kBlock;
-        // K: rows of kKRow bytes and kGroups scales
-        constexpr int kLanes = F::kKRow / 16;  // 16-byte pieces of a row
+        // Every load of the block is on its way before the first store; a row that holds nothing
+        // reads the pool's first block and is cleared.
+        const bool none = src < 0;
+        if (none) src = 0;
+        const uint32_t empty = __ballot_sync(0xffffffffu, none);  // bit i: row i
+        constexpr int kLanes = F::kKRow / 16;      // 16-byte pieces of a K row
+        constexpr int kKIters = 16 * kLanes / 32;  // two, or one at D = 64
+        constexpr int kVIters = D / 64;
+        int4 kv[kKIters];
 #pragma unroll
-        for (int u = lane; u < 16 * kLanes; u += 32) {
-            const int row = u / kLanes, piece = u % kLanes;
+        for (int i = 0; i < kKIters; ++i) {
+            const int row = (i * 32 + lane) / kLanes, piece = lane % kLanes;
             const int64_t s = __shfl_sync(0xffffffffu, src, row);
             const int sl = __shfl_sync(0xffffffffu, slot, row);
-            int4 v = make_int4(0, 0, 0, 0);
-            if (s >= 0) v = ld_stream_v4(p.pool + s + sl * F::kKRow + piece * 16);
-            st_v4(dst + row * F::kKRow + piece * 16, v);
+            kv[i] = ld_stream_v4(p.pool + s + sl * F::kKRow + piece * 16);
+            if ((empty >> row) & 1u) kv[i] = make_int4(0, 0, 0, 0);
         }
-        {  // two lanes per row: half of its scales each
-            const int row = lane >> 1, part = lane & 1;
+        uint32_t ksc;  // two lanes per row: half of its K scales each
+        constexpr int kHalf = F::kGroups / 2;  // 4 or 2 bytes
+        {
+            const int row = lane >> 1;
             const int64_t s = __shfl_sync(0xffffffffu, src, row);
             const int sl = __shfl_sync(0xffffffffu, slot, row);
-            constexpr int kHalf = F::kGroups / 2;  // 4 or 2 bytes
-            const int koff = F::kKScale + sl * F::kGroups + part * kHalf;
-            const int kdst = F::kKScale + row * F::kGroups + part * kHalf;
-            if constexpr (kHalf == 4)
-                *reinterpret_cast<uint32_t *>(dst + kdst) = s >= 0 ? *reinterpret_cast<const uint32_t *>(p.pool + s + koff) : 0u;
-            else
-                *reinterpret_cast<uint16_t *>(dst + kdst) =
-                    s >= 0 ? *reinterpret_cast<const uint16_t *>(p.pool + s + koff) : (uint16_t)0;
+            const uint8_t *at = p.pool + s + F::kKScale + sl * F::kGroups + (lane & 1) * kHalf;
+            if constexpr (kHalf == 4) ksc = *reinterpret_cast<const uint32_t *>(at);
+            else ksc = *reinterpret_cast<const uint16_t *>(at);
+            if ((empty >> row) & 1u) ksc = 0;
         }
-        // V: each 16-byte unit joins the half bytes of four tokens
+        int4 vv[kVIters][4];  // V codes: the units of the four tokens that this lane's unit joins
+        int from[4];          // where a token's half bytes lie in them
+        const VUnit x(lane);
 #pragma unroll
-        for (int u = lane; u < D / 2; u += 32) {
-            const VUnit x(u);
-            uint32_t res[4] = {0, 0, 0, 0};
+        for (int q = 0; q < 4; ++q) {
+            const int64_t s = __shfl_sync(0xffffffffu, src, 4 * x.t + q);
+            const int sl = __shfl_sync(0xffffffffu, slot, 4 * x.t + q);
+            from[q] = 16 * ((sl >> 1) & 1) + 4 * (sl & 1);
+            // the same dims of the source token's group of four
+            const uint8_t *at = p.pool + s + F::kVCode + (lane - 2 * x.t + 2 * (sl >> 2)) * 16;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int64_t s = __shfl_sync(0xffffffffu, src, 4 * x.t + q);
-                const int sl = __shfl_sync(0xffffffffu, slot, 4 * x.t + q);
-                if (s >= 0) {
-                    // the same dims of the source token's group of four
-                    const int4 w = ld_stream_v4(p.pool + s + F::kVCode + (u - 2 * x.t + 2 * (sl >> 2)) * 16);
-                    const int from = 16 * ((sl >> 1) & 1) + 4 * (sl & 1), to = 16 * (q >> 1) + 4 * (q & 1);
-                    const uint32_t ww[4] = {(uint32_t)w.x, (uint32_t)w.y, (uint32_t)w.z, (uint32_t)w.w};
-#pragma unroll
-                    for (int jr = 0; jr < 4; ++jr) res[jr] |= ((ww[jr] >> from) & 0x0f0fu) << to;
-                }
-            }
-            st_v4(dst + F::kVCode + u * 16, make_int4((int)res[0], (int)res[1], (int)res[2], (int)res[3]));
+            for (int i = 0; i < kVIters; ++i) vv[i][q] = ld_stream_v4(at + i * 512);
         }
-        {  // lane w: the word of four tokens' scales (16 words at D = 64)
+        uint32_t vsc = 0;  // lane w: the word of four tokens' V scales (16 words at D = 64)
+        {
             const int w = lane % (4 * F::kGroups);
             const int t = w / F::kGroups, grp = w % F::kGroups;
-            uint32_t v = 0;
+            uint32_t byte[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int64_t s = __shfl_sync(0xffffffffu, src, 4 * t + q);
                 const int sl = __shfl_sync(0xffffffffu, slot, 4 * t + q);
-                if (s >= 0)
-                    v |= (uint32_t)p.pool[s + F::kVScale + (sl >> 2) * F::kVScaleT + grp * 4 + (sl & 3)] << (8 * q);
+                byte[q] = p.pool[s + F::kVScale + (sl >> 2) * F::kVScaleT + grp * 4 + (sl & 3)];
             }
-            if (lane < 4 * F::kGroups) *reinterpret_cast<uint32_t *>(dst + F::kVScale + w * 4) = v;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (!((empty >> (4 * t + q)) & 1u)) vsc |= byte[q] << (8 * q);
         }
+#pragma unroll
+        for (int i = 0; i < kKIters; ++i) st_v4(dst + (i * 32 + lane) * 16, kv[i]);
+        if constexpr (kHalf == 4) *reinterpret_cast<uint32_t *>(dst + F::kKScale + lane * 4) = ksc;
+        else *reinterpret_cast<uint16_t *>(dst + F::kKScale + lane * 2) = (uint16_t)ksc;
+#pragma unroll
+        for (int i = 0; i < kVIters; ++i) {
+            uint32_t res[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t w[4] = {(uint32_t)vv[i][q].x, (uint32_t)vv[i][q].y, (uint32_t)vv[i][q].z, (uint32_t)vv[i][q].w};
+                const uint32_t keep = (empty >> (4 * x.t + q)) & 1u ? 0u : 0x0f0fu;
+#pragma unroll
+                for (int jr = 0; jr < 4; ++jr) res[jr] |= ((w[jr] >> from[q]) & keep) << (16 * (q >> 1) + 4 * (q & 1));
+            }
+            st_v4(dst + F::kVCode + i * 512 + lane * 16, make_int4((int)res[0], (int)res[1], (int)res[2], (int)res[3]));
+        }
+        if (lane < 4 * F::kGroups) *reinterpret_cast<uint32_t *>(dst + F::kVScale + lane * 4) = vsc;
     }
 }
 
