@@ -342,8 +342,29 @@ def sfi_fast_decode_attn_noalloc(shape: AttnShape, kv: PagedKV, compact: Compact
     _check(st, "sfi_fast_decode_attn_noalloc")
 
 
+class _Handle:
+    """Tensors that one C structure points to. The structure is checked and made when it is
+    first needed, and again when a field has been assigned or a tensor's memory has moved: a
+    call that finds it ready spends 0.7 us on it instead of 2."""
+    _tensors = ()
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        self.__dict__.pop("_c", None)
+
+    def c(self):
+        d = self.__dict__
+        c = d.get("_c")
+        if c is not None and d["_at"] == [d[n].data_ptr() for n in self._tensors]:
+            return c
+        c = self._make()
+        d["_at"] = [d[n].data_ptr() for n in self._tensors]
+        d["_c"] = c
+        return c
+
+
 @dataclass
-class Rope:
+class Rope(_Handle):
     """The position rotation of sfi_qk_norm_rope: turns int64 [rot_dim / 2] (rope_turns),
     axis uint8 [rot_dim / 2] or None, the number of position axes, and whether pairs are
     adjacent dims (interleaved) or dims rot_dim / 2 apart."""
@@ -352,7 +373,11 @@ class Rope:
     num_axes: int = 1
     interleaved: bool = False
 
-    def c(self) -> _abi.sfi_rope:
+    @property
+    def _tensors(self):
+        return ("turns",) if self.axis is None else ("turns", "axis")
+
+    def _make(self) -> _abi.sfi_rope:
         _need(self.turns, torch.int64, "rope.turns")
         axis = _ptr(self.axis, torch.uint8, "rope.axis")
         if self.axis is not None and self.axis.numel() != self.turns.numel():
@@ -372,23 +397,20 @@ def rope_turns(inv_freq, device="cuda") -> torch.Tensor:
     return torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
 
 
-def _requests(kv, batch, req_ids, **arrays) -> int:
-    """The number of requests a call takes; arrays indexed by request id must cover the table's
-    requests."""
-    B = kv.page_table.shape[0]
-    if kv.seq_lens.numel() != B:
-        raise ValueError("seq_lens needs one entry per row of page_table")
-    for name, t in arrays.items():
-        if t is not None and t.shape[0] != B:
-            raise ValueError(f"{name} needs one entry for each of {B} requests, has {t.shape[0]}")
-    if req_ids is not None:
-        n = req_ids.numel()
-        if batch is not None and batch > n:
-            raise ValueError(f"batch {batch} is beyond the {n} req_ids")
-        return n if batch is None else int(batch)
-    if batch is not None and batch > B:
-        raise ValueError(f"batch {batch} is beyond the {B} requests")
-    return B if batch is None else int(batch)
+def _count(requests: int, batch, req_ids) -> int:
+    """The number of requests a call takes out of `requests`."""
+    n = requests if req_ids is None else req_ids.numel()
+    if batch is None:
+        return n
+    if batch > n:
+        raise ValueError(f"batch {batch} is beyond the {n} requests given")
+    return int(batch)
+
+
+def _indexed(t: Optional[torch.Tensor], requests: int, name: str):
+    """Arrays indexed by request id cover all requests of the table."""
+    if t is not None and t.shape[0] != requests:
+        raise ValueError(f"{name} needs one entry for each of {requests} requests, has {t.shape[0]}")
 
 
 def _on_current_device(t: torch.Tensor, name: str):
@@ -396,8 +418,9 @@ def _on_current_device(t: torch.Tensor, name: str):
         raise ValueError(f"{name} is on {t.device}, not on the current device")
 
 
-def _token_rows(t: torch.Tensor, heads: int, dim: int, name: str) -> int:
-    """Elements between the tokens of a [B][T][heads][dim] tensor whose heads are contiguous."""
+def _token_rows(t: torch.Tensor, heads: int, dim: int, name: str):
+    """Requests, tokens and elements between tokens of a [B][T][heads][dim] tensor whose heads
+    are contiguous."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype is not torch.bfloat16:
@@ -410,7 +433,7 @@ def _token_rows(t: torch.Tensor, heads: int, dim: int, name: str) -> int:
     step = s[1] if n > 1 else (s[0] if b > 1 else heads * dim)
     if s[3] != 1 or (heads > 1 and s[2] != dim) or (b > 1 and s[0] != n * step):
         raise ValueError(f"{name} needs contiguous heads and one stride between all tokens")
-    return step
+    return b, n, step
 
 
 def sfi_qk_norm_rope(shape: AttnShape, rope: Optional[Rope], q: torch.Tensor, k: torch.Tensor,
@@ -418,49 +441,46 @@ def sfi_qk_norm_rope(shape: AttnShape, rope: Optional[Rope], q: torch.Tensor, k:
                      k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
                      positions: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
                      seq_lens: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
-                     kv: Optional[PagedKV] = None,
-                     req_ids: Optional[torch.Tensor] = None, batch: Optional[int] = None,
-                     dev_status: Optional[torch.Tensor] = None, stream=None):
+                     kv: Optional[PagedKV] = None, req_ids: Optional[torch.Tensor] = None,
+                     batch: Optional[int] = None, dev_status: Optional[torch.Tensor] = None, stream=None):
     """Head norm and rotation of the new tokens; q, k, v [B][T][heads][D] may be views of one
     fused projection. positions int32 [num_axes][B][T] (or [B][T] with one axis)."""
     hq, hkv, d = shape.num_q_heads, shape.num_kv_heads, shape.head_dim
     _on_current_device(q, "q")
-    qs, ks = _token_rows(q, hq, d, "q"), _token_rows(k, hkv, d, "k")
-    vs = 0 if v is None else _token_rows(v, hkv, d, "v")
-    B, T = q.shape[0], q.shape[1]
-    if k.shape[0] != B or k.shape[1] != T or (v is not None and (v.shape[0] != B or v.shape[1] != T)):
+    B, T, qs = _token_rows(q, hq, d, "q")
+    kb, kt, ks = _token_rows(k, hkv, d, "k")
+    vb, vt, vs = (B, T, 0) if v is None else _token_rows(v, hkv, d, "v")
+    if kb != B or kt != T or vb != B or vt != T:
         raise ValueError("q, k and v need the same requests and tokens")
+    _need(q_out, torch.bfloat16, "q_out")
     if q_out.shape != q.shape or (k_out is not None and k_out.shape != k.shape):
         raise ValueError("q_out and k_out need the shapes of q and k")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and w.numel() != d:
-            raise ValueError(f"{name} must have {d} values")
+    if (q_weight is not None and q_weight.numel() != d) or (k_weight is not None and k_weight.numel() != d):
+        raise ValueError(f"q_weight and k_weight must have {d} values")
     if positions is not None and positions.numel() != (rope.num_axes if rope is not None else 1) * B * T:
         raise ValueError("positions must be [num_axes][B][T]")
     if (new_lens is not None and new_lens.numel() != B) or (seq_lens is not None and seq_lens.numel() != B):
         raise ValueError("new_lens and seq_lens need one entry per request")
+    kv_c = None
     if kv is not None:
-        n = _requests(kv, batch, req_ids, q=q)
-        if kv.k_pool.shape != kv.v_pool.shape or tuple(kv.k_pool.shape[1:]) != (hkv, shape.page_size, d):
+        kv_c = ctypes.byref(kv.c())
+        dims = kv.k_pool.shape
+        if len(dims) != 4 or dims[1] != hkv or dims[2] != shape.page_size or dims[3] != d or kv.v_pool.shape != dims:
             raise ValueError(f"the pools must be [num_pages][{hkv}][{shape.page_size}][{d}]")
-    else:
-        n = B if req_ids is None else req_ids.numel()
-        if batch is not None and batch > n:
-            raise ValueError(f"batch {batch} is beyond the {n} requests")
-        n = n if batch is None else int(batch)
+        if kv.seq_lens.numel() != B:
+            raise ValueError("q, k and v need one entry for each request of the pages")
     st = _abi.lib().sfi_qk_norm_rope(
         ctypes.byref(shape.c()), None if rope is None else ctypes.byref(rope.c()), q.data_ptr(), qs, k.data_ptr(), ks,
         None if v is None else v.data_ptr(), vs, _ptr(q_weight, torch.bfloat16, "q_weight"),
-        _ptr(k_weight, torch.bfloat16, "k_weight"), float(eps), _ptr(positions, torch.int32, "positions"), B * T, T,
-        _ptr(new_lens, torch.int32, "new_lens"), _ptr(seq_lens, torch.int32, "seq_lens"),
-        _ptr(q_out, torch.bfloat16, "q_out"),
-        _ptr(k_out, torch.bfloat16, "k_out"), None if kv is None else ctypes.byref(kv.c()),
-        _ptr(req_ids, torch.int32, "req_ids"), n, _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+        _ptr(k_weight, torch.bfloat16, "k_weight"), eps, _ptr(positions, torch.int32, "positions"), B * T, T,
+        _ptr(new_lens, torch.int32, "new_lens"), _ptr(seq_lens, torch.int32, "seq_lens"), q_out.data_ptr(),
+        _ptr(k_out, torch.bfloat16, "k_out"), kv_c, _ptr(req_ids, torch.int32, "req_ids"), _count(B, batch, req_ids),
+        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
     _check(st, "sfi_qk_norm_rope")
 
 
 @dataclass
-class PagedKV4:
+class PagedKV4(_Handle):
     """Paged 4-bit cache: pool uint8 [num_pages][Hkv][18 D] (alloc_kv4_pool), page_table int32
     [B][max_pages], seq_lens int32 [B]; k_scale and v_scale are powers of two."""
     pool: torch.Tensor
@@ -469,16 +489,25 @@ class PagedKV4:
     k_scale: float = 1.0
     v_scale: float = 1.0
 
-    def c(self) -> _abi.sfi_paged_kv4:
+    _tensors = ("pool", "page_table", "seq_lens")
+
+    def _make(self) -> _abi.sfi_paged_kv4:
         _need(self.pool, torch.uint8, "pool")
         _need(self.page_table, torch.int32, "page_table")
         _need(self.seq_lens, torch.int32, "seq_lens")
+        _on_current_device(self.pool, "pool")
+        if self.pool.dim() != 3:
+            raise ValueError(f"pool must be [num_pages][Hkv][18 D], got {list(self.pool.shape)}")
+        if self.page_table.dim() != 2 or self.seq_lens.numel() != self.page_table.shape[0]:
+            raise ValueError("seq_lens needs one entry per row of page_table")
+        self.__dict__["_dims"] = tuple(self.pool.shape[1:])
+        self.__dict__["_requests"] = self.page_table.shape[0]
         return _abi.sfi_paged_kv4(self.pool.data_ptr(), self.pool.shape[0], self.page_table.shape[1],
                                   self.page_table.data_ptr(), self.seq_lens.data_ptr(), self.k_scale, self.v_scale)
 
 
 @dataclass
-class CompactKV4:
+class CompactKV4(_Handle):
     """4-bit compact blocks: pool uint8 [total_pages][18 D]; page_offset int64 [B]; capacity
     (blocks per KV head) and count (selected rows) int32 [B]."""
     pool: torch.Tensor
@@ -486,26 +515,40 @@ class CompactKV4:
     capacity: torch.Tensor
     count: torch.Tensor
 
-    def c(self) -> _abi.sfi_compact_kv4:
+    _tensors = ("pool", "page_offset", "capacity", "count")
+
+    def _make(self) -> _abi.sfi_compact_kv4:
         _need(self.pool, torch.uint8, "compact.pool")
         _need(self.page_offset, torch.int64, "compact.page_offset")
         _need(self.capacity, torch.int32, "compact.capacity")
         _need(self.count, torch.int32, "compact.count")
+        self.__dict__["_requests"] = self.page_offset.numel()
+        if self.capacity.numel() != self.page_offset.numel() or self.count.numel() != self.page_offset.numel():
+            raise ValueError("compact.page_offset, capacity and count need one entry per request")
+        if self.pool.dim() != 2:
+            raise ValueError(f"compact.pool must be [total_pages][18 D], got {list(self.pool.shape)}")
+        self.__dict__["_bytes"] = self.pool.shape[1]
         return _abi.sfi_compact_kv4(self.pool.data_ptr(), self.pool.shape[0], self.page_offset.data_ptr(),
                                     self.capacity.data_ptr(), self.count.data_ptr())
 
 
 def _kv4(shape: AttnShape, kv: PagedKV4):
-    _on_current_device(kv.pool, "pool")
-    dims = kv.pool.shape
-    if len(dims) != 3 or dims[1] != shape.num_kv_heads or dims[2] != 18 * shape.head_dim:
-        raise ValueError(f"pool must be [num_pages][{shape.num_kv_heads}][{18 * shape.head_dim}], got {list(dims)}")
-    return ctypes.byref(kv.c())
+    c = kv.c()
+    if kv._dims != (shape.num_kv_heads, 18 * shape.head_dim):
+        raise ValueError(f"pool must be [num_pages][{shape.num_kv_heads}][{18 * shape.head_dim}], "
+                         f"got {list(kv.pool.shape)}")
+    if kv.pool.get_device() != torch._C._cuda_getDevice():
+        _on_current_device(kv.pool, "pool")
+    return ctypes.byref(c)
 
 
-def _compact4(shape: AttnShape, compact: CompactKV4):
-    if compact.pool.dim() != 2 or compact.pool.shape[1] != 18 * shape.head_dim:
+def _compact4(shape: AttnShape, kv: PagedKV4, compact: CompactKV4):
+    c = compact.c()
+    if compact._bytes != 18 * shape.head_dim:
         raise ValueError(f"compact.pool must be [total_pages][{18 * shape.head_dim}]")
+    if compact._requests != kv._requests:
+        raise ValueError(f"compact needs one entry for each of {kv._requests} requests, has {compact._requests}")
+    return ctypes.byref(c)
 
 
 def alloc_kv4_pool(shape: AttnShape, num_pages: int, device="cuda") -> torch.Tensor:
@@ -535,15 +578,17 @@ def sfi_kv4_append(shape: AttnShape, kv: PagedKV4, k_new: torch.Tensor, v_new: t
                    new_lens: Optional[torch.Tensor] = None, req_ids: Optional[torch.Tensor] = None,
                    batch: Optional[int] = None, dev_status: Optional[torch.Tensor] = None, stream=None):
     """k_new, v_new [B][T][Hkv][D]; either may be a view of a fused projection (contiguous heads)."""
-    ks = _token_rows(k_new, shape.num_kv_heads, shape.head_dim, "k_new")
-    vs = _token_rows(v_new, shape.num_kv_heads, shape.head_dim, "v_new")
-    if v_new.shape != k_new.shape:
-        raise ValueError("k_new and v_new need the same shape")
-    n = _requests(kv, batch, req_ids, k_new=k_new, new_lens=new_lens)
+    kb, T, ks = _token_rows(k_new, shape.num_kv_heads, shape.head_dim, "k_new")
+    vb, vt, vs = _token_rows(v_new, shape.num_kv_heads, shape.head_dim, "v_new")
+    kv_c = _kv4(shape, kv)
+    B = kv._requests
+    if kb != B or vb != B or vt != T:
+        raise ValueError(f"k_new and v_new need the same shape, with one entry for each of {B} requests")
+    _indexed(new_lens, B, "new_lens")
     st = _abi.lib().sfi_kv4_append(
-        ctypes.byref(shape.c()), _kv4(shape, kv), k_new.data_ptr(), ks, v_new.data_ptr(), vs, k_new.shape[1],
-        _ptr(new_lens, torch.int32, "new_lens"), _ptr(req_ids, torch.int32, "req_ids"),
-        n, _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+        ctypes.byref(shape.c()), kv_c, k_new.data_ptr(), ks, v_new.data_ptr(), vs, T,
+        _ptr(new_lens, torch.int32, "new_lens"), _ptr(req_ids, torch.int32, "req_ids"), _count(B, batch, req_ids),
+        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
     _check(st, "sfi_kv4_append")
 
 
@@ -551,35 +596,43 @@ def sfi_kv4_read(shape: AttnShape, kv: PagedKV4, k_out: torch.Tensor, v_out: tor
                  first: Optional[torch.Tensor] = None, req_ids: Optional[torch.Tensor] = None,
                  batch: Optional[int] = None, dev_status: Optional[torch.Tensor] = None, stream=None):
     T = _rows4(k_out, torch.bfloat16, shape, shape.num_kv_heads, "k_out")
-    if _rows4(v_out, torch.bfloat16, shape, shape.num_kv_heads, "v_out") != T or v_out.shape != k_out.shape:
+    _need(v_out, torch.bfloat16, "v_out")
+    if v_out.shape != k_out.shape:
         raise ValueError("k_out and v_out need the same shape")
-    n = _requests(kv, batch, req_ids, k_out=k_out, first=first)
+    kv_c = _kv4(shape, kv)
+    B = kv._requests
+    _indexed(k_out, B, "k_out")
+    _indexed(first, B, "first")
     st = _abi.lib().sfi_kv4_read(
-        ctypes.byref(shape.c()), _kv4(shape, kv), k_out.data_ptr(), v_out.data_ptr(), T,
-        _ptr(first, torch.int32, "first"), _ptr(req_ids, torch.int32, "req_ids"),
-        n, _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+        ctypes.byref(shape.c()), kv_c, k_out.data_ptr(), v_out.data_ptr(), T, _ptr(first, torch.int32, "first"),
+        _ptr(req_ids, torch.int32, "req_ids"), _count(B, batch, req_ids), _ptr(dev_status, torch.int32, "dev_status"),
+        _stream(stream))
     _check(st, "sfi_kv4_read")
 
 
 def sfi_kv4_compact_gather(shape: AttnShape, kv: PagedKV4, idx: torch.Tensor, count: torch.Tensor, sink: int,
                            compact: CompactKV4, req_ids: Optional[torch.Tensor] = None, batch: Optional[int] = None,
                            dev_status: Optional[torch.Tensor] = None, stream=None):
-    if idx.dim() != 3 or idx.shape[1] != shape.num_kv_heads:
-        raise ValueError(f"idx must be [B][{shape.num_kv_heads}][k_cap]")
-    _compact4(shape, compact)
-    n = _requests(kv, batch, req_ids, idx=idx, count=count, page_offset=compact.page_offset, capacity=compact.capacity)
+    kv_c = _kv4(shape, kv)
+    B = kv._requests
+    dims = idx.shape
+    if len(dims) != 3 or dims[0] != B or dims[1] != shape.num_kv_heads:
+        raise ValueError(f"idx must be [{B}][{shape.num_kv_heads}][k_cap], got {list(dims)}")
+    _indexed(count, B, "count")
     st = _abi.lib().sfi_kv4_compact_gather(
-        ctypes.byref(shape.c()), _kv4(shape, kv), _ptr(idx, torch.int32, "idx"), _ptr(count, torch.int32, "count"),
-        int(idx.shape[-1]), int(sink), ctypes.byref(compact.c()), _ptr(req_ids, torch.int32, "req_ids"),
-        n, _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+        ctypes.byref(shape.c()), kv_c, _ptr(idx, torch.int32, "idx"), _ptr(count, torch.int32, "count"), dims[2],
+        int(sink), _compact4(shape, kv, compact), _ptr(req_ids, torch.int32, "req_ids"), _count(B, batch, req_ids),
+        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
     _check(st, "sfi_kv4_compact_gather")
 
 
-def _kv4_query(shape: AttnShape, q: torch.Tensor, out: torch.Tensor, lse: Optional[torch.Tensor]) -> int:
+def _kv4_query(shape: AttnShape, kv: PagedKV4, q: torch.Tensor, out: torch.Tensor, lse: Optional[torch.Tensor]) -> int:
     T = _rows4(q, torch.bfloat16, shape, shape.num_q_heads, "q")
     _need(out, torch.float32, "out")
-    if out.shape != q.shape or (lse is not None and tuple(lse.shape) != tuple(q.shape)[:3]):
+    dims = q.shape
+    if out.shape != dims or (lse is not None and lse.shape != dims[:3]):
         raise ValueError("out needs the shape of q, lse that without its last dimension")
+    _indexed(q, kv._requests, "q")
     return T
 
 
@@ -590,15 +643,18 @@ def sfi_kv4_dense_attn(shape: AttnShape, kv: PagedKV4, sink: int, recent: int, q
                        stream=None):
     """q [B][T][Hq][D] (T query tokens per request), out fp32 of that shape, lse [B][T][Hq],
     scores [B][Hkv][score_stride]."""
-    T = _kv4_query(shape, q, out, lse)
-    if scores is not None and (scores.dim() != 3 or scores.shape[1] != shape.num_kv_heads):
-        raise ValueError(f"scores must be [B][{shape.num_kv_heads}][score_stride]")
-    n = _requests(kv, batch, req_ids, q=q, scores=scores)
+    kv_c = _kv4(shape, kv)
+    T = _kv4_query(shape, kv, q, out, lse)
+    B, stride = kv._requests, 0
+    if scores is not None:
+        dims = scores.shape
+        if len(dims) != 3 or dims[0] != B or dims[1] != shape.num_kv_heads:
+            raise ValueError(f"scores must be [{B}][{shape.num_kv_heads}][score_stride], got {list(dims)}")
+        stride = dims[2]
     st = _abi.lib().sfi_kv4_dense_attn(
-        ctypes.byref(shape.c()), _kv4(shape, kv), int(sink), int(recent), q.data_ptr(), T, out.data_ptr(),
-        _ptr(lse, torch.float32, "lse"), _ptr(scores, torch.float32, "scores"),
-        0 if scores is None else int(scores.shape[-1]), _ptr(req_ids, torch.int32, "req_ids"),
-        n, _ptr(workspace, torch.uint8, "workspace"),
+        ctypes.byref(shape.c()), kv_c, int(sink), int(recent), q.data_ptr(), T, out.data_ptr(),
+        _ptr(lse, torch.float32, "lse"), _ptr(scores, torch.float32, "scores"), stride,
+        _ptr(req_ids, torch.int32, "req_ids"), _count(B, batch, req_ids), _ptr(workspace, torch.uint8, "workspace"),
         0 if workspace is None else workspace.numel(), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
     _check(st, "sfi_kv4_dense_attn")
 
@@ -608,13 +664,12 @@ def sfi_kv4_fast_attn(shape: AttnShape, kv: PagedKV4, compact: CompactKV4, sink:
                       batch: Optional[int] = None, workspace: Optional[torch.Tensor] = None,
                       dev_status: Optional[torch.Tensor] = None, stream=None):
     """q [B][T][Hq][D] (T query tokens per request), out fp32 of that shape, lse [B][T][Hq]."""
-    T = _kv4_query(shape, q, out, lse)
-    _compact4(shape, compact)
-    n = _requests(kv, batch, req_ids, q=q, page_offset=compact.page_offset, capacity=compact.capacity, count=compact.count)
+    kv_c = _kv4(shape, kv)
+    T = _kv4_query(shape, kv, q, out, lse)
     st = _abi.lib().sfi_kv4_fast_attn(
-        ctypes.byref(shape.c()), _kv4(shape, kv), ctypes.byref(compact.c()), int(sink), int(recent), q.data_ptr(), T,
+        ctypes.byref(shape.c()), kv_c, _compact4(shape, kv, compact), int(sink), int(recent), q.data_ptr(), T,
         out.data_ptr(), _ptr(lse, torch.float32, "lse"), _ptr(req_ids, torch.int32, "req_ids"),
-        n, _ptr(workspace, torch.uint8, "workspace"),
+        _count(kv._requests, batch, req_ids), _ptr(workspace, torch.uint8, "workspace"),
         0 if workspace is None else workspace.numel(), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
     _check(st, "sfi_kv4_fast_attn")
 
@@ -629,14 +684,16 @@ def alloc_kv4_workspace(shape: AttnShape, batch: int, num_tokens: int = 1, devic
 
 
 @dataclass
-class PageMap:
+class PageMap(_Handle):
     """Who holds which page: page_table int32 [num_reqs][max_pages], seq_lens int32 [num_reqs],
     ref_count int32 [num_pages] (holders of each page)."""
     page_table: torch.Tensor
     seq_lens: torch.Tensor
     ref_count: torch.Tensor
 
-    def c(self) -> _abi.sfi_page_map:
+    _tensors = ("page_table", "seq_lens", "ref_count")
+
+    def _make(self) -> _abi.sfi_page_map:
         _need(self.page_table, torch.int32, "page_table")
         _need(self.seq_lens, torch.int32, "seq_lens")
         _need(self.ref_count, torch.int32, "ref_count")
