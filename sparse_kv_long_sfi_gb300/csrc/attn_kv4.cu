@@ -155,14 +155,42 @@ __device__ __forceinline__ Place locate(const int64_t *prefix, int batch, int hk
     return at;
 }
 
-// Four values of an output row (at `at`) from the merged sum and normaliser; lse_at >= 0: its log-sum-exp too.
-__device__ __forceinline__ void write_row(const Kv4AttnParams &p, int64_t at, float4 acc, float mx, float sum,
-                                          int64_t lse_at) {
-    const float w = sum == 0.f ? 0.f : p.v_scale / sum;
+// Four dims of a row, gathered from partial states by log-sum-exp.
+struct Gathered {
+    float mx = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    // N parts (m = -inf, l = 0, x = 0 where there is none)
+    template <int N>
+    __device__ __forceinline__ void add(const float2 (&ml)[N], const float4 (&x)[N]) {
+        float now = mx;
+#pragma unroll
+        for (int i = 0; i < N; ++i) now = fmaxf(now, ml[i].x);
+        const float keep = mx == now ? 1.f : fast_exp2(mx - now);
+        mx = now;
+        sum *= keep;
+        acc.x *= keep;
+        acc.y *= keep;
+        acc.z *= keep;
+        acc.w *= keep;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float w = ml[i].x == now ? 1.f : fast_exp2(ml[i].x - now);
+            sum = fmaf(w, ml[i].y, sum);
+            acc.x = fmaf(w, x[i].x, acc.x);
+            acc.y = fmaf(w, x[i].y, acc.y);
+            acc.z = fmaf(w, x[i].z, acc.z);
+            acc.w = fmaf(w, x[i].w, acc.w);
+        }
+    }
+};
+
+// Four values of an output row (at `at`); lse_at >= 0: its log-sum-exp too.
+__device__ __forceinline__ void write_row(const Kv4AttnParams &p, int64_t at, const Gathered &g, int64_t lse_at) {
+    const float w = g.sum == 0.f ? 0.f : p.v_scale / g.sum;
     float2 *out = reinterpret_cast<float2 *>(p.out + at);
-    out[0] = make_float2(acc.x * w, acc.y * w);
-    out[1] = make_float2(acc.z * w, acc.w * w);
-    if (p.lse && lse_at >= 0) p.lse[lse_at] = sum == 0.f ? -INFINITY : (mx - kLift + log2f(sum)) * kLn2;
+    out[0] = make_float2(g.acc.x * w, g.acc.y * w);
+    out[1] = make_float2(g.acc.z * w, g.acc.w * w);
+    if (p.lse && lse_at >= 0) p.lse[lse_at] = g.sum == 0.f ? -INFINITY : (g.mx - kLift + log2f(g.sum)) * kLn2;
 }
 
 // Run w of `parts` nearly equal runs of [0, total): the first total % parts are one longer.
@@ -360,8 +388,21 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
             looked_at = at.b;
             const int32_t *row = p.page_table + (int64_t)r * p.max_pages;
             bool out = false;
+            auto look = [&](int id) { out |= (uint32_t)id >= (uint32_t)p.num_pages; };
+            int done = 0;
+            if ((reinterpret_cast<uintptr_t>(row) & 15u) == 0) {  // four ids at a time
+                done = plan.n & ~3;
 #pragma unroll 8
-            for (int i = lane; i < plan.n; i += 32) out |= (uint32_t)row[i] >= (uint32_t)p.num_pages;
+                for (int i = lane * 4; i < done; i += 128) {
+                    const int4 id = *reinterpret_cast<const int4 *>(row + i);
+                    look(id.x);
+                    look(id.y);
+                    look(id.z);
+                    look(id.w);
+                }
+            }
+#pragma unroll 4
+            for (int i = done + lane; i < plan.n; i += 32) look(row[i]);
             drop = __any_sync(0xffffffffu, out);
         }
         {
@@ -848,31 +889,33 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
         }
         for (int e = tid; e < p.rows * (D / 4) && !(complete && bad); e += kThreads) {
             const int row = e / (D / 4), d = e % (D / 4) * 4;
-            float mx = -INFINITY, sum = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            // loops over the parts that are there, kept rolled: most of their time is fetching code
+            Gathered got;
+            // four parts at a time, rolled: most of this code's time is its own fetching
 #pragma unroll 1
-            for (uint32_t left = parts; left; left &= left - 1) mx = fmaxf(mx, s_ml[__ffs(left) - 1][row][0]);
-#pragma unroll 1
-            for (uint32_t left = parts; left; left &= left - 1) {
-                const int k = __ffs(left) - 1;
-                const float m = s_ml[k][row][0];
-                const float w = m == mx ? 1.f : fast_exp2(m - mx);
-                const uint8_t *part = smem + ((k & 1) ? (k >> 1) * T::kRing : T::kFirst + (k >> 1) * T::kPart);
-                const float4 x = *reinterpret_cast<const float4 *>(part + (row * D + d) * 4);
-                sum = fmaf(w, s_ml[k][row][1], sum);
-                acc.x = fmaf(w, x.x, acc.x);
-                acc.y = fmaf(w, x.y, acc.y);
-                acc.z = fmaf(w, x.z, acc.z);
-                acc.w = fmaf(w, x.w, acc.w);
+            for (uint32_t left = parts; left;) {
+                float2 ml[4];
+                float4 x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int k = __ffs(left) - 1;
+                    ml[i] = make_float2(-INFINITY, 0.f);
+                    x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (k >= 0) {
+                        ml[i] = make_float2(s_ml[k][row][0], s_ml[k][row][1]);
+                        x[i] = *reinterpret_cast<const float4 *>(
+                            smem + ((k & 1) ? (k >> 1) * T::kRing : T::kFirst + (k >> 1) * T::kPart) + (row * D + d) * 4);
+                    }
+                    left &= left - 1;  // 0 stays 0
+                }
+                got.add(ml, x);
             }
             if (complete) {
                 const int64_t to = ((int64_t)r * p.tokens + row / p.group) * p.hq + h * p.group + row % p.group;
-                write_row(p, to * D + d, acc, mx, sum, d == 0 ? to : -1);
+                write_row(p, to * D + d, got, d == 0 ? to : -1);
             } else {
-                __stcg(reinterpret_cast<float4 *>(p.ws_part + (ws_row + row) * D + d), acc);
+                __stcg(reinterpret_cast<float4 *>(p.ws_part + (ws_row + row) * D + d), got.acc);
                 // a maximum of NaN: the part met a bad page id (its sums are not read)
-                if (d == 0) __stcg(reinterpret_cast<float2 *>(p.ws_ml) + ws_row + row, make_float2(bad ? NAN : mx, sum));
+                if (d == 0) __stcg(reinterpret_cast<float2 *>(p.ws_ml) + ws_row + row, make_float2(bad ? NAN : got.mx, got.sum));
             }
         }
     }
@@ -904,76 +947,53 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
         const int parts = c1 - c0 + 1;
         // slot of part c: a unit lies in the second slot of the CTA it begins in, else in the first
         auto row_at = [&](int c, int row) { return ((int64_t)(c0 + c) * 2 + (c == 0)) * kMaxRows + row; };
-        // a thread takes four dims of a row; where there are fewer such items than threads, `ways`
-        // threads share one, each with every ways-th part
+        // a thread takes four dims of a row, eight parts at a time; where there are more parts and
+        // threads to spare, `ways` threads share an item, each with every ways-th part
+        constexpr int kBatch = 8;
         const int items = p.rows * (D / 4);
-        const int ways = max(1, kThreads / items), wide = min(items, kThreads);
+        const int ways = max(1, min(kThreads / items, (parts + kBatch - 1) / kBatch)), wide = min(items, kThreads);
         float2 *red_ml = reinterpret_cast<float2 *>(smem);
         float4 *red = reinterpret_cast<float4 *>(smem + kThreads * 8);
         for (int e0 = 0; e0 < items; e0 += kThreads) {
             const int e = e0 + tid % wide, way = tid / wide;
             const int row = e / (D / 4), d = e % (D / 4) * 4;
             const bool busy = e < items && way < ways;
-            float mx = -INFINITY, sum = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            Gathered got;
             bool bad = false;
-            auto add = [&](float m, float v, const float4 &x) {  // weight 2^(m - mx)
-                const float w = m == mx ? 1.f : fast_exp2(m - mx);
-                sum = fmaf(w, v, sum);
-                acc.x = fmaf(w, x.x, acc.x);
-                acc.y = fmaf(w, x.y, acc.y);
-                acc.z = fmaf(w, x.z, acc.z);
-                acc.w = fmaf(w, x.w, acc.w);
-            };
-            auto raise = [&](float m) {
-                const float now = fmaxf(mx, m), w = mx == now ? 1.f : fast_exp2(mx - now);
-                mx = now;
-                sum *= w;
-                acc.x *= w;
-                acc.y *= w;
-                acc.z *= w;
-                acc.w *= w;
-            };
-            constexpr int kBatch = 8;  // parts in flight
+#pragma unroll 1
             for (int c = way; c < parts && busy; c += ways * kBatch) {
-                float2 y[kBatch];
+                float2 ml[kBatch];
                 float4 x[kBatch];
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
                     const int k = c + i * ways;
-                    y[i] = make_float2(-INFINITY, 0.f);
+                    ml[i] = make_float2(-INFINITY, 0.f);
                     x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (k < parts) {
-                        y[i] = __ldcg(reinterpret_cast<const float2 *>(p.ws_ml) + row_at(k, row));
+                        ml[i] = __ldcg(reinterpret_cast<const float2 *>(p.ws_ml) + row_at(k, row));
                         x[i] = __ldcg(reinterpret_cast<const float4 *>(p.ws_part + row_at(k, row) * D + d));
                     }
                 }
-                float top = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    bad |= isnan(y[i].x);
-                    top = fmaxf(top, y[i].x);
-                }
-                raise(top);
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) add(y[i].x, y[i].y, x[i]);
+                for (int i = 0; i < kBatch; ++i) bad |= isnan(ml[i].x);
+                got.add(ml, x);
             }
             if (ways > 1) {
                 __syncthreads();
-                red_ml[tid] = make_float2(bad ? NAN : mx, sum);
-                red[tid] = acc;
+                red_ml[tid] = make_float2(bad ? NAN : got.mx, got.sum);
+                red[tid] = got.acc;
                 __syncthreads();
                 if (way == 0)
                     for (int k = 1; k < ways; ++k) {
-                        const float2 y = red_ml[k * wide + e];
-                        bad |= isnan(y.x);
-                        raise(y.x);
-                        add(y.x, y.y, red[k * wide + e]);
+                        const float2 ml[1] = {red_ml[k * wide + e]};
+                        const float4 x[1] = {red[k * wide + e]};
+                        bad |= isnan(ml[0].x);
+                        got.add(ml, x);
                     }
             }
             if (busy && way == 0 && !bad) {
                 const int64_t to = ((int64_t)r * p.tokens + row / p.group) * p.hq + h * p.group + row % p.group;
-                write_row(p, to * D + d, acc, mx, sum, d == 0 ? to : -1);
+                write_row(p, to * D + d, got, d == 0 ? to : -1);
             }
         }
     }

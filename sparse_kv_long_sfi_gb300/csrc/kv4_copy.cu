@@ -43,7 +43,7 @@ __device__ __forceinline__ uint32_t quantise8(int4 raw, float inv6g, float g, ui
     const float step = e4m3_to_f32(s) * g;
     const float inv = reciprocal(step);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = round16(x[i] * inv);
+    for (int i = 0; i < 8; ++i) x[i] *= inv;
     return fine && step > 0.f ? f32x8_to_e2m1(x) : 0u;
 }
 
@@ -125,7 +125,7 @@ __device__ void write_block(uint8_t *block, Kv4Tile<D> &tile, const __nv_bfloat1
 }
 
 template <int D>
-__global__ void __launch_bounds__(kKv4Warps * 32) kv4_append_kernel(const Kv4CopyParams p, int batch, int page_slots) {
+__global__ void __launch_bounds__(kKv4Warps * 32, 4) kv4_append_kernel(const Kv4CopyParams p, int batch, int page_slots) {
     __shared__ Kv4Tile<D> s_tile[kKv4Warps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t items = (int64_t)batch * page_slots * p.hkv * 2;

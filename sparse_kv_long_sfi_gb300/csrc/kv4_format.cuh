@@ -77,14 +77,19 @@ __device__ __forceinline__ float e4m3_to_f32(uint32_t s) {
     return __low2float(*reinterpret_cast<const __half2 *>(&h));
 }
 
-// Eight values over the group's step -> eight e2m1 codes (value i in bits 4i..4i+3).
+// Eight values over the group's step -> eight e2m1 codes (value i in bits 4i..4i+3), by way
+// of fp16: its 11 bits do for the codes what round16 does for the scale.
 __device__ __forceinline__ uint32_t f32x8_to_e2m1(const float (&y)[8]) {
     uint32_t w;
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t.reg .b32 h0, h1, h2, h3;\n\t"
+        "cvt.rn.f16x2.f32 h0, %2, %1;\n\t"
+        "cvt.rn.f16x2.f32 h1, %4, %3;\n\t"
+        "cvt.rn.f16x2.f32 h2, %6, %5;\n\t"
+        "cvt.rn.f16x2.f32 h3, %8, %7;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f16x2 b0, h0;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f16x2 b1, h1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f16x2 b2, h2;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f16x2 b3, h3;\n\t"
         "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
         : "=r"(w)
         : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
