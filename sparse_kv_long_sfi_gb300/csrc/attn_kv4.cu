@@ -31,14 +31,18 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.f;   // the maximum may lag by this (in powers of two)
 constexpr float kLift = 7.f;   // P is computed times 2^7
-constexpr int kMinPages = 2;   // blocks per warp at least, before fewer CTAs work
+// Blocks per warp at least, before fewer CTAs work: a refresh and fast step of 16 x 1024 rows
+// takes 33.9 us with 2, 35.3 with 4, 38.4 with 8.
+constexpr int kMinPages = 2;
 
 enum Kv4Mode : int { kKv4Dense = 0, kKv4Scores = 1, kKv4Fast = 2 };
 
 // ROWS: the query rows of a KV head that a variant takes. Up to four, P's two terms share
 // the N tile (columns 0..3 the first, 4..7 the second, over the same rows); up to eight,
 // they take an instruction each; up to sixteen, there are two N tiles, whose accumulators leave
-// room for one CTA per SM.
+// room for one CTA per SM. Two rows (the slow step of 16 x 16K tokens, 16/8/128 heads) take
+// 67.2 us in the first variant, 75.0 in the second, 101 in the third; eight rows (refresh and
+// fast step of 32 x 1792 rows, 2 tokens x 4 heads) 98 us in the second and 109 in the third.
 template <int D, int ROWS>
 struct Tile {
     static constexpr int kNt = ROWS > 8 ? 2 : 1;
@@ -225,7 +229,7 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
     __shared__ int s_unit[kParts];                  // its unit, or -1
     __shared__ int s_bad[kParts];                   // its run met a bad page id
     __shared__ float s_ml[kParts][ROWS][2];
-    __shared__ int s_last[2], s_open[2];
+    __shared__ int s_last[2], s_open[2], s_lead[kParts];
     __shared__ int64_t s_open0[2];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -871,11 +875,17 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
     const int my_unit = lane < kParts ? s_unit[lane] : -1;
     const uint32_t mine = __match_any_sync(0xffffffffu, my_unit);
     const uint32_t bads = __ballot_sync(0xffffffffu, lane < kParts && my_unit >= 0 && s_bad[min(lane, kParts - 1)]);
-    for (uint32_t todo = __ballot_sync(0xffffffffu, my_unit >= 0); todo;) {
-        const int first = __ffs(todo) - 1;
+    // the units in order of their first part; all items of all of them are spread over the threads
+    const bool leads = my_unit >= 0 && __ffs(mine) - 1 == lane;
+    const uint32_t leaders = __ballot_sync(0xffffffffu, leads);
+    if (leads) s_lead[__popc(leaders & ((1u << lane) - 1u))] = lane;  // the same from every warp
+    __syncwarp();
+    const int items = p.rows * (D / 4), all_items = __popc(leaders) * items;
+    for (int e0 = warp * 32; e0 < all_items; e0 += kThreads) {
+        const int i = min(e0 + lane, all_items - 1), e = i % items;
+        const int first = s_lead[i / items];
         const int u = __shfl_sync(0xffffffffu, my_unit, first);
         const uint32_t parts = __shfl_sync(0xffffffffu, mine, first);
-        todo &= ~parts;
         const bool bad = bads & parts;
         const int b = u / p.hkv, h = u - b * p.hkv;
         const int r = request_id(p, b);
@@ -883,11 +893,11 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
         const bool complete = u0 >= cta0 && u1 <= cta1;
         const int side = u0 < cta0 ? 0 : 1;  // this CTA's slot for it in the workspace
         const int64_t ws_row = ((int64_t)blockIdx.x * 2 + side) * kMaxRows;
-        if (!complete && tid == 0) {
+        if (!complete && e == 0) {
             s_open[side] = u;
             s_open0[side] = u0;
         }
-        for (int e = tid; e < p.rows * (D / 4) && !(complete && bad); e += kThreads) {
+        if (e0 + lane < all_items && !(complete && bad)) {
             const int row = e / (D / 4), d = e % (D / 4) * 4;
             Gathered got;
             // four parts at a time, rolled: most of this code's time is its own fetching
@@ -937,8 +947,12 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
         s_last[tid] = last;
     }
     __syncthreads();
-    for (int side = 0; side < 2; ++side) {
-        if (!s_last[side]) continue;
+    if (!s_last[0] && !s_last[1]) return;
+    {
+        // where the CTA is the last for both of its units, half of the threads take each
+        const bool both = s_last[0] && s_last[1];
+        const int threads = both ? kThreads / 2 : kThreads;
+        const int side = both ? tid / threads : (s_last[0] ? 0 : 1), me = tid % threads;
         const int u = s_open[side];
         const int b = u / p.hkv, h = u - b * p.hkv;
         const int r = request_id(p, b);
@@ -948,14 +962,15 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
         // slot of part c: a unit lies in the second slot of the CTA it begins in, else in the first
         auto row_at = [&](int c, int row) { return ((int64_t)(c0 + c) * 2 + (c == 0)) * kMaxRows + row; };
         // a thread takes four dims of a row, eight parts at a time; where there are more parts and
-        // threads to spare, `ways` threads share an item, each with every ways-th part
+        // threads to spare, `ways` threads share an item, each with every ways-th part (as many as
+        // half of the CTA has to spare, in both cases: the order of the sums may not depend on
+        // which CTA came last)
         constexpr int kBatch = 8;
-        const int items = p.rows * (D / 4);
-        const int ways = max(1, min(kThreads / items, (parts + kBatch - 1) / kBatch)), wide = min(items, kThreads);
+        const int ways = max(1, min(kThreads / 2 / items, (parts + kBatch - 1) / kBatch)), wide = min(items, threads);
         float2 *red_ml = reinterpret_cast<float2 *>(smem);
         float4 *red = reinterpret_cast<float4 *>(smem + kThreads * 8);
-        for (int e0 = 0; e0 < items; e0 += kThreads) {
-            const int e = e0 + tid % wide, way = tid / wide;
+        for (int e0 = 0; e0 < items; e0 += threads) {
+            const int e = e0 + me % wide, way = me / wide;
             const int row = e / (D / 4), d = e % (D / 4) * 4;
             const bool busy = e < items && way < ways;
             Gathered got;
@@ -978,15 +993,14 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
                 for (int i = 0; i < kBatch; ++i) bad |= isnan(ml[i].x);
                 got.add(ml, x);
             }
-            if (ways > 1) {
-                __syncthreads();
+            if (__syncthreads_or(ways > 1)) {  // (either half may need it)
                 red_ml[tid] = make_float2(bad ? NAN : got.mx, got.sum);
                 red[tid] = got.acc;
                 __syncthreads();
-                if (way == 0)
+                if (way == 0 && busy)
                     for (int k = 1; k < ways; ++k) {
-                        const float2 ml[1] = {red_ml[k * wide + e]};
-                        const float4 x[1] = {red[k * wide + e]};
+                        const float2 ml[1] = {red_ml[tid + k * wide]};
+                        const float4 x[1] = {red[tid + k * wide]};
                         bad |= isnan(ml[0].x);
                         got.add(ml, x);
                     }

@@ -225,8 +225,9 @@ __global__ void __launch_bounds__(kNormWarps * 32, HALVES ? 3 : 2) qk_norm_rope_
 cudaError_t launch_qk_norm_rope(const NormRopeParams &p, int head_dim, int batch, cudaStream_t stream) {
     const int sms = sm_count_current_device();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    // Few tokens are spread over warps by their rows (one load each: 16 tokens of 32 rows
-    // take 64 warps); many tokens keep a warp per token, which computes its cosines once.
+    // Few tokens are spread over warps by their rows (one round of loads each: 16 tokens of 32
+    // rows take 64 warps and 4.2 us, 6.7 us with a warp per token); many tokens keep a warp per
+    // token, which computes its cosines once.
     const int rows = p.hq + p.hkv + (p.v ? p.hkv : 0);
     const int step = (head_dim == 128 ? 2 : 4) * kNormBatch;
     const int64_t tokens = (int64_t)batch * p.tokens;
@@ -237,6 +238,7 @@ cudaError_t launch_qk_norm_rope(const NormRopeParams &p, int head_dim, int batch
     const int chunks = (rows + rows_per_item - 1) / rows_per_item;
     const int64_t ctas = (tokens * chunks + kNormWarps - 1) / kNormWarps;
     const int grid = (int)std::min<int64_t>(ctas, (int64_t)sms * 64);
+    // both members of a pair in a lane: 73 us for 2 x 8192 tokens of 32/8/128 heads, 96 us by shuffles
     const bool halves = p.rot_dim == head_dim && !p.interleaved;
     auto kernel = head_dim == 128 ? (halves ? qk_norm_rope_kernel<128, true> : qk_norm_rope_kernel<128, false>)
                                   : (halves ? qk_norm_rope_kernel<64, true> : qk_norm_rope_kernel<64, false>);
