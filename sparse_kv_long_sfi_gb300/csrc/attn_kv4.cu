@@ -31,9 +31,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.f;   // the maximum may lag by this (in powers of two)
 constexpr float kLift = 7.f;   // P is computed times 2^7
-// Blocks per warp at least, before fewer CTAs work: a refresh and fast step of 16 x 1024 rows
-// takes 33.9 us with 2, 35.3 with 4, 38.4 with 8.
-constexpr int kMinPages = 2;
 
 enum Kv4Mode : int { kKv4Dense = 0, kKv4Scores = 1, kKv4Fast = 2 };
 
@@ -41,8 +38,8 @@ enum Kv4Mode : int { kKv4Dense = 0, kKv4Scores = 1, kKv4Fast = 2 };
 // the N tile (columns 0..3 the first, 4..7 the second, over the same rows); up to eight,
 // they take an instruction each; up to sixteen, there are two N tiles, whose accumulators leave
 // room for one CTA per SM. Two rows (the slow step of 16 x 16K tokens, 16/8/128 heads) take
-// 67.2 us in the first variant, 75.0 in the second, 101 in the third; eight rows (refresh and
-// fast step of 32 x 1792 rows, 2 tokens x 4 heads) 98 us in the second and 109 in the third.
+// 65.2 us in the first variant, 73.0 in the second, 99.9 in the third; eight rows (refresh and
+// fast step of 32 x 1792 rows, 2 tokens x 4 heads) 97.8 us in the second and 108 in the third.
 template <int D, int ROWS>
 struct Tile {
     static constexpr int kNt = ROWS > 8 ? 2 : 1;
@@ -207,11 +204,18 @@ struct Runs {
     }
 };
 
-// The warps' runs: as many CTAs as give each warp kMinPages blocks, at most the grid's.
+// The warps' runs over as many CTAs as there is work for. Where a full grid would get less than
+// one or two blocks per warp, fewer warps take that many: one is the shortest chain (1K tokens of
+// one request: 9.4 us, 10.9 with two at least). Up to four, long units are better cut into whole
+// pairs (one request of 16K tokens: 16.7 us with four blocks, 18.3 with 3.3 on average; 4 tokens of
+// one request of 8K: 24.9 and 27.7), while short ones, with their many edges, are better spread
+// (64 requests of 200 tokens: 22.4 us with 2.7 blocks on average, 25.0 with four).
 template <int kWarps>
 __device__ __forceinline__ Runs runs_of(const Kv4AttnParams &p, const int64_t *prefix) {
-    const int64_t total = prefix[p.batch] * p.hkv;
-    const int64_t ctas = min((int64_t)gridDim.x, (total + kWarps * kMinPages - 1) / (kWarps * kMinPages));
+    const int64_t total = prefix[p.batch] * p.hkv, grid = (int64_t)gridDim.x * kWarps;
+    const bool long_units = prefix[p.batch] >= 128 * (int64_t)p.batch;  // 2K tokens on average
+    const int least = total <= grid ? 1 : (total > 2 * grid && total <= 4 * grid && long_units ? 4 : 2);
+    const int64_t ctas = min((int64_t)gridDim.x, (total + kWarps * least - 1) / (kWarps * least));
     return Runs(total, max(ctas * kWarps, (int64_t)1));
 }
 
