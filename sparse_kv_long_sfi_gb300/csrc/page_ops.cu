@@ -59,13 +59,37 @@ __device__ __forceinline__ int pages_of(int len) { return (len + kSubTokens - 1)
 
 }  // namespace
 
+// Row r of the table by the new page ids (entries out of range, and those behind the
+// request's length, as they are).
+__device__ void renumber_row(const PageMapParams &m, int r, const int32_t *new_ids, int32_t *table_out,
+                             int32_t *dev_status) {
+    const int L = m.seq_lens[r];
+    const bool fine = L >= 0 && pages_of(L) <= m.max_pages;
+    if (!fine && threadIdx.x == 0) report(dev_status, SFI_DEV_BAD_LEN);
+    const int held = fine ? pages_of(L) : 0;
+    for (int i = threadIdx.x; i < m.max_pages; i += kPageThreads) {
+        int page = m.page_table[(int64_t)r * m.max_pages + i];
+        if (i < held) {
+            if (page < 0 || page >= m.num_pages)
+                report(dev_status, SFI_DEV_BAD_PAGE);
+            else
+                page = new_ids[page];
+        }
+        table_out[(int64_t)r * m.max_pages + i] = page;
+    }
+}
+
 // ---- copy: page src[i] -> dst[i] of every pool, in chunks ------------------------------
+// (table_out: a compaction's new table is written in the same launch)
 __global__ void __launch_bounds__(kPageThreads) page_copy_kernel(void *const *pools, int num_pools, int64_t page_bytes,
                                                                  int num_pages, const int32_t *src, const int32_t *dst,
-                                                                 int n_host, const int32_t *n_dev,
+                                                                 int n_host, const int32_t *n_dev, const PageMapParams m,
+                                                                 const int32_t *new_ids, int32_t *table_out,
                                                                  int32_t *dev_status) {
     constexpr int kLoads = kCopyChunk / 16 / kPageThreads;
     grid_dependency_wait();
+    if (table_out)
+        for (int r = blockIdx.x; r < m.num_reqs; r += gridDim.x) renumber_row(m, r, new_ids, table_out, dev_status);
     const int n = n_dev ? *n_dev : n_host;
     const int chunks = (int)((page_bytes + kCopyChunk - 1) / kCopyChunk);
     const int64_t items = (int64_t)n * num_pools * chunks;
@@ -322,9 +346,23 @@ __global__ void __launch_bounds__(kPlanThreads) page_compact_plan_kernel(const P
         movers += both >> 16;
     }
     __syncthreads();
-    for (int i = tid; i < movers; i += kPlanThreads) {
-        lists.ids[lists.src[i]] = lists.dst[i];
-        ref_out[lists.dst[i]] = m.ref_count[lists.src[i]];
+    constexpr int kMoves = 4;  // moves of a thread whose loads are in flight together
+    for (int i0 = tid; i0 < movers; i0 += kPlanThreads * kMoves) {
+        int from[kMoves], to[kMoves], held[kMoves];
+#pragma unroll
+        for (int k = 0; k < kMoves; ++k) {
+            const int i = i0 + k * kPlanThreads;
+            from[k] = i < movers ? lists.src[i] : -1;
+            to[k] = i < movers ? lists.dst[i] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kMoves; ++k) held[k] = from[k] >= 0 ? m.ref_count[from[k]] : 0;
+#pragma unroll
+        for (int k = 0; k < kMoves; ++k)
+            if (from[k] >= 0) {
+                lists.ids[from[k]] = to[k];
+                ref_out[to[k]] = held[k];
+            }
     }
     if (tid == 0) {
         lists.moves[0] = movers;
@@ -332,38 +370,18 @@ __global__ void __launch_bounds__(kPlanThreads) page_compact_plan_kernel(const P
     }
 }
 
-__global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageMapParams m, int32_t *table_out, void *ws,
-                                                                  int32_t *dev_status) {
-    grid_dependency_wait();
-    const PageLists lists(ws, m.num_pages);
-    const int r = blockIdx.x;
-    const int L = m.seq_lens[r];
-    const bool fine = L >= 0 && pages_of(L) <= m.max_pages;
-    if (!fine && threadIdx.x == 0) report(dev_status, SFI_DEV_BAD_LEN);
-    const int held = fine ? pages_of(L) : 0;
-    for (int i = threadIdx.x; i < m.max_pages; i += kPageThreads) {
-        int page = m.page_table[(int64_t)r * m.max_pages + i];
-        if (i < held) {
-            if (page < 0 || page >= m.num_pages)
-                report(dev_status, SFI_DEV_BAD_PAGE);
-            else
-                page = lists.ids[page];
-        }
-        table_out[(int64_t)r * m.max_pages + i] = page;
-    }
-}
-
 namespace {
 
 cudaError_t launch_copy(const PagePoolParams &q, const int32_t *src, const int32_t *dst, int n, int most,
-                        const int32_t *n_dev, int32_t *dev_status, cudaStream_t stream) {
+                        const int32_t *n_dev, const PageMapParams &m, const int32_t *new_ids, int32_t *table_out,
+                        int32_t *dev_status, cudaStream_t stream) {
     const int sms = sm_count_current_device();
     if (sms <= 0) return cudaErrorInvalidDevice;
     const int64_t chunks = (q.page_bytes + kCopyChunk - 1) / kCopyChunk;
-    const int64_t items = (int64_t)most * q.num_pools * chunks;
+    const int64_t items = std::max<int64_t>((int64_t)most * q.num_pools * chunks, table_out ? m.num_reqs : 0);
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(items, (int64_t)sms * 8));
     return launch_dependent(page_copy_kernel, grid, kPageThreads, 0, stream, q.pools, q.num_pools, q.page_bytes,
-                            q.num_pages, src, dst, n, n_dev, dev_status);
+                            q.num_pages, src, dst, n, n_dev, m, new_ids, table_out, dev_status);
 }
 
 }  // namespace
@@ -372,7 +390,7 @@ size_t page_workspace_bytes(int32_t num_pages) { return ((size_t)num_pages * 3 +
 
 cudaError_t launch_page_copy(const PagePoolParams &q, const int32_t *src, const int32_t *dst, int n,
                              int32_t *dev_status, cudaStream_t stream) {
-    return launch_copy(q, src, dst, n, n, nullptr, dev_status, stream);
+    return launch_copy(q, src, dst, n, n, nullptr, PageMapParams{}, nullptr, nullptr, dev_status, stream);
 }
 
 cudaError_t launch_page_fork(const PageMapParams &m, const int32_t *src, const int32_t *dst, const int32_t *fork_lens,
@@ -391,18 +409,16 @@ cudaError_t launch_page_reserve(const PageMapParams &m, const PagePoolParams *q,
                                            q != nullptr ? 1 : 0, ws, dev_status);
     if (e != cudaSuccess || !q) return e;
     const PageLists lists(ws, m.num_pages);
-    return launch_copy(*q, lists.src, lists.dst, 0, n, lists.moves, dev_status, stream);
+    return launch_copy(*q, lists.src, lists.dst, 0, n, lists.moves, PageMapParams{}, nullptr, nullptr, dev_status, stream);
 }
 
 cudaError_t launch_page_compact(const PageMapParams &m, const PagePoolParams &q, int32_t *table_out, int32_t *ref_out,
                                 int32_t *live_out, void *ws, int32_t *dev_status, cudaStream_t stream) {
-    cudaError_t e = launch_dependent(page_compact_plan_kernel, 1, kPlanThreads, 0, stream, m, ref_out, live_out, ws);
+    const cudaError_t e = launch_dependent(page_compact_plan_kernel, 1, kPlanThreads, 0, stream, m, ref_out, live_out, ws);
+    if (e != cudaSuccess) return e;
     const PageLists lists(ws, m.num_pages);
-    if (e == cudaSuccess)
-        e = launch_copy(q, lists.src, lists.dst, 0, m.num_pages / 2, lists.moves, dev_status, stream);
-    if (e == cudaSuccess && m.num_reqs > 0)
-        e = launch_dependent(page_table_kernel, m.num_reqs, kPageThreads, 0, stream, m, table_out, ws, dev_status);
-    return e;
+    return launch_copy(q, lists.src, lists.dst, 0, m.num_pages / 2, lists.moves, m, lists.ids, table_out, dev_status,
+                       stream);
 }
 
 }  // namespace sfi
