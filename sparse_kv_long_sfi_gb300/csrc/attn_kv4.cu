@@ -10,6 +10,9 @@
 // workspace, where the last CTA of a unit adds the parts in order (the result does not
 // depend on which one that is).
 //
+// A fast step of few requests is latency: there, a unit belongs to a cluster of CTAs, which
+// finds its blocks without the others' lengths and adds up its parts in shared memory.
+//
 // Per block (16 tokens): S^T = K Q^T and O^T += V^T P^T with mma.m16n8k16, the tokens (or
 // dims) as the M side, so that eight query rows take one N tile. Codes become fp16 by
 // conversion and one multiplication by their scale: a product of an e2m1 and an e4m3
@@ -31,6 +34,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.f;   // the maximum may lag by this (in powers of two)
 constexpr float kLift = 7.f;   // P is computed times 2^7
+constexpr int kKv4MaxCluster = 8;  // CTAs of a cluster
 
 enum Kv4Mode : int { kKv4Dense = 0, kKv4Scores = 1, kKv4Fast = 2 };
 
@@ -39,7 +43,7 @@ enum Kv4Mode : int { kKv4Dense = 0, kKv4Scores = 1, kKv4Fast = 2 };
 // they take an instruction each; up to sixteen, there are two N tiles, whose accumulators leave
 // room for one CTA per SM. Two rows (the slow step of 16 x 16K tokens, 16/8/128 heads) take
 // 65.2 us in the first variant, 73.0 in the second, 99.9 in the third; eight rows (refresh and
-// fast step of 32 x 1792 rows, 2 tokens x 4 heads) 97.8 us in the second and 108 in the third.
+// fast step of 32 x 1792 rows, 2 tokens x 4 heads, as runs of the row) 97.8 us in the second and 108 in the third.
 template <int D, int ROWS>
 struct Tile {
     static constexpr int kNt = ROWS > 8 ? 2 : 1;
@@ -52,6 +56,9 @@ struct Tile {
     static constexpr int kPart = ROWS * D * 4;  // a partial O
     static constexpr int kFirst = kWarps * kRing;  // partials of first runs
     static constexpr int kSmem = kFirst + kWarps * kPart;
+    // in clusters, behind that: a CTA's share of all CTAs' sums (D / 4 items of 24 bytes a row, rounded up)
+    static constexpr int kClusterSmem = kSmem + (ROWS * (D / 4) + kKv4MaxCluster) * 24;
+    static_assert(ROWS * (D / 4) <= 2 * kThreads, "a thread takes one item of a CTA's share");
     static_assert(kRing >= kPart, "a warp's ring holds its last partial");
     static_assert(kSmem >= kThreads * 24, "the merge's arrays lie where the rings were");
 };
@@ -102,6 +109,13 @@ __device__ __forceinline__ ReqPlan plan_request(const Kv4AttnParams &p, int b, u
     const int r = request_id(p, b);
     ReqPlan q{};
     q.L = p.seq_lens[r];
+    int cnt = 0, cap = 0;
+    int64_t off = 0;
+    if (MODE == kKv4Fast) {  // all on their way before the first is looked at
+        cnt = p.c_count[r];
+        cap = p.c_capacity[r];
+        off = p.c_page_offset[r];
+    }
     if (q.L < p.tokens || q.L > p.max_pages * kSubTokens || (MODE == kKv4Scores && q.L > p.score_stride)) {
         *err |= SFI_DEV_BAD_LEN;
         return q;
@@ -110,8 +124,6 @@ __device__ __forceinline__ ReqPlan plan_request(const Kv4AttnParams &p, int b, u
         q.n = (q.L + 15) / 16;
         return q;
     }
-    const int cnt = p.c_count[r], cap = p.c_capacity[r];
-    const int64_t off = p.c_page_offset[r];
     const int64_t rows = (int64_t)min(p.sink, q.L) + cnt;
     const int ncomp = (int)((rows + 15) / 16);
     if (cnt < 0 || cap < 0 || ncomp > cap || (cnt > 0 && q.L - p.tokens + 1 < p.sink)) {
@@ -221,7 +233,8 @@ __device__ __forceinline__ Runs runs_of(const Kv4AttnParams &p, const int64_t *p
 
 }  // namespace
 
-template <int D, int ROWS, int MODE>
+// CLUSTER: a cluster of CTAs takes one unit, see cluster_of; otherwise a warp takes a run of the row.
+template <int D, int ROWS, int MODE, bool CLUSTER>
 __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv4_attn_kernel(const Kv4AttnParams p) {
     using F = Kv4<D>;
     using T = Tile<D, ROWS>;
@@ -241,93 +254,11 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
 
     grid_launch_dependents();
     grid_dependency_wait();
-    // ---- the row of work: blocks of each request, summed up (every warp for itself) ----
-    {
-        uint32_t err = 0;
-        int64_t carry = 0;
-        for (int base = 0; base < p.batch; base += 32) {
-            const int b = base + lane;
-            const int64_t v = b < p.batch ? plan_request<MODE>(p, b, &err).n : 0;
-            int64_t incl = v;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
-                if (lane >= off) incl += o;
-            }
-            if (b < p.batch) s_prefix[b] = carry + incl - v;
-            carry += __shfl_sync(0xffffffffu, incl, 31);
-        }
-        if (lane == 0) s_prefix[p.batch] = carry;
-        if (err && blockIdx.x == 0 && warp == 0) report(p.dev_status, err);
-    }
-    if (lane < 2) s_unit[2 * warp + lane] = -1;
-    if (tid < 2) s_open[tid] = -1;
-    __syncwarp();
-    int64_t f0, f1;
-    {
-        const Runs runs = runs_of<kWarps>(p, s_prefix);
-        if (s_prefix[p.batch] == 0 || (int64_t)blockIdx.x * kWarps >= runs.parts) return;
-        f0 = runs.start((int64_t)blockIdx.x * kWarps + warp);
-        f1 = runs.start((int64_t)blockIdx.x * kWarps + warp + 1);
-    }
-
-    // ---- copies: this warp's blocks, kDepth of them in flight ----
-    uint8_t *ring = smem + warp * T::kRing;
-    const uint64_t policy = l2_policy_evict_first();
-    Place ahead{};
+    uint32_t none = 0;  // (a request's errors are reported once, where its blocks are counted)
+    Place at{};
     ReqPlan aplan{};
-    int ids = 0, ids_base = 0;     // page ids of the unit, 32 at a time (lane i: number ids_base + i)
-    const int32_t *id_row = nullptr;
-    const int run = (int)(f1 - f0);  // blocks of this warp
-    int left = run;                  // those still to be copied
-    uint32_t bad_units = 0;        // bit (number of the unit in this run) % 32: it has a bad page id
-    int unit_ahead = 0, unit_here = 0;
-    uint32_t none = 0;
-    auto load_ids = [&](int first) {
-        ids_base = first;
-        ids = first + lane < aplan.n - aplan.ncomp ? id_row[first + lane] : 0;
-        const bool out = (uint32_t)ids >= (uint32_t)p.num_pages;
-        if (out) ids = 0;  // any page: the unit writes nothing
-        if (__any_sync(0xffffffffu, out)) {
-            bad_units |= 1u << (unit_ahead & 31);
-            if (lane == 0) report(p.dev_status, SFI_DEV_BAD_PAGE);
-        }
-    };
-    auto enter_ahead = [&]() {
-        aplan = plan_request<MODE>(p, ahead.b, &none);
-        id_row = p.page_table + (int64_t)request_id(p, ahead.b) * p.max_pages + aplan.page0;
-        bad_units &= ~(1u << (unit_ahead & 31));
-        load_ids(max(0, ahead.pg - aplan.ncomp));
-    };
-    auto issue = [&](int slot) {
-        if (left > 0) {
-            const uint8_t *src;
-            if (MODE == kKv4Fast && ahead.pg < aplan.ncomp) {
-                src = p.c_pool + (aplan.cblock + (int64_t)ahead.h * aplan.cap + ahead.pg) * F::kBlock;
-            } else {
-                const int i = ahead.pg - aplan.ncomp;
-                if (i >= ids_base + 32) load_ids(i);
-                const int page = __shfl_sync(0xffffffffu, ids, i - ids_base);
-                src = p.pool + ((int64_t)page * p.hkv + ahead.h) * F::kBlock;
-            }
-            src += lane * 16;
-            uint8_t *dst = ring + slot * F::kBlock + lane * 16;
-#pragma unroll
-            for (int c = 0; c < F::kBlock / 16; c += 32)
-                if (c + 32 <= F::kBlock / 16 || lane < F::kBlock / 16 - c) cp_async16(dst + c * 16, src + c * 16, policy);
-            --left;
-            if (++ahead.pg == aplan.n && left > 0) {
-                ahead.pg = 0;
-                if (++ahead.h == p.hkv) {
-                    ahead.h = 0;
-                    do ++ahead.b; while (s_prefix[ahead.b + 1] == s_prefix[ahead.b]);
-                }
-                ++unit_ahead;
-                enter_ahead();
-            }
-        }
-        cp_async_commit();
-    };
+    int run;  // blocks of this warp
+    int64_t f0 = 0;
     const int gshift = __ffs(p.group) - 1;  // the group size is a power of two
     // a unit's query rows as they lie (lane (g, t): dims t D/4 .. of row g)
     auto load_query = [&](const Place &x, int4 (&raw_q)[NT][D / 32]) {
@@ -345,14 +276,123 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
             }
         }
     };
-    Place at{};
     int4 raw_query[NT][D / 32];
-    if (run > 0) {
-        at = locate(s_prefix, p.batch, p.hkv, f0);
-        load_query(at, raw_query);  // on their way while page ids and blocks are fetched
-        ahead = at;
-        enter_ahead();
+    if constexpr (CLUSTER) {
+        // ---- this cluster's unit, in equal runs over its warps ----
+        const int unit = blockIdx.x / cluster_nctarank(), rank = cluster_ctarank();
+        const int parts = kWarps * cluster_nctarank(), part = rank * kWarps + warp;
+        at.b = unit / p.hkv;
+        at.h = unit - at.b * p.hkv;
+        if (cluster_nctarank() > 1) cluster_arrive_relaxed();  // (waited for before the first remote store)
+        load_query(at, raw_query);  // on their way while the plan and the blocks are fetched
+        uint32_t err = 0;
+        aplan = plan_request<MODE>(p, at.b, &err);
+        if (err && tid == 0 && rank == 0 && at.h == 0) report(p.dev_status, err);
+        if (aplan.n == 0) {  // every CTA of the cluster
+            if (cluster_nctarank() > 1) cluster_wait();
+            return;
+        }
+        const int q = aplan.n / parts, r = aplan.n - q * parts;
+        at.pg = part * q + min(part, r);
+        run = q + (part < r);
+    } else {
+        // ---- the row of work: blocks of each request, summed up (every warp for itself) ----
+        uint32_t err = 0;
+        int64_t carry = 0;
+        for (int base = 0; base < p.batch; base += 32) {
+            const int b = base + lane;
+            const int64_t v = b < p.batch ? plan_request<MODE>(p, b, &err).n : 0;
+            int64_t incl = v;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += o;
+            }
+            if (b < p.batch) s_prefix[b] = carry + incl - v;
+            carry += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) s_prefix[p.batch] = carry;
+        if (err && blockIdx.x == 0 && warp == 0) report(p.dev_status, err);
+        if (lane < 2) s_unit[2 * warp + lane] = -1;
+        if (tid < 2) s_open[tid] = -1;
+        __syncwarp();
+        const Runs runs = runs_of<kWarps>(p, s_prefix);
+        if (s_prefix[p.batch] == 0 || (int64_t)blockIdx.x * kWarps >= runs.parts) return;
+        f0 = runs.start((int64_t)blockIdx.x * kWarps + warp);
+        run = (int)(runs.start((int64_t)blockIdx.x * kWarps + warp + 1) - f0);
+        if (run > 0) {
+            at = locate(s_prefix, p.batch, p.hkv, f0);
+            load_query(at, raw_query);  // on their way while page ids and blocks are fetched
+            aplan = plan_request<MODE>(p, at.b, &none);
+        }
     }
+
+    // ---- copies: this warp's blocks, kDepth of them in flight ----
+    uint8_t *ring = smem + warp * T::kRing;
+    const uint64_t policy = l2_policy_evict_first();
+    Place ahead = at;
+    int ids = 0, ids_base = 0;     // page ids of the unit, 32 at a time (lane i: number ids_base + i)
+    const int32_t *id_row = nullptr;
+    int left = run;                  // those still to be copied
+    uint32_t bad_units = 0;        // bit (number of the unit in this run) % 32: it has a bad page id
+    int unit_ahead = 0, unit_here = 0;
+    bool unchecked = false;        // ids are on their way (a cluster's first copies do not wait for them)
+    auto load_ids = [&](int first) {
+        ids_base = first;
+        ids = first + lane < aplan.n - aplan.ncomp ? id_row[first + lane] : 0;
+    };
+    auto check_ids = [&]() {
+        const bool out = (uint32_t)ids >= (uint32_t)p.num_pages;
+        if (out) ids = 0;  // any page: the unit writes nothing
+        if (__any_sync(0xffffffffu, out)) {
+            bad_units |= 1u << (unit_ahead & 31);
+            if (lane == 0) report(p.dev_status, SFI_DEV_BAD_PAGE);
+        }
+    };
+    auto enter_ahead = [&]() {
+        id_row = p.page_table + (int64_t)request_id(p, ahead.b) * p.max_pages + aplan.page0;
+        bad_units &= ~(1u << (unit_ahead & 31));
+        load_ids(max(0, ahead.pg - aplan.ncomp));
+        if constexpr (CLUSTER) unchecked = true;
+        else check_ids();
+    };
+    auto issue = [&](int slot) {
+        if (left > 0) {
+            const uint8_t *src;
+            if (MODE == kKv4Fast && ahead.pg < aplan.ncomp) {
+                src = p.c_pool + (aplan.cblock + (int64_t)ahead.h * aplan.cap + ahead.pg) * F::kBlock;
+            } else {
+                const int i = ahead.pg - aplan.ncomp;
+                if (i >= ids_base + 32) {
+                    load_ids(i);
+                    check_ids();
+                } else if (CLUSTER && unchecked) {
+                    check_ids();
+                }
+                unchecked = false;
+                const int page = __shfl_sync(0xffffffffu, ids, i - ids_base);
+                src = p.pool + ((int64_t)page * p.hkv + ahead.h) * F::kBlock;
+            }
+            src += lane * 16;
+            uint8_t *dst = ring + slot * F::kBlock + lane * 16;
+#pragma unroll
+            for (int c = 0; c < F::kBlock / 16; c += 32)
+                if (c + 32 <= F::kBlock / 16 || lane < F::kBlock / 16 - c) cp_async16(dst + c * 16, src + c * 16, policy);
+            --left;
+            if (++ahead.pg == aplan.n && left > 0) {  // (not in a cluster, whose warps have one unit)
+                ahead.pg = 0;
+                if (++ahead.h == p.hkv) {
+                    ahead.h = 0;
+                    do ++ahead.b; while (s_prefix[ahead.b + 1] == s_prefix[ahead.b]);
+                }
+                ++unit_ahead;
+                aplan = plan_request<MODE>(p, ahead.b, &none);
+                enter_ahead();
+            }
+        }
+        cp_async_commit();
+    };
+    if (run > 0) enter_ahead();
 #pragma unroll
     for (int i = 0; i < T::kDepth; ++i) issue(i);
 
@@ -388,7 +428,8 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
     const float second = T::kShared && t >= 2 ? -1.f : 0.f;  // this lane's columns take P's second term
 
     auto enter_unit = [&](const int4 (&raw_q)[NT][D / 32]) {
-        plan = plan_request<MODE>(p, at.b, &none);
+        if constexpr (CLUSTER) plan = aplan;
+        else plan = plan_request<MODE>(p, at.b, &none);
         unit0 = f - at.pg;
         const int r = request_id(p, at.b);
         if (MODE == kKv4Scores && looked_at != at.b) {
@@ -759,11 +800,13 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
 
     // the end of this warp's run of a unit: its output when the run is the whole unit, else a partial
     auto leave_unit = [&](int run0, int run1) {
-        const bool whole = run0 == unit0 && run1 == unit0 + plan.n;
+        const bool whole = !CLUSTER && run0 == unit0 && run1 == unit0 + plan.n;
         const bool bad = drop || ((bad_units >> (unit_here & 31)) & 1u);
-        const bool last = run1 == run;
-        const int part = warp * 2 + (last ? 1 : 0);
-        if (lane == 0 && !whole) {
+        const bool last = !CLUSTER && run1 == run;
+        const int part = CLUSTER ? warp : warp * 2 + (last ? 1 : 0);
+        if constexpr (CLUSTER) {
+            if (bad && lane < ROWS) s_ml[part][lane][0] = NAN;
+        } else if (lane == 0 && !whole) {
             s_unit[part] = at.b * p.hkv + at.h;
             s_unit0[part] = runs_of<kWarps>(p, s_prefix).start((int64_t)blockIdx.x * kWarps + warp) + unit0;
             s_bad[part] = bad;
@@ -854,7 +897,7 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
             ++f;
             ++at.pg;
         }
-        if (at.pg == plan.n || f == run) {
+        if ((!CLUSTER && at.pg == plan.n) || f == run) {
             leave_unit(run0, f);
             run0 = f;
             if (f < run) {
@@ -870,6 +913,105 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
         }
     }
     cp_async_wait<0>();
+    if constexpr (CLUSTER) {
+        // ---- the CTA's eight partials are added up, `ways` lanes to four dims of a row; the sums go to
+        // the CTA of the cluster that writes these dims (`share` items of the unit each) ----
+        const int ctas = cluster_nctarank(), rank = cluster_ctarank();
+        const int items = p.rows * (D / 4), share = (items + ctas - 1) / ctas;
+        float4 *got_x = reinterpret_cast<float4 *>(smem + T::kSmem);  // [CTA][share]
+        float2 *got_ml = reinterpret_cast<float2 *>(got_x + ctas * share);
+        int ways = 1;
+        while (ways < kWarps && 2 * ways * items <= kThreads) ways *= 2;
+        const int wide = 32 / ways, way = lane / wide;
+        const int64_t row0 = (int64_t)request_id(p, at.b) * p.tokens;
+        auto write = [&](int e, const Gathered &got) {
+            const int row = e / (D / 4), d = e % (D / 4) * 4;
+            const int64_t to = (row0 + (row >> gshift)) * p.hq + at.h * p.group + (row & (p.group - 1));
+            write_row(p, to * D + d, got, d == 0 ? to : -1);
+        };
+        if (run == 0 && lane < ROWS) {
+            s_ml[warp][lane][0] = -INFINITY;
+            s_ml[warp][lane][1] = 0.f;
+        }
+        __syncthreads();
+        if (ctas > 1) cluster_wait();  // the others have begun: their shared memory is there
+        for (int e0 = warp * wide; e0 < items; e0 += kWarps * wide) {
+            const int e = min(e0 + lane % wide, items - 1);
+            const int row = e / (D / 4), d = e % (D / 4) * 4;
+            Gathered got;
+            bool bad = false;
+#pragma unroll 1
+            for (int c = way; c < kWarps; c += ways * 4) {
+                float2 ml[4];
+                float4 x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int k = c + i * ways;
+                    ml[i] = make_float2(-INFINITY, 0.f);
+                    x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (k < kWarps) {
+                        ml[i] = make_float2(s_ml[k][row][0], s_ml[k][row][1]);
+                        if (ml[i].x > -INFINITY)  // (a warp without blocks has written no sums)
+                            x[i] = *reinterpret_cast<const float4 *>(smem + T::kFirst + k * T::kPart + (row * D + d) * 4);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) bad |= isnan(ml[i].x);
+                got.add(ml, x);
+            }
+            // the lanes' sums, brought to one maximum first
+            float top = got.mx;
+            for (int off = wide; off < 32; off *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const float w = got.mx == top ? 1.f : fast_exp2(got.mx - top);
+            got.mx = top;
+            got.sum *= w;
+            got.acc.x *= w;
+            got.acc.y *= w;
+            got.acc.z *= w;
+            got.acc.w *= w;
+            for (int off = wide; off < 32; off *= 2) {
+                got.sum += __shfl_xor_sync(0xffffffffu, got.sum, off);
+                got.acc.x += __shfl_xor_sync(0xffffffffu, got.acc.x, off);
+                got.acc.y += __shfl_xor_sync(0xffffffffu, got.acc.y, off);
+                got.acc.z += __shfl_xor_sync(0xffffffffu, got.acc.z, off);
+                got.acc.w += __shfl_xor_sync(0xffffffffu, got.acc.w, off);
+            }
+            bad = __any_sync(0xffffffffu, bad);  // any part of the unit: nothing of it is written
+            if (way == 0 && e0 + lane < items) {
+                if (ctas > 1) {
+                    const int owner = e / share, to = rank * share + e - owner * share;
+                    st_cluster_f32x4(cluster_map(smem_u32(got_x + to), owner), got.acc);
+                    st_cluster_f32x2(cluster_map(smem_u32(got_ml + to), owner), bad ? NAN : got.mx, got.sum);
+                } else if (!bad) {
+                    write(e, got);
+                }
+            }
+        }
+        if (ctas == 1) return;
+        __syncwarp();
+        cluster_sync();
+        // ---- this CTA's share of the unit: a part from each CTA ----
+        const int e = rank * share + tid;
+        if (tid < share && e < items) {
+            float2 ml[kKv4MaxCluster];
+            float4 x[kKv4MaxCluster];
+            bool bad = false;
+#pragma unroll
+            for (int k = 0; k < kKv4MaxCluster; ++k) {
+                ml[k] = make_float2(-INFINITY, 0.f);
+                x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k < ctas) {
+                    ml[k] = got_ml[k * share + tid];
+                    x[k] = got_x[k * share + tid];
+                }
+                bad |= isnan(ml[k].x);
+            }
+            Gathered got;
+            got.add(ml, x);
+            if (!bad) write(e, got);
+        }
+        return;
+    }
     __syncthreads();
 
     // ---- the CTA's partials, unit by unit: the unit's output where the CTA holds all of it, else
@@ -1019,28 +1161,96 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
 
 namespace {
 
-template <int D, int ROWS, int MODE>
-cudaError_t launch_one(const Kv4AttnParams &p, int ctas, cudaStream_t stream) {
-    auto kernel = kv4_attn_kernel<D, ROWS, MODE>;
-    // The shared-memory opt-in is a per-device function attribute: set it once per device.
+template <int D, int ROWS, bool CLUSTER>
+constexpr int smem_of = CLUSTER ? Tile<D, ROWS>::kClusterSmem : Tile<D, ROWS>::kSmem;
+
+// The shared-memory opt-in is a per-device function attribute: set it once per device.
+template <int D, int ROWS, int MODE, bool CLUSTER>
+cudaError_t configure(int dev) {
     static std::atomic<uint64_t> configured{0};
+    const uint64_t bit = (dev >= 0 && dev < 64) ? (uint64_t(1) << dev) : 0;
+    if (bit && (configured.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kv4_attn_kernel<D, ROWS, MODE, CLUSTER>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of<D, ROWS, CLUSTER>);
+    if (e == cudaSuccess) configured.fetch_or(bit, std::memory_order_acq_rel);
+    return e;
+}
+
+// cluster: CTAs per unit, or 0 for runs of the row of work.
+template <int D, int ROWS, int MODE, bool CLUSTER>
+cudaError_t launch_one(const Kv4AttnParams &p, int ctas, int cluster, cudaStream_t stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = configure<D, ROWS, MODE, CLUSTER>(dev);
     if (e != cudaSuccess) return e;
-    const uint64_t bit = (dev >= 0 && dev < 64) ? (uint64_t(1) << dev) : 0;
-    if (!bit || !(configured.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Tile<D, ROWS>::kSmem);
-        if (e != cudaSuccess) return e;
-        configured.fetch_or(bit, std::memory_order_acq_rel);
+    return launch_dependent_clusters(kv4_attn_kernel<D, ROWS, MODE, CLUSTER>, ctas, cluster, Tile<D, ROWS>::kThreads,
+                                     smem_of<D, ROWS, CLUSTER>, stream, p);
+}
+
+// How many clusters of `size` CTAs the device holds at once (0: not known).
+template <int D, int ROWS>
+int resident_clusters(int size) {
+    static std::atomic<int> cache[64][kKv4MaxCluster + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    const int known = cache[dev][size].load(std::memory_order_relaxed);
+    if (known > 0) return known;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)size);
+    cfg.blockDim = dim3(Tile<D, ROWS>::kThreads);
+    cfg.dynamicSmemBytes = smem_of<D, ROWS, true>;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)size;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (configure<D, ROWS, kKv4Fast, true>(dev) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kv4_attn_kernel<D, ROWS, kKv4Fast, true>, &cfg) != cudaSuccess) {
+        cudaGetLastError();  // leave no error behind for the next launch's check
+        return 0;
     }
-    return launch_dependent(kernel, ctas, Tile<D, ROWS>::kThreads, Tile<D, ROWS>::kSmem, stream, p);
+    if (n > 0) cache[dev][size].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// The CTAs that each unit of a fast step gets as a cluster of its own, or 0 for the row of work.
+// Clusters need no prefix over the requests and meet through shared memory, so they begin and end
+// about 6 us sooner: 16 requests of 64 + 704 + 256 rows, 16/8/128 heads, take 10.1 us and 15.9 with
+// the row of work, one request 6.8 and 11.4, four tokens of 32/8/128 heads 16.4 and 29.3. So it is
+// clusters of as many CTAs as are all resident at once, where that is possible (64 of these requests
+// would take several waves: 26.4 us in the row), except for units so long that the CTAs left idle
+// cost more: a warp gets blocks / (8 size) of them instead of blocks units / (8 slots). With 160
+// units of 304 slots, 110 blocks of D = 128 each take about as long either way, 88 take 15.5 us and
+// 18.0 in the row, 183 take 25.5 and 22.8; with 240 units 128 blocks take 19.9 and 23.2, 270 blocks
+// 34.9 and 32.5. At D = 64 a block takes half as long (160 units, 128 blocks: 14.1 and 16.3, 270:
+// 24.1 and 20.5), and sixteen rows gain more (88 units of 152 slots, 128 blocks: 21.1 and 29.8, 270:
+// 36.8 and 35.4; D = 64: 14.2 and 19.4, 24.4 and 23.1).
+// The lengths are known on the device alone: the compact pool's size stands for them, so a batch of
+// very unequal selections may get clusters where the row would be better (one of 8000 rows among
+// fifteen of 300: 32 us and 17; 32 to 8192 rows over eight requests: 20.9 and 17.5). Both in one
+// kernel, chosen by the real lengths, cost every fast step 0.5 us and the row 3 us more.
+template <int D, int ROWS>
+int cluster_of(const Kv4AttnParams &p, int64_t slots) {
+    const int64_t units = (int64_t)p.batch * p.hkv;
+    int64_t size = std::min<int64_t>(kKv4MaxCluster, slots / units);
+    while (size > 0 && resident_clusters<D, ROWS>((int)size) < units) --size;
+    const int64_t blocks = p.c_total_pages / units + p.recent / 16 + 1;
+    constexpr int64_t kEven = ROWS > 8 || D == 64 ? 96 : 48;  // the blocks that a CTA may have more than in the row
+    return blocks * (slots - units * size) > kEven * size * slots ? 0 : (int)size;
 }
 
 template <int D, int ROWS>
 cudaError_t launch_mode(const Kv4AttnParams &p, int ctas, cudaStream_t stream) {
-    if (p.c_pool) return launch_one<D, ROWS, kKv4Fast>(p, ctas, stream);
-    return p.scores ? launch_one<D, ROWS, kKv4Scores>(p, ctas, stream)
-                    : launch_one<D, ROWS, kKv4Dense>(p, ctas, stream);
+    if (p.c_pool) {
+        const int size = cluster_of<D, ROWS>(p, ctas);
+        if (size > 0) return launch_one<D, ROWS, kKv4Fast, true>(p, p.batch * p.hkv * size, size, stream);
+        return launch_one<D, ROWS, kKv4Fast, false>(p, ctas, 0, stream);
+    }
+    return p.scores ? launch_one<D, ROWS, kKv4Scores, false>(p, ctas, 0, stream)
+                    : launch_one<D, ROWS, kKv4Dense, false>(p, ctas, 0, stream);
 }
 
 template <int D>

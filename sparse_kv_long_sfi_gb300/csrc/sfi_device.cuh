@@ -109,6 +109,11 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
     return r;
 }
 
+__device__ __forceinline__ uint32_t cluster_nctarank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
 // Barrier over every thread of every CTA in the cluster, right after one thread per
 // CTA initialised the CTA's mbarriers and ran fence_barrier_init: the CTA barrier
 // orders that thread's other shared-memory writes for its own CTA, the init fence
@@ -121,6 +126,17 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
 __device__ __forceinline__ void cluster_arrive_after_init() {
     __syncthreads();
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+// An arrival that orders no memory (the CTA has begun); each thread waits for it once.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+// Barrier over every thread of the cluster; shared memory written before it is visible to
+// all of its CTAs after it.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile(
+        "barrier.cluster.arrive.release.aligned;\n\t"
+        "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
@@ -150,6 +166,9 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t caddr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(caddr), "f"(v) : "memory");
 }
 
+__device__ __forceinline__ void st_cluster_f32x2(uint32_t caddr, float x, float y) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(caddr), "f"(x), "f"(y) : "memory");
+}
 __device__ __forceinline__ void st_cluster_f32x4(uint32_t caddr, float4 v) {
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(caddr), "f"(v.x), "f"(v.y), "f"(v.z),
                  "f"(v.w)
@@ -219,20 +238,30 @@ __device__ __forceinline__ void grid_launch_dependents() {
 // Launch with programmatic stream serialisation: the CTAs may become resident while the
 // stream's previous kernel drains; the kernel calls grid_dependency_wait() before it
 // touches memory.
+// `cluster` > 0: as clusters of that many CTAs.
 template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), int grid, int block, size_t smem, cudaStream_t stream,
-                             Args... args) {
+cudaError_t launch_dependent_clusters(void (*kernel)(Params...), int grid, int cluster, int block, size_t smem,
+                                      cudaStream_t stream, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3((unsigned)block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 0 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), int grid, int block, size_t smem, cudaStream_t stream,
+                             Args... args) {
+    return launch_dependent_clusters(kernel, grid, 0, block, smem, stream, args...);
 }
 
 // ---- TMA (tensor copies global -> shared, completion on an mbarrier) ---------
