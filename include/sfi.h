@@ -594,8 +594,9 @@ SFI_API sfi_status sfi_kv4_compact_gather(const sfi_attn_shape *shape, const sfi
 /*
  * sfi_kv4_dense_attn - sfi_dense_verify_attn (num_tokens query tokens, causal; with one
  * token sfi_slow_dense_attn_with_scores) over the 4-bit cache, whose newest tokens are in
- * the pages already. The work is split over the GPU by the requests' real lengths, so the
- * call takes no bound on them. num_tokens x G <= 16.
+ * the pages already. The work is split over the GPU by the requests' real lengths (few
+ * requests with narrow page tables: by KV head), so the call takes no bound on them.
+ * num_tokens x G <= 16.
  *   q : bf16 [B][num_tokens][Hq][D];  out : fp32 of that shape, 8-byte aligned
  *   lse : fp32 [B][num_tokens][Hq] or NULL;  scores, score_stride : as there, or NULL
  *   workspace : sfi_kv4_workspace_size(shape, batch, num_tokens) bytes, 256-byte aligned,

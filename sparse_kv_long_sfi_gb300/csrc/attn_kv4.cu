@@ -10,8 +10,8 @@
 // workspace, where the last CTA of a unit adds the parts in order (the result does not
 // depend on which one that is).
 //
-// A fast step of few requests is latency: there, a unit belongs to a cluster of CTAs, which
-// finds its blocks without the others' lengths and adds up its parts in shared memory.
+// Few units of few blocks are latency: there, a unit belongs to a cluster of CTAs, which finds
+// its blocks without the others' lengths and adds up its parts in shared memory (cluster_of).
 //
 // Per block (16 tokens): S^T = K Q^T and O^T += V^T P^T with mma.m16n8k16, the tokens (or
 // dims) as the M side, so that eight query rows take one N tile. Codes become fp16 by
@@ -217,8 +217,8 @@ struct Runs {
 };
 
 // The warps' runs over as many CTAs as there is work for. Where a full grid would get less than
-// one or two blocks per warp, fewer warps take that many: one is the shortest chain (1K tokens of
-// one request: 9.4 us, 10.9 with two at least). Up to four, long units are better cut into whole
+// one or two blocks per warp, fewer warps take that many (figures of page tables too wide for
+// clusters): one is the shortest chain (1K tokens of one request: 9.4 us, 10.9 with two at least). Up to four, long units are better cut into whole
 // pairs (one request of 16K tokens: 16.7 us with four blocks, 18.3 with 3.3 on average; 4 tokens of
 // one request of 8K: 24.9 and 27.7), while short ones, with their many edges, are better spread
 // (64 requests of 200 tokens: 22.4 us with 2.7 blocks on average, 25.0 with four).
@@ -1188,7 +1188,7 @@ cudaError_t launch_one(const Kv4AttnParams &p, int ctas, int cluster, cudaStream
 }
 
 // How many clusters of `size` CTAs the device holds at once (0: not known).
-template <int D, int ROWS>
+template <int D, int ROWS, int MODE>
 int resident_clusters(int size) {
     static std::atomic<int> cache[64][kKv4MaxCluster + 1];
     int dev = 0;
@@ -1207,8 +1207,8 @@ int resident_clusters(int size) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (configure<D, ROWS, kKv4Fast, true>(dev) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, kv4_attn_kernel<D, ROWS, kKv4Fast, true>, &cfg) != cudaSuccess) {
+    if (configure<D, ROWS, MODE, true>(dev) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kv4_attn_kernel<D, ROWS, MODE, true>, &cfg) != cudaSuccess) {
         cudaGetLastError();  // leave no error behind for the next launch's check
         return 0;
     }
@@ -1216,7 +1216,7 @@ int resident_clusters(int size) {
     return n;
 }
 
-// The CTAs that each unit of a fast step gets as a cluster of its own, or 0 for the row of work.
+// The CTAs that each unit gets as a cluster of its own, or 0 for the row of work.
 // Clusters need no prefix over the requests and meet through shared memory, so they begin and end
 // about 6 us sooner: 16 requests of 64 + 704 + 256 rows, 16/8/128 heads, take 10.1 us and 15.9 with
 // the row of work, one request 6.8 and 11.4, four tokens of 32/8/128 heads 16.4 and 29.3. So it is
@@ -1232,25 +1232,34 @@ int resident_clusters(int size) {
 // very unequal selections may get clusters where the row would be better (one of 8000 rows among
 // fifteen of 300: 32 us and 17; 32 to 8192 rows over eight requests: 20.9 and 17.5). Both in one
 // kernel, chosen by the real lengths, cost every fast step 0.5 us and the row 3 us more.
-template <int D, int ROWS>
+//
+// Dense attention: lengths differ more, and the page table's width bounds them. Clusters take what they
+// take in sixteen blocks a warp at most: 1000 tokens of one request, 8/2/64 heads with scores, take
+// 5.8 us and 9.7 in the row; 16 requests of 4000 tokens, 16/8/128 heads with scores 22.7 and 29.3
+// (lengths of 60 to 4000: 20.1 and 17.4); 4 tokens of 4 requests of 4000, 32/8/128 heads 14.4 and 26.7.
+template <int D, int ROWS, int MODE>
 int cluster_of(const Kv4AttnParams &p, int64_t slots) {
     const int64_t units = (int64_t)p.batch * p.hkv;
     int64_t size = std::min<int64_t>(kKv4MaxCluster, slots / units);
-    while (size > 0 && resident_clusters<D, ROWS>((int)size) < units) --size;
+    while (size > 0 && resident_clusters<D, ROWS, MODE>((int)size) < units) --size;
+    if (MODE != kKv4Fast) return p.max_pages <= 16 * Tile<D, ROWS>::kWarps * size ? (int)size : 0;
     const int64_t blocks = p.c_total_pages / units + p.recent / 16 + 1;
     constexpr int64_t kEven = ROWS > 8 || D == 64 ? 96 : 48;  // the blocks that a CTA may have more than in the row
     return blocks * (slots - units * size) > kEven * size * slots ? 0 : (int)size;
 }
 
+template <int D, int ROWS, int MODE>
+cudaError_t launch_choice(const Kv4AttnParams &p, int ctas, cudaStream_t stream) {
+    const int size = cluster_of<D, ROWS, MODE>(p, ctas);
+    if (size > 0) return launch_one<D, ROWS, MODE, true>(p, p.batch * p.hkv * size, size, stream);
+    return launch_one<D, ROWS, MODE, false>(p, ctas, 0, stream);
+}
+
 template <int D, int ROWS>
 cudaError_t launch_mode(const Kv4AttnParams &p, int ctas, cudaStream_t stream) {
-    if (p.c_pool) {
-        const int size = cluster_of<D, ROWS>(p, ctas);
-        if (size > 0) return launch_one<D, ROWS, kKv4Fast, true>(p, p.batch * p.hkv * size, size, stream);
-        return launch_one<D, ROWS, kKv4Fast, false>(p, ctas, 0, stream);
-    }
-    return p.scores ? launch_one<D, ROWS, kKv4Scores, false>(p, ctas, 0, stream)
-                    : launch_one<D, ROWS, kKv4Dense, false>(p, ctas, 0, stream);
+    if (p.c_pool) return launch_choice<D, ROWS, kKv4Fast>(p, ctas, stream);
+    return p.scores ? launch_choice<D, ROWS, kKv4Scores>(p, ctas, stream)
+                    : launch_choice<D, ROWS, kKv4Dense>(p, ctas, stream);
 }
 
 template <int D>
