@@ -252,8 +252,8 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
 
-    grid_launch_dependents();
     grid_dependency_wait();
+    grid_launch_dependents();  // not before the wait: see launch_dependent_clusters
     uint32_t none = 0;  // (a request's errors are reported once, where its blocks are counted)
     Place at{};
     ReqPlan aplan{};

@@ -129,8 +129,8 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 4) kv4_append_kernel(const Kv4
     __shared__ Kv4Tile<D> s_tile[kKv4Warps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t items = (int64_t)batch * page_slots * p.hkv * 2;
-    grid_launch_dependents();
     grid_dependency_wait();
+    grid_launch_dependents();  // not before the wait: see launch_dependent_clusters
     for (int64_t item = (int64_t)blockIdx.x * kKv4Warps + warp; item < items;
          item += (int64_t)gridDim.x * kKv4Warps) {
         const Kv4Item x(item, p.hkv, page_slots);
@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(kKv4Warps * 32) kv4_read_kernel(const Kv4CopyP
     __shared__ Kv4Tile<D> s_tile[kKv4Warps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t items = (int64_t)batch * page_slots * p.hkv * 2;
-    grid_launch_dependents();
     grid_dependency_wait();
+    grid_launch_dependents();  // not before the wait: see launch_dependent_clusters
     for (int64_t item = (int64_t)blockIdx.x * kKv4Warps + warp; item < items;
          item += (int64_t)gridDim.x * kKv4Warps) {
         const Kv4Item x(item, p.hkv, page_slots);
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32) kv4_compact_kernel(const Kv4Co
     using F = Kv4<D>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t items = (int64_t)batch * slots * p.hkv;
-    grid_launch_dependents();
+    grid_launch_dependents();  // (an ordinary launch: everything before it on the stream has finished)
     for (int64_t item = (int64_t)blockIdx.x * kKv4Warps + warp; item < items;
          item += (int64_t)gridDim.x * kKv4Warps) {
         const int h = (int)(item % p.hkv);

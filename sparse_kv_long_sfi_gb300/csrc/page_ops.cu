@@ -9,7 +9,8 @@
 //
 // The kernels wait for the stream's previous kernel as dependent launches, but none releases
 // its own dependents early: they write page tables, lengths and pages, which an attention
-// launch may be allowed to read ahead of its wait (SFI_ATTN_EARLY_KV_PREFETCH).
+// launch may be allowed to read ahead of its wait (SFI_ATTN_EARLY_KV_PREFETCH). (Nor would any
+// kernel do so before its own wait: see launch_dependent_clusters.)
 #include <algorithm>
 
 #include "sfi_device.cuh"

@@ -237,7 +237,10 @@ __device__ __forceinline__ void grid_launch_dependents() {
 
 // Launch with programmatic stream serialisation: the CTAs may become resident while the
 // stream's previous kernel drains; the kernel calls grid_dependency_wait() before it
-// touches memory.
+// touches memory, and grid_launch_dependents() only after that. So at most two kernels of a
+// stream overlap: an attention launch that reads ahead of its own wait because its direct
+// predecessor writes nothing of it (SFI_ATTN_EARLY_KV_PREFETCH) finds the kernels before that
+// one finished. Released before the wait, it would start while they still write its pages.
 // `cluster` > 0: as clusters of that many CTAs.
 template <typename... Params, typename... Args>
 cudaError_t launch_dependent_clusters(void (*kernel)(Params...), int grid, int cluster, int block, size_t smem,
