@@ -56,7 +56,9 @@ __device__ __forceinline__ int block_scan(int v, int *s_warp, int *total) {
     return (warp ? before : 0) + incl - v;
 }
 
-__device__ __forceinline__ int pages_of(int len) { return (len + kSubTokens - 1) / kSubTokens; }
+// Pages that len >= 0 tokens take. (No sum that a length near 2^31 could carry past it: every
+// length, those that only device data can say too, compares with the table's width.)
+__device__ __forceinline__ int pages_of(int len) { return len / kSubTokens + (len % kSubTokens != 0); }
 
 }  // namespace
 

@@ -1,0 +1,61 @@
+"""The page operators at the ends of their ranges: lengths that only device data can say, sums
+past 32 bits, pages of several chunks."""
+import numpy as np
+import pytest
+import torch
+
+from tests.gpu_harness import dev_i32
+from tests.test_gpu_pages import Device, Model
+
+pytestmark = pytest.mark.gpu
+
+BAD_LEN, NO_PAGE = 2, 64
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    from sparse_kv_long_sfi_gb300 import build
+    build.build()
+
+
+def _sfi():
+    import sparse_kv_long_sfi_gb300 as sfi
+    return sfi
+
+
+@pytest.mark.parametrize("length", [2 ** 31 - 1, 2 ** 31 - 15, 2 ** 31 - 16, 2 ** 31 - 17, 49, -1, -2 ** 31])
+def test_a_length_out_of_range_is_no_length(length):
+    """A length beyond the table, up to the largest a 32-bit word holds, or below zero: the request
+    is refused by every call, and nothing changes."""
+    sfi = _sfi()
+    m = Model(5, 3, 12, 2, 32, 4)
+    assert m.reserve([20, 40], [0, 1])
+    m.lens[3] = length
+    d = Device(m)
+
+    def refused(what, call):
+        d.st.zero_()
+        call()
+        assert d.st.item() == BAD_LEN, what
+        d.same(m, (length, what))
+
+    refused("fork", lambda: sfi.sfi_page_fork(d.map, dev_i32([3]), dev_i32([4]), dev_status=d.st))
+    for part in (0, 16, max(0, length - 20)):
+        refused(("fork", part), lambda: sfi.sfi_page_fork(d.map, dev_i32([3]), dev_i32([4]), dev_i32([part]), dev_status=d.st))
+    refused("free", lambda: sfi.sfi_page_free(d.map, dev_i32([3]), dev_status=d.st))
+    refused("free twice", lambda: sfi.sfi_page_free(d.map, dev_i32([3, 3]), dev_status=d.st))
+    for new in (48, 2 ** 31 - 1):
+        refused(("reserve", new), lambda: sfi.sfi_page_reserve(d.map, d.pp, dev_i32([new]), dev_i32([3]), workspace=d.ws,
+                                                               dev_status=d.st))
+    refused("reserve that far", lambda: sfi.sfi_page_reserve(d.map, d.pp, dev_i32([2 ** 31 - 1]), dev_i32([0]),
+                                                             workspace=d.ws, dev_status=d.st))
+    # a compaction copies the row of such a request as it is
+    table, ref, live = torch.empty_like(d.map.page_table), torch.empty_like(d.map.ref_count), dev_i32([0])
+    d.st.zero_()
+    sfi.sfi_page_compact(d.map, d.pp, table, ref, live, workspace=d.ws, dev_status=d.st)
+    assert d.st.item() == BAD_LEN and live.item() == 5
+    m.lens[3] = 0
+    m.compact()
+    assert np.array_equal(table.cpu().numpy(), m.table) and np.array_equal(ref.cpu().numpy(), m.ref)
