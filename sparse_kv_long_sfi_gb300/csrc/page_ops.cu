@@ -56,6 +56,13 @@ __device__ __forceinline__ int block_scan(int v, int *s_warp, int *total) {
     return (warp ? before : 0) + incl - v;
 }
 
+// Adds v >= 0 of all of the CTA's threads to *sum in 64 bits (complete after the next barrier).
+__device__ __forceinline__ void block_sum(int v, unsigned long long *sum) {
+    const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)v & 0xffffu);
+    const uint32_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)v >> 16);
+    if ((threadIdx.x & 31) == 0) atomicAdd(sum, ((unsigned long long)hi << 16) + lo);
+}
+
 // Pages that len >= 0 tokens take. (No sum that a length near 2^31 could carry past it: every
 // length, those that only device data can say too, compares with the table's width.)
 __device__ __forceinline__ int pages_of(int len) { return len / kSubTokens + (len % kSubTokens != 0); }
@@ -194,6 +201,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_reserve_kernel(const PageMa
     __shared__ int s_warp[kPlanWarps];
     __shared__ int2 s_entry[kPlanThreads];  // request and part-filled last page (or -1) of list entry i
     __shared__ int s_first[kPlanThreads];   // rank of its first page among those handed out
+    __shared__ unsigned long long s_need;   // pages that all of them need
     grid_dependency_wait();
     const PageLists lists(ws, m.num_pages);
     const int tid = threadIdx.x;
@@ -221,7 +229,10 @@ __global__ void __launch_bounds__(kPlanThreads) page_reserve_kernel(const PageMa
         }
     }
     s_entry[tid] = make_int2(r, last);
-    if (tid == 0) lists.moves[0] = 0;
+    if (tid == 0) {
+        lists.moves[0] = 0;
+        s_need = 0;
+    }
     __syncthreads();
     int before = 0;  // holders of the same last page that come earlier in the list
     bool twice = false;
@@ -242,12 +253,19 @@ __global__ void __launch_bounds__(kPlanThreads) page_reserve_kernel(const PageMa
     // a shared last page is copied, except by the last of its holders in the list when they
     // are all there are
     const bool copy = last >= 0 && m.ref_count[last] - before > 1;
+    // (a row of the table may have 2^27 pages, so 1024 requests may ask for more than 32 bits count;
+    // the scan's sums hold when there are that many pages at all)
+    block_sum(fresh + copy, &s_need);
     int total = 0, copies = 0;
     const int first = block_scan(fresh + copy, s_warp, &total);
     const int move = block_scan(copy, s_warp, &copies);
     s_first[tid] = first;
     if (copies && !can_copy) {
         if (tid == 0) report(dev_status, SFI_DEV_BAD_PAGE);
+        return;
+    }
+    if (s_need > (unsigned long long)m.num_pages) {
+        if (tid == 0) report(dev_status, SFI_DEV_NO_PAGE);
         return;
     }
     // the `total` lowest free pages

@@ -59,3 +59,32 @@ def test_a_length_out_of_range_is_no_length(length):
     m.lens[3] = 0
     m.compact()
     assert np.array_equal(table.cpu().numpy(), m.table) and np.array_equal(ref.cpu().numpy(), m.ref)
+
+
+def test_a_need_past_32_bits_is_refused():
+    """1024 requests that ask for 2^31 pages and more between them (a table of 17 GB): the sum of
+    what they need does not wrap, the reservation is refused, and nothing changes."""
+    sfi = _sfi()
+    n, maxp = 1024, (1 << 22) + 8
+    table = torch.zeros(n, maxp, dtype=torch.int32, device="cuda")
+    lens, ref = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.zeros(300, dtype=torch.int32, device="cuda")
+    pm = sfi.PageMap(table, lens, ref)
+    ws, st = sfi.alloc_page_workspace(pm), torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def reserve(pages):
+        st.zero_()
+        sfi.sfi_page_reserve(pm, None, dev_i32(np.asarray(pages, np.int64) * 16), workspace=ws, dev_status=st)
+        return st.item()
+
+    half, whole = np.full(n, 1 << 21), np.full(n, 1 << 22)
+    more = whole.copy()
+    more[3] += 5
+    # 2^31, 2^32, 2^32 + 5 (which is 5 modulo 2^32), and one page too many
+    for pages in (half, whole, more, np.r_[np.zeros(n - 1, int), 301], np.r_[150, np.zeros(n - 2, int), 151]):
+        assert reserve(pages) == NO_PAGE
+        assert not lens.any() and not ref.any()
+    assert table.max().item() == 0 == table.min().item()
+    assert reserve(np.r_[150, np.zeros(n - 2, int), 150]) == 0  # as many as there are
+    assert (ref == 1).all() and lens[0].item() == lens[-1].item() == 2400
+    assert torch.equal(table[[0, -1], :150].flatten(), torch.arange(300, dtype=torch.int32, device="cuda"))
+    assert table[:, 150:].max().item() == 0 == table[1:-1].max().item()
