@@ -90,7 +90,14 @@ __device__ void renumber_row(const PageMapParams &m, int r, const int32_t *new_i
 }
 
 // ---- copy: page src[i] -> dst[i] of every pool, in chunks ------------------------------
-// (table_out: a compaction's new table is written in the same launch)
+// (TABLE: with table_out, a compaction's new table is written in the same launch)
+//
+// That part takes registers: 48 against 32, five CTAs per SM against eight. Pages of up to half a
+// chunk leave threads idle and want the eight (2000 pages of 8 x 4608 bytes: 25.3 us, 33.3 with
+// five; 4000 of 8 x 8192: 86.7 and 92.2). Larger ones stream better from the five (4000 of
+// 8 x 12288 bytes: 124 us, 128 with eight; 3500 of 8 x 32768: 281 and 293), so they take the same
+// kernel as a compaction, without a table.
+template <bool TABLE>
 __global__ void __launch_bounds__(kPageThreads) page_copy_kernel(void *const *pools, int num_pools, int64_t page_bytes,
                                                                  int num_pages, const int32_t *src, const int32_t *dst,
                                                                  int n_host, const int32_t *n_dev, const PageMapParams m,
@@ -98,7 +105,7 @@ __global__ void __launch_bounds__(kPageThreads) page_copy_kernel(void *const *po
                                                                  int32_t *dev_status) {
     constexpr int kLoads = kCopyChunk / 16 / kPageThreads;
     grid_dependency_wait();
-    if (table_out)
+    if (TABLE && table_out)
         for (int r = blockIdx.x; r < m.num_reqs; r += gridDim.x) renumber_row(m, r, new_ids, table_out, dev_status);
     const int n = n_dev ? *n_dev : n_host;
     const int chunks = (int)((page_bytes + kCopyChunk - 1) / kCopyChunk);
@@ -401,7 +408,8 @@ cudaError_t launch_copy(const PagePoolParams &q, const int32_t *src, const int32
     const int64_t chunks = (q.page_bytes + kCopyChunk - 1) / kCopyChunk;
     const int64_t items = std::max<int64_t>((int64_t)most * q.num_pools * chunks, table_out ? m.num_reqs : 0);
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(items, (int64_t)sms * 8));
-    return launch_dependent(page_copy_kernel, grid, kPageThreads, 0, stream, q.pools, q.num_pools, q.page_bytes,
+    const bool small = !table_out && q.page_bytes <= kCopyChunk / 2;
+    return launch_dependent(small ? page_copy_kernel<false> : page_copy_kernel<true>, grid, kPageThreads, 0, stream, q.pools, q.num_pools, q.page_bytes,
                             q.num_pages, src, dst, n, n_dev, m, new_ids, table_out, dev_status);
 }
 
