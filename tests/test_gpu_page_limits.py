@@ -88,3 +88,39 @@ def test_a_need_past_32_bits_is_refused():
     assert (ref == 1).all() and lens[0].item() == lens[-1].item() == 2400
     assert torch.equal(table[[0, -1], :150].flatten(), torch.arange(300, dtype=torch.int32, device="cuda"))
     assert table[:, 150:].max().item() == 0 == table[1:-1].max().item()
+
+
+@pytest.mark.parametrize("page_bytes", [8176, 8192, 8208, 16384 + 16, 2 * 16384 + 16])
+def test_pages_of_several_chunks(page_bytes):
+    """Pages that end in, at and behind the first chunk of a copy, and in the third: copied by ids,
+    by a reservation and by a compaction (whose number of moves the device knows), in three pools."""
+    sfi = _sfi()
+    rng = np.random.default_rng(page_bytes)
+    m = Model(30, 6, 160, 3, page_bytes, 11)
+    assert m.reserve(list(rng.integers(1, 96, 20)), list(range(20)))
+    d = Device(m)
+    free = np.flatnonzero(m.ref == 0)
+    src, dst = rng.choice(np.flatnonzero(m.ref), 20), rng.permutation(free)[:20]
+    sfi.sfi_page_copy(d.pp, dev_i32(src), dev_i32(dst), dev_status=d.st)
+    for p in m.pools:
+        p[dst] = p[src]
+    d.same(m, "copy")
+    src, dst = list(range(10)), list(range(20, 30))
+    sfi.sfi_page_fork(d.map, dev_i32(src), dev_i32(dst), dev_status=d.st)
+    m.fork(src, dst)
+    new, reqs = list(m.lens[dst] + 1), dst
+    assert (m.lens[dst] % 16 != 0).sum() > 3
+    sfi.sfi_page_reserve(d.map, d.pp, dev_i32(new), dev_i32(reqs), workspace=d.ws, dev_status=d.st)
+    assert m.reserve(new, reqs)
+    d.same(m, "reserve")
+    sfi.sfi_page_free(d.map, dev_i32(list(range(0, 20, 2))), dev_status=d.st)
+    m.free(list(range(0, 20, 2)))
+    table, ref = torch.empty_like(d.map.page_table), torch.empty_like(d.map.ref_count)
+    live = torch.empty(1, dtype=torch.int32, device="cuda")
+    sfi.sfi_page_compact(d.map, d.pp, table, ref, live, workspace=d.ws, dev_status=d.st)
+    held = int((m.ref > 0).sum())
+    assert (m.ref[held:] > 0).sum() > 5  # some pages move
+    assert live.item() == m.compact() == held
+    d.map = sfi.PageMap(table, d.map.seq_lens, ref)
+    d.same(m, "compact")
+    assert d.st.item() == 0
