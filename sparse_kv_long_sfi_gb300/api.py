@@ -352,6 +352,10 @@ class _Handle:
         object.__setattr__(self, name, value)
         self.__dict__.pop("_c", None)
 
+    def __getstate__(self):
+        # a copy (copy, deepcopy, pickle) makes its own structure, of its own tensors
+        return {k: v for k, v in self.__dict__.items() if not k.startswith("_")}
+
     def c(self):
         d = self.__dict__
         c = d.get("_c")
@@ -724,6 +728,12 @@ class PagePools:
         self.addresses = torch.tensor([t.data_ptr() for t in pools], dtype=torch.int64).to(first.device)
         self._c = _abi.sfi_page_pools(self.addresses.data_ptr(), len(pools), first.nbytes // max(1, first.shape[0]),
                                       first.shape[0])
+
+    def __getstate__(self):
+        return {"pools": self.pools}
+
+    def __setstate__(self, state):
+        self.__init__(state["pools"])
 
     def c(self) -> _abi.sfi_page_pools:
         _on_current_device(self.addresses, "pools")
