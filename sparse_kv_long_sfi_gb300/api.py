@@ -342,11 +342,36 @@ def sfi_fast_decode_attn_noalloc(shape: AttnShape, kv: PagedKV, compact: Compact
     _check(st, "sfi_fast_decode_attn_noalloc")
 
 
+# The launches go to the current device. The calls from here on take tensors of that device alone;
+# dev is its index, asked for once a call.
+def _on_current_device(t: torch.Tensor, name: str):
+    if t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+
+
+def _need_here(t: Optional[torch.Tensor], dtype, name: str, dev: int):
+    if t is not None and t.get_device() == dev and t.dtype is dtype and t.is_contiguous():
+        return
+    _need(t, dtype, name)
+    _on_current_device(t, name)
+
+
+def _ptr_here(t: Optional[torch.Tensor], dtype, name: str, dev: int) -> Optional[int]:
+    if t is None:
+        return None
+    _need_here(t, dtype, name, dev)
+    return t.data_ptr()
+
+
+def _stream_here(stream, dev: int) -> Optional[int]:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
 class _Handle:
     """Tensors that one C structure points to. The structure is checked and made when it is
-    first needed, and again when a field has been assigned or a tensor's memory, shape or strides
-    are no longer what they were (resize_, set_, .data = ...): a call that finds it ready saves
-    itself the checks and the structure."""
+    first needed, and again when a field has been assigned, a tensor's memory, shape or strides
+    are no longer what they were (resize_, set_, .data = ...), or another device is the current
+    one: a call that finds it ready saves itself the checks and the structure."""
     _tensors = ()
 
     def __setattr__(self, name, value):
@@ -357,20 +382,22 @@ class _Handle:
         # a copy (copy, deepcopy, pickle) makes its own structure, of its own tensors
         return {k: v for k, v in self.__dict__.items() if not k.startswith("_")}
 
-    def _now(self):
-        at = []
-        for n in self._tensors:
-            t = self.__dict__[n]
-            at += (t.data_ptr(), t.shape, t.stride())
-        return at
-
-    def c(self):
+    def c(self, dev: Optional[int] = None):
+        """The structure, for calls on device dev (None: the current one)."""
+        if dev is None:
+            dev = torch._C._cuda_getDevice()
         d = self.__dict__
-        c, now = d.get("_c"), self._now()
-        if c is not None and d["_at"] == now:
-            return c
-        c = self._make()
-        d["_at"] = now
+        kept = d.get("_c")
+        if kept is not None and d["_dev"] == dev:
+            for t, ptr, size, stride in d["_at"]:
+                if t.data_ptr() != ptr or t.shape != size or t.stride() != stride:
+                    break
+            else:
+                return kept
+        d.pop("_c", None)
+        c = self._make(dev)
+        d["_dev"] = dev
+        d["_at"] = [(t, t.data_ptr(), t.shape, t.stride()) for t in (d[n] for n in self._tensors)]
         d["_c"] = c
         return c
 
@@ -389,9 +416,9 @@ class Rope(_Handle):
     def _tensors(self):
         return ("turns",) if self.axis is None else ("turns", "axis")
 
-    def _make(self) -> _abi.sfi_rope:
-        _need(self.turns, torch.int64, "rope.turns")
-        axis = _ptr(self.axis, torch.uint8, "rope.axis")
+    def _make(self, dev: int) -> _abi.sfi_rope:
+        _need_here(self.turns, torch.int64, "rope.turns", dev)
+        axis = _ptr_here(self.axis, torch.uint8, "rope.axis", dev)
         if self.axis is not None and self.axis.numel() != self.turns.numel():
             raise ValueError("rope.axis needs one entry for each of rope.turns")
         return _abi.sfi_rope(self.turns.data_ptr(), axis, 2 * self.turns.numel(), int(self.num_axes),
@@ -425,16 +452,13 @@ def _indexed(t: Optional[torch.Tensor], requests: int, name: str):
         raise ValueError(f"{name} needs one entry for each of {requests} requests, has {t.shape[0]}")
 
 
-def _on_current_device(t: torch.Tensor, name: str):
-    if t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{name} is on {t.device}, not on the current device")
-
-
-def _token_rows(t: torch.Tensor, heads: int, dim: int, name: str):
+def _token_rows(t: torch.Tensor, heads: int, dim: int, name: str, dev: int):
     """Requests, tokens and elements between tokens of a [B][T][heads][dim] tensor whose heads
     are contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        _on_current_device(t, name)
     if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     dims = t.shape
@@ -458,13 +482,13 @@ def sfi_qk_norm_rope(shape: AttnShape, rope: Optional[Rope], q: torch.Tensor, k:
     """Head norm and rotation of the new tokens; q, k, v [B][T][heads][D] may be views of one
     fused projection. positions int32 [num_axes][B][T] (or [B][T] with one axis)."""
     hq, hkv, d = shape.num_q_heads, shape.num_kv_heads, shape.head_dim
-    _on_current_device(q, "q")
-    B, T, qs = _token_rows(q, hq, d, "q")
-    kb, kt, ks = _token_rows(k, hkv, d, "k")
-    vb, vt, vs = (B, T, 0) if v is None else _token_rows(v, hkv, d, "v")
+    dev = torch._C._cuda_getDevice()
+    B, T, qs = _token_rows(q, hq, d, "q", dev)
+    kb, kt, ks = _token_rows(k, hkv, d, "k", dev)
+    vb, vt, vs = (B, T, 0) if v is None else _token_rows(v, hkv, d, "v", dev)
     if kb != B or kt != T or vb != B or vt != T:
         raise ValueError("q, k and v need the same requests and tokens")
-    _need(q_out, torch.bfloat16, "q_out")
+    _need_here(q_out, torch.bfloat16, "q_out", dev)
     if q_out.shape != q.shape or (k_out is not None and k_out.shape != k.shape):
         raise ValueError("q_out and k_out need the shapes of q and k")
     if (q_weight is not None and q_weight.numel() != d) or (k_weight is not None and k_weight.numel() != d):
@@ -476,18 +500,23 @@ def sfi_qk_norm_rope(shape: AttnShape, rope: Optional[Rope], q: torch.Tensor, k:
     kv_c = None
     if kv is not None:
         kv_c = ctypes.byref(kv.c())
+        for name in ("k_pool", "v_pool", "page_table", "seq_lens"):
+            if getattr(kv, name).get_device() != dev:
+                _on_current_device(getattr(kv, name), name)
         dims = kv.k_pool.shape
         if len(dims) != 4 or dims[1] != hkv or dims[2] != shape.page_size or dims[3] != d or kv.v_pool.shape != dims:
             raise ValueError(f"the pools must be [num_pages][{hkv}][{shape.page_size}][{d}]")
         if kv.seq_lens.numel() != B:
             raise ValueError("q, k and v need one entry for each request of the pages")
     st = _abi.lib().sfi_qk_norm_rope(
-        ctypes.byref(shape.c()), None if rope is None else ctypes.byref(rope.c()), q.data_ptr(), qs, k.data_ptr(), ks,
-        None if v is None else v.data_ptr(), vs, _ptr(q_weight, torch.bfloat16, "q_weight"),
-        _ptr(k_weight, torch.bfloat16, "k_weight"), eps, _ptr(positions, torch.int32, "positions"), B * T, T,
-        _ptr(new_lens, torch.int32, "new_lens"), _ptr(seq_lens, torch.int32, "seq_lens"), q_out.data_ptr(),
-        _ptr(k_out, torch.bfloat16, "k_out"), kv_c, _ptr(req_ids, torch.int32, "req_ids"), _count(B, batch, req_ids),
-        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+        ctypes.byref(shape.c()), None if rope is None else ctypes.byref(rope.c(dev)), q.data_ptr(), qs,
+        k.data_ptr(), ks, None if v is None else v.data_ptr(), vs, _ptr_here(q_weight, torch.bfloat16, "q_weight", dev),
+        _ptr_here(k_weight, torch.bfloat16, "k_weight", dev), eps,
+        _ptr_here(positions, torch.int32, "positions", dev), B * T, T,
+        _ptr_here(new_lens, torch.int32, "new_lens", dev), _ptr_here(seq_lens, torch.int32, "seq_lens", dev),
+        q_out.data_ptr(), _ptr_here(k_out, torch.bfloat16, "k_out", dev), kv_c,
+        _ptr_here(req_ids, torch.int32, "req_ids", dev), _count(B, batch, req_ids),
+        _ptr_here(dev_status, torch.int32, "dev_status", dev), _stream_here(stream, dev))
     _check(st, "sfi_qk_norm_rope")
 
 
@@ -503,11 +532,10 @@ class PagedKV4(_Handle):
 
     _tensors = ("pool", "page_table", "seq_lens")
 
-    def _make(self) -> _abi.sfi_paged_kv4:
-        _need(self.pool, torch.uint8, "pool")
-        _need(self.page_table, torch.int32, "page_table")
-        _need(self.seq_lens, torch.int32, "seq_lens")
-        _on_current_device(self.pool, "pool")
+    def _make(self, dev: int) -> _abi.sfi_paged_kv4:
+        _need_here(self.pool, torch.uint8, "pool", dev)
+        _need_here(self.page_table, torch.int32, "page_table", dev)
+        _need_here(self.seq_lens, torch.int32, "seq_lens", dev)
         if self.pool.dim() != 3:
             raise ValueError(f"pool must be [num_pages][Hkv][18 D], got {list(self.pool.shape)}")
         if self.page_table.dim() != 2 or self.seq_lens.numel() != self.page_table.shape[0]:
@@ -529,11 +557,11 @@ class CompactKV4(_Handle):
 
     _tensors = ("pool", "page_offset", "capacity", "count")
 
-    def _make(self) -> _abi.sfi_compact_kv4:
-        _need(self.pool, torch.uint8, "compact.pool")
-        _need(self.page_offset, torch.int64, "compact.page_offset")
-        _need(self.capacity, torch.int32, "compact.capacity")
-        _need(self.count, torch.int32, "compact.count")
+    def _make(self, dev: int) -> _abi.sfi_compact_kv4:
+        _need_here(self.pool, torch.uint8, "compact.pool", dev)
+        _need_here(self.page_offset, torch.int64, "compact.page_offset", dev)
+        _need_here(self.capacity, torch.int32, "compact.capacity", dev)
+        _need_here(self.count, torch.int32, "compact.count", dev)
         self.__dict__["_requests"] = self.page_offset.numel()
         if self.capacity.numel() != self.page_offset.numel() or self.count.numel() != self.page_offset.numel():
             raise ValueError("compact.page_offset, capacity and count need one entry per request")
@@ -544,18 +572,16 @@ class CompactKV4(_Handle):
                                     self.capacity.data_ptr(), self.count.data_ptr())
 
 
-def _kv4(shape: AttnShape, kv: PagedKV4):
-    c = kv.c()
+def _kv4(shape: AttnShape, kv: PagedKV4, dev: int):
+    c = kv.c(dev)
     if kv._dims != (shape.num_kv_heads, 18 * shape.head_dim):
         raise ValueError(f"pool must be [num_pages][{shape.num_kv_heads}][{18 * shape.head_dim}], "
                          f"got {list(kv.pool.shape)}")
-    if kv.pool.get_device() != torch._C._cuda_getDevice():
-        _on_current_device(kv.pool, "pool")
     return ctypes.byref(c)
 
 
-def _compact4(shape: AttnShape, kv: PagedKV4, compact: CompactKV4):
-    c = compact.c()
+def _compact4(shape: AttnShape, kv: PagedKV4, compact: CompactKV4, dev: int):
+    c = compact.c(dev)
     if compact._bytes != 18 * shape.head_dim:
         raise ValueError(f"compact.pool must be [total_pages][{18 * shape.head_dim}]")
     if compact._requests != kv._requests:
@@ -577,9 +603,9 @@ def alloc_kv4_compact(shape: AttnShape, rows, device="cuda") -> CompactKV4:
                       torch.zeros(len(cap), dtype=torch.int32, device=device))
 
 
-def _rows4(t: torch.Tensor, dtype, shape: AttnShape, heads: int, name: str) -> int:
+def _rows4(t: torch.Tensor, dtype, shape: AttnShape, heads: int, name: str, dev: int) -> int:
     """Tokens of a [B][T][heads][D] tensor."""
-    _need(t, dtype, name)
+    _need_here(t, dtype, name, dev)
     dims = t.shape
     if len(dims) != 4 or dims[2] != heads or dims[3] != shape.head_dim:
         raise ValueError(f"{name} must be [B][T][{heads}][{shape.head_dim}], got {list(dims)}")
@@ -590,57 +616,62 @@ def sfi_kv4_append(shape: AttnShape, kv: PagedKV4, k_new: torch.Tensor, v_new: t
                    new_lens: Optional[torch.Tensor] = None, req_ids: Optional[torch.Tensor] = None,
                    batch: Optional[int] = None, dev_status: Optional[torch.Tensor] = None, stream=None):
     """k_new, v_new [B][T][Hkv][D]; either may be a view of a fused projection (contiguous heads)."""
-    kb, T, ks = _token_rows(k_new, shape.num_kv_heads, shape.head_dim, "k_new")
-    vb, vt, vs = _token_rows(v_new, shape.num_kv_heads, shape.head_dim, "v_new")
-    kv_c = _kv4(shape, kv)
+    dev = torch._C._cuda_getDevice()
+    kb, T, ks = _token_rows(k_new, shape.num_kv_heads, shape.head_dim, "k_new", dev)
+    vb, vt, vs = _token_rows(v_new, shape.num_kv_heads, shape.head_dim, "v_new", dev)
+    kv_c = _kv4(shape, kv, dev)
     B = kv._requests
     if kb != B or vb != B or vt != T:
         raise ValueError(f"k_new and v_new need the same shape, with one entry for each of {B} requests")
     _indexed(new_lens, B, "new_lens")
     st = _abi.lib().sfi_kv4_append(
         ctypes.byref(shape.c()), kv_c, k_new.data_ptr(), ks, v_new.data_ptr(), vs, T,
-        _ptr(new_lens, torch.int32, "new_lens"), _ptr(req_ids, torch.int32, "req_ids"), _count(B, batch, req_ids),
-        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+        _ptr_here(new_lens, torch.int32, "new_lens", dev), _ptr_here(req_ids, torch.int32, "req_ids", dev),
+        _count(B, batch, req_ids), _ptr_here(dev_status, torch.int32, "dev_status", dev), _stream_here(stream, dev))
     _check(st, "sfi_kv4_append")
 
 
 def sfi_kv4_read(shape: AttnShape, kv: PagedKV4, k_out: torch.Tensor, v_out: torch.Tensor,
                  first: Optional[torch.Tensor] = None, req_ids: Optional[torch.Tensor] = None,
                  batch: Optional[int] = None, dev_status: Optional[torch.Tensor] = None, stream=None):
-    T = _rows4(k_out, torch.bfloat16, shape, shape.num_kv_heads, "k_out")
-    _need(v_out, torch.bfloat16, "v_out")
+    dev = torch._C._cuda_getDevice()
+    T = _rows4(k_out, torch.bfloat16, shape, shape.num_kv_heads, "k_out", dev)
+    _need_here(v_out, torch.bfloat16, "v_out", dev)
     if v_out.shape != k_out.shape:
         raise ValueError("k_out and v_out need the same shape")
-    kv_c = _kv4(shape, kv)
+    kv_c = _kv4(shape, kv, dev)
     B = kv._requests
     _indexed(k_out, B, "k_out")
     _indexed(first, B, "first")
     st = _abi.lib().sfi_kv4_read(
-        ctypes.byref(shape.c()), kv_c, k_out.data_ptr(), v_out.data_ptr(), T, _ptr(first, torch.int32, "first"),
-        _ptr(req_ids, torch.int32, "req_ids"), _count(B, batch, req_ids), _ptr(dev_status, torch.int32, "dev_status"),
-        _stream(stream))
+        ctypes.byref(shape.c()), kv_c, k_out.data_ptr(), v_out.data_ptr(), T,
+        _ptr_here(first, torch.int32, "first", dev), _ptr_here(req_ids, torch.int32, "req_ids", dev),
+        _count(B, batch, req_ids), _ptr_here(dev_status, torch.int32, "dev_status", dev), _stream_here(stream, dev))
     _check(st, "sfi_kv4_read")
 
 
 def sfi_kv4_compact_gather(shape: AttnShape, kv: PagedKV4, idx: torch.Tensor, count: torch.Tensor, sink: int,
                            compact: CompactKV4, req_ids: Optional[torch.Tensor] = None, batch: Optional[int] = None,
                            dev_status: Optional[torch.Tensor] = None, stream=None):
-    kv_c = _kv4(shape, kv)
+    dev = torch._C._cuda_getDevice()
+    kv_c = _kv4(shape, kv, dev)
     B = kv._requests
     dims = idx.shape
     if len(dims) != 3 or dims[0] != B or dims[1] != shape.num_kv_heads:
         raise ValueError(f"idx must be [{B}][{shape.num_kv_heads}][k_cap], got {list(dims)}")
     _indexed(count, B, "count")
     st = _abi.lib().sfi_kv4_compact_gather(
-        ctypes.byref(shape.c()), kv_c, _ptr(idx, torch.int32, "idx"), _ptr(count, torch.int32, "count"), dims[2],
-        int(sink), _compact4(shape, kv, compact), _ptr(req_ids, torch.int32, "req_ids"), _count(B, batch, req_ids),
-        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+        ctypes.byref(shape.c()), kv_c, _ptr_here(idx, torch.int32, "idx", dev),
+        _ptr_here(count, torch.int32, "count", dev), dims[2], int(sink), _compact4(shape, kv, compact, dev),
+        _ptr_here(req_ids, torch.int32, "req_ids", dev), _count(B, batch, req_ids),
+        _ptr_here(dev_status, torch.int32, "dev_status", dev), _stream_here(stream, dev))
     _check(st, "sfi_kv4_compact_gather")
 
 
-def _kv4_query(shape: AttnShape, kv: PagedKV4, q: torch.Tensor, out: torch.Tensor, lse: Optional[torch.Tensor]) -> int:
-    T = _rows4(q, torch.bfloat16, shape, shape.num_q_heads, "q")
-    _need(out, torch.float32, "out")
+def _kv4_query(shape: AttnShape, kv: PagedKV4, q: torch.Tensor, out: torch.Tensor, lse: Optional[torch.Tensor],
+               dev: int) -> int:
+    T = _rows4(q, torch.bfloat16, shape, shape.num_q_heads, "q", dev)
+    _need_here(out, torch.float32, "out", dev)
     dims = q.shape
     if out.shape != dims or (lse is not None and lse.shape != dims[:3]):
         raise ValueError("out needs the shape of q, lse that without its last dimension")
@@ -655,8 +686,9 @@ def sfi_kv4_dense_attn(shape: AttnShape, kv: PagedKV4, sink: int, recent: int, q
                        stream=None):
     """q [B][T][Hq][D] (T query tokens per request), out fp32 of that shape, lse [B][T][Hq],
     scores [B][Hkv][score_stride]."""
-    kv_c = _kv4(shape, kv)
-    T = _kv4_query(shape, kv, q, out, lse)
+    dev = torch._C._cuda_getDevice()
+    kv_c = _kv4(shape, kv, dev)
+    T = _kv4_query(shape, kv, q, out, lse, dev)
     B, stride = kv._requests, 0
     if scores is not None:
         dims = scores.shape
@@ -665,9 +697,10 @@ def sfi_kv4_dense_attn(shape: AttnShape, kv: PagedKV4, sink: int, recent: int, q
         stride = dims[2]
     st = _abi.lib().sfi_kv4_dense_attn(
         ctypes.byref(shape.c()), kv_c, int(sink), int(recent), q.data_ptr(), T, out.data_ptr(),
-        _ptr(lse, torch.float32, "lse"), _ptr(scores, torch.float32, "scores"), stride,
-        _ptr(req_ids, torch.int32, "req_ids"), _count(B, batch, req_ids), _ptr(workspace, torch.uint8, "workspace"),
-        0 if workspace is None else workspace.numel(), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+        _ptr_here(lse, torch.float32, "lse", dev), _ptr_here(scores, torch.float32, "scores", dev), stride,
+        _ptr_here(req_ids, torch.int32, "req_ids", dev), _count(B, batch, req_ids),
+        _ptr_here(workspace, torch.uint8, "workspace", dev), 0 if workspace is None else workspace.numel(),
+        _ptr_here(dev_status, torch.int32, "dev_status", dev), _stream_here(stream, dev))
     _check(st, "sfi_kv4_dense_attn")
 
 
@@ -676,13 +709,15 @@ def sfi_kv4_fast_attn(shape: AttnShape, kv: PagedKV4, compact: CompactKV4, sink:
                       batch: Optional[int] = None, workspace: Optional[torch.Tensor] = None,
                       dev_status: Optional[torch.Tensor] = None, stream=None):
     """q [B][T][Hq][D] (T query tokens per request), out fp32 of that shape, lse [B][T][Hq]."""
-    kv_c = _kv4(shape, kv)
-    T = _kv4_query(shape, kv, q, out, lse)
+    dev = torch._C._cuda_getDevice()
+    kv_c = _kv4(shape, kv, dev)
+    T = _kv4_query(shape, kv, q, out, lse, dev)
     st = _abi.lib().sfi_kv4_fast_attn(
-        ctypes.byref(shape.c()), kv_c, _compact4(shape, kv, compact), int(sink), int(recent), q.data_ptr(), T,
-        out.data_ptr(), _ptr(lse, torch.float32, "lse"), _ptr(req_ids, torch.int32, "req_ids"),
-        _count(kv._requests, batch, req_ids), _ptr(workspace, torch.uint8, "workspace"),
-        0 if workspace is None else workspace.numel(), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+        ctypes.byref(shape.c()), kv_c, _compact4(shape, kv, compact, dev), int(sink), int(recent), q.data_ptr(), T,
+        out.data_ptr(), _ptr_here(lse, torch.float32, "lse", dev), _ptr_here(req_ids, torch.int32, "req_ids", dev),
+        _count(kv._requests, batch, req_ids), _ptr_here(workspace, torch.uint8, "workspace", dev),
+        0 if workspace is None else workspace.numel(), _ptr_here(dev_status, torch.int32, "dev_status", dev),
+        _stream_here(stream, dev))
     _check(st, "sfi_kv4_fast_attn")
 
 
@@ -705,11 +740,10 @@ class PageMap(_Handle):
 
     _tensors = ("page_table", "seq_lens", "ref_count")
 
-    def _make(self) -> _abi.sfi_page_map:
-        _need(self.page_table, torch.int32, "page_table")
-        _need(self.seq_lens, torch.int32, "seq_lens")
-        _need(self.ref_count, torch.int32, "ref_count")
-        _on_current_device(self.page_table, "page_table")
+    def _make(self, dev: int) -> _abi.sfi_page_map:
+        _need_here(self.page_table, torch.int32, "page_table", dev)
+        _need_here(self.seq_lens, torch.int32, "seq_lens", dev)
+        _need_here(self.ref_count, torch.int32, "ref_count", dev)
         dims = self.page_table.shape
         if len(dims) != 2 or self.seq_lens.numel() != dims[0]:
             raise ValueError("page_table must be [num_reqs][max_pages], seq_lens [num_reqs]")
@@ -750,53 +784,62 @@ class PagePools:
 
 def sfi_page_copy(pools: PagePools, src: torch.Tensor, dst: torch.Tensor, dev_status: Optional[torch.Tensor] = None,
                   stream=None):
+    dev = torch._C._cuda_getDevice()
     if src.numel() != dst.numel():
         raise ValueError("src and dst need the same number of pages")
-    st = _abi.lib().sfi_page_copy(ctypes.byref(pools.c()), _ptr(src, torch.int32, "src"), _ptr(dst, torch.int32, "dst"),
-                                  src.numel(), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    st = _abi.lib().sfi_page_copy(
+        ctypes.byref(pools.c()), _ptr_here(src, torch.int32, "src", dev), _ptr_here(dst, torch.int32, "dst", dev),
+        src.numel(), _ptr_here(dev_status, torch.int32, "dev_status", dev), _stream_here(stream, dev))
     _check(st, "sfi_page_copy")
 
 
 def sfi_page_fork(page_map: PageMap, src: torch.Tensor, dst: torch.Tensor, fork_lens: Optional[torch.Tensor] = None,
                   dev_status: Optional[torch.Tensor] = None, stream=None):
+    dev = torch._C._cuda_getDevice()
     if src.numel() != dst.numel() or (fork_lens is not None and fork_lens.numel() != src.numel()):
         raise ValueError("src, dst and fork_lens need one entry per branch")
-    st = _abi.lib().sfi_page_fork(ctypes.byref(page_map.c()), _ptr(src, torch.int32, "src"),
-                                  _ptr(dst, torch.int32, "dst"), _ptr(fork_lens, torch.int32, "fork_lens"), src.numel(),
-                                  _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    st = _abi.lib().sfi_page_fork(
+        ctypes.byref(page_map.c(dev)), _ptr_here(src, torch.int32, "src", dev), _ptr_here(dst, torch.int32, "dst", dev),
+        _ptr_here(fork_lens, torch.int32, "fork_lens", dev), src.numel(),
+        _ptr_here(dev_status, torch.int32, "dev_status", dev), _stream_here(stream, dev))
     _check(st, "sfi_page_fork")
 
 
 def sfi_page_reserve(page_map: PageMap, pools: Optional[PagePools], new_lens: torch.Tensor,
                      reqs: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                      dev_status: Optional[torch.Tensor] = None, stream=None):
+    dev = torch._C._cuda_getDevice()
     if reqs is not None and reqs.numel() != new_lens.numel():
         raise ValueError("reqs and new_lens need one entry per request")
     st = _abi.lib().sfi_page_reserve(
-        ctypes.byref(page_map.c()), None if pools is None else ctypes.byref(pools.c()),
-        _ptr(new_lens, torch.int32, "new_lens"), _ptr(reqs, torch.int32, "reqs"), new_lens.numel(),
-        _ptr(workspace, torch.uint8, "workspace"), 0 if workspace is None else workspace.numel(),
-        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+        ctypes.byref(page_map.c(dev)), None if pools is None else ctypes.byref(pools.c()),
+        _ptr_here(new_lens, torch.int32, "new_lens", dev), _ptr_here(reqs, torch.int32, "reqs", dev),
+        new_lens.numel(), _ptr_here(workspace, torch.uint8, "workspace", dev),
+        0 if workspace is None else workspace.numel(), _ptr_here(dev_status, torch.int32, "dev_status", dev),
+        _stream_here(stream, dev))
     _check(st, "sfi_page_reserve")
 
 
 def sfi_page_free(page_map: PageMap, reqs: torch.Tensor, dev_status: Optional[torch.Tensor] = None, stream=None):
-    st = _abi.lib().sfi_page_free(ctypes.byref(page_map.c()), _ptr(reqs, torch.int32, "reqs"), reqs.numel(),
-                                  _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    dev = torch._C._cuda_getDevice()
+    st = _abi.lib().sfi_page_free(
+        ctypes.byref(page_map.c(dev)), _ptr_here(reqs, torch.int32, "reqs", dev), reqs.numel(),
+        _ptr_here(dev_status, torch.int32, "dev_status", dev), _stream_here(stream, dev))
     _check(st, "sfi_page_free")
 
 
 def sfi_page_compact(page_map: PageMap, pools: PagePools, table_out: torch.Tensor, ref_out: torch.Tensor,
                      live_out: torch.Tensor, workspace: Optional[torch.Tensor] = None,
                      dev_status: Optional[torch.Tensor] = None, stream=None):
+    dev = torch._C._cuda_getDevice()
     if (table_out.shape != page_map.page_table.shape or ref_out.numel() != page_map.ref_count.numel()
             or live_out.numel() < 1):
         raise ValueError("table_out and ref_out need the shapes of page_table and ref_count, live_out one entry")
     st = _abi.lib().sfi_page_compact(
-        ctypes.byref(page_map.c()), ctypes.byref(pools.c()), _ptr(table_out, torch.int32, "table_out"),
-        _ptr(ref_out, torch.int32, "ref_out"), _ptr(live_out, torch.int32, "live_out"),
-        _ptr(workspace, torch.uint8, "workspace"), 0 if workspace is None else workspace.numel(),
-        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+        ctypes.byref(page_map.c(dev)), ctypes.byref(pools.c()), _ptr_here(table_out, torch.int32, "table_out", dev),
+        _ptr_here(ref_out, torch.int32, "ref_out", dev), _ptr_here(live_out, torch.int32, "live_out", dev),
+        _ptr_here(workspace, torch.uint8, "workspace", dev), 0 if workspace is None else workspace.numel(),
+        _ptr_here(dev_status, torch.int32, "dev_status", dev), _stream_here(stream, dev))
     _check(st, "sfi_page_compact")
 
 

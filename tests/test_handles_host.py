@@ -25,8 +25,8 @@ def _i32(*shape):
 def _handles():
     return {
         "PagedKV4": sfi.PagedKV4(torch.zeros(5, 2, 1152, dtype=torch.uint8), _i32(3, 4), _i32(3), 2.0, 0.5),
-        "CompactKV4": sfi.CompactKV4(torch.zeros(6, 1152, dtype=torch.uint8), torch.zeros(3, dtype=torch.int64), _i32(3),
-                                     _i32(3)),
+        "CompactKV4": sfi.CompactKV4(torch.zeros(6, 1152, dtype=torch.uint8), torch.zeros(3, dtype=torch.int64),
+                                     _i32(3), _i32(3)),
         "Rope": sfi.Rope(torch.arange(8), torch.zeros(8, dtype=torch.uint8), 2, True),
         "Rope without axes": sfi.Rope(torch.arange(8)),
         "PageMap": sfi.PageMap(_i32(3, 4), _i32(3), _i32(9)),
@@ -107,3 +107,134 @@ def test_a_tensor_that_changes_in_place_is_looked_at_again(monkeypatch):
         rope.c()
     rope.axis.resize_(4)
     assert rope.c().rot_dim == 8
+
+
+class Fake:
+    """As much of a CUDA tensor as the binding looks at, on a device of choice."""
+    is_cuda = True
+
+    def __init__(self, *shape, dtype=torch.int32, device=0):
+        self.t = torch.zeros(*shape, dtype=dtype)
+        self.index, self.device = device, torch.device("cuda", device)
+        self.dtype, self.shape = dtype, self.t.shape
+
+    def get_device(self):
+        return self.index
+
+    def __getattr__(self, name):
+        if name in ("data_ptr", "stride", "is_contiguous", "numel", "dim", "nbytes"):
+            return getattr(self.t, name)
+        raise AttributeError(name)
+
+
+@pytest.fixture
+def two_devices(monkeypatch):
+    """Two devices, of which 0 is the current one, and a library that only counts its calls."""
+    class State:
+        current, launches = 0, []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: State.launches.append(name) or 0
+
+    State.launches = []
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: State.current, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0, raising=False)
+    monkeypatch.setattr(api._abi, "lib", Lib)
+    return State
+
+
+BF, F32, U8, I64 = torch.bfloat16, torch.float32, torch.uint8, torch.int64
+SHAPE = sfi.AttnShape(4, 2, 64)
+
+
+def _pools(device):
+    t = [Fake(6, 8, dtype=I64, device=device) for _ in range(2)]
+    t[0].device = torch.device("cpu")  # where the addresses can go here
+    pools = sfi.PagePools(t)
+    pools.addresses = Fake(2, dtype=I64, device=device)
+    return pools
+
+
+def _arguments(where=lambda name: 0):
+    """Every tensor that the calls take, by name, on the device where(name)."""
+    f = lambda name, *s, dtype=torch.int32: Fake(*s, dtype=dtype, device=where(name))  # noqa: E731
+    return dict(
+        kv=sfi.PagedKV4(f("pool", 6, 2, 1152, dtype=U8), f("page_table", 3, 4), f("seq_lens", 3)),
+        bf16=sfi.PagedKV(f("k_pool", 6, 2, 16, 64, dtype=BF), f("v_pool", 6, 2, 16, 64, dtype=BF),
+                         f("bf16_table", 3, 4), f("bf16_lens", 3)),
+        compact=sfi.CompactKV4(f("blocks", 12, 1152, dtype=U8), f("offset", 3, dtype=I64), f("capacity", 3),
+                               f("held", 3)),
+        rope=sfi.Rope(f("turns", 32, dtype=I64), f("axis", 32, dtype=U8)),
+        map=sfi.PageMap(f("map_table", 3, 4), f("map_lens", 3), f("ref_count", 6)),
+        pools=_pools(where("page_pool")),
+        q=f("q", 3, 1, 4, 64, dtype=BF), k=f("k", 3, 1, 2, 64, dtype=BF), v=f("v", 3, 1, 2, 64, dtype=BF),
+        q_out=f("q_out", 3, 1, 4, 64, dtype=BF), k_out=f("k_out", 3, 1, 2, 64, dtype=BF),
+        v_out=f("v_out", 3, 1, 2, 64, dtype=BF), weight=f("weight", 64, dtype=BF), positions=f("positions", 3, 1),
+        out=f("out", 3, 1, 4, 64, dtype=F32), lse=f("lse", 3, 1, 4, dtype=F32), scores=f("scores", 3, 2, 64, dtype=F32),
+        ws=f("ws", 256, dtype=U8), per=f("per", 3), ids=f("ids", 3), st=f("st", 1), idx=f("idx", 3, 2, 8),
+        src=f("src", 2), dst=f("dst", 2), table_out=f("table_out", 3, 4), ref_out=f("ref_out", 6), live=f("live", 1))
+
+
+CALLS = {
+    "qk_norm_rope": (lambda a: sfi.sfi_qk_norm_rope(
+        SHAPE, a["rope"], a["q"], a["k"], a["v"], a["q_out"], q_weight=a["weight"], positions=a["positions"],
+        new_lens=a["per"], k_out=a["k_out"], kv=a["bf16"], req_ids=a["ids"], dev_status=a["st"]),
+        "turns axis q k v q_out weight positions per k_out k_pool v_pool bf16_table bf16_lens ids st"),
+    "kv4_append": (lambda a: sfi.sfi_kv4_append(SHAPE, a["kv"], a["k"], a["v"], new_lens=a["per"], req_ids=a["ids"],
+                                                dev_status=a["st"]), "pool page_table seq_lens k v per ids st"),
+    "kv4_read": (lambda a: sfi.sfi_kv4_read(SHAPE, a["kv"], a["k_out"], a["v_out"], first=a["per"], req_ids=a["ids"],
+                                            dev_status=a["st"]), "pool page_table seq_lens k_out v_out per ids st"),
+    "kv4_compact_gather": (lambda a: sfi.sfi_kv4_compact_gather(
+        SHAPE, a["kv"], a["idx"], a["per"], 4, a["compact"], req_ids=a["ids"], dev_status=a["st"]),
+        "pool page_table seq_lens idx per blocks offset capacity held ids st"),
+    "kv4_dense_attn": (lambda a: sfi.sfi_kv4_dense_attn(
+        SHAPE, a["kv"], 4, 8, a["q"], a["out"], lse=a["lse"], scores=a["scores"], req_ids=a["ids"], workspace=a["ws"],
+        dev_status=a["st"]), "pool page_table seq_lens q out lse scores ids ws st"),
+    "kv4_fast_attn": (lambda a: sfi.sfi_kv4_fast_attn(
+        SHAPE, a["kv"], a["compact"], 4, 8, a["q"], a["out"], lse=a["lse"], req_ids=a["ids"], workspace=a["ws"],
+        dev_status=a["st"]), "pool page_table seq_lens blocks offset capacity held q out lse ids ws st"),
+    "page_copy": (lambda a: sfi.sfi_page_copy(a["pools"], a["src"], a["dst"], dev_status=a["st"]),
+                  "page_pool src dst st"),
+    "page_fork": (lambda a: sfi.sfi_page_fork(a["map"], a["src"], a["dst"], a["src"], dev_status=a["st"]),
+                  "map_table map_lens ref_count src dst st"),
+    "page_reserve": (lambda a: sfi.sfi_page_reserve(a["map"], a["pools"], a["per"], a["ids"], workspace=a["ws"],
+                                                    dev_status=a["st"]),
+                     "page_pool map_table map_lens ref_count per ids ws st"),
+    "page_free": (lambda a: sfi.sfi_page_free(a["map"], a["ids"], dev_status=a["st"]),
+                  "map_table map_lens ref_count ids st"),
+    "page_compact": (lambda a: sfi.sfi_page_compact(a["map"], a["pools"], a["table_out"], a["ref_out"], a["live"],
+                                                    workspace=a["ws"], dev_status=a["st"]),
+                     "page_pool map_table map_lens ref_count table_out ref_out live ws st"),
+}
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_no_tensor_of_another_device_reaches_a_launch(two_devices, name):
+    call, tensors = CALLS[name]
+    call(_arguments())
+    assert two_devices.launches == ["sfi_" + name]
+    for t in tensors.split():
+        with pytest.raises(ValueError, match="not on the current device"):
+            call(_arguments(lambda n: int(n == t)))
+            pytest.fail(f"{t} of device 1 was taken")
+    assert two_devices.launches == ["sfi_" + name]
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_the_device_is_looked_at_in_every_call(two_devices, name):
+    """A handle that was used under its own device is refused under another one, and taken again."""
+    call, a = CALLS[name][0], _arguments()
+    call(a)
+    two_devices.current = 1
+    for _ in range(2):
+        with pytest.raises(ValueError, match="not on the current device"):
+            call(a)
+    # all else on the new device: the handles alone say no
+    handles = ("kv", "bf16", "compact", "rope", "map", "pools")
+    b = {**_arguments(lambda n: 1), **{k: a[k] for k in handles}}
+    with pytest.raises(ValueError, match="not on the current device"):
+        call(b)
+    two_devices.current = 0
+    call(a)
+    assert two_devices.launches == ["sfi_" + name] * 2
