@@ -754,7 +754,8 @@ class PageMap(_Handle):
 class PagePools:
     """The pools of a cache whose pages share their ids: contiguous tensors [num_pages][...] of
     one page size (each layer's k_pool and v_pool, or the 4-bit pools). Keeps the tensors and
-    a device array of their addresses."""
+    a device array of their addresses; a call is refused when one of them lies elsewhere by then (the
+    array is not written again in a call, which a graph may be capturing)."""
 
     def __init__(self, pools):
         if not pools:
@@ -767,7 +768,8 @@ class PagePools:
             if t.data_ptr() % 16:
                 raise ValueError("a pool must be 16-byte aligned")
         self.pools = list(pools)
-        self.addresses = torch.tensor([t.data_ptr() for t in pools], dtype=torch.int64).to(first.device)
+        self._at = [t.data_ptr() for t in pools]
+        self.addresses = torch.tensor(self._at, dtype=torch.int64).to(first.device)
         self._c = _abi.sfi_page_pools(self.addresses.data_ptr(), len(pools), first.nbytes // max(1, first.shape[0]),
                                       first.shape[0])
 
@@ -779,6 +781,8 @@ class PagePools:
 
     def c(self) -> _abi.sfi_page_pools:
         _on_current_device(self.addresses, "pools")
+        if [t.data_ptr() for t in self.pools] != self._at:
+            raise ValueError("a pool has other memory than when PagePools was made: make it anew")
         return self._c
 
 

@@ -238,3 +238,20 @@ def test_the_device_is_looked_at_in_every_call(two_devices, name):
     two_devices.current = 0
     call(a)
     assert two_devices.launches == ["sfi_" + name] * 2
+
+
+def test_pools_that_moved_are_refused(host):
+    """The device array of the pools' addresses is written once: a pool whose memory was replaced
+    must not be copied at the old place."""
+    pools = [torch.arange(40).view(5, 8) for _ in range(3)]
+    pp = sfi.PagePools(pools)
+    assert pp.c().num_pages == 5 and pp.c() is pp.c()
+    keep = pools[1].data
+    pools[1].data = torch.zeros(5, 8, dtype=torch.int64)
+    with pytest.raises(ValueError, match="other memory"):
+        pp.c()
+    pools[1].data = keep
+    assert pp.c().num_pages == 5
+    pools[0].resize_(500, 8)
+    with pytest.raises(ValueError, match="other memory"):
+        pp.c()
