@@ -499,6 +499,8 @@ def sfi_qk_norm_rope(shape: AttnShape, rope: Optional[Rope], q: torch.Tensor, k:
         raise ValueError("new_lens and seq_lens need one entry per request")
     kv_c = None
     if kv is not None:
+        if kv.page_table.dim() != 2 or kv.page_table.shape[0] != B or kv.seq_lens.numel() != B:
+            raise ValueError("q, k and v need one entry for each request of the pages (page_table, seq_lens)")
         kv_c = ctypes.byref(kv.c())
         for name in ("k_pool", "v_pool", "page_table", "seq_lens"):
             if getattr(kv, name).get_device() != dev:
@@ -506,8 +508,6 @@ def sfi_qk_norm_rope(shape: AttnShape, rope: Optional[Rope], q: torch.Tensor, k:
         dims = kv.k_pool.shape
         if len(dims) != 4 or dims[1] != hkv or dims[2] != shape.page_size or dims[3] != d or kv.v_pool.shape != dims:
             raise ValueError(f"the pools must be [num_pages][{hkv}][{shape.page_size}][{d}]")
-        if kv.seq_lens.numel() != B:
-            raise ValueError("q, k and v need one entry for each request of the pages")
     st = _abi.lib().sfi_qk_norm_rope(
         ctypes.byref(shape.c()), None if rope is None else ctypes.byref(rope.c(dev)), q.data_ptr(), qs,
         k.data_ptr(), ks, None if v is None else v.data_ptr(), vs, _ptr_here(q_weight, torch.bfloat16, "q_weight", dev),

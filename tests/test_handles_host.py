@@ -255,3 +255,22 @@ def test_pools_that_moved_are_refused(host):
     pools[0].resize_(500, 8)
     with pytest.raises(ValueError, match="other memory"):
         pp.c()
+
+
+def test_the_norm_takes_a_table_with_a_row_for_each_request(two_devices):
+    """qk_norm_rope indexes the page table by request: one with fewer rows than q, k and v have
+    requests (or with more, or not a table) is refused before a launch, as PagedKV4 refuses it."""
+    call, a = CALLS["qk_norm_rope"][0], _arguments()
+    for table in (Fake(2, 4), Fake(1, 4), Fake(4, 4), Fake(3), Fake(3, 4, 1), Fake(12)):
+        a["bf16"].page_table = table
+        with pytest.raises(ValueError):
+            call(a)
+    a["bf16"].page_table = Fake(3, 5)
+    for lens in (Fake(2), Fake(4)):
+        a["bf16"].seq_lens = lens
+        with pytest.raises(ValueError):
+            call(a)
+    assert two_devices.launches == []
+    a["bf16"].seq_lens = Fake(3)
+    call(a)
+    assert two_devices.launches == ["sfi_qk_norm_rope"]
