@@ -600,9 +600,9 @@ SFI_API sfi_status sfi_kv4_compact_gather(const sfi_attn_shape *shape, const sfi
  *   q : bf16 [B][num_tokens][Hq][D];  out : fp32 of that shape, 8-byte aligned
  *   lse : fp32 [B][num_tokens][Hq] or NULL;  scores, score_stride : as there, or NULL
  *   workspace : sfi_kv4_workspace_size(shape, batch, num_tokens) bytes, 256-byte aligned,
- *               zero-filled before its first use, then used with this shape alone (its
- *               counters are left zero); launches sharing it must not overlap, those of
- *               captured graphs included
+ *               zero-filled before its first use (its counters are left zero); calls of
+ *               other shapes may use it too, when it holds their size; launches sharing it
+ *               must not overlap, those of captured graphs included
  * Device errors: SFI_DEV_BAD_LEN (also L < num_tokens, or L > score_stride), SFI_DEV_BAD_PAGE.
  */
 SFI_API sfi_status sfi_kv4_dense_attn(const sfi_attn_shape *shape, const sfi_paged_kv4 *kv, int32_t sink,

@@ -726,7 +726,8 @@ def sfi_kv4_workspace_size(shape: AttnShape, batch: int, num_tokens: int = 1) ->
 
 
 def alloc_kv4_workspace(shape: AttnShape, batch: int, num_tokens: int = 1, device="cuda") -> torch.Tensor:
-    """A zero-filled workspace of the 4-bit attention calls, valid for every batch size 1..batch."""
+    """A zero-filled workspace of the 4-bit attention calls, valid for every batch size 1..batch,
+    and for other shapes whose size it holds."""
     return torch.zeros(max(256, sfi_kv4_workspace_size(shape, batch, num_tokens)), dtype=torch.uint8, device=device)
 
 

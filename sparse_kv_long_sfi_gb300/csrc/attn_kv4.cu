@@ -1083,12 +1083,14 @@ __global__ void __launch_bounds__(Tile<D, ROWS>::kThreads, ROWS <= 8 ? 2 : 1) kv
         int last = 0;
         if (u >= 0) {
             const int64_t u0 = s_open0[tid], u1 = u0 + (s_prefix[u / p.hkv + 1] - s_prefix[u / p.hkv]);
-            const int others = (int)(runs.owner(u1 - 1) / kWarps - runs.owner(u0) / kWarps);
+            // a unit that others share begins in one CTA, whose last unit it is: its counter counts
+            // them (an index that does not depend on the shape, as the workspace's parts do not)
+            const int c0 = (int)(runs.owner(u0) / kWarps), others = (int)(runs.owner(u1 - 1) / kWarps) - c0;
             // releases the CTA's part (ordered before it by the barrier) and acquires the others'
             int old;
-            asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(p.ws_count + u) : "memory");
+            asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(p.ws_count + c0) : "memory");
             last = old == others;
-            if (last) p.ws_count[u] = 0;
+            if (last) p.ws_count[c0] = 0;
         }
         s_last[tid] = last;
     }

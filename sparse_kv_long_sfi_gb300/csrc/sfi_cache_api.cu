@@ -49,8 +49,10 @@ sfi::Kv4CopyParams copy_params(const sfi_attn_shape *shape, const sfi_paged_kv4 
     return p;
 }
 
-// Workspace of the 4-bit attention: the counters of one launch's units, then the partial
-// states (m, l) and O of up to two units per CTA, sixteen rows each.
+// Workspace of the 4-bit attention: a counter per CTA, then the partial states (m, l) and O of
+// up to two units per CTA, sixteen rows each. The counters, which launches leave zero for the
+// next one, take the same first 16 KB whatever the shape, so that calls of several shapes may
+// share a workspace: no shape's partial states lie on another's counters.
 struct Kv4Workspace {
     size_t ml, part, total;
 };
@@ -59,7 +61,8 @@ Kv4Workspace kv4_workspace(const sfi_attn_shape *shape) {
     const int ctas = std::min(sfi::sm_count_current_device() * sfi::kKv4CtasPerSm, sfi::kKv4MaxCtas);
     const size_t slots = (size_t)ctas * 2 * sfi::kMaxRows;
     Kv4Workspace w{};
-    w.ml = ((size_t)sfi::kKv4MaxBatch * shape->num_kv_heads * 4 + 255) / 256 * 256;
+    w.ml = 16384;
+    static_assert(sfi::kKv4MaxCtas * sizeof(int32_t) <= 16384, "a counter per CTA");
     w.part = w.ml + slots * 2 * 4;
     w.total = w.part + slots * shape->head_dim * 4;
     return w;

@@ -215,7 +215,7 @@ struct Kv4AttnParams {
     int32_t sink, recent;
     float k_mul;    // softmax scale * k_scale
     float v_scale;
-    int32_t *ws_count;  // [batch * hkv], zero between launches
+    int32_t *ws_count;  // [CTAs], zero between launches: that of the CTA which a shared unit begins in
     float *ws_ml;       // [CTAs][2][16 rows][2]
     float *ws_part;     // [CTAs][2][16 rows][D]
     int32_t *dev_status;
