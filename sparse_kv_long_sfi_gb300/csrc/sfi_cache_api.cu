@@ -296,7 +296,7 @@ sfi_status sfi_kv4_fast_attn(const sfi_attn_shape *shape, const sfi_paged_kv4 *k
 }
 
 size_t sfi_kv4_workspace_size(const sfi_attn_shape *shape, int32_t batch, int32_t num_tokens) {
-    if (sfi::check_shape(shape) != SFI_OK || batch < 0 || num_tokens < 1) return 0;
+    if (sfi::check_shape(shape) != SFI_OK || batch < 0 || num_tokens < 1 || num_tokens > SFI_MAX_QUERY_TOKENS) return 0;
     if (num_tokens * (shape->num_q_heads / shape->num_kv_heads) > sfi::kMaxRows) return 0;
     return kv4_workspace(shape).total;
 }
