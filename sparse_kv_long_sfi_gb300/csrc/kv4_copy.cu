@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 4) kv4_append_kernel(const Kv4
         }
         const int first = L - n;
         const int pg = first / kSubTokens + x.slot;
+        if (pg > (L - 1) / kSubTokens) continue;  // (before its position, which may pass 32 bits)
         const int pos0 = pg * kSubTokens;
         const int a = max(first - pos0, 0), b = min(L - pos0, kSubTokens);
         if (a >= b) continue;
