@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kPageThreads) page_fork_kernel(const PageMapPa
 __global__ void __launch_bounds__(kPageThreads) page_free_kernel(const PageMapParams m, const int32_t *reqs,
                                                                  int32_t *dev_status) {
     grid_dependency_wait();
-    const int r = reqs ? reqs[blockIdx.x] : blockIdx.x;
+    const int r = reqs[blockIdx.x];
     if (r < 0 || r >= m.num_reqs) {
         if (threadIdx.x == 0) report(dev_status, SFI_DEV_BAD_INDEX);
         return;
