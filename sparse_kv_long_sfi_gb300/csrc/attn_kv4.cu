@@ -16,8 +16,8 @@
 // Per block (16 tokens): S^T = K Q^T and O^T += V^T P^T with mma.m16n8k16, the tokens (or
 // dims) as the M side, so that eight query rows take one N tile. Codes become fp16 by
 // conversion and one multiplication by their scale: a product of an e2m1 and an e4m3
-// value is exact in fp16. Q in fp16 is exact, too: each row is scaled by a power of two to
-// just below 2^15. P goes in as two fp16 terms (22 bits; times 2^7 to keep small
+// value is exact in fp16. So is Q in fp16, each row scaled by a power of two to just below 2^15:
+// a value below 2^-31 of its row's largest loses bits, at most 2^-39 of that largest one. P goes in as two fp16 terms (22 bits; times 2^7 to keep small
 // probabilities off the subnormals), so the output is as good as fp32's. The running
 // maximum moves only when a score passes it by 2^8.
 #include <algorithm>

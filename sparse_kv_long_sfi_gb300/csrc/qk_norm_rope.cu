@@ -12,8 +12,9 @@
 // y = (x A + x' B) / rms, x' the other member of the pair. Where whole heads turn in split
 // halves a lane holds both members (dims 4 l .. and D/2 + 4 l ..); otherwise it holds eight
 // dims in a row and fetches x' from its mate lane. Three CTAs per SM (80 registers) keep enough
-// loads in flight: 2 x 8192 tokens of 32/8/128 heads take 73.9 us (5.4 TB/s) against 85.4 us
-// with two and 77.4 us with four, which spill.
+// loads in flight: 2 x 8192 tokens of 32/8/128 heads take 73 us (5.5 TB/s; two CTAs 12 us longer,
+// four, which spill, 4 us). The variant for the other rotations has two CTAs per SM: 95 us for half
+// of each head in split halves, 91 for adjacent pairs, whose members lie in one lane.
 #include <algorithm>
 
 #include "sfi_device.cuh"
@@ -238,7 +239,7 @@ cudaError_t launch_qk_norm_rope(const NormRopeParams &p, int head_dim, int batch
     const int chunks = (rows + rows_per_item - 1) / rows_per_item;
     const int64_t ctas = (tokens * chunks + kNormWarps - 1) / kNormWarps;
     const int grid = (int)std::min<int64_t>(ctas, (int64_t)sms * 64);
-    // both members of a pair in a lane: 73 us for 2 x 8192 tokens of 32/8/128 heads, 96 us by shuffles
+    // both members of a pair in a lane: 73 us for 2 x 8192 tokens of 32/8/128 heads, 96 by shuffles
     const bool halves = p.rot_dim == head_dim && !p.interleaved;
     auto kernel = head_dim == 128 ? (halves ? qk_norm_rope_kernel<128, true> : qk_norm_rope_kernel<128, false>)
                                   : (halves ? qk_norm_rope_kernel<64, true> : qk_norm_rope_kernel<64, false>);
