@@ -376,7 +376,7 @@ class _Handle:
 
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
-        self.__dict__.pop("_c", None)
+        self.__dict__.pop("_kept", None)  # with its references: a tensor that is let go is free
 
     def __getstate__(self):
         # a copy (copy, deepcopy, pickle) makes its own structure, of its own tensors
@@ -387,18 +387,17 @@ class _Handle:
         if dev is None:
             dev = torch._C._cuda_getDevice()
         d = self.__dict__
-        kept = d.get("_c")
-        if kept is not None and d["_dev"] == dev:
-            for t, ptr, size, stride in d["_at"]:
+        kept = d.get("_kept")
+        if kept is not None and kept[1] == dev:
+            for t, ptr, size, stride in kept[2]:
                 if t.data_ptr() != ptr or t.shape != size or t.stride() != stride:
                     break
             else:
-                return kept
-        d.pop("_c", None)
+                return kept[0]
+        d.pop("_kept", None)
         c = self._make(dev)
-        d["_dev"] = dev
-        d["_at"] = [(t, t.data_ptr(), t.shape, t.stride()) for t in (d[n] for n in self._tensors)]
-        d["_c"] = c
+        at = [(t, t.data_ptr(), t.shape, t.stride()) for t in (d[n] for n in self._tensors)]
+        d["_kept"] = (c, dev, at)
         return c
 
 

@@ -1,7 +1,9 @@
 """The handles that the binding keeps C structures in: what they may be used for between and
 after calls, without a GPU."""
 import copy
+import gc
 import pickle
+import weakref
 
 import pytest
 import torch
@@ -274,3 +276,22 @@ def test_the_norm_takes_a_table_with_a_row_for_each_request(two_devices):
     a["bf16"].seq_lens = Fake(3)
     call(a)
     assert two_devices.launches == ["sfi_qk_norm_rope"]
+
+
+def test_a_handle_lets_go_of_a_replaced_tensor(host):
+    """What a call has kept of a handle's tensors does not outlive their place in it: a pool that is
+    replaced, or set to None to make room, is freed at once."""
+    kv = _handles()["PagedKV4"]
+    kv.c()
+    old = weakref.ref(kv.pool)
+    kv.pool = None
+    gc.collect()
+    assert old() is None
+    with pytest.raises(AttributeError):
+        kv.c()
+    kv.pool = torch.zeros(7, 2, 1152, dtype=torch.uint8)
+    assert kv.c().num_pages == 7
+    old = weakref.ref(kv.page_table)
+    kv.page_table = _i32(3, 6)
+    gc.collect()
+    assert old() is None and kv.c().max_pages_per_req == 6
