@@ -200,14 +200,14 @@ def append_bytes(B, Hkv, D):
 # ---------------------------------------------------------------------------
 # GPU arm
 # ---------------------------------------------------------------------------
-# DRAM bytes (read + write) per launch from `ncu --set full` captures of the attention
+# DRAM bytes (read + write) per launch from `ncu` captures of the attention
 # kernel at the benchmark's per-launch shape (16 requests x 8 KV heads at KV 16K; the
 # summaries under profiles/ give the commands). They describe the kernel built from
 # the sources whose hash is recorded here and are dropped (null) once those change.
 PROFILED_SOURCES = ("sparse_kv_long_sfi_gb300/csrc/attn_kernel.cuh", "sparse_kv_long_sfi_gb300/csrc/attn_decode.cu",
                     "sparse_kv_long_sfi_gb300/csrc/sfi_device.cuh", "sparse_kv_long_sfi_gb300/csrc/sfi_internal.h",
                     "sparse_kv_long_sfi_gb300/csrc/sfi_api.cu")
-PROFILED_TRAFFIC = {"sha256_16": "b1a619051ccb121b", "fast": 68_289_280 + 574_208, "slow": 1_073_954_560 + 6_764_800}
+PROFILED_TRAFFIC = {"sha256_16": "43d6929a2abb2a50", "fast": 68_289_536 + 5_888, "slow": 1_073_962_496 + 6_261_760}
 
 
 def profiled_traffic(kind):
