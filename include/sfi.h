@@ -87,6 +87,7 @@ typedef enum {
 #define SFI_DEV_TIMEOUT 16u     /* an in-kernel pipeline wait ran past its bound */
 #define SFI_DEV_BAD_COMPACT 32u /* compact rows of a request fall outside the buffer */
 #define SFI_DEV_NO_PAGE 64u     /* fewer free pages than a reservation needs */
+#define SFI_DEV_BAD_PROB 128u   /* no probability above zero to sample from */
 
 /* Launch flags of the attention entry points (bitwise OR). */
 /* SFI_ATTN_EARLY_KV_PREFETCH: the kernel that precedes this call on the stream does
@@ -115,6 +116,8 @@ typedef enum {
 /* Most query tokens per request in the multi-token calls (tokens x G must also be
  * <= 16: G = 2 allows 8 tokens, G = 4 four, G = 8 two). */
 #define SFI_MAX_QUERY_TOKENS 16
+/* Largest vocabulary of sfi_verify_tokens. */
+#define SFI_MAX_VOCAB 1048576
 /* Most requests in one sfi_page_reserve call. */
 #define SFI_MAX_PAGE_REQS 1024
 
@@ -718,8 +721,121 @@ SFI_API sfi_status sfi_page_compact(const sfi_page_map *map, const sfi_page_pool
                                     int32_t *ref_out, int32_t *live_out, void *workspace, size_t workspace_bytes,
                                     int32_t *dev_status, void *stream);
 
+/*
+ * sfi_page_trim - request reqs[i] (reqs NULL: request i) keeps its first new_lens[i] tokens: its
+ * length becomes that, and the pages behind it are let go (pages nobody holds are free again).
+ * The counterpart of sfi_page_reserve, for drafts that were refused and evicted caches. A request
+ * may appear once.
+ * Device errors: SFI_DEV_BAD_INDEX, SFI_DEV_BAD_LEN (a length below zero, above the request's or
+ * beyond the table: that request is skipped), SFI_DEV_BAD_PAGE (an id out of range, or a page
+ * with no holder left: that page is skipped).
+ */
+SFI_API sfi_status sfi_page_trim(const sfi_page_map *map, const int32_t *new_lens, const int32_t *reqs, int32_t n,
+                                 int32_t *dev_status, void *stream);
+
 /* Workspace bytes of sfi_page_reserve and sfi_page_compact (0 on invalid input). */
 SFI_API size_t sfi_page_workspace_size(const sfi_page_map *map);
+
+/*
+ * Prompts, caches of a fixed size, drafts. A request's cache is written by its prompt, cut back to
+ * the positions that attention has used most, and extended by drafts that the target verifies.
+ */
+
+/*
+ * sfi_window_attn - attention of the n_r newest tokens of each request (n_r = new_lens[r], or
+ * num_tokens when new_lens is NULL), whose K and V are in the pages already, through a sliding
+ * window with sinks: the token at position p sees every j <= p with j < S or j > p - W (W >= L:
+ * causal attention; the newest token of a request sees what sfi_fast_decode_attn sees with no
+ * selection). Any number of tokens: a whole prompt, a chunk behind cached context, one step.
+ *   q   : bf16, 16-byte aligned; token t of request r starts at element (r num_tokens + t) *
+ *         q_stride, its heads are contiguous [Hq][D]; q_stride is a multiple of 8. q has num_reqs
+ *         requests (request ids are below that). Token t < n_r is at position L_r - n_r + t.
+ *   out : bf16 [B][num_tokens][Hq][D], 16-byte aligned (rounded once from fp32);
+ *   lse : fp32 [B][num_tokens][Hq] or NULL. Rows of tokens t >= n_r are not written. A token that
+ *         sees nothing (S = 0, W = 0) gets out = 0 and lse = -inf.
+ * What a token does not see has no influence on it, NaN and infinities included.
+ * Device errors: SFI_DEV_BAD_INDEX (a request id outside [0, num_reqs)), SFI_DEV_BAD_LEN (n_r < 0,
+ * n_r > num_tokens, L_r < n_r or L_r beyond the page table): that request is skipped.
+ * SFI_DEV_BAD_PAGE, SFI_DEV_TIMEOUT (the tokens whose block reads
+ * that page are not written: up to 256 / G tokens of a KV head's query heads).
+ */
+SFI_API sfi_status sfi_window_attn(const sfi_attn_shape *shape, const sfi_paged_kv *kv, int32_t sink, int32_t recent,
+                                   const void *q, int64_t q_stride, int32_t num_reqs, int32_t num_tokens,
+                                   const int32_t *new_lens, void *out, float *lse, const int32_t *req_ids, int32_t batch, int32_t *dev_status,
+                                   void *stream);
+
+/*
+ * sfi_attn_mass - the attention weight that the new tokens gave to each position, summed over them
+ * and over the query heads of each KV head:
+ *   mass[r][kv][j] = decay * mass[r][kv][j] + sum over t, g of exp(scale q_{t, kv G + g} . k_j - lse_{t, kv G + g})
+ * over the tokens that see j as in sfi_window_attn, for j < L_r. At the new positions (j >= L_r - n_r)
+ * what mass held before does not count; with decay = 0 it does not anywhere. Entries j >= L_r are not
+ * written. sfi_select_topk takes the result as scores; sfi_kv_evict keeps the heaviest positions.
+ *   q, q_stride, num_reqs, num_tokens, new_lens : as for sfi_window_attn
+ *   lse  : fp32 [B][num_tokens][Hq], of the attention of these tokens
+ *   mass : fp32 [B][Hkv][mass_stride], mass_stride >= max L
+ * The result does not depend on the order in which the GPU runs the call.
+ * Device errors: SFI_DEV_BAD_INDEX, SFI_DEV_BAD_LEN (as for sfi_window_attn, or L_r > mass_stride):
+ * that request is skipped. SFI_DEV_BAD_PAGE, SFI_DEV_TIMEOUT (that block of 256 positions is not
+ * written).
+ */
+SFI_API sfi_status sfi_attn_mass(const sfi_attn_shape *shape, const sfi_paged_kv *kv, int32_t sink, int32_t recent,
+                                 const void *q, int64_t q_stride, int32_t num_reqs, int32_t num_tokens,
+                                 const int32_t *new_lens, const float *lse, float *mass, int64_t mass_stride, float decay,
+                                 const int32_t *req_ids, int32_t batch, int32_t *dev_status, void *stream);
+
+/*
+ * sfi_kv_evict - cut each request's cache, per KV head, to the sink [0, S), the recent window
+ * [L - W, L) and the k_r = k_per_req[r] candidates between them with the largest mass (chosen as
+ * sfi_select_topk does: equal ones go to the lower position). The kept rows of K and V move to the
+ * front of the request's pages in place, in the order of their positions, bit for bit. All KV heads
+ * keep equally many rows; seq_lens and the page table are not changed (they serve all layers): when
+ * every layer is cut, sfi_page_trim takes the lengths over. The requests of one call must not share
+ * the pages they hold (sfi_page_reserve gives a branch its last page only: do not evict from pages
+ * with other holders).
+ *   mass      : fp32 [B][Hkv][mass_stride], mass_stride >= max L
+ *   k_per_req : int32 [B], 0 <= k_r <= k_cap
+ *   idx_out   : int32 [B][Hkv][k_cap] (NULL when k_cap is 0), the kept candidates' former positions, ascending; entries past
+ *               the count are not written
+ *   count_out : int32 [B], min(k_r, candidates)
+ *   mass_out  : fp32 [B][Hkv][mass_stride] or NULL: the kept rows' mass, in their new order; not mass
+ *   new_lens  : int32 [B], the rows that are left
+ * Limits: as for sfi_select_topk.
+ * Device errors: SFI_DEV_BAD_LEN (L_r < 0, beyond the page table or > mass_stride), SFI_DEV_K_OVERFLOW
+ * (that request is skipped), SFI_DEV_BAD_PAGE (that row stays as it was).
+ */
+SFI_API sfi_status sfi_kv_evict(const sfi_attn_shape *shape, const sfi_paged_kv *kv, const float *mass,
+                                int64_t mass_stride, int32_t sink, int32_t recent, const int32_t *k_per_req,
+                                int32_t k_cap, int32_t *idx_out, int32_t *count_out, float *mass_out,
+                                int32_t *new_lens, const int32_t *req_ids, int32_t batch, int32_t *dev_status,
+                                void *stream);
+
+/*
+ * sfi_verify_tokens - which drafted tokens the target keeps, and the token behind them, from given
+ * random numbers. Request r has n_r = draft_lens[r] drafts x_t (num_drafts when draft_lens is NULL),
+ * drawn from q_t; p_t is the target's distribution after t of them.
+ *   Draft t is accepted while u_t q_t(x_t) < p_t(x_t); a is the number accepted.
+ *   The next token is the first i with w_0 + ... + w_i > u_T (w_0 + ... + w_{V-1}), where w =
+ *   max(p_a - q_a, 0) when a < n_r, else p_{n_r}; should that be zero everywhere, w = p_a.
+ * With draft NULL the drafts were chosen, not drawn: q_t(x_t) = 1, and 0 elsewhere. The sums are
+ * exact in units of 2^-56, so the result does not depend on any order.
+ *   target : fp32, row t <= n_r of request r at element (r (num_drafts + 1) + t) * target_stride
+ *   draft  : fp32, row t < n_r of request r at element (r num_drafts + t) * draft_stride, or NULL
+ *            (values count as at least 0 and at most 1, a NaN as 0; a row's sum must stay below 64)
+ *   tokens : int32 [B][num_drafts];  u : fp32 [B][num_drafts + 1] in [0, 1), u_T the last of a row
+ *   out_tokens : int32 [B][num_drafts + 1]: the accepted drafts, the next token, then -1
+ *   accepted   : int32 [B]: a
+ *   seq_lens, new_lens : int32 [B] or both NULL: new_lens[r] = seq_lens[r] - n_r + a, the cache
+ *            without the refused drafts (for sfi_page_trim)
+ * vocab <= SFI_MAX_VOCAB.
+ * Device errors: SFI_DEV_BAD_LEN (n_r < 0 or > num_drafts), SFI_DEV_BAD_INDEX (a draft outside the
+ * vocabulary): that request is skipped. SFI_DEV_BAD_PROB (nothing to sample from: the next token is -1).
+ */
+SFI_API sfi_status sfi_verify_tokens(const float *target, int64_t target_stride, const float *draft,
+                                     int64_t draft_stride, const int32_t *tokens, const float *u, int32_t vocab,
+                                     int32_t num_drafts, const int32_t *draft_lens, const int32_t *seq_lens,
+                                     int32_t *out_tokens, int32_t *accepted, int32_t *new_lens, const int32_t *req_ids,
+                                     int32_t batch, int32_t *dev_status, void *stream);
 
 /* Human-readable name of a status code (static string). */
 SFI_API const char *sfi_status_string(sfi_status status);

@@ -13,7 +13,8 @@ from .api import (SFI_ATTN_EARLY_KV_PREFETCH, SFI_ATTN_RAGGED, SFI_ATTN_TEST_WIT
                   sfi_kv4_compact_gather, sfi_kv4_dense_attn, sfi_kv4_fast_attn, sfi_kv4_read,
                   sfi_kv4_workspace_size, SFI_MAX_PAGE_REQS, PageMap, PagePools, alloc_page_workspace,
                   sfi_page_compact, sfi_page_copy, sfi_page_fork, sfi_page_free, sfi_page_reserve,
-                  sfi_page_workspace_size,
+                  sfi_page_trim, sfi_page_workspace_size, SFI_MAX_VOCAB, sfi_attn_mass, sfi_kv_evict,
+                  sfi_verify_tokens, sfi_window_attn,
                   alloc_ragged_workspace, alloc_workspace, sfi_compact_gather, sfi_dense_verify_attn,
                   sfi_fast_decode_attn, sfi_fast_decode_attn_noalloc, sfi_mixed_decode_attn,
                   sfi_mixed_workspace_size, sfi_multi_workspace_size, sfi_paged_kv_append,
@@ -29,7 +30,8 @@ __all__ = [
     "CompactKV4", "PagedKV4", "alloc_kv4_compact", "alloc_kv4_pool", "alloc_kv4_workspace", "sfi_kv4_append",
     "sfi_kv4_compact_gather", "sfi_kv4_dense_attn", "sfi_kv4_fast_attn", "sfi_kv4_read", "sfi_kv4_workspace_size",
     "SFI_MAX_PAGE_REQS", "PageMap", "PagePools", "alloc_page_workspace", "sfi_page_compact", "sfi_page_copy",
-    "sfi_page_fork", "sfi_page_free", "sfi_page_reserve", "sfi_page_workspace_size", "alloc_mixed_workspace", "alloc_multi_workspace", "alloc_ragged_workspace",
+    "sfi_page_fork", "sfi_page_free", "sfi_page_reserve", "sfi_page_trim", "sfi_page_workspace_size",
+    "SFI_MAX_VOCAB", "sfi_attn_mass", "sfi_kv_evict", "sfi_verify_tokens", "sfi_window_attn", "alloc_mixed_workspace", "alloc_multi_workspace", "alloc_ragged_workspace",
     "alloc_workspace", "sfi_compact_gather", "sfi_dense_verify_attn", "sfi_fast_decode_attn",
     "sfi_fast_decode_attn_noalloc", "sfi_mixed_decode_attn", "sfi_mixed_workspace_size",
     "sfi_multi_workspace_size", "sfi_paged_kv_append", "sfi_paged_kv_append_tokens", "sfi_plan_splits",

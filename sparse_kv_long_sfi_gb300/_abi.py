@@ -55,11 +55,13 @@ class sfi_page_pools(ctypes.Structure):
 SFI_OK, SFI_ERR_INVALID_ARG, SFI_ERR_UNSUPPORTED, SFI_ERR_WORKSPACE, SFI_ERR_CUDA = range(5)
 SFI_DEV_BAD_PAGE, SFI_DEV_BAD_LEN, SFI_DEV_K_OVERFLOW = 1, 2, 4
 SFI_DEV_BAD_INDEX, SFI_DEV_TIMEOUT, SFI_DEV_BAD_COMPACT, SFI_DEV_NO_PAGE = 8, 16, 32, 64
+SFI_DEV_BAD_PROB = 128
 SFI_ATTN_EARLY_KV_PREFETCH = 1
 SFI_ATTN_RAGGED = 2
 SFI_ATTN_TEST_WITHHOLD = 4
 SFI_MAX_QUERY_TOKENS = 16
 SFI_MAX_PAGE_REQS = 1024
+SFI_MAX_VOCAB = 1048576
 
 P_SHAPE = ctypes.POINTER(sfi_attn_shape)
 P_PAGED = ctypes.POINTER(sfi_paged_kv)
@@ -113,7 +115,16 @@ PROTOTYPES = {
     "sfi_page_reserve": (c_i32, [P_MAP, P_POOLS, c_vp, c_vp, c_i32, c_vp, c_sz, c_vp, c_vp]),
     "sfi_page_free": (c_i32, [P_MAP, c_vp, c_i32, c_vp, c_vp]),
     "sfi_page_compact": (c_i32, [P_MAP, P_POOLS, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp, c_vp]),
+    "sfi_page_trim": (c_i32, [P_MAP, c_vp, c_vp, c_i32, c_vp, c_vp]),
     "sfi_page_workspace_size": (c_sz, [P_MAP]),
+    "sfi_window_attn": (c_i32, [P_SHAPE, P_PAGED, c_i32, c_i32, c_vp, c_i64, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_i32,
+                                c_vp, c_vp]),
+    "sfi_attn_mass": (c_i32, [P_SHAPE, P_PAGED, c_i32, c_i32, c_vp, c_i64, c_i32, c_i32, c_vp, c_vp, c_vp, c_i64, c_f32,
+                              c_vp, c_i32, c_vp, c_vp]),
+    "sfi_kv_evict": (c_i32, [P_SHAPE, P_PAGED, c_vp, c_i64, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp,
+                             c_i32, c_vp, c_vp]),
+    "sfi_verify_tokens": (c_i32, [c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                  c_i32, c_vp, c_vp]),
     "sfi_status_string": (ctypes.c_char_p, [c_i32]),
     "sfi_version": (c_i32, []),
 }

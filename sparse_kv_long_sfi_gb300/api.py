@@ -20,6 +20,7 @@ from . import _abi
 SFI_ATTN_EARLY_KV_PREFETCH = _abi.SFI_ATTN_EARLY_KV_PREFETCH
 SFI_MAX_QUERY_TOKENS = _abi.SFI_MAX_QUERY_TOKENS
 SFI_MAX_PAGE_REQS = _abi.SFI_MAX_PAGE_REQS
+SFI_MAX_VOCAB = _abi.SFI_MAX_VOCAB
 SFI_ATTN_RAGGED = _abi.SFI_ATTN_RAGGED
 SFI_ATTN_TEST_WITHHOLD = _abi.SFI_ATTN_TEST_WITHHOLD
 
@@ -832,6 +833,18 @@ def sfi_page_free(page_map: PageMap, reqs: torch.Tensor, dev_status: Optional[to
     _check(st, "sfi_page_free")
 
 
+def sfi_page_trim(page_map: PageMap, new_lens: torch.Tensor, reqs: Optional[torch.Tensor] = None,
+                  dev_status: Optional[torch.Tensor] = None, stream=None):
+    dev = torch._C._cuda_getDevice()
+    if reqs is not None and reqs.numel() != new_lens.numel():
+        raise ValueError("reqs and new_lens need one entry per request")
+    st = _abi.lib().sfi_page_trim(
+        ctypes.byref(page_map.c(dev)), _ptr_here(new_lens, torch.int32, "new_lens", dev),
+        _ptr_here(reqs, torch.int32, "reqs", dev), new_lens.numel(), _ptr_here(dev_status, torch.int32, "dev_status", dev),
+        _stream_here(stream, dev))
+    _check(st, "sfi_page_trim")
+
+
 def sfi_page_compact(page_map: PageMap, pools: PagePools, table_out: torch.Tensor, ref_out: torch.Tensor,
                      live_out: torch.Tensor, workspace: Optional[torch.Tensor] = None,
                      dev_status: Optional[torch.Tensor] = None, stream=None):
@@ -854,6 +867,149 @@ def sfi_page_workspace_size(page_map: PageMap) -> int:
 def alloc_page_workspace(page_map: PageMap) -> torch.Tensor:
     """A workspace of sfi_page_reserve and sfi_page_compact for this map."""
     return torch.empty(sfi_page_workspace_size(page_map), dtype=torch.uint8, device=page_map.ref_count.device)
+
+
+def _pages_here(shape: AttnShape, kv: PagedKV, dev: int):
+    """The C view of bf16 pages on the current device whose pools have the shape's heads; the number of requests."""
+    c = kv.c()
+    for name in ("k_pool", "v_pool", "page_table", "seq_lens"):
+        if getattr(kv, name).get_device() != dev:
+            _on_current_device(getattr(kv, name), name)
+    dims, table = kv.k_pool.shape, kv.page_table.shape
+    if len(dims) != 4 or dims[1] != shape.num_kv_heads or dims[2] != shape.page_size or dims[3] != shape.head_dim \
+            or kv.v_pool.shape != dims:
+        raise ValueError(f"the pools must be [num_pages][{shape.num_kv_heads}][{shape.page_size}][{shape.head_dim}]")
+    if len(table) != 2 or kv.seq_lens.numel() != table[0]:
+        raise ValueError("seq_lens needs one entry per row of page_table")
+    return ctypes.byref(c), table[0]
+
+
+def sfi_window_attn(shape: AttnShape, kv: PagedKV, sink: int, recent: int, q: torch.Tensor, out: torch.Tensor,
+                    lse: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
+                    req_ids: Optional[torch.Tensor] = None, batch: Optional[int] = None,
+                    dev_status: Optional[torch.Tensor] = None, stream=None):
+    """Attention of each request's newest tokens through a sliding window with sinks; q [B][T][Hq][D]
+    may be a view of a fused projection (contiguous heads), out bf16 [B][T][Hq][D], lse [B][T][Hq]."""
+    dev = torch._C._cuda_getDevice()
+    B, T, step = _token_rows(q, shape.num_q_heads, shape.head_dim, "q", dev)
+    kv_c, requests = _pages_here(shape, kv, dev)
+    _indexed(q, requests, "q")
+    _indexed(new_lens, requests, "new_lens")
+    _need_here(out, torch.bfloat16, "out", dev)
+    if out.shape != q.shape or (lse is not None and lse.shape != q.shape[:3]):
+        raise ValueError("out needs the shape of q, lse that without its last dimension")
+    st = _abi.lib().sfi_window_attn(
+        ctypes.byref(shape.c()), kv_c, int(sink), int(recent), q.data_ptr(), step, B, T,
+        _ptr_here(new_lens, torch.int32, "new_lens", dev), out.data_ptr(), _ptr_here(lse, torch.float32, "lse", dev),
+        _ptr_here(req_ids, torch.int32, "req_ids", dev), _count(B, batch, req_ids),
+        _ptr_here(dev_status, torch.int32, "dev_status", dev), _stream_here(stream, dev))
+    _check(st, "sfi_window_attn")
+
+
+def _weights(shape: AttnShape, mass: torch.Tensor, requests: int, name: str, dev: int) -> int:
+    """The row stride of a [B][Hkv][stride] tensor of weights."""
+    _need_here(mass, torch.float32, name, dev)
+    dims = mass.shape
+    if len(dims) != 3 or dims[0] != requests or dims[1] != shape.num_kv_heads:
+        raise ValueError(f"{name} must be [{requests}][{shape.num_kv_heads}][stride], got {list(dims)}")
+    return dims[2]
+
+
+def sfi_attn_mass(shape: AttnShape, kv: PagedKV, sink: int, recent: int, q: torch.Tensor, lse: torch.Tensor,
+                  mass: torch.Tensor, decay: float = 1.0, new_lens: Optional[torch.Tensor] = None,
+                  req_ids: Optional[torch.Tensor] = None, batch: Optional[int] = None,
+                  dev_status: Optional[torch.Tensor] = None, stream=None):
+    """The attention weights of the newest tokens, added up per position into mass [B][Hkv][stride] (its former
+    values times decay); q and lse as for sfi_window_attn."""
+    dev = torch._C._cuda_getDevice()
+    B, T, step = _token_rows(q, shape.num_q_heads, shape.head_dim, "q", dev)
+    kv_c, requests = _pages_here(shape, kv, dev)
+    _indexed(q, requests, "q")
+    _indexed(new_lens, requests, "new_lens")
+    _need_here(lse, torch.float32, "lse", dev)
+    if lse.shape != q.shape[:3]:
+        raise ValueError("lse needs the shape of q without its last dimension")
+    st = _abi.lib().sfi_attn_mass(
+        ctypes.byref(shape.c()), kv_c, int(sink), int(recent), q.data_ptr(), step, B, T,
+        _ptr_here(new_lens, torch.int32, "new_lens", dev), lse.data_ptr(), mass.data_ptr(),
+        _weights(shape, mass, requests, "mass", dev), float(decay), _ptr_here(req_ids, torch.int32, "req_ids", dev),
+        _count(B, batch, req_ids), _ptr_here(dev_status, torch.int32, "dev_status", dev), _stream_here(stream, dev))
+    _check(st, "sfi_attn_mass")
+
+
+def sfi_kv_evict(shape: AttnShape, kv: PagedKV, mass: torch.Tensor, sink: int, recent: int, k_per_req: torch.Tensor,
+                 idx_out: torch.Tensor, count_out: torch.Tensor, new_lens: torch.Tensor,
+                 mass_out: Optional[torch.Tensor] = None, req_ids: Optional[torch.Tensor] = None,
+                 batch: Optional[int] = None, dev_status: Optional[torch.Tensor] = None, stream=None):
+    """Cuts each request's pages to its sink, its recent window and the k_per_req heaviest positions between;
+    mass, mass_out [B][Hkv][stride], idx_out int32 [B][Hkv][k_cap], count_out and new_lens int32 [B]."""
+    dev = torch._C._cuda_getDevice()
+    kv_c, requests = _pages_here(shape, kv, dev)
+    stride = _weights(shape, mass, requests, "mass", dev)
+    if mass_out is not None and _weights(shape, mass_out, requests, "mass_out", dev) != stride:
+        raise ValueError("mass and mass_out need the same shape")
+    dims = idx_out.shape
+    if len(dims) != 3 or dims[0] != requests or dims[1] != shape.num_kv_heads:
+        raise ValueError(f"idx_out must be [{requests}][{shape.num_kv_heads}][k_cap], got {list(dims)}")
+    for t, name in ((k_per_req, "k_per_req"), (count_out, "count_out"), (new_lens, "new_lens")):
+        _need_here(t, torch.int32, name, dev)
+        _indexed(t, requests, name)
+    st = _abi.lib().sfi_kv_evict(
+        ctypes.byref(shape.c()), kv_c, mass.data_ptr(), stride, int(sink), int(recent), k_per_req.data_ptr(), dims[2],
+        _ptr_here(idx_out, torch.int32, "idx_out", dev), count_out.data_ptr(),
+        None if mass_out is None else mass_out.data_ptr(), new_lens.data_ptr(),
+        _ptr_here(req_ids, torch.int32, "req_ids", dev), _count(requests, batch, req_ids),
+        _ptr_here(dev_status, torch.int32, "dev_status", dev), _stream_here(stream, dev))
+    _check(st, "sfi_kv_evict")
+
+
+def _probability_rows(t: torch.Tensor, name: str, dev: int):
+    """Requests, rows, values of a row and elements between rows of an fp32 tensor [B][rows][V]."""
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        _on_current_device(t, name)
+    if t.dtype is not torch.float32:
+        raise ValueError(f"{name} must be {torch.float32}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [B][rows][V], got {list(t.shape)}")
+    b, n, v = t.shape
+    s = t.stride()
+    step = s[1] if n > 1 else (s[0] if b > 1 else v)
+    if (v > 1 and s[2] != 1) or step < v or (b > 1 and s[0] != n * step):
+        raise ValueError(f"{name} needs contiguous rows and one stride between all rows")
+    return b, n, v, step
+
+
+def sfi_verify_tokens(target: torch.Tensor, draft: Optional[torch.Tensor], tokens: torch.Tensor, u: torch.Tensor,
+                      out_tokens: torch.Tensor, accepted: torch.Tensor, draft_lens: Optional[torch.Tensor] = None,
+                      seq_lens: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
+                      req_ids: Optional[torch.Tensor] = None, batch: Optional[int] = None,
+                      dev_status: Optional[torch.Tensor] = None, stream=None):
+    """Which drafts the target keeps, and the token behind them: target fp32 [B][T + 1][V], draft fp32 [B][T][V] (None:
+    the drafts were chosen, not drawn), tokens int32 [B][T], u fp32 [B][T + 1], out_tokens int32 [B][T + 1]."""
+    dev = torch._C._cuda_getDevice()
+    B, rows, V, ts = _probability_rows(target, "target", dev)
+    T, ds = rows - 1, 0
+    if draft is not None:
+        db, dt, dv, ds = _probability_rows(draft, "draft", dev)
+        if db != B or dt != T or dv != V:
+            raise ValueError(f"draft must be [{B}][{T}][{V}], got {list(draft.shape)}")
+    for t, dtype, name, dims in ((tokens, torch.int32, "tokens", (B, T)), (u, torch.float32, "u", (B, T + 1)),
+                                 (out_tokens, torch.int32, "out_tokens", (B, T + 1)),
+                                 (accepted, torch.int32, "accepted", (B,))):
+        _need_here(t, dtype, name, dev)
+        if tuple(t.shape) != dims:
+            raise ValueError(f"{name} must be {list(dims)}, got {list(t.shape)}")
+    for t, name in ((draft_lens, "draft_lens"), (seq_lens, "seq_lens"), (new_lens, "new_lens")):
+        _indexed(t, B, name)
+    st = _abi.lib().sfi_verify_tokens(
+        target.data_ptr(), ts, None if draft is None else draft.data_ptr(), ds, tokens.data_ptr(), u.data_ptr(), V, T,
+        _ptr_here(draft_lens, torch.int32, "draft_lens", dev), _ptr_here(seq_lens, torch.int32, "seq_lens", dev),
+        out_tokens.data_ptr(), accepted.data_ptr(), _ptr_here(new_lens, torch.int32, "new_lens", dev),
+        _ptr_here(req_ids, torch.int32, "req_ids", dev), _count(B, batch, req_ids),
+        _ptr_here(dev_status, torch.int32, "dev_status", dev), _stream_here(stream, dev))
+    _check(st, "sfi_verify_tokens")
 
 
 def sfi_workspace_size(shape: AttnShape, batch: int, max_tokens: int, num_splits: int = 0) -> int:

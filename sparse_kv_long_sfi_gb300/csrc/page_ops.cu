@@ -199,6 +199,43 @@ __global__ void __launch_bounds__(kPageThreads) page_free_kernel(const PageMapPa
     }
 }
 
+// ---- trim: one CTA per request ------------------------------------------------------------
+// The length is taken down atomically, so that pages between two lengths are let go once, whatever a
+// list names twice.
+__global__ void __launch_bounds__(kPageThreads) page_trim_kernel(const PageMapParams m, const int32_t *new_lens,
+                                                                 const int32_t *reqs, int32_t *dev_status) {
+    __shared__ int s_len;
+    grid_dependency_wait();
+    const int r = reqs ? reqs[blockIdx.x] : (int)blockIdx.x;
+    if (r < 0 || r >= m.num_reqs) {
+        if (threadIdx.x == 0) report(dev_status, SFI_DEV_BAD_INDEX);
+        return;
+    }
+    const int len = new_lens[blockIdx.x];
+    if (threadIdx.x == 0) {
+        const int L = m.seq_lens[r];
+        // (only calls on this request may change its length meanwhile, and only downwards)
+        if (len < 0 || L < len || pages_of(L) > m.max_pages) {
+            report(dev_status, SFI_DEV_BAD_LEN);
+            s_len = len;
+        } else {
+            s_len = atomicMin(m.seq_lens + r, len);
+        }
+    }
+    __syncthreads();
+    const int32_t *row = m.page_table + (int64_t)r * m.max_pages;
+    const int held = pages_of(max(s_len, 0));
+    for (int i = pages_of(max(len, 0)) + threadIdx.x; i < held; i += kPageThreads) {
+        const int page = row[i];
+        if (page < 0 || page >= m.num_pages) {
+            report(dev_status, SFI_DEV_BAD_PAGE);
+        } else if (atomicSub(m.ref_count + page, 1) <= 0) {
+            atomicAdd(m.ref_count + page, 1);  // nobody held it: as it was
+            report(dev_status, SFI_DEV_BAD_PAGE);
+        }
+    }
+}
+
 // ---- reserve: one CTA plans for all requests --------------------------------------------
 // Three passes: what each request needs (and whether its last page is its own), the lowest
 // free pages, and their distribution; then the copies of shared last pages are launched.
@@ -430,6 +467,11 @@ cudaError_t launch_page_fork(const PageMapParams &m, const int32_t *src, const i
 cudaError_t launch_page_free(const PageMapParams &m, const int32_t *reqs, int n, int32_t *dev_status,
                              cudaStream_t stream) {
     return launch_dependent(page_free_kernel, n, kPageThreads, 0, stream, m, reqs, dev_status);
+}
+
+cudaError_t launch_page_trim(const PageMapParams &m, const int32_t *new_lens, const int32_t *reqs, int n,
+                             int32_t *dev_status, cudaStream_t stream) {
+    return launch_dependent(page_trim_kernel, n, kPageThreads, 0, stream, m, new_lens, reqs, dev_status);
 }
 
 cudaError_t launch_page_reserve(const PageMapParams &m, const PagePoolParams *q, const int32_t *new_lens,

@@ -31,23 +31,37 @@ EncodeTiledFn tensor_map_encoder() {
     return fn;
 }
 
+}  // namespace
+
+namespace sfi {
+
 // 2-D view [rows][D] of a bf16 buffer, boxes of [16 rows][64 elements] with the
 // 128-byte swizzle (one box row = one 128-byte line).
-bool encode_rows(CUtensorMap *map, void *base, int64_t rows, int head_dim) {
+bool encode_rows(CUtensorMap *map, const void *base, int64_t rows, int head_dim) {
     EncodeTiledFn enc = tensor_map_encoder();
     if (!enc) return false;
     cuuint64_t dims[2] = {(cuuint64_t)head_dim, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)head_dim * 2};
-    cuuint32_t box[2] = {64, (cuuint32_t)sfi::kSubTokens};
+    cuuint32_t box[2] = {64, (cuuint32_t)kSubTokens};
     cuuint32_t estr[2] = {1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr,
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-}  // namespace
-
-namespace sfi {
+// 3-D view [tokens][Hq][D] of queries (the box's rows come out as row = token * group + head).
+bool encode_queries(CUtensorMap *map, const void *base, int64_t tokens, int64_t stride, int hq, int head_dim, int group,
+                    int box_tokens) {
+    EncodeTiledFn enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)hq, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)box_tokens};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 int sm_count_current_device() {
     static std::atomic<int> cache[64];
@@ -96,6 +110,7 @@ using sfi::aligned16;
 using sfi::aligned8;
 using sfi::check_paged;
 using sfi::check_shape;
+using sfi::encode_rows;
 using sfi::resolve_scale;
 using sfi::sm_count_current_device;
 

@@ -347,6 +347,16 @@ sfi_status sfi_page_free(const sfi_page_map *map, const int32_t *reqs, int32_t n
     return launched(sfi::launch_page_free(map_params(map), reqs, n, dev_status, static_cast<cudaStream_t>(stream)));
 }
 
+sfi_status sfi_page_trim(const sfi_page_map *map, const int32_t *new_lens, const int32_t *reqs, int32_t n,
+                         int32_t *dev_status, void *stream) {
+    const sfi_status st = check_map(map);
+    if (st != SFI_OK) return st;
+    if (!new_lens || n < 0 || (!reqs && n > map->num_reqs)) return SFI_ERR_INVALID_ARG;
+    if (n == 0) return SFI_OK;
+    return launched(
+        sfi::launch_page_trim(map_params(map), new_lens, reqs, n, dev_status, static_cast<cudaStream_t>(stream)));
+}
+
 sfi_status sfi_page_compact(const sfi_page_map *map, const sfi_page_pools *pools, int32_t *table_out, int32_t *ref_out,
                             int32_t *live_out, void *workspace, size_t workspace_bytes, int32_t *dev_status,
                             void *stream) {

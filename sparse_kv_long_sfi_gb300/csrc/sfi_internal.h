@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/sfi.h"
 
 namespace sfi {
@@ -113,6 +115,8 @@ struct TopkParams {
     int32_t *dev_status;
 };
 cudaError_t launch_select_topk(const TopkParams &p, int batch, cudaStream_t stream);
+// Candidates of one request that the Selector takes.
+constexpr int kTopkMaxCandidates = 262144;
 
 struct CopyParams {
     const __nv_bfloat16 *k_pool_src;
@@ -149,6 +153,23 @@ int sm_count_current_device();
 float resolve_scale(const sfi_attn_shape *s);
 sfi_status check_shape(const sfi_attn_shape *s);
 sfi_status check_paged(const sfi_attn_shape *s, const sfi_paged_kv *kv);
+// TMA map of a pool's rows [rows][D], in boxes of a page's 16 rows by 64 values (128-byte swizzle).
+bool encode_rows(CUtensorMap *map, const void *base, int64_t rows, int head_dim);
+// TMA map of queries [tokens][Hq][D] with `stride` values between tokens, in boxes of 64 values of a
+// group's heads of so many tokens (128-byte swizzle).
+bool encode_queries(CUtensorMap *map, const void *base, int64_t tokens, int64_t stride, int hq, int head_dim, int group,
+                    int box_tokens);
+// A kernel's shared-memory limit is an attribute per device: set once for each.
+inline cudaError_t set_smem_once(const void *kernel, int bytes, std::atomic<uint64_t> &configured) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
+    if (bit && (configured.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) configured.fetch_or(bit, std::memory_order_acq_rel);
+    return e;
+}
 
 struct NormRopeParams {
     const __nv_bfloat16 *q, *k, *v;
@@ -226,6 +247,66 @@ constexpr int kKv4CtasPerSm = 2;
 constexpr int kKv4MaxCtas = 512;
 cudaError_t launch_kv4_attn(const Kv4AttnParams &p, int head_dim, cudaStream_t stream);
 
+// Attention of new tokens over the paged cache through a sliding window with sinks, and their weights.
+struct WindowParams {
+    const __nv_bfloat16 *q;  // token t of request r at (r tokens + t) q_stride, heads contiguous
+    int64_t q_stride;
+    __nv_bfloat16 *out;  // [B][tokens][Hq][D]
+    float *lse;          // [B][tokens][Hq] or null
+    const __nv_bfloat16 *k_pool, *v_pool;
+    const int32_t *page_table, *seq_lens, *new_lens, *req_ids;
+    int32_t max_pages, num_pages;
+    int32_t reqs, hq, hkv, group;
+    int32_t tokens, sink, recent;
+    float scale_log2;  // softmax scale * log2(e)
+    int32_t *dev_status;
+};
+struct WindowMaps {
+    CUtensorMap q, k, v;
+};
+// More than kMaxRows query rows per (request, KV head) (q in boxes of 128 rows), and up to that many.
+constexpr int kPromptBoxRows = 128;
+cudaError_t launch_window_prompt(const WindowMaps &maps, const WindowParams &p, int head_dim, int batch,
+                                 cudaStream_t stream);
+cudaError_t launch_window_step(const WindowMaps &maps, const WindowParams &p, int head_dim, int batch,
+                               cudaStream_t stream);
+struct MassParams {
+    const float *lse;  // [B][tokens][Hq]
+    float *mass;       // [B][Hkv][stride]
+    int64_t stride;
+    float decay;
+};
+int mass_rows(int64_t rows);  // query rows of a box of q
+cudaError_t launch_attn_mass(const WindowMaps &maps, const WindowParams &p, const MassParams &w, int head_dim, int batch,
+                             cudaStream_t stream);
+
+struct EvictParams {
+    __nv_bfloat16 *k_pool, *v_pool;
+    const int32_t *page_table, *seq_lens, *req_ids;
+    int32_t max_pages, num_pages, hkv, head_dim;
+    const float *mass;
+    float *mass_out;  // or null
+    int64_t mass_stride;
+    int32_t sink, recent;
+    const int32_t *k_per_req, *idx;
+    int32_t k_cap;
+    int32_t *new_lens;
+    int32_t *dev_status;
+};
+cudaError_t launch_kv_evict(const EvictParams &p, int batch, cudaStream_t stream);
+
+struct VerifyParams {
+    const float *target, *draft;  // [B][drafts + 1][vocab], [B][drafts][vocab] (or null)
+    int64_t target_stride, draft_stride;
+    const int32_t *tokens;  // [B][drafts]
+    const float *u;         // [B][drafts + 1]
+    int32_t vocab, drafts;
+    const int32_t *draft_lens, *seq_lens, *req_ids;
+    int32_t *out_tokens, *accepted, *new_lens;
+    int32_t *dev_status;
+};
+cudaError_t launch_verify_tokens(const VerifyParams &p, int batch, cudaStream_t stream);
+
 // Page operators.
 struct PageMapParams {
     int32_t *page_table, *seq_lens, *ref_count;
@@ -244,6 +325,8 @@ cudaError_t launch_page_fork(const PageMapParams &m, const int32_t *src, const i
                              int n, int32_t *dev_status, cudaStream_t stream);
 cudaError_t launch_page_free(const PageMapParams &m, const int32_t *reqs, int n, int32_t *dev_status,
                              cudaStream_t stream);
+cudaError_t launch_page_trim(const PageMapParams &m, const int32_t *new_lens, const int32_t *reqs, int n,
+                             int32_t *dev_status, cudaStream_t stream);
 cudaError_t launch_page_reserve(const PageMapParams &m, const PagePoolParams *q, const int32_t *new_lens,
                                 const int32_t *reqs, int n, void *ws, int32_t *dev_status, cudaStream_t stream);
 cudaError_t launch_page_compact(const PageMapParams &m, const PagePoolParams &q, int32_t *table_out, int32_t *ref_out,
