@@ -22,7 +22,8 @@
 // A zero weight times a NaN is a NaN in a matrix product, so V's rows behind the last position (stale
 // bytes of a page's tail) are zeroed in shared memory, and a row whose output is not finite is computed
 // again key by key, from the positions it sees alone.
-// Two prompts of 8192 tokens, 16/8/128 heads, window 1024: 213 us (34% of the measured bf16 rate).
+// Two prompts of 8192 tokens, 16/8/128 heads, window 1024: 164 us (44% of the measured bf16 rate); in the loop a step of
+// 256 rows x 128 keys takes 3080 cycles (84%), of 32000 of a CTA's 47000.
 #include <atomic>
 
 #include "tensor_core.cuh"
@@ -33,7 +34,7 @@ namespace sfi {
 namespace {
 
 constexpr int kPromptThreads = 384;  // two softmax warpgroups; a copy warp and a matrix warp in the third
-constexpr int kCopyWarp = 8, kMmaWarp = 9;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kTailWarp = 11;  // (a matrix warp for each tile: 9 and 10)
 // Registers of a thread: the launch gives 168 (384 x 168 = 64512 of the SM's 65536), the softmax threads take what
 // the third warpgroup gives back: 256 x 208 + 128 x 80 = 63488. (With 168 the softmax spills.)
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
@@ -63,29 +64,29 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *ring = smem + 2 * T::kBytes;
-    __shared__ __align__(8) uint64_t q_full, loads_done;
+    __shared__ __align__(8) uint64_t q_full, loads_done, tail_ready, tail_done;
     __shared__ __align__(8) uint64_t full[T::kStages], empty[T::kStages];
-    __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2];
+    __shared__ __align__(8) uint64_t s_full[2], p_ready[2][2], o_done[2], turn[2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_bad;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int kvh = blockIdx.y;
-    const int r = p.req_ids ? p.req_ids[blockIdx.z] : (int)blockIdx.z;
+    const int kvh = blockIdx.x;
+    const int r = p.req_ids ? p.req_ids[blockIdx.y] : (int)blockIdx.y;
     if (r < 0 || r >= p.reqs) {
-        if (threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0) report(p.dev_status, SFI_DEV_BAD_INDEX);
+        if (threadIdx.x == 0 && blockIdx.z == 0 && kvh == 0) report(p.dev_status, SFI_DEV_BAD_INDEX);
         return;
     }
     const int L = p.seq_lens[r];
     const int n = p.new_lens ? p.new_lens[r] : p.tokens;
     if (n < 0 || n > p.tokens || L < n || L > p.max_pages * kSubTokens) {
-        if (threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0) report(p.dev_status, SFI_DEV_BAD_LEN);
+        if (threadIdx.x == 0 && blockIdx.z == 0 && kvh == 0) report(p.dev_status, SFI_DEV_BAD_LEN);
         return;
     }
-    // the tokens with the most keys first
-    const int G = p.group, per_tile = kTileRows / G;
-    const int tok0 = ((int)gridDim.x - 1 - (int)blockIdx.x) * 2 * per_tile;
+    // the tokens with the most keys first, those of every request and head
+    const int G = p.group, shift = __ffs(G) - 1, per_tile = kTileRows >> shift;  // G is a power of two
+    const int tok0 = ((int)gridDim.z - 1 - (int)blockIdx.z) * 2 * per_tile;
     if (tok0 >= n) return;
     const int tok1 = min(n, tok0 + 2 * per_tile) - 1;
     const int tiles_q = tok1 - tok0 >= per_tile ? 2 : 1;
@@ -99,14 +100,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         tma_prefetch_desc(&tm_v);
         mbar_init(&q_full, 1);
         mbar_init(&loads_done, 1);
+        mbar_init(&tail_ready, 1);
+        mbar_init(&tail_done, 1);
         for (int i = 0; i < T::kStages; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], tiles_q);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], kTileRows);
-            mbar_init(&pv_done[i], 1);
+            mbar_init(&p_ready[i][0], kTileRows);
+            mbar_init(&p_ready[i][1], kTileRows);
+            mbar_init(&turn[i], 1);
+            mbar_init(&o_done[i], 1);
         }
         s_bad = 0;
         fence_barrier_init();
@@ -170,74 +175,96 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&loads_done);  // s_bad is final
-        } else if (warp == kMmaWarp) {
-            // ---- all matrix instructions, issued by lane 0 ----
-            const uint32_t qa = smem_u32(smem), ra = smem_u32(ring);
-            auto scores = [&](int t, int slot) {
-    #pragma unroll
+        } else if ((warp == kMmaWarp || warp == kMmaWarp + 1) && lane == 0 && warp - kMmaWarp < tiles_q && steps > 0) {
+            // ---- a tile's matrix instructions: S(0), then PV(j) and S(j + 1) ----
+            // A thread issues 8 of them in the time that they take, so what it waits for and signals in between has to
+            // run beside the other tile's: hence a thread for each, and one signal (commit) per step. That of S(j + 1)
+            // says that PV(j) is done too, since they run in the order of their issue.
+            const int t = warp - kMmaWarp;
+            const uint32_t qa = smem_u32(smem) + t * T::kBytes, ra = smem_u32(ring);
+            auto scores = [&](int slot) {
+#pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const uint32_t off = (ks >> 2) * T::kHalfBytes + (ks & 3) * 32;
-                    mma_ss(tmem + t * kTileRows, smem_desc(qa + t * T::kBytes + off, 16),
-                           smem_desc(ra + slot * T::kBytes + off, 16), T::kScores, ks > 0);
+                    mma_ss(tmem + t * kTileRows, smem_desc(qa + off, 16), smem_desc(ra + slot * T::kBytes + off, 16),
+                           T::kScores, ks > 0);
                 }
                 mma_commit(&s_full[t]);
             };
-            bool fine = steps > 0 && tc_wait(&q_full, 0) && tc_wait(&full[0], 0);
+            // K of step j is use 2 j of the ring, V use 2 j + 1
+            auto arrived = [&](int use) { return tc_wait_one(&full[use % T::kStages], (use / T::kStages) & 1); };
+            // With two tiles the threads take turns: interleaved, both tiles' instructions would end together, and
+            // both softmaxes would run while the tensor cores wait (a step then took 4400 cycles instead of 3000).
+            auto my_turn = [&](int phase) {
+                return tiles_q == 1 || (t == 0 && phase == 0) || tc_wait_one(&turn[t], (phase - (t == 0)) & 1);
+            };
+            bool fine = tc_wait_one(&q_full, 0) && arrived(0) && my_turn(0);
             if (fine) {
                 tc_fence_after();
-                if (lane == 0) {
-                    for (int t = 0; t < tiles_q; ++t) scores(t, 0);
-                    mma_commit(&empty[0]);
-                }
+                scores(0);
+                if (tiles_q == 2) mbar_arrive(&turn[t ^ 1]);
+                fine = arrived(1);
             }
             for (int j = 0; j < steps && fine; ++j) {
-                const int uv = 2 * j + 1, slot_v = uv % T::kStages;
-                const int uk = 2 * j + 2, slot_k = uk % T::kStages;
+                const int slot_v = (2 * j + 1) % T::kStages;
                 const bool more = j + 1 < steps;
-                fine = tc_wait(&full[slot_v], (uv / T::kStages) & 1);
-                if (fine && !more) {
-                    // what lies behind the last position must not meet a zero weight as a NaN
-                    const int rows = max(0, span.slots - j * kTileRows);
-                    for (int i = rows * 8 + lane; i < kTileRows * 8; i += 32)
-    #pragma unroll
-                        for (int h = 0; h < T::kHalves; ++h)
-                            *reinterpret_cast<int4 *>(ring + slot_v * T::kBytes + h * T::kHalfBytes + i * 16) =
-                                make_int4(0, 0, 0, 0);
-                    fence_async_shared();
-                    __syncwarp();
+                if (more) {
+                    fine = arrived(2 * j + 2);
+                } else {
+                    if (t == 0) mbar_arrive(&tail_ready);  // V's last tile is there
+                    fine = tc_wait_one(&tail_done, 0);
                 }
-                if (fine && more) fine = tc_wait(&full[slot_k], (uk / T::kStages) & 1);
-                for (int t = 0; t < tiles_q && fine; ++t) {
-                    fine = tc_wait(&p_full[t], j & 1);
-                    if (!fine) break;
-                    tc_fence_after();
-                    if (lane == 0) {
-    #pragma unroll
-                        for (int ks = 0; ks < kTileRows / 16; ++ks)
-                            mma_ts(tmem + 2 * kTileRows + t * D, tmem + t * kTileRows + ks * 8,
-                                   smem_desc(ra + slot_v * T::kBytes + ks * 16 * 128, T::kHalfBytes), T::kValues, j + ks > 0);
-                        mma_commit(&pv_done[t]);
-                        if (more) scores(t, slot_k);
-                    }
-                    __syncwarp();
-                }
-                if (fine && lane == 0) {
-                    mma_commit(&empty[slot_v]);
-                    if (more) mma_commit(&empty[slot_k]);
+                fine = fine && tc_wait_one(&p_ready[t][0], j & 1) && my_turn(j + 1);
+                if (!fine) break;
+                tc_fence_after();
+                auto values = [&](int ks0) {
+#pragma unroll
+                    for (int ks = ks0; ks < ks0 + kTileRows / 32; ++ks)
+                        mma_ts(tmem + 2 * kTileRows + t * D, tmem + t * kTileRows + ks * 8,
+                               smem_desc(ra + slot_v * T::kBytes + ks * 16 * 128, T::kHalfBytes), T::kValues, j + ks > 0);
+                };
+                values(0);
+                fine = tc_wait_one(&p_ready[t][1], j & 1);
+                if (!fine) break;
+                tc_fence_after();
+                values(kTileRows / 32);
+                if (more) {
+                    scores((2 * j + 2) % T::kStages);
+                    if (tiles_q == 2) mbar_arrive(&turn[t ^ 1]);
+                    fine = arrived(2 * j + 3);
+                } else {
+                    mma_commit(&o_done[t]);
+                    if (tiles_q == 2 && t == 0) mbar_arrive(&turn[1]);
                 }
             }
-            if (!fine && steps > 0 && lane == 0) report(p.dev_status, SFI_DEV_TIMEOUT);
+            if (!fine) report(p.dev_status, SFI_DEV_TIMEOUT);
+        } else if (warp == kTailWarp && steps > 0) {
+            // ---- what lies behind the last position must not meet a zero weight as a NaN ----
+            const int slot = (2 * steps - 1) % T::kStages;
+            if (tc_wait(&tail_ready, 0)) {
+                const int rows = max(0, span.slots - (steps - 1) * kTileRows);
+                for (int i = rows * 8 + lane; i < kTileRows * 8; i += 32)
+#pragma unroll
+                    for (int h = 0; h < T::kHalves; ++h)
+                        *reinterpret_cast<int4 *>(ring + slot * T::kBytes + h * T::kHalfBytes + i * 16) = make_int4(0, 0, 0, 0);
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tail_done);
+            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // ---- softmax: one query row per thread ----
         const int t = warp >> 2;                      // tile
         const int row = threadIdx.x & (kTileRows - 1);
-        const int token = tok0 + t * per_tile + row / G, head = kvh * G + row % G;
+        const int token = tok0 + t * per_tile + (row >> shift), head = kvh * G + (row & (G - 1));
         const bool mine = token < n;                  // rows behind the request's tokens are not written
         const int pos = L - n + token;
         const RowWindow win(mine ? pos : p1, p.sink, p.recent, span);
-        const RowWindow first(p0, p.sink, p.recent, span), last(p1, p.sink, p.recent, span);
+        // the first and the last token of this warp's rows: what both see needs no mask
+        const int warp_tok = tok0 + t * per_tile + ((warp & 3) * 32 >> shift);
+        const RowWindow first(min(L - n + warp_tok, p1), p.sink, p.recent, span);
+        const RowWindow last(min(L - n + warp_tok + (31 >> shift), p1), p.sink, p.recent, span);
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
         const uint32_t s_addr = lanes + t * kTileRows, o_addr = lanes + 2 * kTileRows + t * D;
         float m = -INFINITY, l = 0.f;
@@ -247,6 +274,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             fine = tc_wait(&s_full[t], j & 1);
             if (!fine) break;
             tc_fence_after();
+            if ((threadIdx.x & (kTileRows - 1)) == 0) {  // this tile is done with K of this step and V of the last
+                mbar_arrive(&empty[(2 * j) % T::kStages]);
+                if (j > 0) mbar_arrive(&empty[(2 * j - 1) % T::kStages]);
+            }
             uint32_t s[4][32];
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_load32(s_addr + c * 32, s[c]);
@@ -254,17 +285,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             const int v0 = j * kTileRows;
             if (!all_see(v0, kTileRows, first, last)) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t see = win.sees32(v0 + c * 32);
+                    if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (!win.sees(v0 + c * 32 + i)) s[c][i] = 0xff800000u;
+                        for (int i = 0; i < 32; ++i)
+                            if (!((see >> i) & 1u)) s[c][i] = 0xff800000u;
+                    }
+                }
             }
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float top[4];
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
+            for (int c = 0; c < 4; ++c) {
+                top[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
 #pragma unroll
-                for (int c = 0; c < 4; ++c) top[c] = fmaxf(top[c], __uint_as_float(s[c][i]));
-            const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
+                for (int i = 2; i < 32; i += 2) top[c] = max3(top[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
+            }
+            const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * p.scale_log2;
             const bool grow = now > m + kGrowth;
             float alpha = 1.f;
             if (grow) {
@@ -273,9 +310,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 l *= alpha;
             }
             if (j > 0 && __any_sync(0xffffffffu, grow)) {
-                fine = tc_wait(&pv_done[t], (j - 1) & 1);
-                if (!fine) break;
-                tc_fence_after();
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
@@ -287,35 +321,42 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 }
             }
             const float base = m == -INFINITY ? 0.f : m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), base2 = pair(-base, -base);
+            uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 uint32_t w[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                    const float a = fast_exp2(fmaf(__uint_as_float(s[2 * c + i / 16][2 * (i % 16)]), p.scale_log2, -base));
-                    const float b = fast_exp2(fmaf(__uint_as_float(s[2 * c + i / 16][2 * (i % 16) + 1]), p.scale_log2, -base));
-                    sum[i & 1] += a;
-                    sum[2 + (i & 1)] += b;
+                    const uint32_t(&x)[32] = s[2 * c + i / 16];
+                    const float2 e = unpair(fma2(pair(__uint_as_float(x[2 * (i % 16)]), __uint_as_float(x[2 * (i % 16) + 1])),
+                                                 scale2, base2));
+                    const float a = fast_exp2(e.x), b = fast_exp2(e.y);
+                    sum[i & 3] = add2(sum[i & 3], pair(a, b));
                     w[i] = pack_bf16x2(a, b);
                 }
                 tmem_store32(s_addr + c * 32, w);
+                tmem_wait_store();
+                tc_fence_before();
+                mbar_arrive(&p_ready[t][c]);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_wait_store();
-            tc_fence_before();
-            mbar_arrive(&p_full[t]);
+            const float2 both = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
+            l += both.x + both.y;
         }
         // ---- the row's output ----
         bool odd = false;
         fine = fine && tc_wait(&loads_done, 0);
-        if (fine && my_steps > 0) fine = tc_wait(&pv_done[t], (my_steps - 1) & 1);
+        if (fine && my_steps > 0) fine = tc_wait(&o_done[t], 0);
         if (!fine && lane == 0) report(p.dev_status, SFI_DEV_TIMEOUT);
         const bool write = fine && t < tiles_q && mine && s_bad == 0;
         if (fine && t < tiles_q) {
             tc_fence_after();
             const int64_t at = ((int64_t)r * p.tokens + token) * p.hq + head;
             const float inv = l == 0.f ? 0.f : 1.f / l;
+            // through the warp's part of Q's tile (nothing reads it any more), so that whole rows leave together:
+            // 16-byte stores to 32 rows at a time took 6000 cycles
+            constexpr int kChunks = D / 8;  // 16-byte pieces of a row
+            uint8_t *stage = smem + t * T::kBytes + (warp & 3) * 32 * D * 2;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
@@ -330,18 +371,27 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) big = max(big, o[i] & 0x7fffffffu);
                 odd |= big >= 0x7f800000u;
-                if (write) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        int4 v;
-                        v.x = (int)pack_bf16x2(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
-                        v.y = (int)pack_bf16x2(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
-                        v.z = (int)pack_bf16x2(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
-                        v.w = (int)pack_bf16x2(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
-                        st_v4(p.out + at * D + c + i, v);
-                    }
+                for (int i = 0; i < 32; i += 8) {
+                    int4 v;
+                    v.x = (int)pack_bf16x2(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
+                    v.y = (int)pack_bf16x2(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
+                    v.z = (int)pack_bf16x2(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
+                    v.w = (int)pack_bf16x2(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
+                    *reinterpret_cast<int4 *>(stage + lane * D * 2 + ((((c + i) / 8) ^ (lane & 7)) << 4)) = v;
                 }
             }
+            __syncwarp();
+            const uint32_t rows = __ballot_sync(0xffffffffu, write);
+            const int row0 = (warp & 3) * 32, chunk = lane % kChunks;
+            __nv_bfloat16 *out = p.out + (((int64_t)r * p.tokens + tok0 + t * per_tile) * p.hq + kvh * G) * D + chunk * 8;
+#pragma unroll 4
+            for (int i = lane / kChunks; i < 32; i += 32 / kChunks) {
+                const int tok = (row0 + i) >> shift, h = (row0 + i) & (G - 1);
+                const int4 v = *reinterpret_cast<const int4 *>(stage + i * D * 2 + ((chunk ^ (i & 7)) << 4));
+                if ((rows >> i) & 1u) st_v4(out + ((int64_t)tok * p.hq + h) * D, v);
+            }
+            __syncwarp();
             if (write && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
             uint32_t again = __ballot_sync(0xffffffffu, odd && write);
             while (again) {
@@ -368,7 +418,7 @@ cudaError_t launch_prompt(const WindowMaps &maps, const WindowParams &p, int bat
     if (e != cudaSuccess) return e;
     const int per_cta = 2 * kTileRows / p.group;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.tokens + per_cta - 1) / per_cta), (unsigned)p.hkv, (unsigned)batch);
+    cfg.gridDim = dim3((unsigned)p.hkv, (unsigned)batch, (unsigned)((p.tokens + per_cta - 1) / per_cta));
     cfg.blockDim = dim3(kPromptThreads);
     cfg.dynamicSmemBytes = PromptTile<D>::kSmem;
     cfg.stream = stream;

@@ -44,6 +44,13 @@ struct RowWindow {
         hi = any ? p + 1 - span.skip : 0;
     }
     __device__ __forceinline__ bool sees(int v) const { return v < sink || (v >= lo && v < hi); }
+    // The same of the slots v .. v + 31, a bit for each.
+    __device__ __forceinline__ uint32_t sees32(int v) const {
+        return below32(sink - v) | (below32(hi - v) & ~below32(lo - v));
+    }
+    static __device__ __forceinline__ uint32_t below32(int n) {
+        return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+    }
 };
 
 // Whether every token of p0 .. p1 sees all of the slots [v, v + n): they end before the first token's
