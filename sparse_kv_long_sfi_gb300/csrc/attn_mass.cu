@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kShortThreads, 2)
         mbar_init(&q_full, 1);
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1 + 4);
+            mbar_init(&empty[i], 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
@@ -410,7 +410,6 @@ __global__ void __launch_bounds__(kShortThreads, 2)
                            smem_desc(ra + slot * T::kKeyBytes + (ks >> 2) * T::kKeyHalf + (ks & 3) * 32, 16),
                            smem_desc(qa + (ks >> 2) * T::kRowHalf + (ks & 3) * 32, 16), T::kScores, ks > 0);
                 mma_commit(&s_full[buf]);
-                mma_commit(&empty[slot]);
             }
             __syncwarp();
             ++use;
@@ -439,6 +438,7 @@ __global__ void __launch_bounds__(kShortThreads, 2)
                 fine = tc_wait(&s_full[group], (at / 2) & 1);
                 if (!fine) break;
                 tc_fence_after();
+                if (lane == 0) mbar_arrive(&empty[slot]);  // the tile has been multiplied
                 const bool whole = (n << shift) == ROWS && k1 <= q0 && (k1 < p.sink || (int64_t)k0 > (int64_t)L - 1 - p.recent);
                 if (whole) {
                     sum = sum_columns<ROWS, true>(addr, s_lse, p.scale_log2, 0, 0);
@@ -450,10 +450,7 @@ __global__ void __launch_bounds__(kShortThreads, 2)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&s_empty[group]);
-                    mbar_arrive(&empty[slot]);
-                }
+                if (lane == 0) mbar_arrive(&s_empty[group]);
             }
             if (key <= k1 && !bad) mass[key] = old + sum;
         }

@@ -1,7 +1,12 @@
-// Eviction's second half: the kept rows of K and V move to the front of a request's pages.
+// Eviction: per (request, KV head) the candidates of [S, L - W) with the largest weights are chosen, and
+// the kept rows of K and V move to the front of the request's pages.
 //
-// The Selector (select_topk.cu) has chosen, per (request, KV head), the candidates of [S, L - W) with
-// the largest weights, in ascending positions. Row i of what remains comes from position
+// The choice is that of the Selector (select_topk.cu), which serves rows of more than 16384 candidates
+// here too. Its passes are laid out for long rows; the caches that are evicted from are short, so up to
+// that length one CTA keeps all keys in registers and counts them in one small histogram per pass of
+// 8 bits, lanes of equal bins first among themselves (16 x 8 units of 1792 candidates: 18 us there, 7 here).
+//
+// Row i of what remains comes from position
 //   src(i) = i for i < min(S, L),  idx[i - S] for the chosen ones,  L - W + (i - S - count) behind them,
 // and src(i) >= i ascends. So rows are moved in place, chunk after chunk: a chunk's rows may be read
 // any number of chunks ahead (its sources lie at or behind its own destinations, behind all earlier
@@ -12,7 +17,8 @@
 // 64- to 256-byte columns until there are enough CTAs; a ring of kEvictStages chunks by cp.async
 // keeps their reads in flight, and positions and page ids are fetched one and two chunks further ahead.
 // Weights go to a second buffer (they are also the Selector's input), in the same launch.
-// 16 requests of 8 x 2112 rows cut to 2048 (128-dim heads): 54.9 us with the Selector (264 MB, 38.9 us).
+// 16 requests of 8 x 2112 rows cut to 2048 (128-dim heads): 46 us, the choice 7 of them (264 MB, 38.9 us of HBM
+// time); 8 of 7001 to 16384 cut to about 1100: 34 us (76 MB, 11.3 us).
 //
 // It writes bf16 pages, so it does not release its dependents early (see page_ops.cu).
 #include <algorithm>
@@ -25,10 +31,133 @@ namespace sfi {
 namespace {
 
 constexpr int kEvictThreads = 256;
-constexpr int kEvictStages = 4;
-constexpr int kEvictLoads = 2;  // 16-byte pieces of a thread in a chunk
+constexpr int kEvictStages = 3;
+constexpr int kEvictLoads = 4;  // 16-byte pieces of a thread in a chunk
+
+constexpr int kSelectEach = 16;        // keys of a thread
+constexpr uint32_t kNoCandidate = 0xffffffffu;  // above +infinity's key, and never chosen
+
+// Ascending keys: -0 as +0, NaN below all.
+__device__ __forceinline__ uint32_t weight_key(float x) {
+    uint32_t u = __float_as_uint(x);
+    if ((u & 0x7fffffffu) > 0x7f800000u) return 0u;
+    if (u == 0x80000000u) u = 0u;
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
 
 }  // namespace
+
+// One CTA per unit, 16 candidates of a thread. What is refused here is reported by kv_evict_kernel.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams p, int32_t *idx_out, int32_t *count_out) {
+    constexpr int kWarps = THREADS / 32;
+    __shared__ uint32_t s_hist[2][256];
+    __shared__ uint32_t s_prefix, s_rem, s_in;
+    __shared__ int2 s_count[kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int kvh = blockIdx.x;
+    const int r = p.req_ids ? p.req_ids[blockIdx.y] : (int)blockIdx.y;
+    const int L = p.seq_lens[r], k = p.k_per_req[r];
+    if (L < 0 || L > p.mass_stride || k < 0 || k > p.k_cap) return;
+    const int n = (int)max((int64_t)0, (int64_t)L - p.recent - p.sink);  // at most THREADS * 16: the row's stride says so
+    const int keep = min(k, n);
+    if (kvh == 0 && tid == 0) count_out[r] = keep;
+    int32_t *out = idx_out + ((int64_t)r * p.hkv + kvh) * p.k_cap;
+    if (keep == n) {
+        for (int i = tid; i < n; i += THREADS) out[i] = p.sink + i;
+        return;
+    }
+    if (keep == 0) return;
+    // a warp's candidates lie in a row: 32 j + lane behind its first
+    const int first = warp * 32 * kSelectEach;
+    const float *row = p.mass + ((int64_t)r * p.hkv + kvh) * p.mass_stride + p.sink;
+    uint32_t key[kSelectEach];
+#pragma unroll
+    for (int j = 0; j < kSelectEach; ++j) {
+        const int i = first + 32 * j + lane;
+        key[j] = i < n ? __float_as_uint(row[i]) : 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < kSelectEach; ++j)
+        key[j] = first + 32 * j + lane < n ? weight_key(__uint_as_float(key[j])) : kNoCandidate;
+    // the bits of the smallest kept key, from the top; `rem` of the keys that share them are kept
+    uint32_t prefix = 0, rem = (uint32_t)keep, mask = 0;
+    for (int i = tid; i < 512; i += THREADS) s_hist[i >> 8][i & 255] = 0;
+    __syncthreads();
+    for (int pass = 0; pass < 4; ++pass) {
+        const int shift = 24 - 8 * pass;
+        uint32_t *hist = s_hist[pass & 1];
+#pragma unroll
+        for (int j = 0; j < kSelectEach; ++j) {
+            const bool in = key[j] != kNoCandidate && (key[j] & mask) == prefix;
+            const uint32_t active = __ballot_sync(0xffffffffu, in);
+            if (in) {
+                const uint32_t bin = (key[j] >> shift) & 255u;
+                const uint32_t same = __match_any_sync(active, bin);
+                if ((same & ((1u << lane) - 1u)) == 0u) atomicAdd(&hist[bin], (uint32_t)__popc(same));
+            }
+        }
+        __syncthreads();
+        if (warp == 0) {
+            // lane i: bins 255 - 8 i down to 248 - 8 i
+            uint32_t h[8], sum = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += h[i] = hist[255 - 8 * lane - i];
+            uint32_t above = sum;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const uint32_t o = __shfl_up_sync(0xffffffffu, above, off);
+                if (lane >= off) above += o;
+            }
+            above -= sum;  // keys in higher bins than this lane's
+            if (above < rem && rem <= above + sum) {
+                uint32_t at = above;
+                int i = 0;
+                for (; at + h[i] < rem; ++i) at += h[i];
+                s_prefix = prefix | (uint32_t)(255 - 8 * lane - i) << shift;
+                s_rem = rem - at;
+                s_in = h[i];
+            }
+        } else if (warp == 1 || kWarps == 1) {
+            for (int i = lane; i < 256; i += 32) s_hist[(pass & 1) ^ 1][i] = 0;  // the next pass's
+        }
+        __syncthreads();
+        prefix = s_prefix;
+        rem = s_rem;
+        mask |= 255u << shift;
+        if (s_in == rem) break;  // all that share these bits are kept
+    }
+    // ranks in the order of positions: kept ones are above the prefix, or share it and are among its first `rem`
+    int above = 0, equal = 0;
+#pragma unroll
+    for (int j = 0; j < kSelectEach; ++j) {
+        const bool valid = key[j] != kNoCandidate;
+        above += __popc(__ballot_sync(0xffffffffu, valid && (key[j] & mask) > prefix));
+        equal += __popc(__ballot_sync(0xffffffffu, valid && (key[j] & mask) == prefix));
+    }
+    if (lane == 0) s_count[warp] = make_int2(above, equal);
+    __syncthreads();
+    int2 before = lane < min(warp, kWarps) ? s_count[lane] : make_int2(0, 0);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        before.x += __shfl_xor_sync(0xffffffffu, before.x, off);
+        before.y += __shfl_xor_sync(0xffffffffu, before.y, off);
+    }
+    const uint32_t lower = (1u << lane) - 1u;
+    int at = before.x + min(before.y, (int)rem), seen = before.y;
+#pragma unroll
+    for (int j = 0; j < kSelectEach; ++j) {
+        const bool valid = key[j] != kNoCandidate, same = valid && (key[j] & mask) == prefix;
+        const uint32_t same_all = __ballot_sync(0xffffffffu, same);
+        const bool take = valid && ((key[j] & mask) > prefix || (same && seen + __popc(same_all & lower) < (int)rem));
+        const uint32_t taken = __ballot_sync(0xffffffffu, take);
+        if (take) out[at + __popc(taken & lower)] = p.sink + first + 32 * j + lane;
+        at += __popc(taken);
+        seen += __popc(same_all);
+    }
+}
 
 __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictParams p, int parts) {
     __shared__ __align__(16) int4 s_ring[kEvictStages][kEvictLoads][kEvictThreads];
@@ -164,9 +293,37 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictPara
     if (err) report(p.dev_status, err);
 }
 
-cudaError_t launch_kv_evict(const EvictParams &p, int batch, cudaStream_t stream) {
+namespace {
+
+template <int THREADS>
+cudaError_t launch_select(const EvictParams &p, const TopkParams &select, int batch, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.hkv, (unsigned)batch);
+    cfg.blockDim = dim3(THREADS);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, evict_select_kernel<THREADS>, p, select.idx_out, select.count_out);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_evict(const EvictParams &p, const TopkParams &select, int batch, cudaStream_t stream) {
     const int sms = sm_count_current_device();
     if (sms <= 0) return cudaErrorInvalidDevice;
+    // No row has more candidates than the weights' stride leaves.
+    const int64_t most = p.mass_stride - p.sink - p.recent;
+    cudaError_t e;
+    if (most <= 256 * kSelectEach)
+        e = launch_select<256>(p, select, batch, stream);
+    else if (most <= 1024 * kSelectEach)
+        e = launch_select<1024>(p, select, batch, stream);
+    else
+        e = launch_select_topk(select, batch, stream);
+    if (e != cudaSuccess) return e;
     // Four CTAs per SM, as far as columns of 64 bytes allow.
     const int64_t units = (int64_t)batch * p.hkv * 2;
     int parts = 1;

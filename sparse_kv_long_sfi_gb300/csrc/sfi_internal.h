@@ -293,7 +293,7 @@ struct EvictParams {
     int32_t *new_lens;
     int32_t *dev_status;
 };
-cudaError_t launch_kv_evict(const EvictParams &p, int batch, cudaStream_t stream);
+cudaError_t launch_kv_evict(const EvictParams &p, const TopkParams &select, int batch, cudaStream_t stream);
 
 struct VerifyParams {
     const float *target, *draft;  // [B][drafts + 1][vocab], [B][drafts][vocab] (or null)

@@ -1,5 +1,6 @@
 // C ABI of the operators around prompts, caches of a fixed size and drafts (declared in include/sfi.h):
 // argument validation and kernel dispatch. Allocates nothing.
+#include <algorithm>
 #include <cmath>
 
 #include "sfi_internal.h"
@@ -106,7 +107,9 @@ sfi_status sfi_kv_evict(const sfi_attn_shape *shape, const sfi_paged_kv *kv, con
     if (mass_stride < 1 || sink < 0 || recent < 0 || k_cap < 0 || batch < 0) return SFI_ERR_INVALID_ARG;
     if (shape->num_kv_heads > 65535 || batch > 65535) return SFI_ERR_UNSUPPORTED;
     if (batch == 0) return SFI_OK;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // (no request is that long; their sum with a length stays within 32 bits)
+    sink = std::min(sink, 1 << 30);
+    recent = std::min(recent, 1 << 30);
     sfi::TopkParams t{};
     t.scores = mass;
     t.score_stride = mass_stride;
@@ -120,7 +123,6 @@ sfi_status sfi_kv_evict(const sfi_attn_shape *shape, const sfi_paged_kv *kv, con
     t.count_out = count_out;
     t.req_ids = req_ids;
     t.dev_status = dev_status;
-    if (sfi::launch_select_topk(t, batch, s) != cudaSuccess) return SFI_ERR_CUDA;
     sfi::EvictParams p{};
     p.k_pool = static_cast<__nv_bfloat16 *>(kv->k_pool);
     p.v_pool = static_cast<__nv_bfloat16 *>(kv->v_pool);
@@ -141,7 +143,7 @@ sfi_status sfi_kv_evict(const sfi_attn_shape *shape, const sfi_paged_kv *kv, con
     p.k_cap = k_cap;
     p.new_lens = new_lens;
     p.dev_status = dev_status;
-    return launched(sfi::launch_kv_evict(p, batch, s));
+    return launched(sfi::launch_kv_evict(p, t, batch, static_cast<cudaStream_t>(stream)));
 }
 
 sfi_status sfi_verify_tokens(const float *target, int64_t target_stride, const float *draft, int64_t draft_stride,

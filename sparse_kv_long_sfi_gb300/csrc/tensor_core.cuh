@@ -180,6 +180,13 @@ __device__ __forceinline__ void tma_tile_3d(void *dst, const CUtensorMap *map, i
         : "memory");
 }
 
+// 32 bytes (32-byte aligned) in one store.
+__device__ __forceinline__ void st_v8(void *p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // Shared-memory writes of this thread, before tensor-core or TMA accesses to the same place.
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 

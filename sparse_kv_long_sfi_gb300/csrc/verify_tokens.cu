@@ -15,7 +15,7 @@
 // drafts end is read whole. A cluster of eight CTAs shares a request's row, so that one request fills
 // eight SMs and the row is read once; every CTA keeps the sum of each run of 128 weights, the CTAs
 // exchange their totals, and the one that holds the sample reads that run again.
-// 64 requests of 150001 tokens with 7 drafts: 72.3 us (77 MB, 11.3 us of HBM time).
+// 64 requests of 150001 tokens with 7 drafts: 24 us (77 MB, 11.3 us of HBM time); one of 32000: 5.6 us (latency).
 #include "sfi_device.cuh"
 #include "sfi_internal.h"
 
@@ -24,14 +24,18 @@ namespace sfi {
 namespace {
 
 constexpr int kVerifyCluster = 8;
-constexpr int kVerifyThreads = 512;
+constexpr int kVerifyThreads = 256;                    // (with 512, 64 requests come in two waves: 33 us)
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyRun = 128;                        // weights of a warp's run, four of each lane
+constexpr int kVerifyBatch = 4;                        // runs of a warp whose loads are in flight together
 constexpr int kVerifyRuns = SFI_MAX_VOCAB / kVerifyCluster / kVerifyRun + kVerifyWarps;
 
-// A probability in units of 2^-56: NaN and values below zero are nothing, values above one are one.
+// A probability in units of 2^-56: NaN and values below zero are nothing, values above one are one. By shifts of
+// its significand (the conversion instruction to 64 bits made the call 65 us instead of 33).
 __device__ __forceinline__ int64_t fixed(float p) {
-    return __float2ll_rz(fminf(fmaxf(p, 0.f), 1.f) * 72057594037927936.f);
+    const uint32_t u = __float_as_uint(fminf(fmaxf(p, 0.f), 1.f));
+    const uint64_t one = (uint64_t)((u & 0x7fffffu) | 0x800000u) << 33;  // as for [1, 2)
+    return (int64_t)(one >> min(127u - (u >> 23), 63u));
 }
 
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {
@@ -109,30 +113,30 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_tokens_kernel(const Ver
     const int runs = (V + kVerifyRun - 1) / kVerifyRun;
     const int per = (runs + kVerifyCluster - 1) / kVerifyCluster;
     const int run0 = min(rank * per, runs), run1 = min(run0 + per, runs);
-    auto weight = [&](int i) -> int64_t {
-        if (i >= V || i == gone) return 0;
-        const int64_t w = fixed(prow[i]);
-        return qrow ? max(w - fixed(qrow[i]), (int64_t)0) : w;
-    };
     int64_t total = 0, before = 0;
     for (int pass = 0; pass < 2; ++pass) {
         int64_t mine = 0;
-        for (int run = run0 + warp; run < run1; run += 2 * kVerifyWarps) {
-            // two runs of this warp: their loads are in flight together
-            int64_t w[2] = {0, 0};
+        for (int run = run0 + warp; run < run1; run += kVerifyBatch * kVerifyWarps) {
+            // all loads of a few runs before the first use
+            float pv[kVerifyBatch][4], qv[kVerifyBatch][4];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int at = run + k * kVerifyWarps;
-                if (at < run1) {
+            for (int k = 0; k < kVerifyBatch; ++k)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) w[k] += weight(at * kVerifyRun + 32 * j + lane);
+                for (int j = 0; j < 4; ++j) {
+                    const int i = (run + k * kVerifyWarps) * kVerifyRun + 32 * j + lane;
+                    const bool in = run + k * kVerifyWarps < run1 && i < V && i != gone;
+                    pv[k][j] = in ? prow[i] : 0.f;
+                    qv[k][j] = in && qrow ? qrow[i] : 0.f;
                 }
-            }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                w[k] = warp_sum(w[k]);
-                if (lane == 0 && run + k * kVerifyWarps < run1) s_run[run + k * kVerifyWarps - run0] = w[k];
-                mine += w[k];
+            for (int k = 0; k < kVerifyBatch; ++k) {
+                int64_t w = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w += max(fixed(pv[k][j]) - fixed(qv[k][j]), (int64_t)0);
+                w = warp_sum(w);
+                const int at = run + k * kVerifyWarps;
+                if (lane == 0 && at < run1) s_run[at - run0] = w;
+                mine += w;
             }
         }
         if (lane == 0) s_warp[warp] = mine;
@@ -184,7 +188,9 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_tokens_kernel(const Ver
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int i = run * kVerifyRun + 32 * j + lane;
-                const int64_t incl = warp_scan(weight(i), lane);
+                const bool in = i < V && i != gone;
+                const float pi = in ? prow[i] : 0.f, qi = in && qrow ? qrow[i] : 0.f;
+                const int64_t incl = warp_scan(max(fixed(pi) - fixed(qi), (int64_t)0), lane);
                 const uint32_t above = __ballot_sync(0xffffffffu, sum + incl > target);
                 if (above && next < 0) next = run * kVerifyRun + 32 * j + __ffs(above) - 1;
                 sum += __shfl_sync(0xffffffffu, incl, 31);
