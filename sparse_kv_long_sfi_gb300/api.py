@@ -53,15 +53,51 @@ class AttnShape:
         return c
 
 
+class _Handle:
+    """Tensors that one C structure points to. The structure is checked and made when it is
+    first needed, and again when a field has been assigned, a tensor's memory, shape or strides
+    are no longer what they were (resize_, set_, .data = ...), or another device is the current
+    one: a call that finds it ready saves itself the checks and the structure."""
+    _tensors = ()
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        self.__dict__.pop("_kept", None)  # with its references: a tensor that is let go is free
+
+    def __getstate__(self):
+        # a copy (copy, deepcopy, pickle) makes its own structure, of its own tensors
+        return {k: v for k, v in self.__dict__.items() if not k.startswith("_")}
+
+    def c(self, dev: Optional[int] = None):
+        """The structure, for calls on device dev (None: the current one)."""
+        if dev is None:
+            dev = torch._C._cuda_getDevice()
+        d = self.__dict__
+        kept = d.get("_kept")
+        if kept is not None and kept[1] == dev:
+            for t, ptr, size, stride in kept[2]:
+                if t.data_ptr() != ptr or t.shape != size or t.stride() != stride:
+                    break
+            else:
+                return kept[0]
+        d.pop("_kept", None)
+        c = self._make(dev)
+        at = [(t, t.data_ptr(), t.shape, t.stride()) for t in (d[n] for n in self._tensors)]
+        d["_kept"] = (c, dev, at)
+        return c
+
+
 @dataclass
-class PagedKV:
+class PagedKV(_Handle):
     """Paged bf16 KV cache: pools [num_pages][Hkv][P][D], page_table int32 [B][max_pages], seq_lens int32 [B]."""
     k_pool: torch.Tensor
     v_pool: torch.Tensor
     page_table: torch.Tensor
     seq_lens: torch.Tensor
 
-    def c(self) -> _abi.sfi_paged_kv:
+    _tensors = ("k_pool", "v_pool", "page_table", "seq_lens")
+
+    def _make(self, dev: int) -> _abi.sfi_paged_kv:
         for name, t, dt in (("k_pool", self.k_pool, torch.bfloat16), ("v_pool", self.v_pool, torch.bfloat16),
                             ("page_table", self.page_table, torch.int32), ("seq_lens", self.seq_lens, torch.int32)):
             _need(t, dt, name)
@@ -366,40 +402,6 @@ def _ptr_here(t: Optional[torch.Tensor], dtype, name: str, dev: int) -> Optional
 
 def _stream_here(stream, dev: int) -> Optional[int]:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
-
-
-class _Handle:
-    """Tensors that one C structure points to. The structure is checked and made when it is
-    first needed, and again when a field has been assigned, a tensor's memory, shape or strides
-    are no longer what they were (resize_, set_, .data = ...), or another device is the current
-    one: a call that finds it ready saves itself the checks and the structure."""
-    _tensors = ()
-
-    def __setattr__(self, name, value):
-        object.__setattr__(self, name, value)
-        self.__dict__.pop("_kept", None)  # with its references: a tensor that is let go is free
-
-    def __getstate__(self):
-        # a copy (copy, deepcopy, pickle) makes its own structure, of its own tensors
-        return {k: v for k, v in self.__dict__.items() if not k.startswith("_")}
-
-    def c(self, dev: Optional[int] = None):
-        """The structure, for calls on device dev (None: the current one)."""
-        if dev is None:
-            dev = torch._C._cuda_getDevice()
-        d = self.__dict__
-        kept = d.get("_kept")
-        if kept is not None and kept[1] == dev:
-            for t, ptr, size, stride in kept[2]:
-                if t.data_ptr() != ptr or t.shape != size or t.stride() != stride:
-                    break
-            else:
-                return kept[0]
-        d.pop("_kept", None)
-        c = self._make(dev)
-        at = [(t, t.data_ptr(), t.shape, t.stride()) for t in (d[n] for n in self._tensors)]
-        d["_kept"] = (c, dev, at)
-        return c
 
 
 @dataclass
@@ -871,13 +873,13 @@ def alloc_page_workspace(page_map: PageMap) -> torch.Tensor:
 
 def _pages_here(shape: AttnShape, kv: PagedKV, dev: int):
     """The C view of bf16 pages on the current device whose pools have the shape's heads; the number of requests."""
-    c = kv.c()
-    for name in ("k_pool", "v_pool", "page_table", "seq_lens"):
-        if getattr(kv, name).get_device() != dev:
+    c = kv.c(dev)
+    k, v, table = kv.k_pool, kv.v_pool, kv.page_table
+    if k.get_device() != dev or v.get_device() != dev or table.get_device() != dev or kv.seq_lens.get_device() != dev:
+        for name in kv._tensors:
             _on_current_device(getattr(kv, name), name)
-    dims, table = kv.k_pool.shape, kv.page_table.shape
-    if len(dims) != 4 or dims[1] != shape.num_kv_heads or dims[2] != shape.page_size or dims[3] != shape.head_dim \
-            or kv.v_pool.shape != dims:
+    dims, table = k.shape, table.shape
+    if dims != (dims[0], shape.num_kv_heads, shape.page_size, shape.head_dim) or v.shape != dims:
         raise ValueError(f"the pools must be [num_pages][{shape.num_kv_heads}][{shape.page_size}][{shape.head_dim}]")
     if len(table) != 2 or kv.seq_lens.numel() != table[0]:
         raise ValueError("seq_lens needs one entry per row of page_table")

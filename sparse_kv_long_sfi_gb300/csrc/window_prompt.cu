@@ -18,7 +18,7 @@
 //    tiles; a thread per tile issues its matrix instructions.
 //  * A CTA that is done takes over one that has not begun (cluster launch control), so that the next
 //    item's Q and first keys are on their way, and its first scores formed, while the last rows are written.
-// P is rounded to bf16 for the second product (2^-9 of each weight at most, which averages out over
+// P is rounded to bf16 for the second product (2^-8 of each weight at most, which averages out over
 // the keys); sums of P are taken before that, in fp32.
 //
 // A zero weight times a NaN is a NaN in a matrix product, so V's rows behind the last position (stale
