@@ -4,7 +4,7 @@
 // The choice is that of the Selector (select_topk.cu), which serves rows of more than 16384 candidates
 // here too. Its passes are laid out for long rows; the caches that are evicted from are short, so up to
 // that length one CTA keeps all keys in registers and counts them in one small histogram per pass of
-// 8 bits, lanes of equal bins first among themselves (16 x 8 units of 1792 candidates: 18 us there, 7 here).
+// 8 bits (16 x 8 units of 1792 candidates: 18 us there, 9 here).
 //
 // Row i of what remains comes from position
 //   src(i) = i for i < min(S, L),  idx[i - S] for the chosen ones,  L - W + (i - S - count) behind them,
@@ -17,8 +17,9 @@
 // 64- to 256-byte columns until there are enough CTAs; a ring of kEvictStages chunks by cp.async
 // keeps their reads in flight, and positions and page ids are fetched one and two chunks further ahead.
 // Weights go to a second buffer (they are also the Selector's input), in the same launch.
-// 16 requests of 8 x 2112 rows cut to 2048 (128-dim heads): 46 us, the choice 7 of them (264 MB, 38.9 us of HBM
-// time); 8 of 7001 to 16384 cut to about 1100: 34 us (76 MB, 11.3 us).
+// 16 requests of 8 x 2112 rows cut to 2048 (128-dim heads): 41 us, the choice 5 of them (264 MB, 38.9 us of HBM
+// time); 8 of 7001 to 16384 cut to about 1100: 32 us, the choice 13 of them
+// (76 MB, 11.3 us).
 //
 // It writes bf16 pages, so it does not release its dependents early (see page_ops.cu).
 #include <algorithm>
@@ -51,7 +52,11 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams p, int32_t *idx_out, int32_t *count_out) {
     constexpr int kWarps = THREADS / 32;
-    __shared__ uint32_t s_hist[2][256];
+    // Long rows have a counter for each bin and lane, so that a warp's atomics hit 32 banks (64 units of up to 16000
+    // candidates: 15.6 us, with one counter per bin 19); short ones need not clear and add up that many (9 and 10.7).
+    constexpr int kCopies = THREADS == 1024 ? 32 : 1;
+    __shared__ uint32_t s_hist[256 * kCopies];
+    __shared__ uint32_t s_bin[256];
     __shared__ uint32_t s_prefix, s_rem, s_in;
     __shared__ int2 s_count[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -84,27 +89,37 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams
         key[j] = first + 32 * j + lane < n ? weight_key(__uint_as_float(key[j])) : kNoCandidate;
     // the bits of the smallest kept key, from the top; `rem` of the keys that share them are kept
     uint32_t prefix = 0, rem = (uint32_t)keep, mask = 0;
-    for (int i = tid; i < 512; i += THREADS) s_hist[i >> 8][i & 255] = 0;
+    for (int i = tid; i < 256 * kCopies; i += THREADS) s_hist[i] = 0;
     __syncthreads();
     for (int pass = 0; pass < 4; ++pass) {
         const int shift = 24 - 8 * pass;
-        uint32_t *hist = s_hist[pass & 1];
 #pragma unroll
         for (int j = 0; j < kSelectEach; ++j) {
             const bool in = key[j] != kNoCandidate && (key[j] & mask) == prefix;
-            const uint32_t active = __ballot_sync(0xffffffffu, in);
-            if (in) {
-                const uint32_t bin = (key[j] >> shift) & 255u;
-                const uint32_t same = __match_any_sync(active, bin);
-                if ((same & ((1u << lane) - 1u)) == 0u) atomicAdd(&hist[bin], (uint32_t)__popc(same));
+            if (in) atomicAdd(&s_hist[((key[j] >> shift) & 255u) * kCopies + (lane & (kCopies - 1))], 1u);
+        }
+        __syncthreads();
+        {
+            // a bin's counters, cleared for the next pass (in an order without bank conflicts)
+            constexpr int kParts = THREADS / 256, kSpan = kCopies / kParts;
+            const int bin = tid / kParts, part = tid % kParts;
+            uint32_t sum = 0;
+#pragma unroll 8
+            for (int i = 0; i < kSpan; ++i) {
+                uint32_t *at = &s_hist[bin * kCopies + part * kSpan + ((i + bin) & (kSpan - 1))];
+                sum += *at;
+                *at = 0;
             }
+#pragma unroll
+            for (int off = 1; off < kParts; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            if (part == 0) s_bin[bin] = sum;
         }
         __syncthreads();
         if (warp == 0) {
             // lane i: bins 255 - 8 i down to 248 - 8 i
             uint32_t h[8], sum = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum += h[i] = hist[255 - 8 * lane - i];
+            for (int i = 0; i < 8; ++i) sum += h[i] = s_bin[255 - 8 * lane - i];
             uint32_t above = sum;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -120,8 +135,6 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams
                 s_rem = rem - at;
                 s_in = h[i];
             }
-        } else if (warp == 1 || kWarps == 1) {
-            for (int i = lane; i < 256; i += 32) s_hist[(pass & 1) ^ 1][i] = 0;  // the next pass's
         }
         __syncthreads();
         prefix = s_prefix;
@@ -324,7 +337,8 @@ cudaError_t launch_kv_evict(const EvictParams &p, const TopkParams &select, int 
     else
         e = launch_select_topk(select, batch, stream);
     if (e != cudaSuccess) return e;
-    // Four CTAs per SM, as far as columns of 64 bytes allow.
+    // Four CTAs per SM, as far as columns of 64 bytes allow. (Sharing the rows that come from behind the end of what
+    // remains between CTAs of a cluster, where most of a cache goes, was slower: 32 us without, 38 with 2 or 4.)
     const int64_t units = (int64_t)batch * p.hkv * 2;
     int parts = 1;
     while (parts < p.head_dim / 32 && units * parts < (int64_t)sms * 4) parts *= 2;

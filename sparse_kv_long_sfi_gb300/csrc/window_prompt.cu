@@ -24,9 +24,9 @@
 // A zero weight times a NaN is a NaN in a matrix product, so V's rows behind the last position (stale
 // bytes of a page's tail) are zeroed in shared memory, and a row whose output is not finite is computed
 // again key by key, from the positions it sees alone.
-// 16/8/128 heads: two prompts of 8192 tokens with window 1024 143 us (51% of the measured bf16 rate: 1280 keys are
-// multiplied for 1088 that are seen, and a CTA's first and last steps are masked), one causal prompt of 8192 209 us (70%);
-// 32/8/128 heads, 16384 tokens: 1.52 ms (77%). In the loop a step of 256 rows x 128 keys takes 3080 cycles (84%).
+// 16/8/128 heads: two prompts of 8192 tokens with window 1024 138 us (53% of the measured bf16 rate: 1280 keys are
+// multiplied for 1088 that are seen, and a CTA's first and last steps are masked), one causal prompt of 8192 208 us (70%);
+// 32/8/128 heads, 16384 tokens: 1.48 ms (79%). In the loop a step of 256 rows x 128 keys takes 3080 cycles (84%).
 #include <algorithm>
 #include <atomic>
 
@@ -46,7 +46,8 @@ constexpr int kTileRows = 128;       // query rows of a tile, keys of a step
 constexpr int kTilePages = kTileRows / kSubTokens;
 constexpr float kGrowth = 8.f;       // the running maximum moves when a score passes it by this (log2)
 constexpr uint32_t kTmemColumns = 512;
-constexpr int64_t kTogether = 48 << 20;
+constexpr int64_t kTogether = 16 << 20, kTailTogether = 48 << 20;
+constexpr int kTailWaves = 3;
 constexpr int kItemReaders = 8 + 3;  // softmax warps, the copy warp, the matrix threads
 
 template <int D>
@@ -76,10 +77,10 @@ struct PromptWork {
           steps((span.pages + kTilePages - 1) / kTilePages) {}
 };
 
-// The order of the items: units (request, KV head) in groups of `group`, whose K and V L2 holds together, in a group the
-// tiles with the most keys of every unit first.
+// The order of the items: units (request, KV head) in groups of `group`, and the units from `tail` on in one; in a group
+// the tiles with the most keys of every unit first.
 struct PromptOrder {
-    int units, group, tiles;
+    int units, group, tail, tiles;
 };
 
 // Takes over a CTA of this grid that has not begun (its index goes to x), if there is one. One thread; `answer`
@@ -328,8 +329,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                             if (!left) break;
                         }
                         ++taken;
-                        const int before = (int)x / (order.group * order.tiles) * order.group;  // units of earlier groups
-                        const int size = min(order.group, order.units - before);
+                        const bool in_tail = (int)x >= order.tail * order.tiles;
+                        // units of earlier groups, and of this one
+                        const int before = in_tail ? order.tail : (int)x / (order.group * order.tiles) * order.group;
+                        const int size = in_tail ? order.units - before : min(order.group, order.tail - before);
                         const int at = (int)x - before * order.tiles, unit = before + at % size, tile = at / size;
                         const int b = unit / p.hkv, kvh = unit - b * p.hkv;
                         const int r = p.req_ids ? p.req_ids[b] : b;
@@ -582,10 +585,15 @@ cudaError_t launch_prompt(const WindowMaps &maps, const WindowParams &p, int bat
     const int tiles = (p.tokens + per_cta - 1) / per_cta;
     const int64_t units = (int64_t)batch * p.hkv, items = units * tiles;
     if (items >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
-    // Units whose K and V, at their longest, take kTogether bytes (a part of L2) are worked on together: one after the
-    // other leaves the last one's long tiles to the end, all at once read K and V from HBM again and again.
+    // A few units at a time keep their K and V in L2 (kTogether bytes at their longest), but the last of them would leave
+    // long tiles to the end: the units with the last kTailWaves CTAs per SM (if L2 holds them) are one group.
+    // Four ragged chunks of 8 heads: 258 us with small groups alone, 293 with large ones, 256 with both; a prompt of 8192:
+    // 250, 211 and 208.
     const int64_t bytes = (int64_t)p.max_pages * kSubTokens * D * 4;
+    const int sms = sm_count_current_device();
     const int group = (int)std::max<int64_t>(1, std::min(units, kTogether / bytes));
+    const int64_t last = std::min<int64_t>((kTailWaves * sms + tiles - 1) / tiles, std::max<int64_t>(1, kTailTogether / bytes));
+    const int tail = (int)std::max<int64_t>(0, units - last);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)items);
     cfg.blockDim = dim3(kPromptThreads);
@@ -596,7 +604,7 @@ cudaError_t launch_prompt(const WindowMaps &maps, const WindowParams &p, int bat
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, maps.q, maps.k, maps.v, p, PromptOrder{(int)units, group, tiles});
+    return cudaLaunchKernelEx(&cfg, kernel, maps.q, maps.k, maps.v, p, PromptOrder{(int)units, group, tail, tiles});
 }
 
 }  // namespace
