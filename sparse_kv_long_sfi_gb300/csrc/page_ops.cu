@@ -280,15 +280,19 @@ __global__ void __launch_bounds__(kPlanThreads) page_reserve_kernel(const PageMa
     __syncthreads();
     int before = 0;  // holders of the same last page that come earlier in the list
     bool twice = false;
+    const int holders = last >= 0 ? m.ref_count[last] : 0;
+    // (nothing to compare where no request is listed by id and no last page is shared: 14 us for 512 requests)
+    if (__syncthreads_or(reqs != nullptr || holders > 1)) {
 #pragma unroll 8
-    for (int i = 0; i < ((tid & ~31) < n ? tid & ~31 : 0); ++i) {  // the warps before this one, then its own lanes
-        const int2 e = s_entry[i];
-        before += e.y == last;
-        twice |= e.x == r;
+        for (int i = 0; i < ((tid & ~31) < n ? tid & ~31 : 0); ++i) {  // the warps before this one, then its own lanes
+            const int2 e = s_entry[i];
+            before += e.y == last;
+            twice |= e.x == r;
+        }
+        const uint32_t lower = (1u << (tid & 31)) - 1u;
+        before += __popc(__match_any_sync(0xffffffffu, last) & lower);
+        twice |= (__match_any_sync(0xffffffffu, r) & lower) != 0;
     }
-    const uint32_t lower = (1u << (tid & 31)) - 1u;
-    before += __popc(__match_any_sync(0xffffffffu, last) & lower);
-    twice |= (__match_any_sync(0xffffffffu, r) & lower) != 0;
     if (tid < n && r >= 0 && twice) err = SFI_DEV_BAD_INDEX;  // named twice
     if (__syncthreads_or(err != 0)) {
         if (err) report(dev_status, err);
@@ -296,7 +300,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_reserve_kernel(const PageMa
     }
     // a shared last page is copied, except by the last of its holders in the list when they
     // are all there are
-    const bool copy = last >= 0 && m.ref_count[last] - before > 1;
+    const bool copy = last >= 0 && holders - before > 1;
     // (a row of the table may have 2^27 pages, so 1024 requests may ask for more than 32 bits count;
     // the scan's sums hold when there are that many pages at all)
     block_sum(fresh + copy, &s_need);
@@ -313,30 +317,29 @@ __global__ void __launch_bounds__(kPlanThreads) page_reserve_kernel(const PageMa
         return;
     }
     // The `total` lowest free pages. A warp takes 32 kEach pages in a row, its ranks come from ballots; the counts of
-    // the next round are on their way meanwhile (512 requests on 340000 pages: 46 us with four pages of a thread,
-    // loaded when needed, 33 us now).
+    // the next two rounds are on their way meanwhile (512 requests on 340000 pages: 46 us with four pages of a thread,
+    // loaded when needed, and list entries compared where nothing can be equal, 22 us now).
     constexpr int kEach = 8, kRound = kPlanThreads * kEach;
     const int lane = tid & 31;
     const uint32_t lower32 = (1u << lane) - 1u;
     int found = 0;
-    int c[kEach];
-    auto counts = [&](int base) {
+    int c[2][kEach];
+    auto counts = [&](int base, int (&v)[kEach]) {  // (base < 0: past 32 bits, behind the last page)
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
             const int p = base + (tid >> 5) * (32 * kEach) + 32 * k + lane;
-            c[k] = p < m.num_pages && p >= 0 ? m.ref_count[p] : 1;
+            v[k] = base >= 0 && p < m.num_pages && p >= 0 ? m.ref_count[p] : 1;
         }
     };
-    if (total) counts(0);
-    for (int base = 0; found < total; base += kRound) {
+    auto round = [&](int base, int (&v)[kEach]) {
         uint32_t hole[kEach];
         int mine = 0;
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            hole[k] = __ballot_sync(0xffffffffu, c[k] == 0);
+            hole[k] = __ballot_sync(0xffffffffu, v[k] == 0);
             mine += __popc(hole[k]);
         }
-        if (m.num_pages - base > kRound) counts(base + kRound);
+        counts(base > m.num_pages - 2 * kRound ? -1 : base + 2 * kRound, v);
         int here = 0;
         // the warp's count enters the scan through its first lane; every lane gets what came before
         int at = found + __shfl_sync(0xffffffffu, block_scan(lane == 0 ? mine : 0, s_warp, &here), 0);
@@ -347,7 +350,13 @@ __global__ void __launch_bounds__(kPlanThreads) page_reserve_kernel(const PageMa
             at += __popc(hole[k]);
         }
         found += here;
-        if (m.num_pages - base <= kRound) break;
+        return found < total && m.num_pages - base > kRound;  // another round
+    };
+    if (total) {
+        counts(0, c[0]);
+        counts(m.num_pages > kRound ? kRound : -1, c[1]);
+        for (int base = 0; round(base, c[0]) && round(base + kRound, c[1]); base += 2 * kRound) {
+        }
     }
     if (found < total) {
         if (tid == 0) report(dev_status, SFI_DEV_NO_PAGE);
