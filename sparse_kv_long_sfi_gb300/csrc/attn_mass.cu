@@ -17,7 +17,7 @@
 //  * Short calls: the query rows (16, 32, 64 or 128 of them) stay in shared memory, and a CTA walks a run of
 //    tiles of 128 positions through a ring; two warpgroups take the tiles in turn.
 // A prompt of 8192 tokens, 16/8/128 heads: 135 us (54% of the measured bf16 rate).
-// The last 64 tokens of 8 x 16384, 16/8/128 heads: 60 us (69% of the measured copy
+// The last 64 tokens of 8 x 16384, 16/8/128 heads: 52 us (80% of the measured copy
 // bandwidth).
 #include <algorithm>
 #include <atomic>
@@ -496,10 +496,10 @@ cudaError_t launch_short(const WindowMaps &maps, const WindowParams &p, const Ma
     static std::atomic<uint64_t> configured{0};
     const int sms = sm_count_current_device();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    // Runs of tiles: about three CTAs for each place (two on an SM), so that ragged lengths even out; a run
-    // pays for its CTA's start from a few tiles on.
+    // Runs of tiles: two CTAs for each place (two on an SM), so that ragged lengths even out; a run pays for its
+    // CTA's start from a few tiles on (64 units of 128 tiles: 62 us with one, 52 with two, 56 with three, 58 with six).
     const int64_t tiles = (most + kKeyTile - 1) / kKeyTile, units = (int64_t)batch * p.hkv;
-    const int64_t places = (int64_t)sms * 2 * 3;
+    const int64_t places = (int64_t)sms * 2 * 2;
     const int64_t per = std::max<int64_t>(1, (tiles * units + places - 1) / places);
     return launch_mass(mass_short_kernel<D, ROWS>, kShortThreads, ShortTile<D, ROWS>::kSmem, configured,
                        dim3((unsigned)((tiles + per - 1) / per), (unsigned)p.hkv, (unsigned)batch), stream, maps.q,

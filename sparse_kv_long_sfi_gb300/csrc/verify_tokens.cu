@@ -15,7 +15,8 @@
 // drafts end is read whole. A cluster of eight CTAs shares a request's row, so that one request fills
 // eight SMs and the row is read once; every CTA keeps the sum of each run of 128 weights, the CTAs
 // exchange their totals, and the one that holds the sample reads that run again.
-// 64 requests of 150001 tokens with 7 drafts: 24 us (77 MB, 11.3 us of HBM time); one of 32000: 5.6 us (latency).
+// 64 requests of 150001 tokens with 7 drafts: 26 us (77 MB, 11.3 us of HBM time; clusters of seven, three CTAs on every
+// SM, take 29); one of 32000: 5.7 us (latency).
 #include "sfi_device.cuh"
 #include "sfi_internal.h"
 

@@ -8,7 +8,7 @@
 // want 64 rows at least, and its hand-overs between warps cost a short step more than they save).
 // Parts meet once: within a CTA through shared memory, then every CTA pushes each share of the rows to
 // the CTA that writes it, through distributed shared memory, behind one cluster barrier.
-// 32 requests, 32/8/128 heads, window 4096: 88 us (91% of the measured copy bandwidth); 16 requests, 16/8/128
+// 32 requests, 32/8/128 heads, window 4096: 84 us (95% of the measured copy bandwidth); 16 requests, 16/8/128
 // heads, window 256: 6.7 us (latency).
 #include <algorithm>
 #include <atomic>
@@ -331,13 +331,13 @@ __global__ void __launch_bounds__(kStepThreads, 2)
 
 namespace {
 
-// CTAs of a unit: while all of them fit the SMs (two each) and every warp has two pages at least. (More than fit
-// cost their starts: 256 units of 4160 rows take 88 us in 256 CTAs, 91 in 512, 100 in 2048; 128 units of 320 rows take
-// 6.7 us in 256 CTAs, 15 in 512.)
+// CTAs of a unit: while all of them fit the SMs (two each) and every warp has two pages at least; of long units two at
+// least, whose second wave evens out the first. (256 units of 4160 rows: 88 us in 256 CTAs, 84 in 512, 91 in 1024; 128
+// units of 320 rows: 6.7 us in 256 CTAs, 15 in 512.)
 int step_cluster(int64_t units, int pages, int sms) {
     int c = 1;
     while (c < kStepMaxCluster && units * 2 * c <= 2 * (int64_t)sms && pages >= 4 * c * kStepWarps) c *= 2;
-    return c;
+    return c == 1 && pages >= 32 * kStepWarps ? 2 : c;
 }
 
 template <int D>
