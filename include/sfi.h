@@ -753,7 +753,8 @@ SFI_API size_t sfi_page_workspace_size(const sfi_page_map *map);
  *   out : bf16 [B][num_tokens][Hq][D], 16-byte aligned (rounded once from fp32);
  *   lse : fp32 [B][num_tokens][Hq] or NULL. Rows of tokens t >= n_r are not written. A token that
  *         sees nothing (S = 0, W = 0) gets out = 0 and lse = -inf.
- * What a token does not see has no influence on it, NaN and infinities included.
+ * What a token does not see has no influence on it, NaN and infinities included. Outputs must not
+ * overlap inputs.
  * Device errors: SFI_DEV_BAD_INDEX (a request id outside [0, num_reqs)), SFI_DEV_BAD_LEN (n_r < 0,
  * n_r > num_tokens, L_r < n_r or L_r beyond the page table): that request is skipped.
  * SFI_DEV_BAD_PAGE, SFI_DEV_TIMEOUT (the tokens whose block reads

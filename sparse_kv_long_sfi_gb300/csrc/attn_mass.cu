@@ -101,7 +101,8 @@ __device__ __forceinline__ float sum_columns(uint32_t addr, const float *lse, fl
 
 template <int D>
 __global__ void __launch_bounds__(kLongThreads, 1)
-    mass_long_kernel(const __grid_constant__ CUtensorMap tm_q, const WindowParams p, const MassParams w) {
+    mass_long_kernel(const __grid_constant__ CUtensorMap tm_q, const WindowParams p, const MassParams w,
+                     int units) {
     using T = LongTile<D>;
     constexpr int ROWS = T::kRows;
     extern __shared__ uint8_t smem_raw[];
@@ -116,19 +117,20 @@ __global__ void __launch_bounds__(kLongThreads, 1)
     grid_dependency_wait();
     grid_launch_dependents();
     // (the blocks with the most query rows, the first of every request and head, first)
-    const int kvh = blockIdx.x;
-    const int r = p.req_ids ? p.req_ids[blockIdx.y] : (int)blockIdx.y;
+    const int block = (int)blockIdx.x / units, unit = (int)blockIdx.x - block * units;
+    const int b = unit / p.hkv, kvh = unit - b * p.hkv;
+    const int r = p.req_ids ? p.req_ids[b] : b;
     if (r < 0 || r >= p.reqs) {
-        if (threadIdx.x == 0 && blockIdx.z == 0 && kvh == 0) report(p.dev_status, SFI_DEV_BAD_INDEX);
+        if (threadIdx.x == 0 && block == 0 && kvh == 0) report(p.dev_status, SFI_DEV_BAD_INDEX);
         return;
     }
     const int L = p.seq_lens[r];
     const int n = p.new_lens ? p.new_lens[r] : p.tokens;
     if (n < 0 || n > p.tokens || L < n || L > p.max_pages * kSubTokens || L > w.stride) {
-        if (threadIdx.x == 0 && blockIdx.z == 0 && kvh == 0) report(p.dev_status, SFI_DEV_BAD_LEN);
+        if (threadIdx.x == 0 && block == 0 && kvh == 0) report(p.dev_status, SFI_DEV_BAD_LEN);
         return;
     }
-    const int k0 = blockIdx.z * kMassKeys;
+    const int k0 = block * kMassKeys;
     if (k0 >= L) return;
     const int k1 = min(k0 + kMassKeys, L) - 1;
     const int G = p.group, shift = __ffs(G) - 1, per_tile = ROWS >> shift;
@@ -485,9 +487,9 @@ template <int D>
 cudaError_t launch_long(const WindowMaps &maps, const WindowParams &p, const MassParams &w, int64_t most, int batch,
                         cudaStream_t stream) {
     static std::atomic<uint64_t> configured{0};
+    const int64_t units = (int64_t)batch * p.hkv;
     return launch_mass(mass_long_kernel<D>, kLongThreads, LongTile<D>::kSmem, configured,
-                       dim3((unsigned)p.hkv, (unsigned)batch, (unsigned)((most + kMassKeys - 1) / kMassKeys)), stream,
-                       maps.q, p, w);
+                       dim3((unsigned)(units * ((most + kMassKeys - 1) / kMassKeys))), stream, maps.q, p, w, (int)units);
 }
 
 template <int D, int ROWS>

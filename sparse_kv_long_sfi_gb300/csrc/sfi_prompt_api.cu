@@ -73,6 +73,8 @@ sfi_status sfi_window_attn(const sfi_attn_shape *shape, const sfi_paged_kv *kv, 
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.lse = lse;
     const bool step = (int64_t)num_tokens * p.group <= sfi::kMaxRows;
+    // (a CTA for each 256 query rows of a KV head)
+    if ((int64_t)batch * p.hkv * (((int64_t)num_tokens * p.group + 255) / 256) >= (int64_t(1) << 31)) return SFI_ERR_UNSUPPORTED;
     sfi::WindowMaps maps{};
     if (!window_maps(shape, kv, p, step ? 0 : sfi::kPromptBoxRows, maps)) return SFI_ERR_CUDA;
     const auto launch = step ? sfi::launch_window_step : sfi::launch_window_prompt;
@@ -89,6 +91,9 @@ sfi_status sfi_attn_mass(const sfi_attn_shape *shape, const sfi_paged_kv *kv, in
     if (st != SFI_OK) return st;
     if (!lse || !mass || mass_stride < 1 || !std::isfinite(decay)) return SFI_ERR_INVALID_ARG;
     if (batch == 0 || num_reqs == 0) return SFI_OK;
+    // (a CTA for each 128 positions of a KV head at most)
+    const int64_t most = std::min<int64_t>((int64_t)kv->max_pages_per_req * sfi::kSubTokens, mass_stride);
+    if ((int64_t)batch * p.hkv * ((most + 127) / 128) >= (int64_t(1) << 31)) return SFI_ERR_UNSUPPORTED;
     sfi::WindowMaps maps{};
     if (!window_maps(shape, kv, p, sfi::mass_rows((int64_t)num_tokens * p.group), maps)) return SFI_ERR_CUDA;
     const sfi::MassParams w{lse, mass, mass_stride, decay};

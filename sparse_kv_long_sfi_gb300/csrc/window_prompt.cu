@@ -584,7 +584,6 @@ cudaError_t launch_prompt(const WindowMaps &maps, const WindowParams &p, int bat
     const int per_cta = 2 * kTileRows / p.group;
     const int tiles = (p.tokens + per_cta - 1) / per_cta;
     const int64_t units = (int64_t)batch * p.hkv, items = units * tiles;
-    if (items >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
     // A few units at a time keep their K and V in L2 (kTogether bytes at their longest), but the last of them would leave
     // long tiles to the end: the units with the last kTailWaves CTAs per SM (if L2 holds them) are one group.
     // Four ragged chunks of 8 heads: 258 us with small groups alone, 293 with large ones, 256 with both; a prompt of 8192:
