@@ -17,12 +17,13 @@
 // 64- to 256-byte columns until there are enough CTAs; a ring of kEvictStages chunks by cp.async
 // keeps their reads in flight, and positions and page ids are fetched one and two chunks further ahead.
 // Weights go to a second buffer (they are also the Selector's input), in the same launch.
-// 16 requests of 8 x 2112 rows cut to 2048 (128-dim heads): 41 us, the choice 5 of them (264 MB, 38.9 us of HBM
-// time); 8 of 7001 to 16384 cut to about 1100: 32 us, the choice 13 of them
+// 16 requests of 8 x 2112 rows cut to 2048 (128-dim heads): 31 us, the choice 5 of them (264 MB, 38.9 us of HBM
+// time, but most of it stays in L2); 8 of 7001 to 16384 cut to about 1100: 32 us, the choice 13 of them
 // (76 MB, 11.3 us).
 //
 // It writes bf16 pages, so it does not release its dependents early (see page_ops.cu).
 #include <algorithm>
+#include <atomic>
 
 #include "sfi_device.cuh"
 #include "sfi_internal.h"
@@ -32,7 +33,7 @@ namespace sfi {
 namespace {
 
 constexpr int kEvictThreads = 256;
-constexpr int kEvictStages = 3;
+constexpr int kEvictStages = 3, kEvictTables = 5;
 constexpr int kEvictLoads = 4;  // 16-byte pieces of a thread in a chunk
 
 constexpr int kSelectEach = 16;        // keys of a thread
@@ -173,7 +174,12 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams
 }
 
 __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictParams p, int parts) {
-    __shared__ __align__(16) int4 s_ring[kEvictStages][kEvictLoads][kEvictThreads];
+    extern __shared__ __align__(16) int4 s_dyn[];
+    int4(*ring)[kEvictLoads][kEvictThreads] = reinterpret_cast<int4(*)[kEvictLoads][kEvictThreads]>(s_dyn);
+    // A chunk's rows: where each comes from (or -1: it is not moved) and goes to, as rows of the pool. A thread
+    // works out one row, not each of the 16 pieces that the threads move (61% of issue slots then: 37 us for
+    // 16 x 8 x 2048 rows that lie in L2, 26 now).
+    int2(*table)[kEvictThreads] = reinterpret_cast<int2(*)[kEvictThreads]>(s_dyn + kEvictStages * kEvictLoads * kEvictThreads);
     const int tid = threadIdx.x;
     grid_dependency_wait();
     const int r = p.req_ids ? p.req_ids[blockIdx.z] : (int)blockIdx.z;
@@ -205,6 +211,7 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictPara
     if (weights) {
         if (!p.mass_out) return;
         const int64_t row = ((int64_t)r * p.hkv + kvh) * p.mass_stride;
+#pragma unroll 4
         for (int i = tid; i < kept; i += kEvictThreads) {
             const int s = source(i);
             if ((uint32_t)s < (uint32_t)L) p.mass_out[row + i] = p.mass[row + s];
@@ -214,93 +221,81 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictPara
     if (all) return;
     const bool is_v = (int)blockIdx.x >= parts;
     const int part = (int)blockIdx.x - (is_v ? parts : 0);
-    const int per_row = p.head_dim * 2 / parts / 16;  // 16-byte pieces of a row's part: a power of two
-    const int rows = kEvictThreads / per_row;         // rows of one load; a chunk has kEvictLoads times as many
-    const int mine = tid / per_row;
-    char *pool = reinterpret_cast<char *>(is_v ? p.v_pool : p.k_pool) + part * (p.head_dim * 2 / parts) + (tid % per_row) * 16;
+    const int per_row = p.head_dim * 2 / parts / 16;  // 16-byte pieces of a row's part: a power of two, 4 to 16
+    const int shift = __ffs(per_row) - 1;
+    const int rows = kEvictThreads >> shift;          // rows of one load; a chunk has kEvictLoads times as many
+    const int mine = tid >> shift;
+    const int row_bytes = p.head_dim * 2;
+    char *pool = reinterpret_cast<char *>(is_v ? p.v_pool : p.k_pool) + part * (row_bytes / parts) + (tid & (per_row - 1)) * 16;
     const int32_t *ptab = p.page_table + (int64_t)r * p.max_pages;
     const int first = min(p.sink, L);  // sink rows stay where they are
-    const int chunk_rows = rows * kEvictLoads;
+    const int chunk_rows = rows * kEvictLoads;  // (at most a row for each thread)
     const int chunks = (kept - first + chunk_rows - 1) / chunk_rows;
     uint32_t err = 0;
-    // the row behind (page, position), or null
-    auto at = [&](int page, int pos) -> char * {
-        if (page < 0 || page >= p.num_pages) {
-            err |= SFI_DEV_BAD_PAGE;
-            return nullptr;
-        }
-        return pool + (((int64_t)page * p.hkv + kvh) * kSubTokens + pos % kSubTokens) * p.head_dim * 2;
+    // this thread's row of a chunk: its place, where it comes from (-1: it stays, or there is none), and their pages
+    int src = -1, src_page = 0, dst_page = 0, next = -1;
+    auto fetch_pos = [&](int c) -> int {
+        const int i = first + c * chunk_rows + tid;
+        if (c >= chunks || tid >= chunk_rows || i >= kept) return -1;
+        return source(i);
     };
-    int src_pos[kEvictLoads], src_page[kEvictLoads], next_pos[kEvictLoads];
-    auto fetch_pos = [&](int c, int (&pos)[kEvictLoads]) {
-#pragma unroll
-        for (int j = 0; j < kEvictLoads; ++j) {
-            const int i = first + c * chunk_rows + j * rows + mine;
-            const int s = c < chunks && i < kept ? source(i) : -1;
-            // (a selection that is not the Selector's could lead anywhere)
-            if (s >= L || (s >= 0 && s < i)) err |= SFI_DEV_BAD_INDEX;
-            pos[j] = s >= L || s <= i ? -1 : s;  // rows that stay are not moved
+    auto fetch_pages = [&](int c) {  // of chunk c, whose source is in `src`
+        const int i = first + c * chunk_rows + tid;
+        // (a selection that is not the Selector's could lead anywhere)
+        if (src >= L || (src >= 0 && src < i)) err |= SFI_DEV_BAD_INDEX;
+        if (src >= L || src <= i) src = -1;  // (rows that stay are not moved)
+        if (src >= 0) {
+            src_page = ptab[src / kSubTokens];
+            dst_page = ptab[i / kSubTokens];
         }
     };
-    auto fetch_page = [&](const int (&pos)[kEvictLoads], int (&page)[kEvictLoads]) {
-#pragma unroll
-        for (int j = 0; j < kEvictLoads; ++j) page[j] = pos[j] >= 0 ? ptab[pos[j] / kSubTokens] : -1;
+    auto write_table = [&](int c) {
+        int2 e = make_int2(-1, -1);
+        if (src >= 0) {
+            const int i = first + c * chunk_rows + tid;
+            if ((uint32_t)src_page >= (uint32_t)p.num_pages || (uint32_t)dst_page >= (uint32_t)p.num_pages)
+                err |= SFI_DEV_BAD_PAGE;
+            else
+                e = make_int2((src_page * p.hkv + kvh) * kSubTokens + src % kSubTokens,
+                              (dst_page * p.hkv + kvh) * kSubTokens + i % kSubTokens);
+        }
+        table[c % kEvictTables][tid] = e;
     };
-    // Which rows of the chunks in the ring are moved: bit stage * kEvictLoads + j.
-    uint32_t moved = 0;
-    auto issue = [&](int c, const int (&pos)[kEvictLoads], const int (&page)[kEvictLoads]) {
-        const int st = c % kEvictStages;
+    // chunk 0's rows, the pages of chunk 1 and the positions of chunk 2 before the loop
+    src = fetch_pos(0);
+    next = fetch_pos(1);
+    fetch_pages(0);
+    write_table(0);
+    src = next;
+    next = fetch_pos(2);
+    fetch_pages(1);
+    __syncthreads();
+    for (int c = 0; c < chunks + kEvictStages - 1; ++c) {
+        // chunk c is requested, chunk c - (stages - 1) is written; the rows of chunk c + 1 are put down, the pages of
+        // c + 2 and the positions of c + 3 are on their way
+        write_table(c + 1);
+        src = next;
+        next = fetch_pos(c + 3);
+        fetch_pages(c + 2);
+        if (c < chunks) {
 #pragma unroll
-        for (int j = 0; j < kEvictLoads; ++j) {
-            const uint32_t bit = 1u << (st * kEvictLoads + j);
-            moved &= ~bit;
-            if (pos[j] >= 0) {
-                const char *from = at(page[j], pos[j]);
-                if (from) {
-                    moved |= bit;
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&s_ring[st][j][tid])),
-                                 "l"(from)
+            for (int j = 0; j < kEvictLoads; ++j) {
+                const int from = table[c % kEvictTables][j * rows + mine].x;
+                if (from >= 0)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&ring[c % kEvictStages][j][tid])),
+                                 "l"(pool + (int64_t)from * row_bytes)
                                  : "memory");
-                }
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    fetch_pos(0, src_pos);
-    fetch_pos(1, next_pos);
-    fetch_page(src_pos, src_page);
-    int dst_page[kEvictLoads];
-    auto fetch_dst = [&](int c) {
-#pragma unroll
-        for (int j = 0; j < kEvictLoads; ++j) {
-            const int i = first + c * chunk_rows + j * rows + mine;
-            dst_page[j] = c < chunks && i < kept ? ptab[i / kSubTokens] : -1;
-        }
-    };
-    fetch_dst(0);
-    for (int c = 0; c < chunks + kEvictStages - 1; ++c) {
-        // chunk c is requested, chunk c - (stages - 1) is written
-        int pos[kEvictLoads], page[kEvictLoads];
-#pragma unroll
-        for (int j = 0; j < kEvictLoads; ++j) pos[j] = src_pos[j], page[j] = src_page[j], src_pos[j] = next_pos[j];
-        fetch_page(src_pos, src_page);
-        fetch_pos(c + 2, next_pos);
-        issue(c, pos, page);
         const int done = c - (kEvictStages - 1);
-        if (done < 0) continue;
         asm volatile("cp.async.wait_group %0;" ::"n"(kEvictStages - 1) : "memory");
-        __syncthreads();  // every thread's reads up to this chunk have arrived
-        const int st = done % kEvictStages;
-        int to_page[kEvictLoads];
-#pragma unroll
-        for (int j = 0; j < kEvictLoads; ++j) to_page[j] = dst_page[j];
-        fetch_dst(done + 1);
+        __syncthreads();  // every thread's reads up to chunk `done` have arrived; the rows of chunk c + 1 are there
+        if (done < 0) continue;
 #pragma unroll
         for (int j = 0; j < kEvictLoads; ++j) {
-            if (!((moved >> (st * kEvictLoads + j)) & 1u)) continue;
-            const int i = first + done * chunk_rows + j * rows + mine;
-            char *to = at(to_page[j], i);
-            if (to) st_v4(to, s_ring[st][j][tid]);
+            const int to = table[done % kEvictTables][j * rows + mine].y;
+            if (to >= 0) st_v4(pool + (int64_t)to * row_bytes, ring[done % kEvictStages][j][tid]);
         }
     }
     if (err) report(p.dev_status, err);
@@ -329,7 +324,10 @@ cudaError_t launch_kv_evict(const EvictParams &p, const TopkParams &select, int 
     if (sms <= 0) return cudaErrorInvalidDevice;
     // No row has more candidates than the weights' stride leaves.
     const int64_t most = p.mass_stride - p.sink - p.recent;
-    cudaError_t e;
+    constexpr int kSmem = kEvictThreads * (kEvictStages * kEvictLoads * 16 + kEvictTables * 8);
+    static std::atomic<uint64_t> configured{0};
+    cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kv_evict_kernel), kSmem, configured);
+    if (e != cudaSuccess) return e;
     if (most <= 256 * kSelectEach)
         e = launch_select<256>(p, select, batch, stream);
     else if (most <= 1024 * kSelectEach)
@@ -345,6 +343,7 @@ cudaError_t launch_kv_evict(const EvictParams &p, const TopkParams &select, int 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * parts + 1), (unsigned)p.hkv, (unsigned)batch);
     cfg.blockDim = dim3(kEvictThreads);
+    cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
