@@ -18,7 +18,7 @@
 // keeps their reads in flight, and positions and page ids are fetched one and two chunks further ahead.
 // Weights go to a second buffer (they are also the Selector's input), in the same launch.
 // 16 requests of 8 x 2112 rows cut to 2048 (128-dim heads): 31 us, the choice 5 of them (264 MB, 38.9 us of HBM
-// time, but most of it stays in L2); 8 of 7001 to 16384 cut to about 1100: 32 us, the choice 13 of them
+// time, but most of it stays in L2); 8 of 7001 to 16384 cut to about 1100: 30 us, the choice 14 of them
 // (76 MB, 11.3 us).
 //
 // It writes bf16 pages, so it does not release its dependents early (see page_ops.cu).
@@ -37,12 +37,12 @@ constexpr int kEvictStages = 3, kEvictTables = 5;
 constexpr int kEvictLoads = 4;  // 16-byte pieces of a thread in a chunk
 
 constexpr int kSelectEach = 16;        // keys of a thread
-constexpr uint32_t kNoCandidate = 0xffffffffu;  // above +infinity's key, and never chosen
+constexpr uint32_t kNoCandidate = 0u;  // below every key
 
 // Ascending keys: -0 as +0, NaN below all.
 __device__ __forceinline__ uint32_t weight_key(float x) {
     uint32_t u = __float_as_uint(x);
-    if ((u & 0x7fffffffu) > 0x7f800000u) return 0u;
+    if ((u & 0x7fffffffu) > 0x7f800000u) return 1u;
     if (u == 0x80000000u) u = 0u;
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
@@ -53,9 +53,9 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams p, int32_t *idx_out, int32_t *count_out) {
     constexpr int kWarps = THREADS / 32;
-    // Long rows have a counter for each bin and lane, so that a warp's atomics hit 32 banks (64 units of up to 16000
-    // candidates: 15.6 us, with one counter per bin 19); short ones need not clear and add up that many (9 and 10.7).
-    constexpr int kCopies = THREADS == 1024 ? 32 : 1;
+    // Long rows have four counters for each bin, so that fewer of a warp's atomics meet in one (8 requests of up to 16384
+    // rows, the whole call: 30.2 us; with 8, 16 and 32 counters, which have to be added up, 30.8, 31.6 and 31.9).
+    constexpr int kCopies = THREADS == 1024 ? 4 : 1;
     __shared__ uint32_t s_hist[256 * kCopies];
     __shared__ uint32_t s_bin[256];
     __shared__ uint32_t s_prefix, s_rem, s_in;
@@ -88,16 +88,18 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams
 #pragma unroll
     for (int j = 0; j < kSelectEach; ++j)
         key[j] = first + 32 * j + lane < n ? weight_key(__uint_as_float(key[j])) : kNoCandidate;
-    // the bits of the smallest kept key, from the top; `rem` of the keys that share them are kept
-    uint32_t prefix = 0, rem = (uint32_t)keep, mask = 0;
+    // The bits of the smallest kept key, from the top: the keys that share them are those in [low, high], `rem` of
+    // them are kept.
+    uint32_t low = 1u, high = 0xffffffffu, rem = (uint32_t)keep;
+    uint32_t prefix = 0;
+    bool whole = false;  // all of them are
     for (int i = tid; i < 256 * kCopies; i += THREADS) s_hist[i] = 0;
     __syncthreads();
     for (int pass = 0; pass < 4; ++pass) {
         const int shift = 24 - 8 * pass;
 #pragma unroll
         for (int j = 0; j < kSelectEach; ++j) {
-            const bool in = key[j] != kNoCandidate && (key[j] & mask) == prefix;
-            if (in) atomicAdd(&s_hist[((key[j] >> shift) & 255u) * kCopies + (lane & (kCopies - 1))], 1u);
+            if (key[j] >= low && key[j] <= high) atomicAdd(&s_hist[((key[j] >> shift) & 255u) * kCopies + (lane & (kCopies - 1))], 1u);
         }
         __syncthreads();
         {
@@ -132,40 +134,57 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams
                 uint32_t at = above;
                 int i = 0;
                 for (; at + h[i] < rem; ++i) at += h[i];
-                s_prefix = prefix | (uint32_t)(255 - 8 * lane - i) << shift;
+                s_prefix = (uint32_t)(255 - 8 * lane - i) << shift;
                 s_rem = rem - at;
                 s_in = h[i];
             }
         }
         __syncthreads();
-        prefix = s_prefix;
+        // (bits above this digit are the same in low and high)
+        prefix |= s_prefix;
         rem = s_rem;
-        mask |= 255u << shift;
-        if (s_in == rem) break;  // all that share these bits are kept
+        low = max(prefix, 1u);
+        high = prefix | ((1u << shift) - 1u);
+        whole = s_in == rem;
+        if (whole) break;
     }
-    // ranks in the order of positions: kept ones are above the prefix, or share it and are among its first `rem`
+    // ranks in the order of positions: kept ones are above `high`, or in [low, high] and among its first `rem`
+    const uint32_t lower = (1u << lane) - 1u;
+    if (whole) {
+        int mine = 0;
+#pragma unroll
+        for (int j = 0; j < kSelectEach; ++j) mine += key[j] >= low;
+        mine = __reduce_add_sync(0xffffffffu, mine);
+        if (lane == 0) s_count[warp].x = mine;
+        __syncthreads();
+        int at = __reduce_add_sync(0xffffffffu, lane < warp ? s_count[lane].x : 0);
+#pragma unroll
+        for (int j = 0; j < kSelectEach; ++j) {
+            const bool take = key[j] >= low;
+            const uint32_t taken = __ballot_sync(0xffffffffu, take);
+            if (take) out[at + __popc(taken & lower)] = p.sink + first + 32 * j + lane;
+            at += __popc(taken);
+        }
+        return;
+    }
     int above = 0, equal = 0;
 #pragma unroll
     for (int j = 0; j < kSelectEach; ++j) {
-        const bool valid = key[j] != kNoCandidate;
-        above += __popc(__ballot_sync(0xffffffffu, valid && (key[j] & mask) > prefix));
-        equal += __popc(__ballot_sync(0xffffffffu, valid && (key[j] & mask) == prefix));
+        above += key[j] > high;
+        equal += key[j] >= low && key[j] <= high;
     }
+    above = __reduce_add_sync(0xffffffffu, above);
+    equal = __reduce_add_sync(0xffffffffu, equal);
     if (lane == 0) s_count[warp] = make_int2(above, equal);
     __syncthreads();
-    int2 before = lane < min(warp, kWarps) ? s_count[lane] : make_int2(0, 0);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        before.x += __shfl_xor_sync(0xffffffffu, before.x, off);
-        before.y += __shfl_xor_sync(0xffffffffu, before.y, off);
-    }
-    const uint32_t lower = (1u << lane) - 1u;
-    int at = before.x + min(before.y, (int)rem), seen = before.y;
+    const int2 before = lane < warp ? s_count[lane] : make_int2(0, 0);
+    int seen = __reduce_add_sync(0xffffffffu, before.y);
+    int at = __reduce_add_sync(0xffffffffu, before.x) + min(seen, (int)rem);
 #pragma unroll
     for (int j = 0; j < kSelectEach; ++j) {
-        const bool valid = key[j] != kNoCandidate, same = valid && (key[j] & mask) == prefix;
+        const bool same = key[j] >= low && key[j] <= high;
         const uint32_t same_all = __ballot_sync(0xffffffffu, same);
-        const bool take = valid && ((key[j] & mask) > prefix || (same && seen + __popc(same_all & lower) < (int)rem));
+        const bool take = key[j] > high || (same && seen + __popc(same_all & lower) < (int)rem);
         const uint32_t taken = __ballot_sync(0xffffffffu, take);
         if (take) out[at + __popc(taken & lower)] = p.sink + first + 32 * j + lane;
         at += __popc(taken);
