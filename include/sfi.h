@@ -757,13 +757,13 @@ SFI_API size_t sfi_page_workspace_size(const sfi_page_map *map);
  * overlap inputs.
  * Device errors: SFI_DEV_BAD_INDEX (a request id outside [0, num_reqs)), SFI_DEV_BAD_LEN (n_r < 0,
  * n_r > num_tokens, L_r < n_r or L_r beyond the page table): that request is skipped.
- * SFI_DEV_BAD_PAGE, SFI_DEV_TIMEOUT (the tokens whose block reads
- * that page are not written: up to 256 / G tokens of a KV head's query heads).
+ * SFI_DEV_BAD_PAGE, SFI_DEV_TIMEOUT (the tokens whose block reads that page are not written: up to
+ * 256 / G tokens of a KV head's query heads).
  */
 SFI_API sfi_status sfi_window_attn(const sfi_attn_shape *shape, const sfi_paged_kv *kv, int32_t sink, int32_t recent,
                                    const void *q, int64_t q_stride, int32_t num_reqs, int32_t num_tokens,
-                                   const int32_t *new_lens, void *out, float *lse, const int32_t *req_ids, int32_t batch, int32_t *dev_status,
-                                   void *stream);
+                                   const int32_t *new_lens, void *out, float *lse, const int32_t *req_ids,
+                                   int32_t batch, int32_t *dev_status, void *stream);
 
 /*
  * sfi_attn_mass - the attention weight that the new tokens gave to each position, summed over them
@@ -775,7 +775,7 @@ SFI_API sfi_status sfi_window_attn(const sfi_attn_shape *shape, const sfi_paged_
  *   q, q_stride, num_reqs, num_tokens, new_lens : as for sfi_window_attn
  *   lse  : fp32 [B][num_tokens][Hq], of the attention of these tokens
  *   mass : fp32 [B][Hkv][mass_stride], mass_stride >= max L
- * The result does not depend on the order in which the GPU runs the call.
+ * The result does not depend on the order in which the GPU runs the call. A request may appear once in it.
  * Device errors: SFI_DEV_BAD_INDEX, SFI_DEV_BAD_LEN (as for sfi_window_attn, or L_r > mass_stride):
  * that request is skipped. SFI_DEV_BAD_PAGE, SFI_DEV_TIMEOUT (that block of 256 positions is not
  * written).
@@ -796,11 +796,12 @@ SFI_API sfi_status sfi_attn_mass(const sfi_attn_shape *shape, const sfi_paged_kv
  * with other holders).
  *   mass      : fp32 [B][Hkv][mass_stride], mass_stride >= max L
  *   k_per_req : int32 [B], 0 <= k_r <= k_cap
- *   idx_out   : int32 [B][Hkv][k_cap] (NULL when k_cap is 0), the kept candidates' former positions, ascending; entries past
- *               the count are not written
+ *   idx_out   : int32 [B][Hkv][k_cap] (NULL when k_cap is 0), the kept candidates' former positions,
+ *               ascending; entries past the count are not written
  *   count_out : int32 [B], min(k_r, candidates)
  *   mass_out  : fp32 [B][Hkv][mass_stride] or NULL: the kept rows' mass, in their new order; not mass
- *   new_lens  : int32 [B], the rows that are left
+ *   new_lens  : int32 [B], the rows that are left; not seq_lens
+ * A request may appear once in a call.
  * Limits: as for sfi_select_topk.
  * Device errors: SFI_DEV_BAD_LEN (L_r < 0, beyond the page table or > mass_stride), SFI_DEV_K_OVERFLOW
  * (that request is skipped), SFI_DEV_BAD_PAGE (that row stays as it was).

@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kStepThreads, 2)
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = fast_exp2(fmaf(x[h][i], p.scale_log2, -base));
             l[h] = l[h] * alpha[h] + ((w[0] + w[1]) + (w[2] + w[3]));
-            // bf16 weights (2^-9 of each at most): the output has no more bits
+            // bf16 weights (off by 2^-8 of each at most): the output has no more bits
             pa[h][0] = pack_bf16x2(w[0], w[1]);
             pa[h][1] = pack_bf16x2(w[2], w[3]);
         }

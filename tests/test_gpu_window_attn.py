@@ -95,3 +95,14 @@ def test_prompts(heads, sink, recent):
     assert st == 0
     some = set(range(0, 300, 37)) | {0, 1, 15, 16, 17, 31, 32, 63, 64, 127, 128, 129, 255, 256, 299}
     _check(c, q, new, sink, recent, out, lse, tokens=some)
+
+
+@pytest.mark.parametrize("heads", [(8, 1, 64), (4, 4, 128)])
+def test_prompts_of_other_groups(heads):
+    """Eight heads of a group in 64 dims, and none shared in 128."""
+    t, new, lens = 140, [140, 33, 65, 2], [140, 400, 65, 1000]
+    c = ref.Cache(31, lens, *heads, fill=float("nan"))
+    q = ref.queries(32, len(lens), t, heads[0], heads[2])
+    out, lse, st = _run(c, q, new, 20, 70)
+    assert st == 0
+    _check(c, q, new, 20, 70, out, lse)

@@ -206,3 +206,15 @@ def test_verification_shapes(host, wrong):
     with pytest.raises(ValueError):
         _verify({**a, **wrong})
     assert len(host) == 3
+
+
+def test_more_work_than_a_launch_can_name(lib):
+    heads = 65535
+    many = dict(shape=_shape(heads, heads), q_stride=heads * 128, num_reqs=1, batch=65535)
+    assert lib.sfi_window_attn(*{**WINDOW, **many, "num_tokens": 257}.values()) == UNSUPPORTED
+    assert lib.sfi_attn_mass(*{**MASS, **many}.values()) == UNSUPPORTED
+    more = dict(shape=_shape(65536, 65536), q_stride=65536 * 128)
+    assert lib.sfi_window_attn(*{**WINDOW, **more}.values()) == UNSUPPORTED
+    assert lib.sfi_attn_mass(*{**MASS, **more}.values()) == UNSUPPORTED
+    assert lib.sfi_kv_evict(*{**EVICT, "shape": _shape(65536, 65536)}.values()) == UNSUPPORTED
+    assert lib.sfi_verify_tokens(*{**VERIFY, "batch": (1 << 24) + 1}.values()) == UNSUPPORTED
