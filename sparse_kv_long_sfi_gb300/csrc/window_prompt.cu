@@ -83,31 +83,6 @@ struct PromptOrder {
     int units, group, tail, tiles;
 };
 
-// Takes over a CTA of this grid that has not begun (its index goes to x), if there is one. One thread; `answer`
-// is 16 bytes of shared memory, `bar` an mbarrier of count 1 in its phase `parity`. Not called again once it failed.
-__device__ __forceinline__ bool take_next_cta(void *answer, uint64_t *bar, uint32_t parity, uint32_t &x, bool &late) {
-    fence_async_shared();  // the last answer has been read
-    mbar_arrive_expect_tx(bar, 16);
-    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                     smem_u32(answer)),
-                 "r"(smem_u32(bar))
-                 : "memory");
-    late = !tc_wait_one(bar, parity);
-    if (late) return false;
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .b128 a;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
-        "ld.shared.b128 a, [%2];\n\t"
-        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t"
-        "mov.u32 %1, 0;\n\t"
-        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, a;\n\t}"
-        : "=r"(ok), "=r"(x)
-        : "r"(smem_u32(answer))
-        : "memory");
-    return ok != 0;
-}
-
 }  // namespace
 
 template <int D>

@@ -128,3 +128,19 @@ def test_a_nan_that_no_query_sees_stays_alone():
     got, st = _run(c, q, lse, new, sink, recent, mass, 1.0)
     assert st == 0
     _check(got, *want, lens, mass)
+
+
+@pytest.mark.parametrize("heads,d_lens", [((8, 2, 64), (300, 560)), ((4, 2, 128), (128, 400))])
+def test_more_blocks_than_the_gpu_holds(heads, d_lens):
+    """Many requests in a call of more than 128 query rows: a CTA works through several blocks, of all lengths."""
+    t = 160 * heads[1] // heads[0]
+    g = torch.Generator().manual_seed(21)
+    lens = torch.randint(*d_lens, (60,), generator=g).tolist()
+    new = [0 if r % 11 == 3 else min(t, lens[r]) - r % 7 for r in range(60)]
+    c, q, lse = _problem(22, lens, heads, new, 5, 200, t)
+    mass = torch.rand(60, heads[1], max(lens) + 5, generator=g)
+    got, st = _run(c, q, lse, new, 5, 200, mass, 0.5)
+    assert st == 0
+    _check(got, *_expected(c, q, lse, new, 5, 200, mass, 0.5), lens, mass)
+    again, _ = _run(c, q, lse, new, 5, 200, mass, 0.5)
+    assert torch.equal(got, again)
