@@ -16,8 +16,9 @@
 //    bf16 or fp32), so O is hardly ever rescaled; that is done by the softmax threads themselves.
 //  * One warp fetches Q, K and V, page by page, by TMA with the 128-byte swizzle, K and V into a ring of
 //    tiles; a thread per tile issues its matrix instructions.
-//  * A CTA that is done takes over one that has not begun (cluster launch control), so that the next
+//  * A CTA that is nearly done takes over one that has not begun (cluster launch control), so that the next
 //    item's Q and first keys are on their way, and its first scores formed, while the last rows are written.
+//    (Taken when an item begins, the longest had others behind them: ragged chunks 267 us instead of 245.)
 // P is rounded to bf16 for the second product (2^-8 of each weight at most, which averages out over
 // the keys); sums of P are taken before that, in fp32.
 //
@@ -25,8 +26,8 @@
 // bytes of a page's tail) are zeroed in shared memory, and a row whose output is not finite is computed
 // again key by key, from the positions it sees alone.
 // 16/8/128 heads: two prompts of 8192 tokens with window 1024 138 us (53% of the measured bf16 rate: 1280 keys are
-// multiplied for 1088 that are seen, and a CTA's first and last steps are masked), one causal prompt of 8192 208 us (70%);
-// 32/8/128 heads, 16384 tokens: 1.48 ms (79%). In the loop a step of 256 rows x 128 keys takes 3080 cycles (84%).
+// multiplied for 1088 that are seen, and a CTA's first and last steps are masked), one causal prompt of 8192 206 us (71%);
+// 32/8/128 heads, 16384 tokens: 1.47 ms (80%). In the loop a step of 256 rows x 128 keys takes 3080 cycles (84%).
 #include <algorithm>
 #include <atomic>
 
@@ -48,6 +49,7 @@ constexpr float kGrowth = 8.f;       // the running maximum moves when a score p
 constexpr uint32_t kTmemColumns = 512;
 constexpr int64_t kTogether = 16 << 20, kTailTogether = 48 << 20;
 constexpr int kTailWaves = 3;
+constexpr int kAhead = 2;  // steps of an item that are left to load when the next is taken
 constexpr int kItemReaders = 8 + 3;  // softmax warps, the copy warp, the matrix threads
 
 template <int D>
@@ -96,7 +98,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     uint8_t *ring = smem + 2 * T::kBytes;
     __shared__ __align__(16) uint4 s_answer;
     __shared__ __align__(8) uint64_t answered, item_full[2], item_read[2];
-    __shared__ __align__(8) uint64_t q_full[2], q_free, loads_done, tail_ready, tail_done;
+    __shared__ __align__(8) uint64_t q_full[2], q_free, loads_done, near_end, tail_ready, tail_done;
     __shared__ __align__(8) uint64_t full[T::kStages], empty[T::kStages];
     __shared__ __align__(8) uint64_t s_full[2], p_ready[2][2], o_done[2], turn[2];
     __shared__ PromptItem s_item[2];
@@ -110,6 +112,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         mbar_init(&answered, 1);
         mbar_init(&q_free, 8);
         mbar_init(&loads_done, 1);
+        mbar_init(&near_end, 1);
         mbar_init(&tail_ready, 1);
         mbar_init(&tail_done, 1);
         for (int i = 0; i < T::kStages; ++i) {
@@ -172,6 +175,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 };
                 int next = page_of(0);
                 for (int j = 0; j < w.steps && fine; ++j) {
+                    if (lane == 0 && j == max(0, w.steps - kAhead)) mbar_arrive(&near_end);
                     const int page = next;
                     next = j + 1 < w.steps ? page_of(j + 1) : -1;
                     const bool listed = j * kTilePages + (lane & 7) < w.span.pages;
@@ -334,9 +338,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             };
             PromptItem it = publish(0);
             for (int i = 0; it.kvh >= 0; ++i) {
+                const PromptWork w(it, p, per_tile);
+                // (not before this one is near its end: the longest should have none behind them)
+                if (w.steps > 0) fine = tc_wait(&near_end, loaded & 1);
+                if (!fine) break;
                 const PromptItem next = publish(i + 1);
                 if (__any_sync(0xffffffffu, !fine)) break;
-                const PromptWork w(it, p, per_tile);
                 it = next;
                 if (w.steps == 0) continue;
                 // what lies behind the last position must not meet a zero weight as a NaN
@@ -561,8 +568,9 @@ cudaError_t launch_prompt(const WindowMaps &maps, const WindowParams &p, int bat
     const int64_t units = (int64_t)batch * p.hkv, items = units * tiles;
     // A few units at a time keep their K and V in L2 (kTogether bytes at their longest), but the last of them would leave
     // long tiles to the end: the units with the last kTailWaves CTAs per SM (if L2 holds them) are one group.
-    // Four ragged chunks of 8 heads: 258 us with small groups alone, 293 with large ones, 256 with both; a prompt of 8192:
-    // 250, 211 and 208.
+    // As items are taken late this matters little: between groups of 1 and 64 MB and one and six waves a prompt of 8192
+    // takes 204 to 210 us and ragged chunks 245 to 254; but 4 x 4096 tokens of 8/2/64 heads take 114 with one wave, 103
+    // with two and 99 with three.
     const int64_t bytes = (int64_t)p.max_pages * kSubTokens * D * 4;
     const int sms = sm_count_current_device();
     const int group = (int)std::max<int64_t>(1, std::min(units, kTogether / bytes));
