@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     uint8_t *ring = smem + 2 * T::kBytes;
     __shared__ __align__(16) uint4 s_answer;
     __shared__ __align__(8) uint64_t answered, item_full[2], item_read[2];
-    __shared__ __align__(8) uint64_t q_full[2], q_free, loads_done, near_end, tail_ready, tail_done;
+    __shared__ __align__(8) uint64_t q_full[2], q_free, loads_done, near_end, tail_ready, tail_done[2];
     __shared__ __align__(8) uint64_t full[T::kStages], empty[T::kStages];
     __shared__ __align__(8) uint64_t s_full[2], p_ready[2][2], o_done[2], turn[2];
     __shared__ PromptItem s_item[2];
@@ -114,7 +114,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         mbar_init(&loads_done, 1);
         mbar_init(&near_end, 1);
         mbar_init(&tail_ready, 1);
-        mbar_init(&tail_done, 1);
         for (int i = 0; i < T::kStages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 2);
@@ -123,6 +122,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             mbar_init(&item_full[i], 1);
             mbar_init(&item_read[i], kItemReaders);
             mbar_init(&q_full[i], 1);
+            mbar_init(&tail_done[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_ready[i][0], kTileRows);
             mbar_init(&p_ready[i][1], kTileRows);
@@ -224,8 +224,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 mma_commit(&s_full[t]);
             };
             auto arrived = [&](int use) { return tc_wait_one(&full[use % T::kStages], (use / T::kStages) & 1); };
-            // uses of the ring, items, and this tile's items, steps and turns so far
-            int base = 0, loaded = 0, mine = 0, step = 0, phase = 0;
+            // uses of the ring, and this tile's items, steps and turns so far
+            int base = 0, mine = 0, step = 0, phase = 0;
             bool fine = true;
             for (int i = 0; fine; ++i) {
                 fine = tc_wait_one(&item_full[i & 1], (i >> 1) & 1);
@@ -235,10 +235,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 if (it.kvh < 0) break;
                 const PromptWork w(it, p, per_tile);
                 if (w.steps == 0) continue;
-                const int first = base, item = loaded;
+                const int first = base;
                 base += 2 * w.steps;
-                ++loaded;
                 if (t >= w.tiles) continue;
+                const int own = mine++;
                 // With two tiles the threads take turns: interleaved, both tiles' instructions would end together, and
                 // both softmaxes would run while the tensor cores wait (a step then took 4400 cycles instead of 3000).
                 auto my_turn = [&]() {
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     if (w.tiles == 2) mbar_arrive(&turn[t ^ 1]);
                 };
                 // K of step j is use first + 2 j of the ring, V the one behind it
-                fine = tc_wait_one(&q_full[t], mine++ & 1) && arrived(first) && my_turn();
+                fine = tc_wait_one(&q_full[t], own & 1) && arrived(first) && my_turn();
                 if (!fine) break;
                 tc_fence_after();
                 scores(first % T::kStages);
@@ -263,7 +263,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                         fine = arrived(first + 2 * j + 2);
                     } else {
                         if (t == 0) mbar_arrive(&tail_ready);  // V's last tile is there
-                        fine = tc_wait_one(&tail_done, item & 1);
+                        // (a barrier for each tile: an item of one tile could go by meanwhile, and a phase of a common
+                        // one with it, whose parity this thread would then wait for in vain)
+                        fine = tc_wait_one(&tail_done[t], own & 1);
                     }
                     fine = fine && tc_wait_one(&p_ready[t][0], step & 1) && my_turn();
                     if (!fine) break;
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                         *reinterpret_cast<int4 *>(ring + slot * T::kBytes + h * T::kHalfBytes + c * 16) = make_int4(0, 0, 0, 0);
                 fence_async_shared();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&tail_done);
+                if (lane < w.tiles) mbar_arrive(&tail_done[lane]);
             }
             if (!fine) report(p.dev_status, SFI_DEV_TIMEOUT);
         }
