@@ -23,8 +23,8 @@
 // the keys); sums of P are taken before that, in fp32.
 //
 // A zero weight times a NaN is a NaN in a matrix product, so V's rows behind the last position (stale
-// bytes of a page's tail) are zeroed in shared memory, and a row whose output is not finite is computed
-// again key by key, from the positions it sees alone.
+// bytes of a page's tail) are zeroed in shared memory, and a row whose output is not finite, because of what
+// it does not see, is computed again from the positions it sees alone (mend_rows).
 // 16/8/128 heads: two prompts of 8192 tokens with window 1024 138 us (53% of the measured bf16 rate: 1280 keys are
 // multiplied for 1088 that are seen, and a CTA's first and last steps are masked), one causal prompt of 8192 206 us (71%);
 // 32/8/128 heads, 16384 tokens: 1.47 ms (80%). In the loop a step of 256 rows x 128 keys takes 3080 cycles (84%).
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     __shared__ __align__(8) uint64_t q_full[2], q_free, loads_done, near_end, tail_ready, tail_done[2];
     __shared__ __align__(8) uint64_t full[T::kStages], empty[T::kStages];
     __shared__ __align__(8) uint64_t s_full[2], p_ready[2][2], o_done[2], turn[2];
-    __shared__ PromptItem s_item[2];
+    __shared__ PromptItem s_item[2], s_mine[8];  // s_mine: of each softmax warp, for what hardly ever happens at its end
     __shared__ uint32_t s_tmem;
     __shared__ int s_bad[2];  // of an item (even, odd): it writes no output
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -381,7 +381,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             if (!fine) break;
             const PromptItem it = s_item[i & 1];
             __syncwarp();
-            if (lane == 0) mbar_arrive(&item_read[i & 1]);
+            if (lane == 0) {
+                mbar_arrive(&item_read[i & 1]);
+                s_mine[warp] = it;
+            }
             if (it.kvh < 0) break;
             const PromptWork w(it, p, per_tile);
             const int use0 = base, item = loaded;
@@ -539,14 +542,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 odd |= big >= 0x7f800000u;
             }
             if (write && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-            __syncwarp();
-            uint32_t again = __ballot_sync(0xffffffffu, odd && write);
-            while (again) {
-                const int from = __ffs(again) - 1;
-                again &= again - 1;
-                window_row<D>(p, it.r, __shfl_sync(0xffffffffu, token, from), __shfl_sync(0xffffffffu, head, from),
-                              __shfl_sync(0xffffffffu, pos, from), __shfl_sync(0xffffffffu, m, from),
-                              __shfl_sync(0xffffffffu, l, from), 0, D);
+            if (__any_sync(0xffffffffu, odd && write)) {
+                __syncwarp();
+                const PromptItem own = s_mine[warp];
+                const PromptWork all(own, p, per_tile);
+                mend_rows<D>(p, own.r, own.kvh, own.L, own.n, all.p0, all.p1,
+                             (own.tok0 << shift) + t * kTileRows + (warp & 3) * 32, odd && write, m, l, 0, 32 * (D / 4));
             }
             tc_fence_before();  // O has been read: the next item's first weights let it be overwritten
         }

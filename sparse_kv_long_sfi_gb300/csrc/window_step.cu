@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(kStepThreads, 2)
     __shared__ float s_pm[kStepMaxCluster][kMaxRows], s_pl[kStepMaxCluster][kMaxRows];  // per CTA of the cluster
     __shared__ float s_scale[kMaxRows], s_top[kMaxRows], s_sum[kMaxRows];
     __shared__ float s_weight[kStepMaxCluster][kMaxRows];
+    __shared__ uint32_t s_odd;  // rows of this CTA's share that are not finite
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ctas = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
     cluster_arrive_relaxed();
@@ -235,6 +236,7 @@ __global__ void __launch_bounds__(kStepThreads, 2)
         s_l[warp][g] = l[0];
         s_l[warp][g + 8] = l[1];
     }
+    if (threadIdx.x == 0) s_odd = 0;
     cluster_wait();  // every CTA of the cluster has begun
     const bool failed = __syncthreads_or(bad || late);
     // this CTA's part of each share goes to the CTA that writes it
@@ -295,38 +297,31 @@ __global__ void __launch_bounds__(kStepThreads, 2)
         }
     }
     __syncthreads();
-    for (int i0 = rank * share; i0 < min(pieces, (rank + 1) * share); i0 += kStepThreads) {
-        const int i = i0 + (int)threadIdx.x;
-        const bool have = i < min(pieces, (rank + 1) * share);
-        const int row = have ? i / (D / 4) : 0, d = (i % (D / 4)) * 4;
+    const int piece1 = min(pieces, (rank + 1) * share);
+    for (int i = rank * share + (int)threadIdx.x; i < piece1; i += kStepThreads) {
+        const int row = i / (D / 4), d = (i % (D / 4)) * 4;
         const float scale = s_scale[row];
-        const bool write = have && !(scale < 0.f);
-        bool odd = false;
-        if (write) {
-            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int c = 0; c < ctas; ++c) {
-                const float f = s_weight[c][row];
-                const float4 v = *reinterpret_cast<const float4 *>(recv + (c * share + i - rank * share) * 4);
-                sum.x += v.x * f;
-                sum.y += v.y * f;
-                sum.z += v.z * f;
-                sum.w += v.w * f;
-            }
-            odd = n > 1 && !(fabsf(sum.x) + fabsf(sum.y) + fabsf(sum.z) + fabsf(sum.w) < INFINITY);
-            const int64_t at = ((int64_t)r * p.tokens + row / G) * p.hq + (int64_t)kvh * G + row % G;
-            *reinterpret_cast<uint2 *>(p.out + at * D + d) =
-                make_uint2(pack_bf16x2(sum.x * scale, sum.y * scale), pack_bf16x2(sum.z * scale, sum.w * scale));
+        if (scale < 0.f) continue;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < ctas; ++c) {
+            const float f = s_weight[c][row];
+            const float4 v = *reinterpret_cast<const float4 *>(recv + (c * share + i - rank * share) * 4);
+            sum.x += v.x * f;
+            sum.y += v.y * f;
+            sum.z += v.z * f;
+            sum.w += v.w * f;
         }
-        // (with several tokens a row may have met the NaN of a position that only later tokens see)
-        uint32_t again = __ballot_sync(0xffffffffu, odd);
-        while (again) {
-            const int from = __ffs(again) - 1;
-            again &= again - 1;
-            const int bad_row = __shfl_sync(0xffffffffu, row, from), bad_d = __shfl_sync(0xffffffffu, d, from);
-            window_row<D>(p, r, bad_row / G, kvh * G + bad_row % G, L - n + bad_row / G, s_top[bad_row], s_sum[bad_row],
-                          bad_d, bad_d + 4);
-        }
+        if (n > 1 && !(fabsf(sum.x) + fabsf(sum.y) + fabsf(sum.z) + fabsf(sum.w) < INFINITY)) atomicOr(&s_odd, 1u << row);
+        const int64_t at = ((int64_t)r * p.tokens + row / G) * p.hq + (int64_t)kvh * G + row % G;
+        *reinterpret_cast<uint2 *>(p.out + at * D + d) =
+            make_uint2(pack_bf16x2(sum.x * scale, sum.y * scale), pack_bf16x2(sum.z * scale, sum.w * scale));
     }
+    if (n == 1) return;
+    // (with several tokens a row may have met the NaN of a position that only later tokens see)
+    __syncthreads();
+    if (warp > 0 || s_odd == 0) return;
+    const int row = min(lane, rows - 1);
+    mend_rows<D>(p, r, kvh, L, n, L - n, L - 1, 0, lane < rows && (s_odd >> row & 1u), s_top[row], s_sum[row], rank * share, piece1);
 }
 
 namespace {

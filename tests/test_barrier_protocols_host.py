@@ -431,7 +431,7 @@ def test_the_kernel_has_a_tail_barrier_for_each_tile():
     here = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     with open(os.path.join(here, "sparse_kv_long_sfi_gb300", "csrc", "window_prompt.cu")) as f:
         source = f.read()
-    assert "tc_wait_one(&tail_done[t], own & 1)" in source and "if (lane < w.tiles) mbar_arrive(&tail_done[lane])" in source
+    assert "wait_one(&tail_done[t], own & 1)" in source and "if (lane < w.tiles) mbar_arrive(&tail_done[lane])" in source
 
 
 @pytest.mark.parametrize("last", [None] + WEIGHT_ROLES)
