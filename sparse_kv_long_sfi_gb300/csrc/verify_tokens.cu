@@ -31,10 +31,13 @@ constexpr int kVerifyRun = 128;                        // weights of a warp's ru
 constexpr int kVerifyBatch = 4;                        // runs of a warp whose loads are in flight together
 constexpr int kVerifyRuns = SFI_MAX_VOCAB / kVerifyCluster / kVerifyRun + kVerifyWarps;
 
-// A probability in units of 2^-56: NaN and values below zero are nothing, values above one are one. By shifts of
-// its significand (the conversion instruction to 64 bits made the call 65 us instead of 33).
+// What a given value counts as: NaN and values below zero are nothing, values above one are one.
+__device__ __forceinline__ float probability(float p) { return fminf(fmaxf(p, 0.f), 1.f); }
+
+// A probability in units of 2^-56, by shifts of its significand (the conversion instruction to 64 bits made the call
+// 65 us instead of 33).
 __device__ __forceinline__ int64_t fixed(float p) {
-    const uint32_t u = __float_as_uint(fminf(fmaxf(p, 0.f), 1.f));
+    const uint32_t u = __float_as_uint(probability(p));
     const uint64_t one = (uint64_t)((u & 0x7fffffu) | 0x800000u) << 33;  // as for [1, 2)
     return (int64_t)(one >> min(127u - (u >> 23), 63u));
 }
@@ -83,8 +86,8 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_tokens_kernel(const Ver
                 const int x = tok[t];
                 bad = x < 0 || x >= V;
                 if (!bad) {
-                    const float pt = p.target[((int64_t)r * (T + 1) + t) * p.target_stride + x];
-                    const float qt = p.draft ? p.draft[((int64_t)r * T + t) * p.draft_stride + x] : 1.f;
+                    const float pt = probability(p.target[((int64_t)r * (T + 1) + t) * p.target_stride + x]);
+                    const float qt = p.draft ? probability(p.draft[((int64_t)r * T + t) * p.draft_stride + x]) : 1.f;
                     // 24 by 24 bits: exact in fp64
                     ok = (double)p.u[(int64_t)r * (T + 1) + t] * (double)qt < (double)pt;
                 }
