@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictParams
     const int kvh = blockIdx.x;
     const int r = p.req_ids ? p.req_ids[blockIdx.y] : (int)blockIdx.y;
     const int L = p.seq_lens[r], k = p.k_per_req[r];
-    if (L < 0 || L > p.mass_stride || k < 0 || k > p.k_cap) return;
+    if (L < 0 || L > p.max_pages * kSubTokens || L > p.mass_stride || k < 0 || k > p.k_cap) return;
     const int n = (int)max((int64_t)0, (int64_t)L - p.recent - p.sink);  // at most THREADS * 16: the row's stride says so
     const int keep = min(k, n);
     if (kvh == 0 && tid == 0) count_out[r] = keep;
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kEvictThreads) kv_evict_kernel(const EvictPara
     const bool lead = tid == 0 && blockIdx.x == 0 && kvh == 0;
     const int L = p.seq_lens[r];
     const int k = p.k_per_req[r];
-    // (the Selector has refused what is refused here for its own reasons; lengths are checked against the table here)
+    // (the choice has refused the same requests: nothing of theirs is written)
     const int64_t cand = (int64_t)L - p.recent - p.sink;
     if (L < 0 || L > p.max_pages * kSubTokens || L > p.mass_stride) {
         if (lead) report(p.dev_status, SFI_DEV_BAD_LEN);

@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kTopkThreads) select_topk_kernel(const TopkPar
     __syncthreads();
     auto drain = [&]() { mbar_wait_warp(&s_bar[0], 0); };  // the first copy has landed (bounded)
     const int L = p.seq_lens[r];
-    if (L < 0 || L > p.score_stride) {
+    if (L < 0 || L > p.max_len) {
         if (tid == 0 && kvh == 0) report(p.dev_status, SFI_DEV_BAD_LEN);
         drain();
         return;

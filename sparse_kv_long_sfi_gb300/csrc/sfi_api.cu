@@ -664,7 +664,7 @@ sfi_status sfi_select_topk(const float *scores, int64_t score_stride, int32_t nu
     if (batch == 0) return SFI_OK;
     sfi::TopkParams p{};
     p.scores = scores;
-    p.score_stride = score_stride;
+    p.score_stride = p.max_len = score_stride;
     p.hkv = num_kv_heads;
     p.seq_lens = seq_lens;
     p.sink = sink;
@@ -732,7 +732,7 @@ sfi_status sfi_select_compact(const sfi_attn_shape *shape, const sfi_paged_kv *k
     if (batch == 0) return SFI_OK;
     sfi::TopkParams p{};
     p.scores = scores;
-    p.score_stride = score_stride;
+    p.score_stride = p.max_len = score_stride;
     p.hkv = shape->num_kv_heads;
     p.seq_lens = kv->seq_lens;
     p.sink = sink;

@@ -104,6 +104,7 @@ cudaError_t launch_attention_multi(int head_dim, int mode, const AttnMaps &maps,
 struct TopkParams {
     const float *scores;
     int64_t score_stride;
+    int64_t max_len;  // longer requests are refused (score_stride, or less where a page table ends before)
     int32_t hkv;
     const int32_t *seq_lens;
     int32_t sink, recent;

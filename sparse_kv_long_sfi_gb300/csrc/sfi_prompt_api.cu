@@ -118,6 +118,7 @@ sfi_status sfi_kv_evict(const sfi_attn_shape *shape, const sfi_paged_kv *kv, con
     sfi::TopkParams t{};
     t.scores = mass;
     t.score_stride = mass_stride;
+    t.max_len = std::min<int64_t>(mass_stride, (int64_t)kv->max_pages_per_req * sfi::kSubTokens);
     t.hkv = shape->num_kv_heads;
     t.seq_lens = kv->seq_lens;
     t.sink = sink;
