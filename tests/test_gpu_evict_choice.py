@@ -87,6 +87,35 @@ def _weights(kind, b, hkv, n, seed):
     return w
 
 
+KINDS = ["any", "few values", "all equal", "one digit", "special"]
+EDGES = [4095, 4096, 4097, 9000, 16383, 16384, 16385, 32768, 40001]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("candidates", EDGES)
+def test_rows_as_long_as_the_buffer(candidates, kind):
+    """The longest row fills the weights, on both sides of each choice's limit."""
+    n = candidates + SINK + RECENT
+    lens = [n, n - 1, max(100, n // 3)]
+    c = ref.Cache(81, lens, 2, 2, 64)
+    mass = _weights(kind, 3, 2, n, candidates)
+    for k in ([candidates // 8, 1000, 700], [candidates - 1, 1, 0]):
+        e = Evicted(c, mass, k)
+        assert e.status == 0
+        e.check()
+
+
+@pytest.mark.parametrize("width", [300, 4096 + SINK + RECENT + 1, 16384 + SINK + RECENT, 16384 + SINK + RECENT + 1, 70001])
+def test_short_rows_in_wide_buffers(width):
+    """What the buffer's width chooses makes no difference."""
+    lens = [0, 1, 36, 37, 100, 255, 300, 290]
+    c = ref.Cache(83, lens, 8, 2, 128)
+    mass = _weights("special", 8, 2, width, 5)
+    e = Evicted(c, mass, [5, 5, 5, 1, 20, 200, 100, 300])
+    assert e.status == 0
+    e.check()
+
+
 @pytest.mark.parametrize("width", [400, 9000, 20000])
 def test_nothing_of_a_refused_request_is_written(width):
     """Lengths beyond the table but within the weights, below zero; more rows than idx holds."""
@@ -104,3 +133,13 @@ def test_nothing_of_a_refused_request_is_written(width):
     e = Evicted(c, mass, [50, -1, 70, 80])
     assert e.status == 4
     e.check(skip=(1,))
+
+
+@pytest.mark.parametrize("more", [0, 1])
+def test_the_most_candidates(more):
+    """262144 candidates are taken, one more is not; the other request is cut all the same."""
+    n = 262144 + more + SINK + RECENT
+    c = ref.Cache(87, [n, 500], 1, 1, 64)
+    e = Evicted(c, _weights("any", 2, 1, n, 7), [3000, 100])
+    assert e.status == 4 * more
+    e.check(skip=(0,) if more else ())
