@@ -324,11 +324,12 @@ __global__ void __launch_bounds__(kPlanThreads) page_reserve_kernel(const PageMa
     const uint32_t lower32 = (1u << lane) - 1u;
     int found = 0;
     int c[2][kEach];
-    auto counts = [&](int base, int (&v)[kEach]) {  // (base < 0: past 32 bits, behind the last page)
+    auto counts = [&](int base, int (&v)[kEach]) {  // (base < 0: behind the last page)
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            const int p = base + (tid >> 5) * (32 * kEach) + 32 * k + lane;
-            v[k] = base >= 0 && p < m.num_pages && p >= 0 ? m.ref_count[p] : 1;
+            // (a round may end past 2^31: unsigned, as a signed sum would have no value there)
+            const uint32_t p = (uint32_t)base + (tid >> 5) * (32 * kEach) + 32 * k + lane;
+            v[k] = base >= 0 && p < (uint32_t)m.num_pages ? m.ref_count[p] : 1;
         }
     };
     auto round = [&](int base, int (&v)[kEach]) {
