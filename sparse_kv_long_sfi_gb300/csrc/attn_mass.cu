@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kLongThreads, 1)
     __shared__ __align__(16) uint4 s_answer;
     __shared__ __align__(8) uint64_t answered, item_full[2], item_read[2];
     __shared__ __align__(8) uint64_t k_full[2], part_full[2], full[T::kStages], empty[T::kStages];
-    __shared__ __align__(8) uint64_t s_full[2][4], s_empty[2][4];  // of a tile's products, in turn
+    __shared__ __align__(8) uint64_t s_full[2][4], s_empty[2][4], products_end[2];  // of a tile's products, in turn
     __shared__ MassItem s_item[2];
     __shared__ __align__(16) float s_lse[T::kStages][ROWS];  // -lse in log2 units
     __shared__ int s_bad[T::kStages];                        // a tile of K: a page of the item is out of range
@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(kLongThreads, 1)
             mbar_init(&item_read[i], kLongWarps + 2);
             mbar_init(&k_full[i], kLongWarps / 2 * 32);
             mbar_init(&part_full[i], kLongWarps / 4);
+            mbar_init(&products_end[i], 1);
         }
         fence_barrier_init();
     }
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(kLongThreads, 1)
             auto next_slot = [&]() {
                 const int slot = use % T::kStages;
                 fine = use < T::kStages || tc_wait(&empty[slot], (use / T::kStages - 1) & 1);
-                ++use;
+                use += fine;
                 return slot;
             };
             for (int i = 0; fine; ++i) {
@@ -301,6 +302,7 @@ __global__ void __launch_bounds__(kLongThreads, 1)
                     __syncwarp();
                 }
             }
+            drain_ring(full, use);
         } else if (warp < kLongWarps + 3) {
             // ---- one thread for each of the two tiles (see tc_wait_one) ----
             const int t = warp - kLongWarps - 1;
@@ -332,6 +334,7 @@ __global__ void __launch_bounds__(kLongThreads, 1)
                         mma_commit(&s_full[t][own & 3]);
                     }
                 }
+                drain_products(&products_end[t]);
             }
         }
     } else {
@@ -485,7 +488,7 @@ __global__ void __launch_bounds__(kShortThreads, 2)
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *ring = smem + T::kRowBytes;
     __shared__ __align__(8) uint64_t q_full, full[kStages], empty[kStages];
-    __shared__ __align__(8) uint64_t s_full[2], s_empty[2];
+    __shared__ __align__(8) uint64_t s_full[2], s_empty[2], products_end;
     __shared__ __align__(16) float s_lse[ROWS];  // -lse in log2 units
     __shared__ int s_bad[kStages];               // a page of the slot's tile is out of range
     __shared__ uint32_t s_tmem;
@@ -518,6 +521,7 @@ __global__ void __launch_bounds__(kShortThreads, 2)
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
         mbar_init(&q_full, 1);
+        mbar_init(&products_end, 1);
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 4);
@@ -582,6 +586,8 @@ __global__ void __launch_bounds__(kShortThreads, 2)
                             (page * p.hkv + kvh) * kSubTokens, &full[slot]);
             }
         }
+        drain_ring(full, use);
+        tc_wait(&q_full, 0);
     } else if (warp == kShortWarps + 1) {
         const uint32_t qa = smem_u32(smem), ra = smem_u32(ring);
         fine = tc_wait(&q_full, 0);
@@ -603,6 +609,7 @@ __global__ void __launch_bounds__(kShortThreads, 2)
             __syncwarp();
             ++use;
         }
+        if (lane == 0) drain_products(&products_end);
     } else {
         // ---- one position per thread; the warpgroups take the seen tiles in turn ----
         const int group = warp >> 2;

@@ -136,6 +136,19 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
                  : "memory");
 }
 
+// The end of a role: what it has on its way should not land when the CTA's shared and tensor memory are another's. While
+// all goes well there is nothing to wait for; once a wait of the CTA has run out there may be (bounded like every wait).
+// The copies of `used` uses of a ring (by a warp; each slot's earlier ones have been waited for):
+template <int STAGES>
+__device__ __forceinline__ void drain_ring(uint64_t (&full)[STAGES], int used) {
+    for (int u = max(0, used - STAGES); u < used; ++u) tc_wait(&full[u % STAGES], (u / STAGES) & 1);
+}
+// the products that this thread has issued (`bar` has a count of 1 and no other use):
+__device__ __forceinline__ void drain_products(uint64_t *bar) {
+    mma_commit(bar);
+    tc_wait_one(bar, 0);
+}
+
 // ---- arithmetic on pairs and triples ---------------------------------------------------------------
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
@@ -201,7 +214,10 @@ __device__ __forceinline__ bool take_next_cta(void *answer, uint64_t *bar, uint3
                  "r"(smem_u32(bar))
                  : "memory");
     late = !tc_wait_one(bar, parity);
-    if (late) return false;
+    if (late) {
+        tc_wait_one(bar, parity);  // (the answer should not land in another CTA's shared memory)
+        return false;
+    }
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .b128 a;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"

@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     __shared__ __align__(8) uint64_t answered, item_full[2], item_read[2];
     __shared__ __align__(8) uint64_t q_full[2], q_free, loads_done, near_end, tail_ready, tail_done[2];
     __shared__ __align__(8) uint64_t full[T::kStages], empty[T::kStages];
-    __shared__ __align__(8) uint64_t s_full[2], p_ready[2][2], o_done[2], turn[2];
+    __shared__ __align__(8) uint64_t s_full[2], p_ready[2][2], o_done[2], turn[2], products_end[2];
     __shared__ PromptItem s_item[2], s_mine[8];  // s_mine: of each softmax warp, for what hardly ever happens at its end
     __shared__ uint32_t s_tmem;
     __shared__ int s_bad[2];  // of an item (even, odd): it writes no output
@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             mbar_init(&p_ready[i][1], kTileRows);
             mbar_init(&o_done[i], 1);
             mbar_init(&turn[i], 1);
+            mbar_init(&products_end[i], 1);
         }
         fence_barrier_init();
     }
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kCopyWarp) {
             // ---- Q, then K and V tile by tile ----
-            int use = 0, loaded = 0;  // tiles of K and V, items with any
+            int use = 0, loaded = 0, pairs = 0;  // tiles of K and V, items with any, and with two tiles of Q
             bool fine = true;
             for (int i = 0; fine; ++i) {
                 fine = tc_wait(&item_full[i & 1], (i >> 1) & 1);
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 // (an item's scores are all formed then, and its page errors read)
                 fine = loaded == 0 || tc_wait(&q_free, (loaded - 1) & 1);
                 if (!fine) break;
+                pairs += w.tiles == 2;
                 if (lane == 0) {
                     s_bad[loaded & 1] = 0;
                     for (int t = 0; t < w.tiles; ++t) {
@@ -168,6 +170,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     }
                 }
                 __syncwarp();
+                ++loaded;
                 const int32_t *ptab = p.page_table + (int64_t)it.r * p.max_pages;
                 auto page_of = [&](int step) -> int {
                     const int v = step * kTilePages + (lane & 7);
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     const uint32_t take = __ballot_sync(0xffffffffu, ok && lane < kTilePages);
                     if (listed && !ok && lane < kTilePages) {
                         report(p.dev_status, SFI_DEV_BAD_PAGE);
-                        s_bad[loaded & 1] = 1;
+                        s_bad[(loaded - 1) & 1] = 1;
                     }
                     for (int kv = 0; kv < 2; ++kv, ++use) {
                         const int slot = use % T::kStages;
@@ -204,9 +207,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 }
                 __syncwarp();
                 if (lane == 0 && fine) mbar_arrive(&loads_done);  // s_bad of this item is final
-                ++loaded;
             }
             if (!fine && lane == 0) report(p.dev_status, SFI_DEV_TIMEOUT);
+            drain_ring(full, use);
+            if (loaded > 0) tc_wait(&q_full[0], (loaded - 1) & 1);
+            if (pairs > 0) tc_wait(&q_full[1], (pairs - 1) & 1);
         } else if ((warp == kMmaWarp || warp == kMmaWarp + 1) && lane == 0) {
             // ---- a tile's matrix instructions: S(0), then PV(j) and S(j + 1) ----
             // A thread issues 8 of them in the time that they take, so what it waits for and signals in between has to
@@ -293,6 +298,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 }
             }
             if (!fine) report(p.dev_status, SFI_DEV_TIMEOUT);
+            drain_products(&products_end[t]);
         } else if (warp == kItemWarp) {
             // ---- the items, and the tails of V ----
             bool fine = true, left = true;

@@ -139,6 +139,9 @@ __global__ void __launch_bounds__(kStepThreads, 2)
         const int st = (v - page0) % T::kStages;
         if (!mbar_wait_warp(&full[warp][st], ((v - page0) / T::kStages) & 1)) {
             late = true;
+            // (the ring has another use below: what is on its way lands first, within the same limits)
+            for (int u = v - page0; u < min(page1, v + T::kStages) - page0; ++u)
+                mbar_wait_warp(&full[warp][u % T::kStages], (u / T::kStages) & 1);
             break;
         }
         const uint32_t ka = smem_u32(ring + st * 2 * T::kPageBytes), va = ka + T::kPageBytes;
