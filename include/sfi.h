@@ -120,6 +120,8 @@ typedef enum {
 #define SFI_MAX_VOCAB 1048576
 /* Most requests in one sfi_page_reserve call. */
 #define SFI_MAX_PAGE_REQS 1024
+/* Most pages of a map in sfi_page_compact (its plan counts past the last one in 32 bits). */
+#define SFI_MAX_COMPACT_PAGES 2147475456
 
 /* Attention geometry shared by all calls. */
 typedef struct {
@@ -714,6 +716,7 @@ SFI_API sfi_status sfi_page_free(const sfi_page_map *map, const int32_t *reqs, i
  *   workspace : sfi_page_workspace_size(map) bytes, 16-byte aligned; no initial contents;
  *               launches sharing it must not overlap
  * table_out and ref_out must not be the map's own arrays.
+ * num_pages <= SFI_MAX_COMPACT_PAGES.
  * Device errors: SFI_DEV_BAD_LEN, SFI_DEV_BAD_PAGE (entries that are out of range are copied
  * as they are).
  */

@@ -11,7 +11,7 @@ from .api import (SFI_ATTN_EARLY_KV_PREFETCH, SFI_ATTN_RAGGED, SFI_ATTN_TEST_WIT
                   alloc_multi_workspace, rope_turns, sfi_qk_norm_rope,
                   CompactKV4, PagedKV4, alloc_kv4_compact, alloc_kv4_pool, alloc_kv4_workspace, sfi_kv4_append,
                   sfi_kv4_compact_gather, sfi_kv4_dense_attn, sfi_kv4_fast_attn, sfi_kv4_read,
-                  sfi_kv4_workspace_size, SFI_MAX_PAGE_REQS, PageMap, PagePools, alloc_page_workspace,
+                  sfi_kv4_workspace_size, SFI_MAX_PAGE_REQS, SFI_MAX_COMPACT_PAGES, PageMap, PagePools, alloc_page_workspace,
                   sfi_page_compact, sfi_page_copy, sfi_page_fork, sfi_page_free, sfi_page_reserve,
                   sfi_page_trim, sfi_page_workspace_size, SFI_MAX_VOCAB, sfi_attn_mass, sfi_kv_evict,
                   sfi_verify_tokens, sfi_window_attn,
@@ -29,7 +29,7 @@ __all__ = [
     "PagedKV", "Rope", "SFIError", "rope_turns", "sfi_qk_norm_rope",
     "CompactKV4", "PagedKV4", "alloc_kv4_compact", "alloc_kv4_pool", "alloc_kv4_workspace", "sfi_kv4_append",
     "sfi_kv4_compact_gather", "sfi_kv4_dense_attn", "sfi_kv4_fast_attn", "sfi_kv4_read", "sfi_kv4_workspace_size",
-    "SFI_MAX_PAGE_REQS", "PageMap", "PagePools", "alloc_page_workspace", "sfi_page_compact", "sfi_page_copy",
+    "SFI_MAX_PAGE_REQS", "SFI_MAX_COMPACT_PAGES", "PageMap", "PagePools", "alloc_page_workspace", "sfi_page_compact", "sfi_page_copy",
     "sfi_page_fork", "sfi_page_free", "sfi_page_reserve", "sfi_page_trim", "sfi_page_workspace_size",
     "SFI_MAX_VOCAB", "sfi_attn_mass", "sfi_kv_evict", "sfi_verify_tokens", "sfi_window_attn", "alloc_mixed_workspace", "alloc_multi_workspace", "alloc_ragged_workspace",
     "alloc_workspace", "sfi_compact_gather", "sfi_dense_verify_attn", "sfi_fast_decode_attn",

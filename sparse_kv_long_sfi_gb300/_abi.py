@@ -61,6 +61,7 @@ SFI_ATTN_RAGGED = 2
 SFI_ATTN_TEST_WITHHOLD = 4
 SFI_MAX_QUERY_TOKENS = 16
 SFI_MAX_PAGE_REQS = 1024
+SFI_MAX_COMPACT_PAGES = 2147475456
 SFI_MAX_VOCAB = 1048576
 
 P_SHAPE = ctypes.POINTER(sfi_attn_shape)

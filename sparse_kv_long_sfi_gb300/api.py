@@ -20,6 +20,7 @@ from . import _abi
 SFI_ATTN_EARLY_KV_PREFETCH = _abi.SFI_ATTN_EARLY_KV_PREFETCH
 SFI_MAX_QUERY_TOKENS = _abi.SFI_MAX_QUERY_TOKENS
 SFI_MAX_PAGE_REQS = _abi.SFI_MAX_PAGE_REQS
+SFI_MAX_COMPACT_PAGES = _abi.SFI_MAX_COMPACT_PAGES
 SFI_MAX_VOCAB = _abi.SFI_MAX_VOCAB
 SFI_ATTN_RAGGED = _abi.SFI_ATTN_RAGGED
 SFI_ATTN_TEST_WITHHOLD = _abi.SFI_ATTN_TEST_WITHHOLD

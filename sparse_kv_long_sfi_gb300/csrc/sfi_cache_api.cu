@@ -363,6 +363,7 @@ sfi_status sfi_page_compact(const sfi_page_map *map, const sfi_page_pools *pools
     sfi_status st = check_map(map);
     if (st != SFI_OK) return st;
     if ((st = check_pools(pools)) != SFI_OK) return st;
+    if (map->num_pages > SFI_MAX_COMPACT_PAGES) return SFI_ERR_UNSUPPORTED;
     if (!table_out || !ref_out || !live_out || pools->num_pages < map->num_pages) return SFI_ERR_INVALID_ARG;
     if (table_out == map->page_table || ref_out == map->ref_count) return SFI_ERR_INVALID_ARG;
     if (!workspace || !aligned16(workspace) || workspace_bytes < sfi::page_workspace_bytes(map->num_pages))
