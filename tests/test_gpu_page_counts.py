@@ -34,3 +34,5 @@ def test_the_last_of_all_page_ids(free):
     assert table[0, :len(ids)].tolist() == sorted(ids) and (ref_count[ids] == 1).all()
     sfi.sfi_page_reserve(m, None, want + 16, workspace=ws, dev_status=st)
     assert st.item() == 64 and lens.item() == want.item()
+    del ref_count, ws, m
+    torch.cuda.empty_cache()
