@@ -753,7 +753,9 @@ SFI_API size_t sfi_page_workspace_size(const sfi_page_map *map);
  *   q   : bf16, 16-byte aligned; token t of request r starts at element (r num_tokens + t) *
  *         q_stride, its heads are contiguous [Hq][D]; q_stride is a multiple of 8. q has num_reqs
  *         requests (request ids are below that). Token t < n_r is at position L_r - n_r + t.
- *   out : bf16 [B][num_tokens][Hq][D], 16-byte aligned (rounded once from fp32);
+ *   out : bf16 [B][num_tokens][Hq][D], 16-byte aligned (sums in fp32, rounded at the end). The weights
+ *         that meet V have two bf16 terms in calls of up to 16 query rows per KV head (num_tokens G),
+ *         one in longer calls (off by 2^-8 of sum w |v| at most).
  *   lse : fp32 [B][num_tokens][Hq] or NULL. Rows of tokens t >= n_r are not written. A token that
  *         sees nothing (S = 0, W = 0) gets out = 0 and lse = -inf.
  * What a token does not see has no influence on it, NaN and infinities included. Outputs must not

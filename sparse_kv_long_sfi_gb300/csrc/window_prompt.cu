@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 __syncwarp();
                 const PromptItem own = s_mine[warp];
                 const PromptWork all(own, p, per_tile);
-                mend_rows<D>(p, own.r, own.kvh, own.L, own.n, all.p0, all.p1,
+                mend_rows<D, false>(p, own.r, own.kvh, own.L, own.n, all.p0, all.p1,
                              (own.tok0 << shift) + t * kTileRows + (warp & 3) * 32, odd && write, m, l, 0, 32 * (D / 4));
             }
             tc_fence_before();  // O has been read: the next item's first weights let it be overwritten

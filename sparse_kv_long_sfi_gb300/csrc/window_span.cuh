@@ -67,6 +67,15 @@ __device__ __forceinline__ bool all_see(int v, int n, const RowWindow &first, co
 // block do not see, but were multiplied with, lies at the edges of their windows: a few hundred positions at most,
 // however long the context is.
 
+// Weights as two bf16 terms each. The first is the weight cut off, so that the second, with 2^-23 of the weight added,
+// is above zero when the weight is: an infinity of V stays one in both products.
+__device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t &hi, uint32_t &lo) {
+    constexpr float kMore = 1.f + 0x1p-23f;
+    const uint32_t x = __float_as_uint(a) & 0xffff0000u, y = __float_as_uint(b) & 0xffff0000u;
+    hi = x >> 16 | y;
+    lo = pack_bf16x2(fmaf(a, kMore, -__uint_as_float(x)), fmaf(b, kMore, -__uint_as_float(y)));
+}
+
 // A pair of bf16 values with a NaN or infinity among them.
 __device__ __forceinline__ bool nonfinite_pair(uint32_t v) {
     return (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
@@ -82,7 +91,8 @@ __device__ __forceinline__ bool hidden_nonfinite(const WindowParams &p, int r, i
     for (int v0 = from / kSubTokens * kSubTokens; v0 < to; v0 += kSubTokens) {
         const int page = p.page_table[(int64_t)r * p.max_pages + span.page(v0 / kSubTokens)];
         if (page < 0 || page >= p.num_pages) continue;
-        const uint32_t *v = reinterpret_cast<const uint32_t *>(p.v_pool + ((int64_t)page * p.hkv + kvh) * kSubTokens * D) + lane;
+        const int64_t row = ((int64_t)page * p.hkv + kvh) * kSubTokens;
+        const uint32_t *v = reinterpret_cast<const uint32_t *>(p.v_pool + row * D) + lane;
         uint32_t odd = 0;
 #pragma unroll
         for (int j = 0; j < kSubTokens; ++j)
@@ -98,13 +108,14 @@ __device__ __forceinline__ bool hidden_nonfinite(const WindowParams &p, int r, i
 }
 
 // The rows `need` (a bit each) of the 16 rows from row0 on (row = token * G + head of one KV head) computed again from
-// the positions that each sees, by a whole warp. Lane i < 16 has row i's maximum m (log2 units) and sum l. Values that are
-// not finite stay out of the product and are added to the rows that see them. Writes the values 4 piece0 .. 4 piece1 - 1
-// of the 16 x D. Fragments come straight from memory: 16 rows of 131072 positions take 30 ms, 256 rows of
-// eight warps 120 (the prompt kernel's other roles wait two seconds for them, some two million positions).
-template <int D>
-__device__ __forceinline__ void window_rows(const WindowParams &p, int r, int kvh, int L, int n, int row0, uint32_t need, float m,
-                                            float l, int piece0, int piece1) {
+// the positions that each sees, by a whole warp, with weights of one or two bf16 terms. Lane i < 16 has row i's maximum
+// m (log2 units) and sum l. Values that are not finite stay out of the product and are added to the rows that see them.
+// Writes the values 4 piece0 .. 4 piece1 - 1 of the 16 x D. Fragments come straight from memory: 16 rows of 131072
+// positions take 30 ms, 256 rows of eight warps 120 (the prompt kernel's other roles wait two seconds for them, some two
+// million positions).
+template <int D, bool TWO_TERMS>
+__device__ __forceinline__ void window_rows(const WindowParams &p, int r, int kvh, int L, int n, int row0, uint32_t need,
+                                            float m, float l, int piece0, int piece1) {
     constexpr int kDims = 64, kTiles = kDims / 8;  // dims of a pass (few registers: the caller keeps its own)
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, G = p.group;
     int pos[2];  // of rows g and g + 8
@@ -118,7 +129,8 @@ __device__ __forceinline__ void window_rows(const WindowParams &p, int r, int kv
         const float top = __shfl_sync(0xffffffffu, m, i), sum = __shfl_sync(0xffffffffu, l, i);
         base[half] = top == -INFINITY ? 0.f : top;
         inv[half] = sum == 0.f ? 0.f : 1.f / sum;
-        q[half] = p.q + ((int64_t)r * p.tokens + tok) * p.q_stride + ((int64_t)kvh * G + row % G) * D + 2 * t;
+        const int64_t head = (int64_t)kvh * G + row % G;
+        q[half] = p.q + ((int64_t)r * p.tokens + tok) * p.q_stride + head * D + 2 * t;
     }
     const int high = __reduce_max_sync(0xffffffffu, max(pos[0], pos[1]));
     const int low = __reduce_min_sync(0xffffffffu, min(pos[0] < 0 ? high : pos[0], pos[1] < 0 ? high : pos[1]));
@@ -147,10 +159,11 @@ __device__ __forceinline__ void window_rows(const WindowParams &p, int r, int kv
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    mma_bf16_16816(s[h], qa[0], qa[1], qa[2], qa[3], *reinterpret_cast<const uint32_t *>(k + h * 8 * D + ks),
+                    mma_bf16_16816(s[h], qa[0], qa[1], qa[2], qa[3],
+                                   *reinterpret_cast<const uint32_t *>(k + h * 8 * D + ks),
                                    *reinterpret_cast<const uint32_t *>(k + h * 8 * D + ks + 8));
             }
-            uint32_t see[2], pa[2][2];
+            uint32_t see[2], pa[2][2], pb[2][2];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int end = pos[half] + 1;
@@ -164,7 +177,8 @@ __device__ __forceinline__ void window_rows(const WindowParams &p, int r, int kv
                         w[e] = see[half] >> (8 * h + 2 * t + e) & 1u
                                    ? fast_exp2(fmaf(s[h][2 * half + e], p.scale_log2, -base[half]))
                                    : 0.f;
-                    pa[half][h] = pack_bf16x2(w[0], w[1]);
+                    if (TWO_TERMS) split_bf16x2(w[0], w[1], pa[half][h], pb[half][h]);
+                    else pa[half][h] = pack_bf16x2(w[0], w[1]);
                 }
             }
             const uint16_t *v = reinterpret_cast<const uint16_t *>(p.v_pool + at) + 2 * t * D + d0 + g;
@@ -180,6 +194,7 @@ __device__ __forceinline__ void window_rows(const WindowParams &p, int r, int kv
                     b[h] = x | y << 16;
                 }
                 mma_bf16_16816(o[i], pa[0][0], pa[1][0], pa[0][1], pa[1][1], b[0], b[1]);
+                if (TWO_TERMS) mma_bf16_16816(o[i], pb[0][0], pb[1][0], pb[0][1], pb[1][1], b[0], b[1]);
             }
             if (!__any_sync(0xffffffffu, odd)) continue;
 #pragma unroll 1
@@ -206,18 +221,19 @@ __device__ __forceinline__ void window_rows(const WindowParams &p, int r, int kv
             for (int j = 0; j < kTiles; ++j) {
                 const int d = d0 + j * 8 + 2 * t, piece = i * (D / 4) + d / 4;
                 if (piece >= piece0 && piece < piece1)
-                    *reinterpret_cast<uint32_t *>(out + d) = pack_bf16x2(o[j][2 * half] * inv[half], o[j][2 * half + 1] * inv[half]);
+                    *reinterpret_cast<uint32_t *>(out + d) =
+                        pack_bf16x2(o[j][2 * half] * inv[half], o[j][2 * half + 1] * inv[half]);
             }
         }
     }
 }
 
 // What a warp does about rows of a block (tokens at p0 .. p1) that came out not finite: those of row0 + lane where `odd`
-// is set, with their maxima and sums. Writes the values 4 piece0 .. 4 piece1 - 1 of the 32 x D. (Not inline, and
-// in passes of 64 dims: inline, or with all dims at once, it cost the prompt kernel registers and 1 to 6% of its speed.)
-template <int D>
-__device__ __noinline__ void mend_rows(const WindowParams &p, int r, int kvh, int L, int n, int p0, int p1, int row0, bool odd,
-                                       float m, float l, int piece0, int piece1) {
+// is set, with their maxima and sums. Writes the values 4 piece0 .. 4 piece1 - 1 of the 32 x D. (Not inline, and in
+// passes of 64 dims: inline, or with all dims at once, it cost the prompt kernel registers and 1 to 6% of its speed.)
+template <int D, bool TWO_TERMS>
+__device__ __noinline__ void mend_rows(const WindowParams &p, int r, int kvh, int L, int n, int p0, int p1, int row0,
+                                       bool odd, float m, float l, int piece0, int piece1) {
     const int lane = threadIdx.x & 31, G = p.group;
     const WindowSpan span(p0, p1, p.sink, p.recent);
     const RowWindow first(min(L - n + row0 / G, p1), p.sink, p.recent, span);
@@ -230,10 +246,11 @@ __device__ __noinline__ void mend_rows(const WindowParams &p, int r, int kvh, in
     // (a score that is not finite leaves nothing finite)
     const uint32_t need = __ballot_sync(0xffffffffu, odd && hit && l < INFINITY);
     for (int half = 0; half < 32; half += 16) {
-        const float top = __shfl_sync(0xffffffffu, m, half | (lane & 15)), sum = __shfl_sync(0xffffffffu, l, half | (lane & 15));
+        const float top = __shfl_sync(0xffffffffu, m, half | (lane & 15));
+        const float sum = __shfl_sync(0xffffffffu, l, half | (lane & 15));
         if (need >> half & 0xffffu)
-            window_rows<D>(p, r, kvh, L, n, row0 + half, need >> half & 0xffffu, top, sum, piece0 - half * (D / 4),
-                           piece1 - half * (D / 4));
+            window_rows<D, TWO_TERMS>(p, r, kvh, L, n, row0 + half, need >> half & 0xffffu, top, sum,
+                                      piece0 - half * (D / 4), piece1 - half * (D / 4));
     }
 }
 

@@ -5,7 +5,8 @@
 // arithmetic is small. So a unit (request, KV head) is spread over a cluster of up to eight CTAs of four
 // warps; each warp takes an equal run of the unit's pages and streams it through its own ring of pages
 // by TMA, with no barrier between warps. S = Q K^T and O += P V are mma.sync.m16n8k16 (tcgen05 would
-// want 64 rows at least, and its hand-overs between warps cost a short step more than they save).
+// want 64 rows at least, and its hand-overs between warps cost a short step more than they save). P has two
+// bf16 terms (as in the decode attention), which costs nothing: up to eight rows leave half of a fragment free.
 // Parts meet once: within a CTA through shared memory, then every CTA pushes each share of the rows to
 // the CTA that writes it, through distributed shared memory, behind one cluster barrier.
 // 32 requests, 32/8/128 heads, window 4096: 84 us (95% of the measured copy bandwidth); 16 requests, 16/8/128
@@ -35,7 +36,8 @@ struct StepTile {
 
 }  // namespace
 
-template <int D>
+// EIGHT: at most eight query rows per unit (the other half of a fragment's rows holds the low parts of P).
+template <int D, bool EIGHT>
 __global__ void __launch_bounds__(kStepThreads, 2)
     window_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ WindowParams p) {
@@ -171,11 +173,13 @@ __global__ void __launch_bounds__(kStepThreads, 2)
                     keep[i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
             }
         }
-        uint32_t pa[2][2];  // P of rows g, g + 8: slots 0-7 and 8-15
+        // P of rows g, g + 8: slots 0-7 and 8-15. As two bf16 terms (2^-16 of a weight at most is lost): the low ones
+        // are rows 8 to 15 of the same product where those are free, else a product of their own.
+        uint32_t pa[2][2], pb[2][2];
         bool moved = false;
         float alpha[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < (EIGHT ? 1 : 2); ++h) {
             float top = fmaxf(fmaxf(x[h][0], x[h][1]), fmaxf(x[h][2], x[h][3]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -188,9 +192,13 @@ __global__ void __launch_bounds__(kStepThreads, 2)
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = fast_exp2(fmaf(x[h][i], p.scale_log2, -base));
             l[h] = l[h] * alpha[h] + ((w[0] + w[1]) + (w[2] + w[3]));
-            // bf16 weights (off by 2^-8 of each at most): the output has no more bits
-            pa[h][0] = pack_bf16x2(w[0], w[1]);
-            pa[h][1] = pack_bf16x2(w[2], w[3]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) split_bf16x2(w[2 * i], w[2 * i + 1], pa[h][i], pb[h][i]);
+        }
+        if (EIGHT) {
+            alpha[1] = alpha[0];
+            pa[1][0] = pb[0][0];
+            pa[1][1] = pb[0][1];
         }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -215,6 +223,10 @@ __global__ void __launch_bounds__(kStepThreads, 2)
             }
             mma_bf16_16816(o[2 * j], pa[0][0], pa[1][0], pa[0][1], pa[1][1], b0, b1);
             mma_bf16_16816(o[2 * j + 1], pa[0][0], pa[1][0], pa[0][1], pa[1][1], b2, b3);
+            if (!EIGHT) {
+                mma_bf16_16816(o[2 * j], pb[0][0], pb[1][0], pb[0][1], pb[1][1], b0, b1);
+                mma_bf16_16816(o[2 * j + 1], pb[0][0], pb[1][0], pb[0][1], pb[1][1], b2, b3);
+            }
         }
         __syncwarp();  // the page has been read
         if (v + T::kStages < page1) request(v + T::kStages);
@@ -230,8 +242,13 @@ __global__ void __launch_bounds__(kStepThreads, 2)
     float *mine = reinterpret_cast<float *>(ring);  // [16][D]
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) {
-        *reinterpret_cast<float2 *>(mine + g * D + ((i * 8 + 2 * t) ^ ((g & 3) << 3))) = make_float2(o[i][0], o[i][1]);
-        *reinterpret_cast<float2 *>(mine + (g + 8) * D + ((i * 8 + 2 * t) ^ ((g & 3) << 3))) = make_float2(o[i][2], o[i][3]);
+        float *to = mine + g * D + ((i * 8 + 2 * t) ^ ((g & 3) << 3));
+        if (EIGHT) {
+            *reinterpret_cast<float2 *>(to) = make_float2(o[i][0] + o[i][2], o[i][1] + o[i][3]);
+        } else {
+            *reinterpret_cast<float2 *>(to) = make_float2(o[i][0], o[i][1]);
+            *reinterpret_cast<float2 *>(to + 8 * D) = make_float2(o[i][2], o[i][3]);
+        }
     }
     if (t == 0) {
         s_m[warp][g] = m[0];
@@ -324,7 +341,8 @@ __global__ void __launch_bounds__(kStepThreads, 2)
     __syncthreads();
     if (warp > 0 || s_odd == 0) return;
     const int row = min(lane, rows - 1);
-    mend_rows<D>(p, r, kvh, L, n, L - n, L - 1, 0, lane < rows && (s_odd >> row & 1u), s_top[row], s_sum[row], rank * share, piece1);
+    mend_rows<D, true>(p, r, kvh, L, n, L - n, L - 1, 0, lane < rows && (s_odd >> row & 1u), s_top[row], s_sum[row],
+                       rank * share, piece1);
 }
 
 namespace {
@@ -338,9 +356,9 @@ int step_cluster(int64_t units, int pages, int sms) {
     return c == 1 && pages >= 32 * kStepWarps ? 2 : c;
 }
 
-template <int D>
+template <int D, bool EIGHT>
 cudaError_t launch_step(const WindowMaps &maps, const WindowParams &p, int batch, cudaStream_t stream) {
-    auto kernel = window_step_kernel<D>;
+    auto kernel = window_step_kernel<D, EIGHT>;
     static std::atomic<uint64_t> configured{0};
     cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kernel), StepTile<D>::kSmem, configured);
     if (e != cudaSuccess) return e;
@@ -371,7 +389,10 @@ cudaError_t launch_step(const WindowMaps &maps, const WindowParams &p, int batch
 
 cudaError_t launch_window_step(const WindowMaps &maps, const WindowParams &p, int head_dim, int batch,
                                cudaStream_t stream) {
-    return head_dim == 128 ? launch_step<128>(maps, p, batch, stream) : launch_step<64>(maps, p, batch, stream);
+    const bool eight = (int64_t)p.tokens * p.group <= 8;
+    const auto launch = head_dim == 128 ? (eight ? launch_step<128, true> : launch_step<128, false>)
+                                        : (eight ? launch_step<64, true> : launch_step<64, false>);
+    return launch(maps, p, batch, stream);
 }
 
 }  // namespace sfi
