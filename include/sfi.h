@@ -39,17 +39,19 @@
  *     SFI_ERR_CUDA.
  *   - Device-side errors never trap: the kernel ORs an SFI_DEV_* bit into
  *     *dev_status (optional; may be NULL) and skips the offending unit's writes.
- *     In the attention calls the unit is a (request, KV head): when any of its
- *     page ids is out of range, or one of its waits runs out, none of its outputs,
- *     log-sum-exps or score entries is written (the caller's values stay), in every
- *     split plan; other units are unaffected.
+ *     In the attention calls the unit is a (request, KV head), or what the call says:
+ *     when any of its page ids is out of range, or one of its waits runs out, none of
+ *     its outputs, log-sum-exps or score entries is written (the caller's values stay),
+ *     in every split plan; other units are unaffected.
  *   - Per-request arrays (q, out, lse, scores, seq_lens, page_table rows,
  *     k_per_req, counts, compact rows) are indexed by the request id r. An entry
  *     point processes `batch` requests: r = req_ids[b] when req_ids is non-NULL
  *     (a subset of a larger batch, e.g. the slow subset of a mixed step), else
- *     r = b. req_ids must not repeat an id within one call.
+ *     r = b. req_ids must not repeat an id within one call. A call that is not told how
+ *     many requests there are takes the ids as they are.
  *   - Supported: head_dim 64 or 128, page_size 16, G in {1, 2, 4, 8}. Q/K/V are
- *     bf16; outputs, LSE and scores are fp32; positions are int32.
+ *     bf16; outputs, LSE and scores are fp32 unless the call says otherwise; positions
+ *     are int32.
  *   - LSE is the natural log of sum_j exp(scale * q . k_j) over the attended
  *     positions.
  */
@@ -763,7 +765,7 @@ SFI_API size_t sfi_page_workspace_size(const sfi_page_map *map);
  * Device errors: SFI_DEV_BAD_INDEX (a request id outside [0, num_reqs)), SFI_DEV_BAD_LEN (n_r < 0,
  * n_r > num_tokens, L_r < n_r or L_r beyond the page table): that request is skipped.
  * SFI_DEV_BAD_PAGE, SFI_DEV_TIMEOUT (the tokens whose block reads that page are not written: up to
- * 256 / G tokens of a KV head's query heads).
+ * 256 / G tokens of a KV head's query heads; of up to 16 query rows per KV head, all of them).
  */
 SFI_API sfi_status sfi_window_attn(const sfi_attn_shape *shape, const sfi_paged_kv *kv, int32_t sink, int32_t recent,
                                    const void *q, int64_t q_stride, int32_t num_reqs, int32_t num_tokens,
@@ -782,8 +784,8 @@ SFI_API sfi_status sfi_window_attn(const sfi_attn_shape *shape, const sfi_paged_
  *   mass : fp32 [B][Hkv][mass_stride], mass_stride >= max L
  * The result does not depend on the order in which the GPU runs the call. A request may appear once in it.
  * Device errors: SFI_DEV_BAD_INDEX, SFI_DEV_BAD_LEN (as for sfi_window_attn, or L_r > mass_stride):
- * that request is skipped. SFI_DEV_BAD_PAGE, SFI_DEV_TIMEOUT (that block of 256 positions is not
- * written).
+ * that request is skipped. SFI_DEV_BAD_PAGE, SFI_DEV_TIMEOUT (the block of positions that holds the page
+ * is not written: 128 in calls of up to 128 query rows per KV head, else 256).
  */
 SFI_API sfi_status sfi_attn_mass(const sfi_attn_shape *shape, const sfi_paged_kv *kv, int32_t sink, int32_t recent,
                                  const void *q, int64_t q_stride, int32_t num_reqs, int32_t num_tokens,
@@ -808,8 +810,8 @@ SFI_API sfi_status sfi_attn_mass(const sfi_attn_shape *shape, const sfi_paged_kv
  *   new_lens  : int32 [B], the rows that are left; not seq_lens
  * A request may appear once in a call.
  * Limits: as for sfi_select_topk.
- * Device errors: SFI_DEV_BAD_LEN (L_r < 0, beyond the page table or > mass_stride), SFI_DEV_K_OVERFLOW
- * (that request is skipped), SFI_DEV_BAD_PAGE (that row stays as it was).
+ * Device errors: SFI_DEV_BAD_LEN (L_r < 0, beyond the page table or > mass_stride), SFI_DEV_K_OVERFLOW:
+ * nothing of that request is written. SFI_DEV_BAD_PAGE (that row stays as it was).
  */
 SFI_API sfi_status sfi_kv_evict(const sfi_attn_shape *shape, const sfi_paged_kv *kv, const float *mass,
                                 int64_t mass_stride, int32_t sink, int32_t recent, const int32_t *k_per_req,

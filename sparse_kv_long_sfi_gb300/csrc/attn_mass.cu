@@ -25,8 +25,8 @@
 // tensor memory (480 cycles of a warp beside the products) and waits are not hidden by four warps per scheduler. Slower:
 // half of a step's columns read while half of the last are summed (317 us where this takes 256), both tiles' positions in
 // each thread (304, with half of the reads of shared memory).
-// The last 64 tokens of 8 x 16384, 16/8/128 heads: 52 us (80% of the measured copy
-// bandwidth).
+// The last 64 tokens of 8 x 16384, 16/8/128 heads: 52 us (79% of the measured copy
+// bandwidth). A CTA's run follows the table's and the weights' width: 123 us where these are 131072 positions wide.
 #include <algorithm>
 #include <atomic>
 

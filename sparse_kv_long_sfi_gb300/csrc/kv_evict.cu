@@ -4,7 +4,7 @@
 // The choice is that of the Selector (select_topk.cu), which serves rows of more than 16384 candidates
 // here too. Its passes are laid out for long rows; the caches that are evicted from are short, so up to
 // that length one CTA keeps all keys in registers and counts them in one small histogram per pass of
-// 8 bits (16 x 8 units of 1792 candidates: 18 us there, 9 here).
+// 8 bits (16 x 8 units of 1792 candidates: 18 us there, 10 here, each alone).
 //
 // Row i of what remains comes from position
 //   src(i) = i for i < min(S, L),  idx[i - S] for the chosen ones,  L - W + (i - S - count) behind them,
@@ -17,9 +17,10 @@
 // 64- to 256-byte columns until there are enough CTAs; a ring of kEvictStages chunks by cp.async
 // keeps their reads in flight, and positions and page ids are fetched one and two chunks further ahead.
 // Weights go to a second buffer (they are also the Selector's input), in the same launch.
-// 16 requests of 8 x 2112 rows cut to 2048 (128-dim heads): 31 us, the choice 5 of them (264 MB, 38.9 us of HBM
-// time, but most of it stays in L2); 8 of 7001 to 16384 cut to about 1100: 30 us, the choice 14 of them
-// (76 MB, 11.3 us).
+// 16 requests of 8 x 2112 rows cut to 2048 (128-dim heads): 31 us, the move alone 28 (264 MB, 38.9 us of HBM
+// time, but most of it stays in L2); 8 of 7001 to 16384 cut to about 1100: 30 us, the choice alone 14.5 and the move
+// 19.5 (76 MB, 11.3 us). Which kernel chooses follows the width of the weights, not the rows' lengths: the first of
+// these takes 40 us in weights of 131072.
 //
 // It writes bf16 pages, so it does not release its dependents early (see page_ops.cu).
 #include <algorithm>

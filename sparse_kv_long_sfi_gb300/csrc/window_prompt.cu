@@ -25,9 +25,11 @@
 // A zero weight times a NaN is a NaN in a matrix product, so V's rows behind the last position (stale
 // bytes of a page's tail) are zeroed in shared memory, and a row whose output is not finite, because of what
 // it does not see, is computed again from the positions it sees alone (mend_rows).
-// 16/8/128 heads: two prompts of 8192 tokens with window 1024 138 us (53% of the measured bf16 rate: 1280 keys are
+// 16/8/128 heads: two prompts of 8192 tokens with window 1024 139 us (53% of the measured bf16 rate: 1280 keys are
 // multiplied for 1088 that are seen, and a CTA's first and last steps are masked), one causal prompt of 8192 206 us (71%);
-// 32/8/128 heads, 16384 tokens: 1.47 ms (80%). In the loop a step of 256 rows x 128 keys takes 3080 cycles (84%).
+// 32/8/128 heads, 16384 tokens: 1.47 ms (80%). In the loop a step of 256 rows x 128 keys takes 3080 cycles, its 32
+// products nominally 2048 of them. A NaN of V that all rows of a prompt of 8192 see: 230 us; one that all but its last
+// token do not see: 6.1 ms, for the rows of that one block.
 #include <algorithm>
 #include <atomic>
 

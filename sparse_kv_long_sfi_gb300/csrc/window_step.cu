@@ -6,10 +6,11 @@
 // warps; each warp takes an equal run of the unit's pages and streams it through its own ring of pages
 // by TMA, with no barrier between warps. S = Q K^T and O += P V are mma.sync.m16n8k16 (tcgen05 would
 // want 64 rows at least, and its hand-overs between warps cost a short step more than they save). P has two
-// bf16 terms (as in the decode attention), which costs nothing: up to eight rows leave half of a fragment free.
+// bf16 terms (as in the decode attention), which costs nothing up to eight rows, which leave half of a fragment free,
+// and 1% above.
 // Parts meet once: within a CTA through shared memory, then every CTA pushes each share of the rows to
 // the CTA that writes it, through distributed shared memory, behind one cluster barrier.
-// 32 requests, 32/8/128 heads, window 4096: 84 us (95% of the measured copy bandwidth); 16 requests, 16/8/128
+// 32 requests, 32/8/128 heads, window 4096: 85 us (94% of the measured copy bandwidth); 16 requests, 16/8/128
 // heads, window 256: 6.7 us (latency).
 #include <algorithm>
 #include <atomic>
